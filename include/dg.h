@@ -304,6 +304,190 @@ dg_status dg_decode_step_weights(const dg_linear* ops, int n_ops, void* ws, size
  * 0 for n_ops <= 0.  Host-only; touches no device. */
 size_t dg_workspace_bytes(const dg_linear* ops, int n_ops);
 
+/* ---- the rest of a decoder layer -------------------------------------------------
+ * What a decoder runs between its weight products, for the 1..16 new tokens per
+ * sequence of a decode or verify step: norms, rotary positions and the cache
+ * append, attention over the cache, and (sparse decoders) an expert layer.
+ * The pages name these steps without formulas (single-request decode over a
+ * KV cache and draft / verify tokens: EdgeFM, sections 2.B and 2.C); each
+ * declaration states the definition.  All arithmetic is fp32 or wider; each
+ * 16-bit output is rounded to nearest even once. */
+
+/* A paged key / value cache of `batch` sequences.  Sequence b's position j lies
+ * in page block_table[b * table_stride + j / page_size], slot j % page_size;
+ * its key of head g starts at
+ *   k + page * page_stride + slot * token_stride + g * head_stride
+ * (strides in elements, the same for k and v; the head_dim values of one head
+ * are contiguous), so [page][slot][head][dim] and [page][head][slot][dim] both
+ * fit.  seq_lens[b] counts the step's new tokens too.  Positions from
+ * max_pages * page_size on and positions whose page id is outside
+ * [0, num_pages) do not exist: the append writes nothing there and no token
+ * sees them.  The table and the lengths are device memory, read when the
+ * kernels run, so a captured graph follows them. */
+typedef struct {
+    int32_t type;      /* dg_ftype of the cache and of q, k, v, out */
+    int32_t batch;
+    int32_t kv_heads;
+    int32_t head_dim;  /* multiple of 8, at most 256 */
+    int32_t page_size;
+    int32_t num_pages;
+    int32_t max_pages; /* pages per sequence in block_table */
+    int32_t reserved;  /* must be 0 */
+    void* k;
+    void* v;
+    int64_t page_stride;
+    int64_t token_stride;
+    int64_t head_stride;
+    const int32_t* block_table;
+    int64_t table_stride;
+    const int32_t* seq_lens; /* [batch] */
+} dg_paged_kv;
+
+/* Rotary positions on a step's q and k, and k and v into their cache slots.
+ * Token t = b * q_len + i (i < q_len) has position p = seq_lens[b] - q_len + i.
+ * With half = rot_dim / 2, c = cos[p][j], s = sin[p][j] (fp32 [max_pos][half])
+ * and the pair (x, y) at dims (j, j + half), or (2j, 2j + 1) if interleaved:
+ *   (x, y) -> (x c - y s, y c + x s)           fp32, one rounding
+ * dims from rot_dim on are copied.  q [batch * q_len][heads][head_dim] goes to
+ * q_out (which may be q), k and v [batch * q_len][kv_heads][head_dim] to the
+ * cache; *_stride are the elements from one token to the next, so q, k and v
+ * may be columns of one q|k|v result.  A token with p < 0 (a sequence shorter
+ * than the step) or, when rotating, p >= max_pos writes zeros to q_out and
+ * nothing to the cache.  q may be NULL (heads 0): no q to rotate; rot_dim 0:
+ * cos and sin are not read.  Two sequences must not share the page that they
+ * append to.  Any 2-byte alignment works; 16-byte aligned pointers and strides
+ * and rot_dim a multiple of 16 take the vector path. */
+typedef struct {
+    dg_paged_kv kv;
+    int32_t q_len;       /* 1..16 */
+    int32_t heads;
+    int32_t rot_dim;     /* even, at most head_dim */
+    int32_t interleaved; /* 0 or 1 */
+    int32_t max_pos;
+    int32_t reserved;    /* must be 0 */
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    const float* cos;
+    const float* sin;
+} dg_append;
+dg_status dg_kv_append(const dg_append* op, dg_stream stream);
+
+/* Attention of a step's new tokens over the paged cache (which already holds
+ * their keys and values).  Query head h reads key / value head
+ * h / (heads / kv_heads).  Token i of sequence b stands at
+ * p = seq_lens[b] - q_len + i and sees the existing positions j with
+ *   j <= p  and  (window == 0  or  j > p - window  or  j < sinks):
+ * all of the past, or the last `window` positions plus the first `sinks` ones.
+ *   z_j = scale * (q . k_j),  out = sum_j e^(z_j) v_j / sum_j e^(z_j),
+ *   lse = log sum_j e^(z_j)                       (lse may be NULL)
+ * A token that sees nothing (p < 0, no existing page), or whose visible scores
+ * are all -infinity, gets out = 0 and lse = -infinity.  Values at positions a
+ * token does not see never reach it, whatever they hold (NaN and infinity
+ * too); visible ones follow IEEE.  q [batch * q_len][heads][head_dim] with
+ * q_stride elements between tokens, out likewise; lse fp32
+ * [batch * q_len][heads].  heads is a multiple of kv_heads, 1 <= q_len <= 16.
+ * q, out, k, v 16-byte aligned, strides multiples of 8.  Sums, the running
+ * maximum and the joined parts are fp32; the result does not depend on the
+ * order in which CTAs run.  ws: dg_attn_workspace_bytes(op) bytes, 16-byte
+ * aligned, overwritten (nothing needs to be zeroed); a call that may overlap
+ * another needs its own. */
+typedef struct {
+    dg_paged_kv kv;
+    int32_t q_len;
+    int32_t heads;
+    int32_t window; /* 0: no window */
+    int32_t sinks;
+    float scale;
+    int32_t reserved; /* must be 0 */
+    const void* q;
+    void* out;
+    float* lse;
+    int64_t q_stride, out_stride;
+} dg_attn;
+dg_status dg_attn_decode(const dg_attn* op, void* ws, size_t ws_bytes, dg_stream stream);
+/* Workspace of dg_attn_decode; 0 for an op that it would refuse. */
+size_t dg_attn_workspace_bytes(const dg_attn* op);
+
+/* The norms around a block, with its gate and residual scale.  Per row:
+ *   r  = y, then (w_post) norm(r; w_post, b_post), then (gate) r * gate
+ *   h' = alpha * h + beta * r             -> h_out    (r absent without y)
+ *   x  = norm(h'; w_pre, b_pre)           -> x_out    (h' before its rounding)
+ * with norm(v; w, b) = u / sqrt(mean(u^2) + eps) * (w_offset + w) + b, where
+ * u = v (DG_NORM_RMS) or v - mean(v) (DG_NORM_LAYER), evaluated in fp32.
+ * y, x_out, gate and the weights have type `type`; h and h_out have type
+ * `type`, or are fp32 with h_f32.  All [rows][N] row-major; gate is [rows][N],
+ * or one row [N] for all with gate_rows = 1.  May be NULL: y (with w_post and
+ * gate), w_post, b_post, gate, b_pre, h (alpha * h is then absent; y must be
+ * given), h_out or x_out (not both; w_pre is needed only with x_out).  h_out
+ * may be h or (same type) y, x_out may be y or (same type) h; other overlaps
+ * are not allowed.  1 <= N <= 32768; any 2-byte (fp32: 4-byte) alignment
+ * works, 16-byte aligned pointers and N a multiple of 8 take the vector path. */
+typedef enum { DG_NORM_RMS = 0, DG_NORM_LAYER = 1 } dg_norm_kind;
+typedef struct {
+    int32_t type; /* dg_ftype */
+    int32_t kind; /* dg_norm_kind */
+    int32_t rows, N;
+    int32_t h_f32;
+    int32_t gate_rows; /* 0 without gate, else 1 or rows */
+    float alpha, beta, eps, w_offset;
+    const void* y;
+    const void* w_post;
+    const void* b_post;
+    const void* gate;
+    const void* h;
+    const void* w_pre;
+    const void* b_pre;
+    void* h_out;
+    void* x_out;
+} dg_norm;
+dg_status dg_norm_residual(const dg_norm* op, dg_stream stream);
+
+/* A mixture-of-experts layer for a few tokens, 1 <= M <= 16.
+ *   z = x * router^T;  prob = softmax(z) (or sigmoid(z) with DG_MOE_SIGMOID)
+ *   the top_k experts of each token by prob, the lowest index on ties; a NaN
+ *   counts below every number; weight = prob, divided by the chosen ones' sum
+ *   with renormalize; times route_scale
+ *   h_e = silu(x * W_gate[e]^T) * (x * W_up[e]^T)
+ *   y = sum over the chosen e of weight_e * (h_e * W_down[e]^T)   (+ residual)
+ * x, y, residual [M][K]; router [E][K] in x's type; W_gate, W_up [E][I][K] and
+ * W_down [E][K][I] in the format `kind`: DG_LINEAR_F16, DG_LINEAR_BF16, or
+ * DG_LINEAR_W4A16 (packed int4 [E][rows][cols / 2], fp16 scales
+ * [E][rows][cols / group_size], x and y fp16).  h is kept in fp32.  ids int32 [M][top_k] and weights fp32
+ * [M][top_k], both optional, receive the routing in descending order of prob.  Each expert's
+ * weights are read once for all of its tokens.  K and I multiples of 8 (fp16,
+ * bf16) or of group_size, itself a multiple of 32 (int4); 1 <= E <= 1024,
+ * 1 <= top_k <= min(E, 16); pointers 16-byte aligned (scales 2, residual 2,
+ * ids and weights 4).  y may be residual or x.  ws: dg_moe_workspace_bytes(op)
+ * bytes, 16-byte aligned, overwritten; a call that may overlap another needs
+ * its own. */
+typedef enum { DG_MOE_SOFTMAX = 0, DG_MOE_SIGMOID = 1 } dg_moe_score;
+typedef struct {
+    int32_t kind; /* dg_kind */
+    int32_t M, K, I, E, top_k;
+    int32_t group_size; /* int4 only */
+    int32_t score;      /* dg_moe_score */
+    int32_t renormalize;
+    float route_scale;
+    const void* x;
+    const void* router;
+    const void* W_gate;
+    const void* W_up;
+    const void* W_down;
+    const void* gate_scale; /* int4 only */
+    const void* up_scale;
+    const void* down_scale;
+    const void* residual; /* optional */
+    void* y;
+    int32_t* ids;   /* optional */
+    float* weights; /* optional */
+} dg_moe;
+dg_status dg_moe_forward(const dg_moe* op, void* ws, size_t ws_bytes, dg_stream stream);
+/* Workspace of dg_moe_forward; 0 for an op that it would refuse. */
+size_t dg_moe_workspace_bytes(const dg_moe* op);
+
 /* Synchronizes `stream`, then reports DG_ERR_CUDA for a sticky CUDA error or
  * DG_ERR_TIMEOUT if a bounded device-side wait gave up on the current device
  * since the last call (clearing that flag).  DG_OK otherwise. */

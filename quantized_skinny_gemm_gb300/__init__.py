@@ -16,6 +16,9 @@ __all__ = [
     "quantize_act_i8", "lm_head_argmax", "lm_head_argmax_noalloc", "decode_step_weights", "workspace_bytes",
     "EPI_NONE", "EPI_RESIDUAL", "EPI_SWIGLU", "ACT_NONE", "ACT_SILU", "linear_forward", "swiglu",
     "residual_add", "causal_conv1d_update", "quantize_weights_i8", "quantize_weights_w4",
+    "NORM_RMS", "NORM_LAYER", "MOE_SOFTMAX", "MOE_SIGMOID", "PagedKV", "Append", "Attention",
+    "Norm", "Moe", "paged_kv", "append", "kv_append", "attention", "attn_decode",
+    "attn_workspace_bytes", "norm", "norm_residual", "moe", "moe_forward", "moe_workspace_bytes",
     "check_device_status", "selftest_wait_timeout", "status_string", "probe_copy", "probe_read", "version",
     "library_path", "load",
 ]
@@ -27,6 +30,8 @@ F16, BF16 = 0, 1
 LINEAR_F16, LINEAR_BF16, LINEAR_W8A8, LINEAR_W4A16, LINEAR_W4A8 = range(5)
 EPI_NONE, EPI_RESIDUAL, EPI_SWIGLU = range(3)
 ACT_NONE, ACT_SILU = range(2)
+NORM_RMS, NORM_LAYER = range(2)
+MOE_SOFTMAX, MOE_SIGMOID = range(2)
 _STATUS = ["DG_OK", "DG_ERR_INVALID_ARG", "DG_ERR_UNSUPPORTED", "DG_ERR_MISALIGNED",
            "DG_ERR_WORKSPACE", "DG_ERR_CUDA", "DG_ERR_TIMEOUT"]
 
@@ -48,6 +53,70 @@ class Linear(ctypes.Structure):
         ("logits", ctypes.c_void_p), ("token", ctypes.c_void_p), ("acc_out", ctypes.c_void_p),
         ("epilogue", ctypes.c_int32), ("reserved", ctypes.c_int32), ("residual", ctypes.c_void_p),
         ("W2", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p),
+    ]
+
+
+class PagedKV(ctypes.Structure):
+    """Mirror of the C struct dg_paged_kv."""
+    _fields_ = [
+        ("type", ctypes.c_int32), ("batch", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64), ("block_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p),
+    ]
+
+
+class Append(ctypes.Structure):
+    """Mirror of the C struct dg_append."""
+    _fields_ = [
+        ("kv", PagedKV), ("q_len", ctypes.c_int32), ("heads", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("max_pos", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+        ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+    ]
+
+
+class Attention(ctypes.Structure):
+    """Mirror of the C struct dg_attn."""
+    _fields_ = [
+        ("kv", PagedKV), ("q_len", ctypes.c_int32), ("heads", ctypes.c_int32),
+        ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32), ("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+    ]
+
+
+class Norm(ctypes.Structure):
+    """Mirror of the C struct dg_norm."""
+    _fields_ = [
+        ("type", ctypes.c_int32), ("kind", ctypes.c_int32), ("rows", ctypes.c_int32),
+        ("N", ctypes.c_int32), ("h_f32", ctypes.c_int32), ("gate_rows", ctypes.c_int32),
+        ("alpha", ctypes.c_float), ("beta", ctypes.c_float), ("eps", ctypes.c_float),
+        ("w_offset", ctypes.c_float), ("y", ctypes.c_void_p), ("w_post", ctypes.c_void_p),
+        ("b_post", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("h", ctypes.c_void_p),
+        ("w_pre", ctypes.c_void_p), ("b_pre", ctypes.c_void_p), ("h_out", ctypes.c_void_p),
+        ("x_out", ctypes.c_void_p),
+    ]
+
+
+class Moe(ctypes.Structure):
+    """Mirror of the C struct dg_moe."""
+    _fields_ = [
+        ("kind", ctypes.c_int32), ("M", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("I", ctypes.c_int32), ("E", ctypes.c_int32), ("top_k", ctypes.c_int32),
+        ("group_size", ctypes.c_int32), ("score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32), ("route_scale", ctypes.c_float),
+        ("x", ctypes.c_void_p), ("router", ctypes.c_void_p), ("W_gate", ctypes.c_void_p),
+        ("W_up", ctypes.c_void_p), ("W_down", ctypes.c_void_p), ("gate_scale", ctypes.c_void_p),
+        ("up_scale", ctypes.c_void_p), ("down_scale", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ids", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
     ]
 
 
@@ -85,6 +154,10 @@ def load():
         "dg_quantize_weights_i8": [P, P, P, I, I, P],
         "dg_quantize_weights_w4": [P, P, P, I, I, I, P],
         "dg_probe_read": [P, Z, P, P],
+        "dg_kv_append": [P, P],
+        "dg_attn_decode": [P, P, Z, P],
+        "dg_norm_residual": [P, P],
+        "dg_moe_forward": [P, P, Z, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -92,6 +165,9 @@ def load():
         f.restype = ctypes.c_int
     lib.dg_workspace_bytes.argtypes = [P, I]
     lib.dg_workspace_bytes.restype = Z
+    for name in ("dg_attn_workspace_bytes", "dg_moe_workspace_bytes"):
+        getattr(lib, name).argtypes = [P]
+        getattr(lib, name).restype = Z
     lib.dg_status_string.argtypes = [I]
     lib.dg_status_string.restype = ctypes.c_char_p
     lib.dg_version.argtypes = []
@@ -230,6 +306,199 @@ def decode_step_weights(plan, ws=None, stream=None):
 def workspace_bytes(ops):
     arr = (Linear * len(ops))(*ops)
     return int(load().dg_workspace_bytes(ctypes.cast(arr, ctypes.c_void_p), len(ops)))
+
+
+# ---- the rest of a decoder layer ---------------------------------------------------
+# Builders make a descriptor from tensors (pointers, shapes and strides only;
+# keep the tensors alive), raising DGError where the tensors themselves do not
+# fit together; the entry points of the same C name then run it.
+
+def _fits(ok, where):
+    if not ok:
+        raise DGError(_STATUS.index("DG_ERR_INVALID_ARG"), where)
+
+
+def _ftype(t, where):
+    import torch
+    _fits(t.dtype in (torch.float16, torch.bfloat16), where)
+    return F16 if t.dtype == torch.float16 else BF16
+
+
+def _contiguous(where, dtype, *tensors):
+    for t in tensors:
+        _fits(t is None or (t.dtype == dtype and t.is_contiguous()), where)
+
+
+def _head_rows(t, tokens, heads, dim, dtype, where):
+    """Elements between the tokens of t [tokens][heads][dim], heads adjacent."""
+    if t.is_contiguous() and t.numel() == tokens * heads * dim:
+        t = t.view(tokens, heads, dim)
+    _fits(t.dtype == dtype and tuple(t.shape) == (tokens, heads, dim) and t.stride(2) == 1 and
+          (heads == 1 or t.stride(1) == dim), where)
+    return t.stride(0) if tokens > 1 else heads * dim
+
+
+def paged_kv(k_cache, v_cache, block_table, seq_lens):
+    """A paged cache: k_cache and v_cache [pages][page_size][kv_heads][head_dim]
+    (any strides with the last dimension contiguous and both alike, so a
+    [pages][kv_heads][page_size][head_dim] cache is passed transposed),
+    block_table int32 [batch][max_pages], seq_lens int32 [batch]."""
+    import torch
+    where = "paged_kv"
+    kind = _ftype(k_cache, where)
+    _fits(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and
+          k_cache.dtype == v_cache.dtype and k_cache.stride() == v_cache.stride() and
+          k_cache.stride(3) == 1, where)
+    _fits(block_table.dim() == 2 and block_table.dtype == torch.int32 and
+          (block_table.shape[1] <= 1 or block_table.stride(1) == 1), where)
+    _fits(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and
+          0 < seq_lens.numel() == block_table.shape[0], where)
+    pages, page_size, heads, dim = k_cache.shape
+    table_stride = max(block_table.stride(0), block_table.shape[1])
+    return PagedKV(kind, block_table.shape[0], heads, dim, page_size, pages,
+                   block_table.shape[1], 0, _ptr(k_cache), _ptr(v_cache), k_cache.stride(0),
+                   k_cache.stride(1), k_cache.stride(2), _ptr(block_table), table_stride,
+                   _ptr(seq_lens))
+
+
+def _kv_dtype(kv):
+    import torch
+    return torch.float16 if kv.type == F16 else torch.bfloat16
+
+
+def append(kv, q, k, v, q_out=None, q_len=1, cos=None, sin=None, interleaved=False):
+    """Describes kv_append: q [batch * q_len][heads][head_dim] (or None), k and v
+    with kv_heads heads; cos and sin fp32 [max_pos][rot_dim / 2], or None for no
+    rotation; q_out is q itself by default."""
+    import torch
+    where, dt = "append", _kv_dtype(kv)
+    _fits(q_len > 0, where)
+    tokens, dim = kv.batch * q_len, kv.head_dim
+    heads = 0 if q is None else q.numel() // (tokens * dim)
+    q_out = q if q_out is None else q_out
+    qs = qos = 0
+    if q is not None:
+        qs = _head_rows(q, tokens, heads, dim, dt, where)
+        qos = _head_rows(q_out, tokens, heads, dim, dt, where)
+    ks = _head_rows(k, tokens, kv.kv_heads, dim, dt, where)
+    vs = _head_rows(v, tokens, kv.kv_heads, dim, dt, where)
+    rot = max_pos = 0
+    if cos is not None:
+        _contiguous(where, torch.float32, cos, sin)
+        _fits(sin is not None and cos.dim() == 2 and cos.shape == sin.shape, where)
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    return Append(kv, q_len, heads, rot, int(interleaved), max_pos, 0, _ptr(q), _ptr(k), _ptr(v),
+                  _ptr(q_out), qs, ks, vs, qos, _ptr(cos), _ptr(sin))
+
+
+def kv_append(op, stream=None):
+    """Rotates a step's q and k and writes k and v into their cache slots."""
+    _call("dg_kv_append", ctypes.byref(op), _stream(stream))
+
+
+def attention(kv, q, out, lse=None, q_len=1, scale=None, window=0, sinks=0):
+    """Describes attn_decode: q and out [batch * q_len][heads][head_dim], lse
+    fp32 [batch * q_len][heads] or None; scale defaults to head_dim ** -0.5."""
+    import torch
+    where, dt = "attention", _kv_dtype(kv)
+    _fits(q_len > 0, where)
+    tokens, dim = kv.batch * q_len, kv.head_dim
+    heads = q.numel() // (tokens * dim)
+    qs = _head_rows(q, tokens, heads, dim, dt, where)
+    os_ = _head_rows(out, tokens, heads, dim, dt, where)
+    _contiguous(where, torch.float32, lse)
+    _fits(lse is None or lse.numel() == tokens * heads, where)
+    return Attention(kv, q_len, heads, window, sinks, dim ** -0.5 if scale is None else scale, 0,
+                     _ptr(q), _ptr(out), _ptr(lse), qs, os_)
+
+
+def attn_workspace_bytes(op):
+    return int(load().dg_attn_workspace_bytes(ctypes.byref(op)))
+
+
+def attn_decode(op, ws, stream=None):
+    """Attention of a step's new tokens over the paged cache."""
+    _call("dg_attn_decode", ctypes.byref(op), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def norm(h, h_out, x_out, w_pre=None, b_pre=None, y=None, w_post=None, b_post=None, gate=None,
+         alpha=1.0, beta=1.0, eps=1e-6, w_offset=0.0, kind=NORM_RMS):
+    """Describes norm_residual: h' = alpha h + beta gate norm_post(y) into h_out,
+    norm_pre(h') into x_out.  h and h_out in the type of the others or fp32;
+    gate has y's shape, or one row."""
+    import torch
+    where = "norm"
+    first = h if h is not None else y
+    _fits(first is not None, where)
+    shape = first.shape
+    N = shape[-1]
+    rows = first.numel() // N if N else 0
+    small = next((t for t in (y, x_out, w_pre, h, h_out) if t is not None and
+                  t.dtype != torch.float32), None)
+    _fits(small is not None, where)
+    dt, ftype = small.dtype, _ftype(small, where)
+    res = [t for t in (h, h_out) if t is not None]
+    h_f32 = int(bool(res) and res[0].dtype == torch.float32)
+    _contiguous(where, torch.float32 if h_f32 else dt, h, h_out)
+    _contiguous(where, dt, y, x_out, w_pre, b_pre, w_post, b_post, gate)
+    for t in (h, h_out, y, x_out):
+        _fits(t is None or t.numel() == rows * N, where)
+    for t in (w_pre, b_pre, w_post, b_post):
+        _fits(t is None or t.numel() == N, where)
+    _fits(gate is None or gate.numel() in (N, rows * N), where)
+    gate_rows = 0 if gate is None else gate.numel() // N
+    return Norm(ftype, kind, rows, N, h_f32, gate_rows, alpha, beta, eps, w_offset, _ptr(y),
+                _ptr(w_post), _ptr(b_post), _ptr(gate), _ptr(h), _ptr(w_pre), _ptr(b_pre),
+                _ptr(h_out), _ptr(x_out))
+
+
+def norm_residual(op, stream=None):
+    """The norms around a block with its gate and residual scale."""
+    _call("dg_norm_residual", ctypes.byref(op), _stream(stream))
+
+
+def moe(kind, x, y, router, W_gate, W_up, W_down, top_k, gate_scale=None, up_scale=None,
+        down_scale=None, residual=None, ids=None, weights=None, group_size=32,
+        score=MOE_SOFTMAX, renormalize=False, route_scale=1.0):
+    """Describes moe_forward: x, y, residual [M][K]; router [E][K]; W_gate, W_up
+    [E][I][K], W_down [E][K][I] (int4: packed, with scales [E][rows][cols / group]);
+    ids int32 and weights fp32 [M][top_k] receive the routing."""
+    import torch
+    where = "moe"
+    w4 = kind == LINEAR_W4A16
+    dt = torch.bfloat16 if kind == LINEAR_BF16 else torch.float16
+    K = x.shape[-1]
+    M = x.numel() // K if K else 0
+    _fits(router.dim() == 2 and W_gate.dim() == 3 and W_down.dim() == 3, where)
+    E, inter = router.shape[0], W_gate.shape[1]
+    _contiguous(where, dt, x, y, router, residual, gate_scale, up_scale, down_scale)
+    _contiguous(where, torch.uint8 if w4 else dt, W_gate, W_up, W_down)
+    _contiguous(where, torch.int32, ids)
+    _contiguous(where, torch.float32, weights)
+    cut = 2 if w4 else 1
+    _fits(router.shape[1] == K and tuple(W_gate.shape) == (E, inter, K // cut) and
+          W_up.shape == W_gate.shape and tuple(W_down.shape) == (E, K, inter // cut), where)
+    for t in (y, residual):
+        _fits(t is None or t.numel() == M * K, where)
+    for t in (ids, weights):
+        _fits(t is None or t.numel() == M * top_k, where)
+    if w4:
+        _fits(group_size > 0, where)
+        for t, rows, cols in ((gate_scale, inter, K), (up_scale, inter, K), (down_scale, K, inter)):
+            _fits(t is not None and t.numel() == E * rows * (cols // group_size), where)
+    return Moe(kind, M, K, inter, E, top_k, group_size if w4 else 0, score, int(renormalize),
+               route_scale, _ptr(x), _ptr(router), _ptr(W_gate), _ptr(W_up), _ptr(W_down),
+               _ptr(gate_scale), _ptr(up_scale), _ptr(down_scale), _ptr(residual), _ptr(y),
+               _ptr(ids), _ptr(weights))
+
+
+def moe_workspace_bytes(op):
+    return int(load().dg_moe_workspace_bytes(ctypes.byref(op)))
+
+
+def moe_forward(op, ws, stream=None):
+    """A mixture-of-experts layer for a few tokens."""
+    _call("dg_moe_forward", ctypes.byref(op), _ptr(ws), _nbytes(ws), _stream(stream))
 
 
 def check_device_status(stream=None):

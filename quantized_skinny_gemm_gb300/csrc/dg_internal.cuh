@@ -357,6 +357,13 @@ cudaError_t launch_conv1d_update(const void* x, void* state, const void* w, cons
 cudaError_t launch_quant_w8(const void* W, int8_t* Wq, float* s, int N, int K, cudaStream_t st);
 cudaError_t launch_quant_w4(const void* W, uint8_t* Wq, void* scales, int N, int K, int G,
                             cudaStream_t st);
+// The rest of a decoder layer (arguments checked by layer_api.cu).
+cudaError_t launch_kv_append(const dg_append& op, cudaStream_t s);
+cudaError_t launch_norm(const dg_norm& op, cudaStream_t s);
+size_t attn_ws_bytes(const dg_attn& op);
+cudaError_t launch_attn(const dg_attn& op, void* ws, cudaStream_t s);
+size_t moe_ws_bytes(const dg_moe& op);
+cudaError_t launch_moe(const dg_moe& op, void* ws, cudaStream_t s);
 cudaError_t launch_probe_read(const void* src, size_t bytes, uint32_t* sink, cudaStream_t s);
 
 }  // namespace dg

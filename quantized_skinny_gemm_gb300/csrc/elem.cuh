@@ -1,0 +1,64 @@
+// 16-bit element access shared by the layer kernels, for fp16 and bf16.
+#pragma once
+
+#include "dg_internal.cuh"
+
+namespace dg {
+
+template <bool BF16>
+__device__ __forceinline__ float elem_f32(uint16_t v) {
+    if (BF16) return __uint_as_float((uint32_t)v << 16);
+    return __half2float(__ushort_as_half(v));
+}
+
+// Round to nearest even into the 16-bit type.
+template <bool BF16>
+__device__ __forceinline__ uint16_t elem_16(float v) {
+    if (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    return __half_as_ushort(__float2half_rn(v));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 pair_f32(uint32_t v) {
+    if (BF16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    return __half22float2(u32_as_h2(v));
+}
+
+// (a in the low half, b in the high half)
+template <bool BF16>
+__device__ __forceinline__ uint32_t pair_16(float a, float b) {
+    if (BF16) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+        uint32_t u;
+        memcpy(&u, &p, 4);
+        return u;
+    }
+    return h2_as_u32(__floats2half2_rn(a, b));
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = pair_f32<BF16>(w[i]);
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pair_16<BF16>(f[0], f[1]), pair_16<BF16>(f[2], f[3]),
+                      pair_16<BF16>(f[4], f[5]), pair_16<BF16>(f[6], f[7]));
+}
+
+// The page of position j of sequence b, or -1 where the cache has none.
+__device__ __forceinline__ int page_of(const dg_paged_kv& kv, int b, int j) {
+    const int at = j / kv.page_size;
+    if (j < 0 || at >= kv.max_pages) return -1;
+    const int page = __ldg(kv.block_table + (long long)b * kv.table_stride + at);
+    return page >= 0 && page < kv.num_pages ? page : -1;
+}
+
+}  // namespace dg

@@ -1,0 +1,215 @@
+// The norms around a block, fused with its gate and residual scale.
+#include "elem.cuh"
+
+namespace dg {
+
+// Sum over the CTA, the same in every thread.  `red` alternates between two
+// halves from call to call, so one barrier per call is enough.
+__device__ __forceinline__ float cta_sum(float v, float (*red)[32], int& turn) {
+    v = warp_sum(v);
+    float* r = red[turn];
+    turn ^= 1;
+    const int warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    return warp_sum(lane < warps ? r[lane] : 0.f);
+}
+
+// Value j of chunk c of this thread is element ((c * blockDim.x + threadIdx.x) * U + j).
+template <int U, int C>
+struct RowRegs {
+    float v[C][U];
+};
+
+template <bool BF16, int U, int C>
+__device__ __forceinline__ void load_row(const void* p, int N, RowRegs<U, C>& r) {
+    const uint16_t* e = static_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int n = (c * blockDim.x + threadIdx.x) * U;
+        if (U == 8) {
+            float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (n < N) unpack8<BF16>(*reinterpret_cast<const uint4*>(e + n), f);
+#pragma unroll
+            for (int j = 0; j < U; ++j) r.v[c][j] = f[j];
+        } else {
+            r.v[c][0] = n < N ? elem_f32<BF16>(e[n]) : 0.f;
+        }
+    }
+}
+
+template <int U, int C>
+__device__ __forceinline__ void load_row_f32(const float* p, int N, RowRegs<U, C>& r) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int n = (c * blockDim.x + threadIdx.x) * U;
+        if (U == 8) {
+            float4 a = make_float4(0, 0, 0, 0), b = a;
+            if (n < N) {
+                a = *reinterpret_cast<const float4*>(p + n);
+                b = *reinterpret_cast<const float4*>(p + n + 4);
+            }
+            const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < U; ++j) r.v[c][j] = f[j];
+        } else {
+            r.v[c][0] = n < N ? p[n] : 0.f;
+        }
+    }
+}
+
+template <bool BF16, int U, int C>
+__device__ __forceinline__ void store_row(void* p, int N, const RowRegs<U, C>& r) {
+    uint16_t* e = static_cast<uint16_t*>(p);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int n = (c * blockDim.x + threadIdx.x) * U;
+        if (n >= N) continue;
+        if (U == 8) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = r.v[c][j % U];
+            *reinterpret_cast<uint4*>(e + n) = pack8<BF16>(f);
+        } else {
+            e[n] = elem_16<BF16>(r.v[c][0]);
+        }
+    }
+}
+
+template <int U, int C>
+__device__ __forceinline__ void store_row_f32(float* p, int N, const RowRegs<U, C>& r) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int n = (c * blockDim.x + threadIdx.x) * U;
+        if (n >= N) continue;
+        if (U == 8) {
+            *reinterpret_cast<float4*>(p + n) =
+                make_float4(r.v[c][0], r.v[c][1 % U], r.v[c][2 % U], r.v[c][3 % U]);
+            *reinterpret_cast<float4*>(p + n + 4) =
+                make_float4(r.v[c][4 % U], r.v[c][5 % U], r.v[c][6 % U], r.v[c][7 % U]);
+        } else {
+            p[n] = r.v[c][0];
+        }
+    }
+}
+
+// r <- norm(r; w, b) of dg_norm.  The row sits in registers, so the mean and
+// the centred squares are two exact passes over it, not one with cancellation.
+template <bool BF16, int U, int C>
+__device__ __forceinline__ void norm_row(const dg_norm& op, const void* w, const void* b,
+                                         RowRegs<U, C>& r, float (*red)[32], int& turn) {
+    const int N = op.N;
+    if (op.kind == DG_NORM_LAYER) {
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < U; ++j) s += r.v[c][j];
+        const float mean = cta_sum(s, red, turn) / (float)N;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if ((c * (int)blockDim.x + (int)threadIdx.x) * U < N) r.v[c][j] -= mean;
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < U; ++j) q = fmaf(r.v[c][j], r.v[c][j], q);
+    const float k = 1.f / sqrtf(cta_sum(q, red, turn) / (float)N + op.eps);
+    RowRegs<U, C> g;
+    load_row<BF16>(w, N, g);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < U; ++j) r.v[c][j] = r.v[c][j] * k * (op.w_offset + g.v[c][j]);
+    if (b) {
+        load_row<BF16>(b, N, g);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < U; ++j) r.v[c][j] += g.v[c][j];
+    }
+}
+
+// One CTA per row, the row held in registers (U values per vector, C vectors
+// per thread), so y and h are read once and h' and x written once.
+template <bool BF16, int U, int C>
+__global__ void __launch_bounds__(1024) k_norm(const dg_norm op) {
+    __shared__ float red[2][32];
+    int turn = 0;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int N = op.N;
+    const size_t at = (size_t)blockIdx.x * N;
+    RowRegs<U, C> hr, r;
+    if (op.h) {
+        if (op.h_f32)
+            load_row_f32(static_cast<const float*>(op.h) + at, N, hr);
+        else
+            load_row<BF16>(static_cast<const uint16_t*>(op.h) + at, N, hr);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < U; ++j) hr.v[c][j] *= op.alpha;
+    }
+    if (op.y) {
+        load_row<BF16>(static_cast<const uint16_t*>(op.y) + at, N, r);
+        if (op.w_post) norm_row<BF16>(op, op.w_post, op.b_post, r, red, turn);
+        if (op.gate) {
+            RowRegs<U, C> g;
+            load_row<BF16>(static_cast<const uint16_t*>(op.gate) + (op.gate_rows == 1 ? 0 : at), N, g);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int j = 0; j < U; ++j) r.v[c][j] *= g.v[c][j];
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                r.v[c][j] = op.h ? fmaf(op.beta, r.v[c][j], hr.v[c][j]) : op.beta * r.v[c][j];
+    } else {
+        r = hr;
+    }
+    if (op.h_out) {
+        if (op.h_f32)
+            store_row_f32(static_cast<float*>(op.h_out) + at, N, r);
+        else
+            store_row<BF16>(static_cast<uint16_t*>(op.h_out) + at, N, r);
+    }
+    if (op.x_out) {
+        norm_row<BF16>(op, op.w_pre, op.b_pre, r, red, turn);
+        store_row<BF16>(static_cast<uint16_t*>(op.x_out) + at, N, r);
+    }
+}
+
+template <bool BF16, int U>
+static const void* norm_fn(int C) {
+    if (C <= 1) return (const void*)k_norm<BF16, U, 1>;
+    if (C <= 2) return (const void*)k_norm<BF16, U, 2>;
+    if (U == 8) return (const void*)k_norm<BF16, U, 4>;
+    if (C <= 4) return (const void*)k_norm<BF16, U == 8 ? 1 : U, 4>;
+    if (C <= 8) return (const void*)k_norm<BF16, U == 8 ? 1 : U, 8>;
+    return (const void*)k_norm<BF16, U == 8 ? 1 : U, 32>;
+}
+
+cudaError_t launch_norm(const dg_norm& op, cudaStream_t s) {
+    bool vec = op.N % 8 == 0;
+    const void* ptrs[] = {op.y, op.w_post, op.b_post, op.gate, op.h, op.w_pre, op.b_pre, op.h_out, op.x_out};
+    for (const void* p : ptrs) vec = vec && ((uintptr_t)p & 15u) == 0;
+    const int U = vec ? 8 : 1;
+    const int vecs = (op.N + U - 1) / U;
+    int threads = (vecs + 31) / 32 * 32;
+    if (threads > 1024) threads = 1024;
+    const int C = (vecs + threads - 1) / threads;
+    const bool bf = op.type == DG_BF16;
+    const void* fn = vec ? (bf ? norm_fn<true, 8>(C) : norm_fn<false, 8>(C))
+                         : (bf ? norm_fn<true, 1>(C) : norm_fn<false, 1>(C));
+    void* args[] = {const_cast<dg_norm*>(&op)};
+    return launch_pdl(fn, dim3(op.rows), dim3(threads), 0, s, args);
+}
+
+}  // namespace dg
