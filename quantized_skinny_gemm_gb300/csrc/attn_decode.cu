@@ -1,92 +1,691 @@
 // Attention of a step's new tokens over the paged key-value cache.
+//
+// The cost is the cache: 4 * head_dim bytes per visible position and key /
+// value head, read once, against 4 * head_dim flops per query row, so up to a
+// few dozen rows per key / value head (query heads of the group x new tokens)
+// the kernel is bound by HBM as long as the rows share each key they read.
+// Rows therefore form 16-row tiles of mma.sync (m16n8k16, fp32 accumulators);
+// one stage of a warp is 16 keys and their values, copied into the warp's own
+// ring of shared memory by cp.async (16 bytes a lane: any page size, stride
+// and head size), so warps never wait for one another while they stream.
+//
+// Work split.  The visible positions of one (sequence, key / value head, row
+// group) are a unit of blocks of kBlockKeys positions.  All blocks of the call,
+// counted on the device from the lengths, are cut into one equal contiguous
+// range per CTA; a unit that lies in one CTA's range is finished there, one
+// that was cut leaves fp32 parts (maximum, sum, output) in the workspace that
+// k_attn_join adds in CTA order.  So ragged batches and single long sequences
+// load every SM alike, and no sum depends on timing.
+//
+// Softmax is one pass: each warp keeps the running maximum m and sum l of its
+// own positions and rescales its output when m grows; scores are kept in
+// units of log2(e), so that e^z = 2^z'.
+#include <climits>
+
 #include "elem.cuh"
+#include "tc_common.cuh"
 
 namespace dg {
 
-constexpr int kAttnThreads = 128;
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = kAttnWarps * 32;
+constexpr int kStageKeys = 16;
+constexpr int kBlockKeys = 2 * kAttnWarps * kStageKeys;  // 128
+constexpr int kAttnMaxCtas = 512;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// One CTA per query row (token and head); its threads share the positions,
-// each keeping its own running maximum, sum and output, joined at the end.
+struct AttnParams {
+    dg_attn op;
+    int groups;          // row groups of RT * 16 rows per (sequence, head)
+    int rows;            // q_len * heads / kv_heads
+    long long* prefix;   // [batch + 1] blocks of one head before each sequence
+    float* part;         // [grid][2] parts of RT * 16 rows
+};
+
+__device__ __forceinline__ float exp2_fast(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 template <bool BF16>
-__global__ void __launch_bounds__(kAttnThreads) k_attn_rows(const dg_attn op) {
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    if (BF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16 bytes from global to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fetch) {
+    const int n = fetch ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The positions some token of sequence b sees: [0, sinks) and [lo, end).
+struct Span {
+    int first;   // position of the step's first token (negative: before the start)
+    int sinks, lo, end;
+    __device__ __forceinline__ int count() const { return sinks + end - lo; }
+    __device__ __forceinline__ int position(int c) const { return c < sinks ? c : c - sinks + lo; }
+};
+__device__ __forceinline__ Span span_of(const dg_attn& op, int b) {
+    const int len = max(0, __ldg(op.kv.seq_lens + b));
+    const long long cap = (long long)op.kv.max_pages * op.kv.page_size;
+    Span s;
+    s.first = len - op.q_len;
+    s.end = (int)min((long long)len, cap);
+    const long long lo = op.window ? (long long)s.first - op.window + 1 : 0;
+    s.lo = (int)max(0ll, min(lo, (long long)s.end));
+    s.sinks = min(op.sinks, s.lo);
+    return s;
+}
+__device__ __forceinline__ int blocks_of(const Span& s) {
+    return max(1, (int)(((long long)s.count() + kBlockKeys - 1) / kBlockKeys));
+}
+
+// First block of CTA c's range.
+__device__ __forceinline__ long long range_at(long long c, long long total, int ctas) {
+    return c * total / ctas;
+}
+
+template <int DP, int RT>
+struct AttnShape {
+    static constexpr int kPitch = DP * 2 + 16;              // bytes; rows 16 bytes apart in banks
+    static constexpr int kStage = 2 * kStageKeys * kPitch;  // keys, then values
+    static constexpr int kStages = DP <= 64 ? 5 : DP <= 128 ? 3 : DP <= 192 ? 2 : 3;
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kRows = RT * 16;
+    static constexpr int kQ = kRows * kPitch;
+    static constexpr size_t kSmem = (size_t)kAttnWarps * kRing + kQ + 2 * kAttnWarps * kRows * 4;
+    static constexpr int kOutPitch = DP + 8;                // floats of a merged row
+    static constexpr int kPart = kRows * (DP + 2);          // floats of a part: m, l, then rows
+    static_assert(kRows * kOutPitch * 4 <= kRing, "a warp's output fits its ring");
+};
+
+template <bool BF16, int DP, int RT>
+__global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
+    using S = AttnShape<DP, RT>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ long long scan[kAttnThreads], found[4];
+    const dg_attn& op = p.op;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int D = op.kv.head_dim, G = op.heads / op.kv.kv_heads, B = op.kv.batch;
+    const int heads = op.kv.kv_heads * p.groups;   // units per sequence
+    unsigned char* ring = smem + warp * S::kRing;
+    const uint32_t ring_a = (uint32_t)__cvta_generic_to_shared(ring);
+    unsigned char* qs = smem + kAttnWarps * S::kRing;
+    const uint32_t qs_a = (uint32_t)__cvta_generic_to_shared(qs);
+    float* sm_m = reinterpret_cast<float*>(qs + S::kQ);
+    float* sm_l = sm_m + kAttnWarps * S::kRows;
+
     griddep_launch_dependents();
+    if (D < DP)  // dims past the head's read as zero, in q and in the ring
+        for (int i = tid; i < (kAttnWarps * S::kRing + S::kQ) / 16; i += kAttnThreads)
+            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     griddep_wait();
-    const int D = op.kv.head_dim, t = blockIdx.x, h = blockIdx.y;
-    const int b = t / op.q_len;
-    const int p = op.kv.seq_lens[b] - op.q_len + t % op.q_len;
-    const int g = h / (op.heads / op.kv.kv_heads);
-    __shared__ float q[256], part[kAttnThreads][33];
-    __shared__ float smax[kAttnThreads], ssum[kAttnThreads];
-    const uint16_t* qr = static_cast<const uint16_t*>(op.q) + t * op.q_stride + (long long)h * D;
-    for (int d = threadIdx.x; d < D; d += kAttnThreads) q[d] = elem_f32<BF16>(qr[d]);
-    __syncthreads();
-    float m = -INFINITY, l = 0.f;
-    const int last = (int)min((long long)p, (long long)op.kv.max_pages * op.kv.page_size - 1);
-    const int lo = op.window ? max(0, p - op.window + 1) : 0;
-    // the positions are walked once for the maximum and sum, then once per 32 dims
-    for (int pass = -1; pass < (D + 31) / 32; ++pass) {
-        float o[32];
+
+    // ---- this CTA's range of blocks -----------------------------------------------------
+    // Pass 0 counts all blocks; pass 1 finds the sequence of the range's first.
+    long long total = 0, begin = 0, end = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        long long carry = 0;
+        for (int b0 = 0; b0 < B; b0 += kAttnThreads) {
+            const int b = b0 + tid;
+            const int n = b < B ? blocks_of(span_of(op, b)) : 0;
+            long long inc = n;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        for (int j = threadIdx.x; j <= last; j += kAttnThreads) {
-            if (j < lo && j >= op.sinks) continue;
-            const int page = page_of(op.kv, b, j);
-            if (page < 0) continue;
-            const long long at = page * op.kv.page_stride +
-                                 (j % op.kv.page_size) * op.kv.token_stride + g * op.kv.head_stride;
-            const uint16_t* k = static_cast<const uint16_t*>(op.kv.k) + at;
-            const uint16_t* v = static_cast<const uint16_t*>(op.kv.v) + at;
-            float z = 0.f;
-            for (int d = 0; d < D; ++d) z = fmaf(q[d], elem_f32<BF16>(k[d]), z);
-            z *= op.scale;
-            if (pass < 0) {
-                const float nm = fmaxf(m, z);
-                if (z != z) {
-                    l = z;
-                } else if (nm != -INFINITY) {
-                    l = l * expf(m - nm) + expf(z - nm);
-                    m = nm;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += t;
+            }
+            if (lane == 31) scan[warp] = inc;
+            __syncthreads();
+            long long before = carry, sum = 0;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                if (w < warp) before += scan[w];
+                sum += scan[w];
+            }
+            const long long at = before + inc - n;
+            if (pass == 1 && b < B) {
+                if (blockIdx.x == 0) {
+                    p.prefix[b] = at;
+                    if (b == B - 1) p.prefix[B] = at + n;
                 }
-            } else {
-                const float w = z != z ? z : m == -INFINITY ? 0.f : expf(z - m);
+                if (begin >= at * heads && begin < (at + n) * heads) {
+                    found[0] = b;
+                    found[1] = at;
+                }
+            }
+            carry += sum;
+            __syncthreads();
+        }
+        if (pass == 0) {
+            total = carry * heads;
+            const int ctas = (int)min((long long)gridDim.x, total);
+            begin = range_at(blockIdx.x, total, ctas);
+            end = blockIdx.x < ctas ? range_at(blockIdx.x + 1, total, ctas) : begin;
+        }
+    }
+    if (begin >= end) return;
+    int b = (int)found[0];
+    long long seq_at = found[1] * heads;     // first block of sequence b
+
+    const float c2 = op.scale * kLog2e;
+    const int g = lane >> 2, t4 = lane & 3;
+    bool first_segment = true;
+
+    // ---- one segment (the range's part of one unit) after another ------------------------
+    for (long long blk = begin; blk < end;) {
+        Span sp = span_of(op, b);
+        int nb = blocks_of(sp);
+        while (blk >= seq_at + (long long)nb * heads) {
+            seq_at += (long long)nb * heads;
+            sp = span_of(op, ++b);
+            nb = blocks_of(sp);
+        }
+        const int unit = (int)((blk - seq_at) / nb);          // head and row group
+        const int kb = (int)(blk - seq_at - (long long)unit * nb);
+        const int ke = (int)min((long long)nb, kb + (end - blk));
+        const int hk = unit / p.groups, row0 = (unit - hk * p.groups) * S::kRows;
+        const int count = sp.count();
+        const int last = sp.first + op.q_len - 1;
+
+        // this warp's stages: keys kb * 128 + 64 i + 16 warp on
+        const int key0 = kb * kBlockKeys + warp * kStageKeys;
+        const int lim = min(count, ke * kBlockKeys);
+        constexpr int kStep = kAttnWarps * kStageKeys;
+        const int n = key0 < lim ? (lim - key0 + kStep - 1) / kStep : 0;
+
+        // Position and cache offset (elements; -1: nothing there) of key `lane` (lanes
+        // 0..15) of stage i.
+        auto locate = [&](int i, int& pos, long long& off) {
+            const int c = key0 + i * kStep + (lane & 15);
+            pos = INT_MAX;
+            off = -1;
+            if (i < n && c < lim) {
+                const int j = sp.position(c);
+                const int page = page_of(op.kv, b, j);
+                if (page >= 0) {
+                    pos = j;
+                    off = page * op.kv.page_stride + (j % op.kv.page_size) * op.kv.token_stride +
+                          hk * op.kv.head_stride;
+                }
+            }
+        };
+        auto issue = [&](int i, long long off) {
+            if (i < n) {
+                const uint32_t dst = ring_a + (i % S::kStages) * S::kStage;
+                constexpr int kChunks = DP / 8;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (pass * 32 + i < D) o[i] = fmaf(w, elem_f32<BF16>(v[pass * 32 + i]), o[i]);
+                for (int it = 0; it < kStageKeys * kChunks / 32; ++it) {
+                    const int idx = it * 32 + lane, row = idx / kChunks, ch = idx % kChunks;
+                    const long long o = __shfl_sync(0xffffffffu, off, row);
+                    if (ch * 8 < D) {
+                        const long long at = o < 0 ? 0 : o + ch * 8;
+                        const uint32_t d = dst + row * S::kPitch + ch * 16;
+                        cp_async16(d, static_cast<const uint16_t*>(op.kv.k) + at, o >= 0);
+                        cp_async16(d + kStageKeys * S::kPitch,
+                                   static_cast<const uint16_t*>(op.kv.v) + at, o >= 0);
+                    }
+                }
+            }
+            cp_commit();
+        };
+
+        int pos[S::kStages];          // positions of the stages in flight, by ring slot
+        long long off_next;
+        int pos_next;
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) {
+            long long off;
+            locate(i, pos[i], off);
+            issue(i, off);
+        }
+        locate(S::kStages - 1, pos_next, off_next);
+
+        // q rows of the unit, zero past the last
+        for (int i = tid; i < S::kRows * (DP / 8); i += kAttnThreads) {
+            const int r = i / (DP / 8), ch = i % (DP / 8), row = row0 + r;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < p.rows && ch * 8 < D) {
+                const int tok = row / G;
+                v = ld_cg16(static_cast<const uint16_t*>(op.q) +
+                            ((long long)b * op.q_len + tok) * op.q_stride +
+                            (long long)(hk * G + row - tok * G) * D + ch * 8);
+            }
+            *reinterpret_cast<uint4*>(qs + r * S::kPitch + ch * 16) = v;
+        }
+        __syncthreads();
+
+        float o[RT][DP / 8][4], m[RT][2], l[RT][2];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+#pragma unroll
+            for (int d = 0; d < DP / 8; ++d) o[r][d][0] = o[r][d][1] = o[r][d][2] = o[r][d][3] = 0.f;
+            m[r][0] = m[r][1] = -INFINITY;
+            l[r][0] = l[r][1] = 0.f;
+        }
+        // one tile: q stays in registers; several tiles read it again for every stage
+        uint32_t qf[RT == 1 ? DP / 16 : 1][4];
+        const uint32_t qa = qs_a + ((lane & 7) + ((lane >> 3) & 1) * 8) * S::kPitch + (lane >> 4) * 16;
+        if (RT == 1) {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) ldsm4(qf[RT == 1 ? k : 0], qa + k * 32);
+        }
+
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            cp_wait<S::kStages - 2>();
+            __syncwarp();
+            const int slot = i % S::kStages;
+            const uint32_t ka = ring_a + slot * S::kStage, va = ka + kStageKeys * S::kPitch;
+            int my_pos = pos[0];
+#pragma unroll
+            for (int q = 1; q < S::kStages; ++q)
+                if (slot == q) my_pos = pos[q];
+            // the slot that the last stage left is free: refill it
+            const int ni = i + S::kStages - 1, nslot = ni % S::kStages;
+#pragma unroll
+            for (int q = 0; q < S::kStages; ++q)
+                if (nslot == q) pos[q] = pos_next;
+            issue(ni, off_next);
+            locate(ni + 1, pos_next, off_next);
+
+            // scores of 16 keys
+            float s[RT][2][4];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) s[r][j][0] = s[r][j][1] = s[r][j][2] = s[r][j][3] = 0.f;
+            const uint32_t kl = ka + ((lane & 7) + (lane >> 4) * 8) * S::kPitch + ((lane >> 3) & 1) * 16;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+                uint32_t kf[4];
+                ldsm4(kf, kl + k * 32);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    uint32_t qr[4];
+                    if (RT > 1) ldsm4(qr, qa + r * 16 * S::kPitch + k * 32);
+                    const uint32_t(&a)[4] = RT == 1 ? qf[RT == 1 ? k : 0] : qr;
+                    mma16816<BF16>(s[r][0], a, kf[0], kf[1]);
+                    mma16816<BF16>(s[r][1], a, kf[2], kf[3]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[r][j][e] *= c2;
+
+            // masks, where some row does not see some key of the stage
+            const bool all = my_pos <= sp.first &&
+                             (!op.window || last - my_pos < op.window || my_pos < op.sinks);
+            unsigned poison = 0;
+            if (!__all_sync(0xffffffffu, all)) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int kp = __shfl_sync(0xffffffffu, my_pos, j * 8 + t4 * 2 + e);
+#pragma unroll
+                        for (int r = 0; r < RT; ++r)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int pr = sp.first + (row0 + r * 16 + g + h * 8) / G;
+                                const bool see = kp <= pr && (!op.window || pr - kp < op.window ||
+                                                              kp < op.sinks);
+                                if (!see) s[r][j][2 * h + e] = -INFINITY;
+                            }
+                    }
+                if (op.q_len > 1) {
+                    // a value that only some rows see must not meet the others' zero
+                    // weights if it is not finite: lanes 2k and 2k + 1 look at key k
+                    bool bad = false;
+                    const unsigned char* vr =
+                        ring + slot * S::kStage + (kStageKeys + (lane >> 1)) * S::kPitch + (lane & 1) * DP;
+                    constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
+#pragma unroll 4
+                    for (int q = 0; q < DP / 16; ++q) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(vr + q * 16);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            bad = bad || (w[x] & kExp) == kExp || ((w[x] >> 16) & kExp) == kExp;
+                    }
+                    poison = __ballot_sync(0xffffffffu, bad);
+                }
+            }
+
+            // running maximum, weights, rescaling
+            uint32_t pf[RT][4];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                float nm[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v = fmaxf(fmaxf(s[r][0][2 * h], s[r][0][2 * h + 1]),
+                                    fmaxf(s[r][1][2 * h], s[r][1][2 * h + 1]));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                    nm[h] = fmaxf(m[r][h], v);
+                }
+                if (__any_sync(0xffffffffu, nm[0] != m[r][0] || nm[1] != m[r][1])) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float f = nm[h] == m[r][h] ? 1.f : exp2_fast(m[r][h] - nm[h]);
+                        m[r][h] = nm[h];
+                        l[r][h] *= f;
+#pragma unroll
+                        for (int d = 0; d < DP / 8; ++d) {
+                            o[r][d][2 * h] *= f;
+                            o[r][d][2 * h + 1] *= f;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float base = m[r][h] == -INFINITY ? 0.f : m[r][h];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float a = exp2_fast(s[r][j][2 * h] - base);
+                        const float c = exp2_fast(s[r][j][2 * h + 1] - base);
+                        l[r][h] += a + c;
+                        // weights in [0, 1] meet the values as 16-bit numbers: what
+                        // the matrix instruction takes, 2^-12 (fp16) or 2^-9 (bf16) off
+                        pf[r][2 * j + h] = pair_16<BF16>(a, c);
+                        s[r][j][2 * h] = a;
+                        s[r][j][2 * h + 1] = c;
+                    }
+                }
+            }
+            if (poison) {
+                unsigned char* vb = ring + slot * S::kStage + kStageKeys * S::kPitch;
+#pragma unroll 1
+                for (int k = 0; k < kStageKeys; ++k) {
+                    if (!((poison >> (2 * k)) & 3u)) continue;
+                    const int kp = __shfl_sync(0xffffffffu, my_pos, k);
+                    const int src = (lane & ~3) | ((k & 7) >> 1);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float w00 = __shfl_sync(0xffffffffu, s[r][0][2 * h], src);
+                            const float w01 = __shfl_sync(0xffffffffu, s[r][0][2 * h + 1], src);
+                            const float w10 = __shfl_sync(0xffffffffu, s[r][1][2 * h], src);
+                            const float w11 = __shfl_sync(0xffffffffu, s[r][1][2 * h + 1], src);
+                            const float w = k < 8 ? ((k & 1) ? w01 : w00) : ((k & 1) ? w11 : w10);
+                            const int pr = sp.first + (row0 + r * 16 + g + h * 8) / G;
+                            const bool see = kp <= pr && (!op.window || pr - kp < op.window ||
+                                                          kp < op.sinks);
+                            if (see) {
+#pragma unroll
+                                for (int d = 0; d < DP / 8; ++d) {
+                                    const float2 v = pair_f32<BF16>(*reinterpret_cast<const uint32_t*>(
+                                        vb + k * S::kPitch + d * 16 + t4 * 4));
+                                    o[r][d][2 * h] = fmaf(w, v.x, o[r][d][2 * h]);
+                                    o[r][d][2 * h + 1] = fmaf(w, v.y, o[r][d][2 * h + 1]);
+                                }
+                            }
+                        }
+                    __syncwarp();
+                    for (int q = lane; q < DP / 8; q += 32)
+                        *reinterpret_cast<uint4*>(vb + k * S::kPitch + q * 16) = make_uint4(0, 0, 0, 0);
+                    __syncwarp();
+                }
+            }
+
+            // output += weights x values
+            const uint32_t vl = va + ((lane & 7) + ((lane >> 3) & 1) * 8) * S::kPitch + (lane >> 4) * 16;
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d) {
+                uint32_t vf[4];
+                ldsm4_t(vf, vl + d * 32);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    mma16816<BF16>(o[r][2 * d], pf[r], vf[0], vf[1]);
+                    mma16816<BF16>(o[r][2 * d + 1], pf[r], vf[2], vf[3]);
+                }
             }
         }
-        if (pass < 0) {
-            smax[threadIdx.x] = m;
-            ssum[threadIdx.x] = l;
-            __syncthreads();
-            float top = -INFINITY, sum = 0.f;
-            for (int i = 0; i < kAttnThreads; ++i) top = fmaxf(top, smax[i]);
-            for (int i = 0; i < kAttnThreads; ++i)
-                if (smax[i] != -INFINITY) sum += ssum[i] * expf(smax[i] - top);
-                else if (ssum[i] != ssum[i]) sum = ssum[i];
-            m = top;
-            l = sum;
-            if (threadIdx.x == 0 && op.lse)
-                op.lse[(long long)t * op.heads + h] = l == 0.f ? -INFINITY : m + logf(l);
-        } else {
-            for (int i = 0; i < 32; ++i) part[threadIdx.x][i] = o[i];
-            __syncthreads();
-            if (threadIdx.x < 32 && pass * 32 + (int)threadIdx.x < D) {
-                float s = 0.f;
-                for (int i = 0; i < kAttnThreads; ++i) s += part[i][threadIdx.x];
-                uint16_t* out = static_cast<uint16_t*>(op.out) + t * op.out_stride + (long long)h * D;
-                out[pass * 32 + threadIdx.x] = elem_16<BF16>(l == 0.f ? 0.f : s / l);
+        cp_wait<0>();
+        __syncwarp();
+
+        // ---- the four warps' parts, through shared memory ---------------------------------
+        float* wo = reinterpret_cast<float*>(ring);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l[r][h] += __shfl_xor_sync(0xffffffffu, l[r][h], 1);
+                l[r][h] += __shfl_xor_sync(0xffffffffu, l[r][h], 2);
+                const int row = r * 16 + g + h * 8;
+                if (t4 == 0) {
+                    sm_m[warp * S::kRows + row] = m[r][h];
+                    sm_l[warp * S::kRows + row] = l[r][h];
+                }
+#pragma unroll
+                for (int d = 0; d < DP / 8; ++d)
+                    *reinterpret_cast<float2*>(wo + row * S::kOutPitch + d * 8 + t4 * 2) =
+                        make_float2(o[r][d][2 * h], o[r][d][2 * h + 1]);
             }
+        }
+        __syncthreads();
+        const bool whole = kb == 0 && ke == nb;
+        float* part = p.part + ((size_t)blockIdx.x * 2 + (first_segment ? 0 : 1)) * S::kPart;
+        for (int i = tid; i < S::kRows * (DP / 8); i += kAttnThreads) {
+            const int r = i / (DP / 8), d = i % (DP / 8) * 8, row = row0 + r;
+            if (row >= p.rows || d >= D) continue;
+            float top = -INFINITY, sum = 0.f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sm_m[w * S::kRows + r]);
+            const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                const float f = exp2_fast(sm_m[w * S::kRows + r] - base);
+                sum = fmaf(f, sm_l[w * S::kRows + r], sum);
+                const float* src = reinterpret_cast<const float*>(smem + w * S::kRing) + r * S::kOutPitch + d;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) v[x] = fmaf(f, src[x], v[x]);
+            }
+            if (whole) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) v[x] *= inv;
+                const int tok = row / G, h = hk * G + row - tok * G;
+                const long long t = (long long)b * op.q_len + tok;
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(op.out) + t * op.out_stride +
+                                          (long long)h * D + d) = pack8<BF16>(v);
+                if (d == 0 && op.lse)
+                    op.lse[t * op.heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            } else {
+                if (d == 0) {
+                    part[r] = top;
+                    part[S::kRows + r] = sum;
+                }
+                float4* dst = reinterpret_cast<float4*>(part + 2 * S::kRows + r * DP + d);
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+        }
+        __syncthreads();
+        if (D < DP) {  // the merge used the ring: its padding is zero again
+            for (int i = tid; i < kAttnWarps * S::kRing / 16; i += kAttnThreads)
+                reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
             __syncthreads();
         }
+        first_segment = false;
+        blk += ke - kb;
     }
 }
 
-size_t attn_ws_bytes(const dg_attn&) { return 16; }
+// One CTA per query row: the parts of its unit, where that was cut between
+// CTAs, added in CTA order (eight interleaved sequences, then those in order).
+template <bool BF16, int DP, int RT>
+__global__ void __launch_bounds__(256) k_attn_join(const AttnParams p, int ctas_max) {
+    using S = AttnShape<DP, RT>;
+    __shared__ float wgt[kAttnMaxCtas + 1], red[8], acc[8][DP];
+    griddep_launch_dependents();
+    griddep_wait();
+    const dg_attn& op = p.op;
+    const int t = blockIdx.x, h = blockIdx.y, D = op.kv.head_dim;
+    const int b = t / op.q_len, G = op.heads / op.kv.kv_heads;
+    const int hk = h / G, row = (t - b * op.q_len) * G + h - hk * G;
+    const int grp = row / S::kRows, r = row - grp * S::kRows;
+    const int heads = op.kv.kv_heads * p.groups;
+    const long long total = p.prefix[op.kv.batch] * heads;
+    const int ctas = (int)min((long long)ctas_max, total);
+    const long long nb = p.prefix[b + 1] - p.prefix[b];
+    const long long u0 = p.prefix[b] * heads + (hk * p.groups + grp) * nb, u1 = u0 + nb;
+    // the CTAs whose ranges hold the unit's first and last block
+    int c0 = (int)(u0 * ctas / total), c1 = (int)((u1 - 1) * ctas / total);
+    while (range_at(c0 + 1, total, ctas) <= u0) ++c0;
+    while (range_at(c1 + 1, total, ctas) <= u1 - 1) ++c1;
+    if (c0 == c1) return;  // finished in place
+    const int n = c1 - c0 + 1;
+    auto part_of = [&](int i) {
+        const int second = i == 0 && range_at(c0, total, ctas) < u0;
+        return p.part + ((size_t)(c0 + i) * 2 + second) * S::kPart;
+    };
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float top = -INFINITY;
+    for (int i = tid; i < n; i += 256) top = fmaxf(top, wgt[i] = part_of(i)[r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, v[DP / 32];
+#pragma unroll
+    for (int x = 0; x < DP / 32; ++x) v[x] = 0.f;
+#pragma unroll 4
+    for (int i = warp; i < n; i += 8) {
+        const float* q = part_of(i);
+        const float f = exp2_fast(wgt[i] - base);
+        sum = fmaf(f, q[S::kRows + r], sum);
+#pragma unroll
+        for (int x = 0; x < DP / 32; ++x)
+            if (x * 32 + lane < D) v[x] = fmaf(f, q[2 * S::kRows + r * DP + x * 32 + lane], v[x]);
+    }
+    __syncthreads();
+    if (lane == 0) red[warp] = sum;
+#pragma unroll
+    for (int x = 0; x < DP / 32; ++x) acc[warp][x * 32 + lane] = v[x];
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += red[w];
+    if (tid < D) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) s += acc[w][tid];
+        static_cast<uint16_t*>(op.out)[(long long)t * op.out_stride + (long long)h * D + tid] =
+            elem_16<BF16>(sum == 0.f ? 0.f : s / sum);
+    }
+    if (tid == 0 && op.lse)
+        op.lse[(long long)t * op.heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
 
-cudaError_t launch_attn(const dg_attn& op, void*, cudaStream_t s) {
-    const void* fn = op.kv.type == DG_BF16 ? (const void*)k_attn_rows<true> : (const void*)k_attn_rows<false>;
-    void* args[] = {const_cast<dg_attn*>(&op)};
-    return launch_pdl(fn, dim3(op.kv.batch * op.q_len, op.heads), dim3(kAttnThreads), 0, s, args);
+// Row tiles of a CTA: as many as share its keys with 128 output registers.
+static int attn_dp(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : D <= 192 ? 192 : 256; }
+static int attn_tiles(const dg_attn& op) {
+    const int rows = op.q_len * (op.heads / op.kv.kv_heads), dp = attn_dp(op.kv.head_dim);
+    const int most = dp <= 64 ? 4 : dp <= 128 ? 2 : 1, want = (rows + 15) / 16;
+    return want >= most ? most : want == 3 ? 4 : want;
+}
+
+static long long max_blocks(const dg_attn& op, int groups) {
+    const long long cap = (long long)op.kv.max_pages * op.kv.page_size;
+    return (long long)op.kv.batch * op.kv.kv_heads * groups * ((cap + kBlockKeys - 1) / kBlockKeys);
+}
+static bool never_split(const dg_attn& op) {
+    return (long long)op.kv.max_pages * op.kv.page_size <= kBlockKeys;
+}
+static size_t prefix_bytes(const dg_attn& op) { return ((size_t)(op.kv.batch + 1) * 8 + 255) & ~(size_t)255; }
+
+size_t attn_ws_bytes(const dg_attn& op) {
+    const int tiles = attn_tiles(op), dp = attn_dp(op.kv.head_dim);
+    const int rows = op.q_len * (op.heads / op.kv.kv_heads), groups = (rows + tiles * 16 - 1) / (tiles * 16);
+    if (never_split(op)) return prefix_bytes(op);
+    const long long ctas = max_blocks(op, groups) < kAttnMaxCtas ? max_blocks(op, groups) : kAttnMaxCtas;
+    return prefix_bytes(op) + (size_t)ctas * 2 * tiles * 16 * (dp + 2) * 4;
+}
+
+template <bool BF16, int DP, int RT>
+static cudaError_t launch_attn_t(const dg_attn& op, void* ws, cudaStream_t s) {
+    using S = AttnShape<DP, RT>;
+    AttnParams p;
+    p.op = op;
+    p.rows = op.q_len * (op.heads / op.kv.kv_heads);
+    p.groups = (p.rows + S::kRows - 1) / S::kRows;
+    p.prefix = static_cast<long long*>(ws);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + prefix_bytes(op));
+    const void* fn = (const void*)k_attn<BF16, DP, RT>;
+    cudaError_t e = tc::smem_attr_once(fn, S::kSmem);
+    if (e != cudaSuccess) return e;
+    const int per_sm = S::kSmem <= 112 * 1024 ? 2 : 1;
+    const long long blocks = max_blocks(op, p.groups);
+    int grid = sm_count() * per_sm;
+    if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
+    if (grid > blocks) grid = (int)blocks;
+    void* args[] = {&p};
+    e = launch_pdl(fn, dim3(grid), dim3(kAttnThreads), S::kSmem, s, args);
+    if (e != cudaSuccess || never_split(op)) return e;
+    void* jargs[] = {&p, &grid};
+    return launch_pdl((const void*)k_attn_join<BF16, DP, RT>, dim3(op.kv.batch * op.q_len, op.heads),
+                      dim3(256), 0, s, jargs);
+}
+
+template <bool BF16>
+static cudaError_t launch_attn_b(const dg_attn& op, void* ws, cudaStream_t s) {
+    const int rt = attn_tiles(op);
+    switch (attn_dp(op.kv.head_dim)) {
+        case 64:
+            return rt == 1   ? launch_attn_t<BF16, 64, 1>(op, ws, s)
+                   : rt == 2 ? launch_attn_t<BF16, 64, 2>(op, ws, s)
+                             : launch_attn_t<BF16, 64, 4>(op, ws, s);
+        case 128:
+            return rt == 1 ? launch_attn_t<BF16, 128, 1>(op, ws, s)
+                           : launch_attn_t<BF16, 128, 2>(op, ws, s);
+        case 192: return launch_attn_t<BF16, 192, 1>(op, ws, s);
+        default: return launch_attn_t<BF16, 256, 1>(op, ws, s);
+    }
+}
+
+cudaError_t launch_attn(const dg_attn& op, void* ws, cudaStream_t s) {
+    return op.kv.type == DG_BF16 ? launch_attn_b<true>(op, ws, s) : launch_attn_b<false>(op, ws, s);
 }
 
 }  // namespace dg
