@@ -4,31 +4,38 @@
 //
 // The cost is the chosen experts' weights (6 * I * K bytes each at 16 bits,
 // 1.7 * I * K at int4), read once whatever the number of tokens, so the
-// products stream weights through shared memory and spend the matrix
-// instruction (m16n8k16: 16 weight rows x 8 tokens) on few tokens: it costs
-// no more for eight than for one.  Each warp has its own ring of cp.async
-// stages (16 weight rows and the expert's token rows, kc columns) and never
-// waits for another warp while it streams.
+// products stream weights and spend the matrix instruction (m16n8k16: 16
+// weight rows x 8 token columns) on few tokens: it costs no more for eight
+// than for one.  Weights go from global memory straight into the
+// instruction's registers: a lane's 16 bytes are 8 columns of its row, and
+// the order of columns inside an instruction is free as long as the tokens'
+// values follow it.  A warp keeps one chunk (16 rows x 256 columns, 8 KB at
+// 16 bits) in flight and reloads each register as soon as it is used.
 //
-//   up:   one warp takes 8 gate and the same 8 up rows of an expert over the
-//         whole of K, so that silu(gate) * up is in one thread's registers.
-//   down: the warps of a CTA share 16 output rows and deal the stages of all
-//         chosen experts among themselves; each adds weight * sum into its own
-//         fp32 rows [token], which are summed in warp order at the end.
+//   up:   a CTA takes 8 gate and the same 8 up rows of an expert at a time, so
+//         that silu(gate) * up meets in one thread; its warps deal the row
+//         tile's chunks along K among themselves, without a break from one
+//         tile to the next, and their sums are added in warp order.
+//   down: a CTA takes 16 output rows at a time; its warps deal the chunks of
+//         all chosen experts, each adding weight * sum into its own fp32 rows
+//         [token], which are summed in warp order.
 //
 // h goes from one to the other as two 16-bit values, hi + lo, that are two
 // columns of the matrix instruction: fp16 hi = h / 256 and lo = the rest x 2048
 // (22 bits, |h| up to 2^24), bf16 hi and lo (16 bits); the products keep fp32
-// sums.  int4 codes become fp16 by bit operations (exact); each group of 32
-// codes is one pair of matrix instructions whose fp32 sum is then scaled.
+// sums.  int4 codes become fp16 by bit operations (exact).  A group of 32
+// codes must be summed on its own before its scale, but a quad's lanes hold
+// parts of several groups (PH = 2 of 8-byte pieces, or 4 of 16-byte ones): each
+// token gets PH columns, column f carrying the token's values for the lanes
+// whose codes belong to group f and zero for the others, so that one
+// instruction sums the groups apart.
 #include "mma16.cuh"
 #include "tc_common.cuh"
 
 namespace dg {
 
-constexpr int kMoeStages = 4;
 constexpr int kMoeMaxSlots = 256;   // tokens x choices
-constexpr int kMoeMaxWarps = 12;
+constexpr int kMoeWarps = 8;
 
 // Workspace: scores [M][E], ids and weights [256], x in int4 order [M][K], h
 // [slots][2][I].
@@ -43,8 +50,7 @@ struct MoeWs {
 struct MoeParams {
     dg_moe op;
     MoeWs ws;
-    int slot_bytes;   // of a ring stage
-    int vec_scales;   // int4: scales come by cp.async
+    int pair_scales;  // int4: two groups' scales are one aligned 4-byte load
 };
 
 // ---- router scores ------------------------------------------------------------------------
@@ -53,50 +59,55 @@ struct MoeParams {
 // (0, 4), (1, 5), (2, 6), (3, 7).
 __device__ __forceinline__ int int4_place(int i) { return i < 4 ? 2 * i : 2 * i - 7; }
 
-// One CTA per expert: its score for every token.  The CTAs also write x in the
-// int4 order, which the up products read.
+// One CTA per expert and four tokens: their scores.  The first row of CTAs also
+// writes x in the int4 order, which the up products read.
+constexpr int kScoreTokens = 4;
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_moe_scores(const MoeParams p) {
     griddep_launch_dependents();
     griddep_wait();
     const dg_moe& op = p.op;
-    const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint16_t* r = static_cast<const uint16_t*>(op.router) + (size_t)e * op.K;
-    const uint16_t* x = static_cast<const uint16_t*>(op.x);
-    float z[16];
+    const int e = blockIdx.x, m0 = blockIdx.y * kScoreTokens;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int K8 = op.K / 8;
+    const uint4* r = static_cast<const uint4*>(op.router) + (size_t)e * K8;
+    const uint4* x = static_cast<const uint4*>(op.x);
+    float z[kScoreTokens];
 #pragma unroll
-    for (int m = 0; m < 16; ++m) z[m] = 0.f;
-    for (int k = tid * 8; k < op.K; k += 2048) {
+    for (int m = 0; m < kScoreTokens; ++m) z[m] = 0.f;
+#pragma unroll 2
+    for (int k = tid; k < K8; k += 256) {
         float w[8];
-        unpack8<BF16>(ld_nc16(r + k), w);
+        const uint4 wv = __ldg(r + k);
+        uint4 xv[kScoreTokens];
 #pragma unroll
-        for (int m = 0; m < 16; ++m) {
-            if (m < op.M) {
-                float v[8];
-                unpack8<BF16>(ld_cg16(x + (size_t)m * op.K + k), v);
+        for (int m = 0; m < kScoreTokens; ++m) xv[m] = __ldcg(x + (size_t)min(m0 + m, op.M - 1) * K8 + k);
+        unpack8<BF16>(wv, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[m] = fmaf(w[i], v[i], z[m]);
-            }
+        for (int m = 0; m < kScoreTokens; ++m) {
+            float v[8];
+            unpack8<BF16>(xv[m], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[m] = fmaf(w[i], v[i], z[m]);
         }
     }
-    __shared__ float part[8][16];
+    __shared__ float part[8][kScoreTokens];
 #pragma unroll
-    for (int m = 0; m < 16; ++m)
-        if (m < op.M) {
-            const float v = warp_sum(z[m]);
-            if (lane == 0) part[warp][m] = v;
-        }
+    for (int m = 0; m < kScoreTokens; ++m) {
+        const float v = warp_sum(z[m]);
+        if (lane == 0) part[warp][m] = v;
+    }
     __syncthreads();
-    if (tid < op.M) {
+    if (tid < kScoreTokens && m0 + tid < op.M) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) v += part[w][tid];
-        p.ws.scores[(size_t)tid * op.E + e] = v;
+        p.ws.scores[(size_t)(m0 + tid) * op.E + e] = v;
     }
-    if (op.kind == DG_LINEAR_W4A16) {
-        const int n8 = op.M * (op.K / 8);
+    if (op.kind == DG_LINEAR_W4A16 && m0 == 0) {
+        const int n8 = op.M * K8;
         for (int i = e * 256 + tid; i < n8; i += gridDim.x * 256) {
-            const uint4 v = ld_cg16(x + (size_t)i * 8);
+            const uint4 v = __ldcg(x + i);
             reinterpret_cast<uint4*>(p.ws.xp)[i] =
                 make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                            __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
@@ -202,77 +213,7 @@ __device__ void build_lists(const dg_moe& op, Lists& L) {
     __syncthreads();
 }
 
-// ---- ring stages ----------------------------------------------------------------------------
-
-// A stage holds 16 weight rows and R token rows of kc columns.  kc shrinks as
-// R grows, so that one stage size serves every expert.  Row pitches put eight
-// rows' 16-byte pieces (ldmatrix; int4 token rows) or 4-byte pieces (int4
-// codes) in different banks.
-template <int KIND>
-struct Stage {
-    static constexpr bool kInt4 = KIND == DG_LINEAR_W4A16;
-    __host__ __device__ static int kc(int R) {
-        return kInt4 ? (R <= 8 ? 256 : R <= 16 ? 128 : 64) : (R <= 8 ? 128 : 64);
-    }
-    __host__ __device__ static int w_pitch(int kc) { return kInt4 ? kc / 2 + 16 : kc * 2 + 16; }
-    __host__ __device__ static int x_pitch(int kc) { return kInt4 ? kc * 2 + 64 : kc * 2 + 16; }
-    __host__ __device__ static int bytes(int R) {
-        return 16 * w_pitch(kc(R)) + R * x_pitch(kc(R));
-    }
-};
-
-// Copies 2^log_pieces 16-byte pieces of each of `rows` rows, from byte `from` of
-// a row of row_bytes bytes on; pieces past its end read as zero.  row(r) is row
-// r's address.
-template <class Row>
-__device__ __forceinline__ void copy_rows(uint32_t dst, int pitch, int rows, int log_pieces, int from,
-                                          int row_bytes, Row row) {
-    const int lane = threadIdx.x & 31;
-    for (int i = lane; i < rows << log_pieces; i += 32) {
-        const int r = i >> log_pieces, at = (i & ((1 << log_pieces) - 1)) * 16;
-        const bool in = from + at < row_bytes;
-        cp_async16(dst + r * pitch + at, reinterpret_cast<const char*>(row(r)) + (in ? from + at : 0), in);
-    }
-}
-
-// Fetches one stage: weight rows row_w(0..15) (null: none), their scales, and
-// R token rows row_x(r), columns [k0, k0 + kc) of Kd.
-template <int KIND, class RowW, class RowS, class RowX>
-__device__ __forceinline__ void fetch_stage(const MoeParams& p, uint32_t dst, int R, int kc, int k0, int Kd,
-                                            RowW row_w, RowS row_s, RowX row_x) {
-    using St = Stage<KIND>;
-    const int wp = St::w_pitch(kc), xp = St::x_pitch(kc);
-    if (St::kInt4) {
-        const int lg = kc == 256 ? 3 : kc == 128 ? 2 : 1;   // 16-byte pieces of a row of codes
-        copy_rows(dst, wp, 16, lg, k0 / 2, Kd / 2, row_w);
-        const int lane = threadIdx.x & 31;
-        if (p.vec_scales) {
-            if (lane < 16) {
-                const char* s = reinterpret_cast<const char*>(row_s(lane)) + k0 / 16;
-                const uint32_t d = dst + lane * wp + kc / 2;
-                if (kc == 256)
-                    cp_async16(d, s, true);
-                else if (kc == 128)
-                    cp_async_small<8>(d, s);
-                else
-                    cp_async_small<4>(d, s);
-            }
-        } else {
-            // any group size, count or alignment: plain loads, one per 32 columns
-            for (int i = lane; i < 16 << lg; i += 32) {
-                const int r = i >> lg, b = i & ((1 << lg) - 1), k = k0 + b * 32;
-                uint16_t v = 0;
-                if (k < Kd) v = ld_stream_u16(reinterpret_cast<const uint16_t*>(row_s(r)) + k / p.op.group_size);
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + r * wp + kc / 2 + b * 2), "h"(v) : "memory");
-            }
-        }
-        copy_rows(dst + 16 * wp, xp, R, lg + 2, k0 * 2, Kd * 2, row_x);
-    } else {
-        const int lg = kc == 128 ? 4 : 3;
-        copy_rows(dst, wp, 16, lg, k0 * 2, Kd * 2, row_w);
-        copy_rows(dst + 16 * wp, xp, R, lg, k0 * 2, Kd * 2, row_x);
-    }
-}
+// ---- weight chunks --------------------------------------------------------------------------
 
 // Four fp16 pairs from eight int4 codes: (0, 4), (1, 5), (2, 6), (3, 7).
 // 0x6400 + u is the fp16 number 1024 + u; the code's sign bit is flipped, so u
@@ -287,69 +228,150 @@ __device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t (&v)[4]) {
     v[3] = h2_as_u32(__hfma2(u32_as_h2(and_xor(h, 0x00F000F0u, 0x64806480u)), k16, k72));
 }
 
-// acc[j] += (16 weight rows) x (token rows 8 j ..), columns of one stage.
-template <int KIND, int NT>
-__device__ __forceinline__ void mma_stage(uint32_t st, int R, int kc, int cols, float (&acc)[NT][4]) {
-    using St = Stage<KIND>;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int wp = St::w_pitch(kc), xp = St::x_pitch(kc);
-    const uint32_t xs = st + 16 * wp;
-    if (St::kInt4) {
-        const uint32_t wa = st + g * wp + t * 4;
-        uint32_t xa[NT];
+// A chunk is 16 rows x kCols columns in kSteps steps of kStep; a lane (g =
+// lane / 4, t = lane % 4) holds kLane columns of rows g and g + 8 per step,
+// from column t * kLane of the step on.  PH: phases of int4 (1 for 16-bit).
+template <int KIND, int PH>
+struct Shape {
+    static constexpr bool kInt4 = KIND == DG_LINEAR_W4A16;
+    static constexpr int kLane = kInt4 ? (PH == 4 ? 32 : 16) : 8;
+    static constexpr int kStep = 4 * kLane;
+    static constexpr int kCols = kInt4 ? 512 : 256;
+    static constexpr int kSteps = kCols / kStep;
+    static constexpr int kWords = kInt4 ? kLane / 8 : 4;   // 32-bit registers of a row and step
+    static constexpr int kTokens = 8 / PH;                 // token rows of 8 columns
+};
+
+// Rows g and g + 8 of a row tile at this lane's first column, and their scales.
+struct Src {
+    const char* w[2];
+    const uint16_t* s[2];
+    int k0;   // first column of the chunk
+};
+
+template <int KIND, int PH>
+struct Chunk {
+    using S = Shape<KIND, PH>;
+    uint32_t v[S::kSteps][2][S::kWords];
+    uint32_t sc[S::kInt4 ? S::kSteps : 1][2];   // this thread's two columns' scales
+
+    __device__ __forceinline__ void load_step(const MoeParams& p, const Src& q, int i, int Kd) {
+        const int t = threadIdx.x & 3;
+        const bool in = q.k0 + i * S::kStep + t * S::kLane < Kd;
+        const size_t at = S::kInt4 ? (q.k0 + i * S::kStep) / 2 : (size_t)(q.k0 + i * S::kStep) * 2;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) xa[j] = xs + min(j * 8 + g, R - 1) * xp + t * 16;
-        const int groups = min(cols, kc) / 32;
-#pragma unroll 2
-        for (int b = 0; b < groups; ++b) {
-            uint32_t lo[4], hi[4];
-            int4_pairs(lds32(wa + b * 16), lo);
-            int4_pairs(lds32(wa + 8 * wp + b * 16), hi);
-            uint16_t s0, s1;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s0) : "r"(st + g * wp + kc / 2 + b * 2) : "memory");
-            asm volatile("ld.shared.u16 %0, [%1];"
-                         : "=h"(s1)
-                         : "r"(st + (g + 8) * wp + kc / 2 + b * 2)
-                         : "memory");
-            const float f0 = elem_f32<false>(s0), f1 = elem_f32<false>(s1);
-            const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                if (j * 8 < R) {
-                    const uint4 x = lds128(xa[j] + b * 64);
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma16816<false>(c, a0, x.x, x.y);
-                    mma16816<false>(c, a1, x.z, x.w);
-                    acc[j][0] = fmaf(f0, c[0], acc[j][0]);
-                    acc[j][1] = fmaf(f0, c[1], acc[j][1]);
-                    acc[j][2] = fmaf(f1, c[2], acc[j][2]);
-                    acc[j][3] = fmaf(f1, c[3], acc[j][3]);
-                }
+        for (int r = 0; r < 2; ++r) {
+            if (S::kWords == 4) {
+                const uint4 x = in ? ld_stream16(q.w[r] + at) : make_uint4(0, 0, 0, 0);
+                v[i][r][0] = x.x, v[i][r][1] = x.y;
+                v[i][r][S::kWords - 2] = x.z, v[i][r][S::kWords - 1] = x.w;
+            } else {
+                uint2 x = make_uint2(0, 0);
+                if (in)
+                    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+                                 : "=r"(x.x), "=r"(x.y)
+                                 : "l"(q.w[r] + at));
+                v[i][r][0] = x.x, v[i][r][1] = x.y;
             }
-        }
-    } else {
-        constexpr bool BF = KIND == DG_LINEAR_BF16;
-        const uint32_t wa = st + ((lane & 7) + ((lane >> 3) & 1) * 8) * wp + (lane >> 4) * 16;
-        uint32_t xa[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) xa[j] = xs + min(j * 8 + (lane & 7), R - 1) * xp + (lane >> 3) * 16;
-        const int steps = kc / 32;
-#pragma unroll 2
-        for (int k = 0; k < steps; ++k) {
-            uint32_t a0[4], a1[4];
-            ldsm4(a0, wa + k * 64);
-            ldsm4(a1, wa + k * 64 + 32);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                if (j * 8 < R) {
-                    uint32_t x[4];
-                    ldsm4(x, xa[j] + k * 64);
-                    mma16816<BF>(acc[j], a0, x[0], x[1]);
-                    mma16816<BF>(acc[j], a1, x[2], x[3]);
+            if (S::kInt4) {
+                // columns 2 t and 2 t + 1: groups f and f + 1 of the step's PH
+                const int grp = (q.k0 + i * S::kStep) / 32 + (PH == 4 ? (t & 1) * 2 : 0);
+                uint32_t two = 0;
+                if (p.pair_scales) {
+                    if (grp * 32 < Kd)
+                        asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];"
+                                     : "=r"(two)
+                                     : "l"(q.s[r] + grp));
+                } else {
+                    // any group size, count or alignment
+                    if (grp * 32 < Kd) two = ld_stream_u16(q.s[r] + grp * 32 / p.op.group_size);
+                    if (grp * 32 + 32 < Kd)
+                        two |= (uint32_t)ld_stream_u16(q.s[r] + (grp * 32 + 32) / p.op.group_size) << 16;
                 }
+                sc[i][r] = two;
             }
         }
     }
+
+    __device__ __forceinline__ void load(const MoeParams& p, const Src& q, int Kd) {
+#pragma unroll
+        for (int i = 0; i < S::kSteps; ++i) load_step(p, q, i, Kd);
+    }
+
+    // acc[j] += (16 weight rows) x (token rows j * kTokens ..), the chunk's
+    // columns; each step's registers are then reloaded from `next` (if any).
+    // x[j]: the token row of this lane's column of block j, from column 0 on.
+    template <int NT>
+    __device__ __forceinline__ void mma(const MoeParams& p, const uint16_t* const (&x)[NT], int R, int k0,
+                                        int Kd, float (&acc)[NT][4], const Src& next, bool more) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const bool mine = PH == 1 || (PH == 2 ? (g & 1) == (t >> 1) : (g & 3) == t);
+#pragma unroll
+        for (int i = 0; i < S::kSteps; ++i) {
+            const int k = k0 + i * S::kStep + t * S::kLane;
+            const bool in = mine && k < Kd;
+            if (S::kInt4) {
+                uint32_t lo[S::kWords][4], hi[S::kWords][4];
+#pragma unroll
+                for (int w = 0; w < S::kWords; ++w) {
+                    int4_pairs(v[i][0][w], lo[w]);
+                    int4_pairs(v[i][1][w], hi[w]);
+                }
+                const float2 f0 = __half22float2(u32_as_h2(sc[i][0])), f1 = __half22float2(u32_as_h2(sc[i][1]));
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    if (j * S::kTokens < R) {
+                        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int w = 0; w < S::kWords; ++w) {
+                            uint4 b = make_uint4(0, 0, 0, 0);
+                            if (in) b = __ldg(reinterpret_cast<const uint4*>(x[j] + k + w * 8));
+                            const uint32_t a0[4] = {lo[w][0], hi[w][0], lo[w][1], hi[w][1]};
+                            const uint32_t a1[4] = {lo[w][2], hi[w][2], lo[w][3], hi[w][3]};
+                            mma16816<false>(c, a0, b.x, b.y);
+                            mma16816<false>(c, a1, b.z, b.w);
+                        }
+                        acc[j][0] = fmaf(f0.x, c[0], acc[j][0]);
+                        acc[j][1] = fmaf(f0.y, c[1], acc[j][1]);
+                        acc[j][2] = fmaf(f1.x, c[2], acc[j][2]);
+                        acc[j][3] = fmaf(f1.y, c[3], acc[j][3]);
+                    }
+                }
+            } else {
+                constexpr bool BF = KIND == DG_LINEAR_BF16;
+                const uint32_t a0[4] = {v[i][0][0], v[i][1][0], v[i][0][1], v[i][1][1]};
+                const uint32_t a1[4] = {v[i][0][S::kWords - 2], v[i][1][S::kWords - 2],
+                                        v[i][0][S::kWords - 1], v[i][1][S::kWords - 1]};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    if (j * S::kTokens < R) {
+                        uint4 b = make_uint4(0, 0, 0, 0);
+                        if (in) b = __ldg(reinterpret_cast<const uint4*>(x[j] + k));
+                        mma16816<BF>(acc[j], a0, b.x, b.y);
+                        mma16816<BF>(acc[j], a1, b.z, b.w);
+                    }
+                }
+            }
+            if (more) load_step(p, next, i, Kd);
+        }
+    }
+
+    // The sums of token row n of block j in acc, after all chunks: for 16-bit
+    // weights columns 2 t and 2 t + 1 are two tokens; for int4 their phases'
+    // sums belong together.  sum(q, h): token row q of this thread's (q < 2 for
+    // PH 1, else 0), weight row g + 8 h.
+    __device__ __forceinline__ static float sum(const float (&a)[4], int q, int h) {
+        if (PH == 1) return a[2 * h + q];
+        const float two = a[2 * h] + a[2 * h + 1];
+        return PH == 2 ? two : two + __shfl_xor_sync(0xffffffffu, two, 1);
+    }
+};
+
+// The token row behind column g of block j (what a lane loads), and behind
+// this thread's accumulators.
+template <int PH>
+__device__ __forceinline__ int column_row(int j) {
+    return j * (8 / PH) + ((threadIdx.x & 31) >> 2) / PH;
 }
 
 // ---- gate and up ----------------------------------------------------------------------------
@@ -359,20 +381,20 @@ __device__ __forceinline__ size_t row_bytes_of(int cols) {
     return KIND == DG_LINEAR_W4A16 ? (size_t)cols / 2 : (size_t)cols * 2;
 }
 
-template <int KIND, int NT>
-__global__ void __launch_bounds__(kMoeMaxWarps * 32) k_moe_up(const MoeParams p) {
-    using St = Stage<KIND>;
+template <int KIND, int PH, int NT>
+__global__ void __launch_bounds__(kMoeWarps * 32, NT >= 8 ? 1 : 2) k_moe_up(const MoeParams p) {
+    using S = Shape<KIND, PH>;
     constexpr bool BF = KIND == DG_LINEAR_BF16;
-    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int kTok = NT * S::kTokens;   // token rows of the accumulators
+    extern __shared__ __align__(16) float dyn[];
     __shared__ Lists L;
     const dg_moe& op = p.op;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     griddep_launch_dependents();
     griddep_wait();
-    // the ring, not yet in use, holds the probabilities
-    for (int m = warp; m < op.M; m += warps)
-        route_token(op, p.ws.scores + (size_t)m * op.E, reinterpret_cast<float*>(smem) + (size_t)warp * op.E,
-                    L.ids + m * op.top_k, L.wts + m * op.top_k);
+    for (int m = warp; m < op.M; m += kMoeWarps)
+        route_token(op, p.ws.scores + (size_t)m * op.E, dyn + (size_t)warp * op.E, L.ids + m * op.top_k,
+                    L.wts + m * op.top_k);
     __syncthreads();
     build_lists(op, L);
     if (blockIdx.x == 0)
@@ -383,92 +405,107 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32) k_moe_up(const MoeParams p)
             if (op.weights) op.weights[s] = L.wts[s];
         }
 
-    const int tiles = op.I / 8, total = L.count * tiles, stride = warps * gridDim.x;
+    // the warps' sums of a row tile, [2 tiles in turn][warps][kTok][16 rows]
+    float* part = dyn;
+    const int tiles = op.I / 8, total = L.count * tiles, n = (op.K + S::kCols - 1) / S::kCols;
     const size_t rb = row_bytes_of<KIND>(op.K);
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kMoeStages * p.slot_bytes;
-    const uint16_t* x = KIND == DG_LINEAR_W4A16 ? p.ws.xp : static_cast<const uint16_t*>(op.x);
+    const uint16_t* x = S::kInt4 ? p.ws.xp : static_cast<const uint16_t*>(op.x);
 
-    // the stage to fetch next, and the stage to compute next
-    struct Cursor {
-        int item, k0;
-    } f = {(int)(warp * gridDim.x + blockIdx.x), 0}, c = f;
-    int fs = 0, cs = 0;
-    auto fetch = [&] {
-        if (f.item < total) {
-            const int li = f.item / tiles, tile = f.item - li * tiles;
-            const int R = L.tokens[li], kc = St::kc(R);
-            const size_t row0 = (size_t)L.expert[li] * op.I + tile * 8;
-            auto row_w = [&](int r) {
-                return static_cast<const char*>(r < 8 ? op.W_gate : op.W_up) + (row0 + (r & 7)) * rb;
-            };
-            auto row_s = [&](int r) {
-                return static_cast<const char*>(r < 8 ? op.gate_scale : op.up_scale) +
-                       (row0 + (r & 7)) * (op.K / op.group_size) * 2;
-            };
-            auto row_x = [&](int r) { return x + (size_t)L.token_of[L.slot[li][r]] * op.K; };
-            fetch_stage<KIND>(p, ring + fs * p.slot_bytes, R, kc, f.k0, op.K, row_w, row_s, row_x);
-            f.k0 += kc;
-            if (f.k0 >= op.K) {
-                f.k0 = 0;
-                f.item += stride;
-            }
-            fs = fs + 1 == kMoeStages ? 0 : fs + 1;
+    // the next chunk to load: chunk fk of the n of row tile `fi`
+    int fi = blockIdx.x, fk = warp;
+    auto settle = [&] {
+        while (fk >= n) {
+            fk -= n;
+            fi += gridDim.x;
         }
-        cp_commit();
     };
-    for (int i = 0; i < kMoeStages - 1; ++i) fetch();
-    float acc[NT][4];
+    Src src{};
+    auto find = [&] {
+        const int li = fi / tiles, tile = fi - li * tiles;
+        const size_t row = (size_t)L.expert[li] * op.I + tile * 8 + g;
+        src.k0 = fk * S::kCols;
+        src.w[0] = static_cast<const char*>(op.W_gate) + row * rb + (S::kInt4 ? t * S::kLane / 2 : t * S::kLane * 2);
+        src.w[1] = static_cast<const char*>(op.W_up) + row * rb + (S::kInt4 ? t * S::kLane / 2 : t * S::kLane * 2);
+        if (S::kInt4) {
+            const size_t at = row * (op.K / op.group_size);
+            src.s[0] = static_cast<const uint16_t*>(op.gate_scale) + at;
+            src.s[1] = static_cast<const uint16_t*>(op.up_scale) + at;
+        }
+    };
+    Chunk<KIND, PH> ch;
+    settle();
+    if (fi < total) {
+        find();
+        ch.load(p, src, op.K);
+    }
+    int k = warp, turn = 0;
+    for (int item = blockIdx.x; item < total; item += gridDim.x) {
+        const int li = item / tiles, tile = item - li * tiles, R = L.tokens[li];
+        const uint16_t* xr[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-    while (c.item < total) {
-        const int li = c.item / tiles, tile = c.item - li * tiles;
-        const int R = L.tokens[li], kc = St::kc(R);
-        cp_wait<kMoeStages - 2>();
-        __syncwarp();
-        fetch();
-        mma_stage<KIND, NT>(ring + cs * p.slot_bytes, R, kc, op.K - c.k0, acc);
-        cs = cs + 1 == kMoeStages ? 0 : cs + 1;
-        c.k0 += kc;
-        if (c.k0 < op.K) continue;
-        // rows g (gate) and g + 8 (up) of tokens 2 t and 2 t + 1: one thread's
-        const int g = lane >> 2, t = lane & 3;
-        const int i = tile * 8 + (KIND == DG_LINEAR_W4A16 ? int4_place(g) : g);
+        for (int j = 0; j < NT; ++j)
+            xr[j] = x + (size_t)L.token_of[L.slot[li][min(column_row<PH>(j), R - 1)]] * op.K;
+        float acc[NT][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+        for (; k < n; k += kMoeWarps) {
+            fk += kMoeWarps;
+            settle();
+            const bool more = fi < total;
+            if (more) find();
+            ch.mma(p, xr, R, k * S::kCols, op.K, acc, src, more);
+        }
+        k -= n;
+        float* mine = part + (size_t)(turn * kMoeWarps + warp) * kTok * 16;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int n = j * 8 + t * 2 + q;
-                if (n < R) {
-                    const float v = silu_f32(acc[j][q]) * acc[j][2 + q];
-                    uint16_t* h = p.ws.h + (size_t)L.slot[li][n] * 2 * op.I + i;
-                    const float s = BF ? v : v * 0.00390625f;
-                    const uint16_t hi = elem_16<BF>(s);
-                    h[0] = hi;
-                    h[op.I] = elem_16<BF>((s - elem_f32<BF>(hi)) * (BF ? 1.f : 2048.f));
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (PH == 1) {
+                    mine[(j * 8 + t * 2) * 16 + g + 8 * h] = ch.sum(acc[j], 0, h);
+                    mine[(j * 8 + t * 2 + 1) * 16 + g + 8 * h] = ch.sum(acc[j], 1, h);
+                } else {
+                    const float v = ch.sum(acc[j], 0, h);
+                    if (PH == 2 || (t & 1) == 0)
+                        mine[(j * S::kTokens + (PH == 2 ? t : t >> 1)) * 16 + g + 8 * h] = v;
                 }
             }
-            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+        __syncthreads();
+        for (int i = tid; i < R * 8; i += kMoeWarps * 32) {
+            const int tok = i >> 3, r = i & 7;
+            const float* q = part + (size_t)turn * kMoeWarps * kTok * 16 + tok * 16 + r;
+            float gate = 0.f, up = 0.f;
+#pragma unroll
+            for (int w = 0; w < kMoeWarps; ++w) {
+                gate += q[w * kTok * 16];
+                up += q[w * kTok * 16 + 8];
+            }
+            const float v = silu_f32(gate) * up;
+            uint16_t* h = p.ws.h + (size_t)L.slot[li][tok] * 2 * op.I + tile * 8 +
+                          (S::kInt4 ? int4_place(r) : r);
+            const float s = BF ? v : v * 0.00390625f;
+            const uint16_t hi = elem_16<BF>(s);
+            h[0] = hi;
+            h[op.I] = elem_16<BF>((s - elem_f32<BF>(hi)) * (BF ? 1.f : 2048.f));
         }
-        c.k0 = 0;
-        c.item += stride;
+        turn ^= 1;
     }
-    cp_wait<0>();
 }
 
 // ---- down and the weighted sum ----------------------------------------------------------------
 
-template <int KIND, int NT>
-__global__ void __launch_bounds__(kMoeMaxWarps * 32) k_moe_down(const MoeParams p) {
-    using St = Stage<KIND>;
+template <int KIND, int PH, int NT>
+__global__ void __launch_bounds__(kMoeWarps * 32, NT >= 8 ? 1 : 2) k_moe_down(const MoeParams p) {
+    using S = Shape<KIND, PH>;
     constexpr bool BF = KIND == DG_LINEAR_BF16;
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(16) float dyn[];
     __shared__ Lists L;
     const dg_moe& op = p.op;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-    const int M = op.M, n0 = blockIdx.x * 16;
-    float* sums = reinterpret_cast<float*>(smem + warps * kMoeStages * p.slot_bytes);  // [warps][16][M]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int M = op.M, tiles = (op.K + 15) / 16, n = (op.I + S::kCols - 1) / S::kCols;
+    float* sums = dyn;   // [warps][M][16]
     griddep_launch_dependents();
-    for (int i = tid; i < warps * 16 * M; i += blockDim.x) sums[i] = 0.f;
+    for (int i = tid; i < kMoeWarps * 16 * M; i += blockDim.x) sums[i] = 0.f;
     griddep_wait();
     for (int s = tid; s < M * op.top_k; s += blockDim.x) {
         L.ids[s] = __ldcg(p.ws.ids + s);
@@ -477,88 +514,104 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32) k_moe_down(const MoeParams 
     __syncthreads();
     build_lists(op, L);
     const size_t rb = row_bytes_of<KIND>(op.I);
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kMoeStages * p.slot_bytes;
     float* mine = sums + warp * 16 * M;
 
-    // the experts' stages in one sequence, dealt to the warps in turn
-    struct Cursor {
-        int li, k;   // stage k of expert li
-    } f = {0, warp}, c = f;
-    auto settle = [&](Cursor& q) {
-        while (q.li < L.count) {
-            const int kc = St::kc(2 * L.tokens[q.li]), n = (op.I + kc - 1) / kc;
-            if (q.k < n) return;
-            q.k -= n;
-            ++q.li;
+    // the next chunk to load: chunk fk of the n of expert fl in row tile ft
+    int ft = blockIdx.x, fl = 0, fk = warp;
+    auto settle = [&] {
+        while (fk >= n) {
+            fk -= n;
+            if (++fl == L.count) {
+                fl = 0;
+                ft += gridDim.x;
+            }
         }
     };
-    settle(f);
-    c = f;
-    int fs = 0, cs = 0;
-    auto fetch = [&] {
-        if (f.li < L.count) {
-            const int li = f.li, R = 2 * L.tokens[li], kc = St::kc(R);
-            const size_t row0 = (size_t)L.expert[li] * op.K;
-            const int last = op.K - 1;   // rows past the end repeat the last one
-            auto row_w = [&](int r) {
-                return static_cast<const char*>(op.W_down) + (row0 + min(n0 + r, last)) * rb;
-            };
-            auto row_s = [&](int r) {
-                return static_cast<const char*>(op.down_scale) +
-                       (row0 + min(n0 + r, last)) * (op.I / op.group_size) * 2;
-            };
-            auto row_x = [&](int r) {
-                return p.ws.h + ((size_t)L.slot[li][r >> 1] * 2 + (r & 1)) * op.I;
-            };
-            fetch_stage<KIND>(p, ring + fs * p.slot_bytes, R, kc, f.k * kc, op.I, row_w, row_s, row_x);
-            f.k += warps;
-            settle(f);
-            fs = fs + 1 == kMoeStages ? 0 : fs + 1;
+    Src src{};
+    auto find = [&] {
+        // op.K is a multiple of 8: a last tile may lack its second half
+        const size_t row = (size_t)L.expert[fl] * op.K + ft * 16 + g;
+        const int half = ft * 16 + 8 < op.K ? 8 : 0;
+        src.k0 = fk * S::kCols;
+        src.w[0] = static_cast<const char*>(op.W_down) + row * rb + (S::kInt4 ? t * S::kLane / 2 : t * S::kLane * 2);
+        src.w[1] = src.w[0] + half * rb;
+        if (S::kInt4) {
+            const int srow = op.I / op.group_size;
+            src.s[0] = static_cast<const uint16_t*>(op.down_scale) + row * srow;
+            src.s[1] = src.s[0] + half * srow;
         }
-        cp_commit();
     };
-    for (int i = 0; i < kMoeStages - 1; ++i) fetch();
-    float acc[NT][4];
+    Chunk<KIND, PH> ch;
+    settle();
+    if (ft < tiles) {
+        find();
+        ch.load(p, src, op.I);
+    }
+    int k = warp;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        for (int li = 0; li < L.count; ++li) {
+            if (k >= n) {   // nothing of this expert is this warp's
+                k -= n;
+                continue;
+            }
+            const int R = 2 * L.tokens[li];
+            const uint16_t* xr[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-    while (c.li < L.count) {
-        const int li = c.li, R = 2 * L.tokens[li], kc = St::kc(R);
-        cp_wait<kMoeStages - 2>();
-        __syncwarp();
-        fetch();
-        mma_stage<KIND, NT>(ring + cs * p.slot_bytes, R, kc, op.I - c.k * kc, acc);
-        cs = cs + 1 == kMoeStages ? 0 : cs + 1;
-        c.k += warps;
-        settle(c);
-        if (c.li == li) continue;
-        // columns 2 i and 2 i + 1 are hi and lo of the expert's token i
-        const int g = lane >> 2, t = lane & 3;
+            for (int j = 0; j < NT; ++j) {
+                const int r = min(column_row<PH>(j), R - 1);
+                xr[j] = p.ws.h + ((size_t)L.slot[li][r >> 1] * 2 + (r & 1)) * op.I;
+            }
+            float acc[NT][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int i = j * 4 + t;
-            if (2 * i < R) {
-                const int s = L.slot[li][i], m = L.token_of[s];
-                const float w = L.wts[s];
+            for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+            for (; k < n; k += kMoeWarps) {
+                fk += kMoeWarps;
+                settle();
+                const bool more = ft < tiles;
+                if (more) find();
+                ch.mma(p, xr, R, k * S::kCols, op.I, acc, src, more);
+            }
+            k -= n;
+            // token rows 2 i and 2 i + 1 are hi and lo of the expert's token i
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float v = BF ? acc[j][2 * q] + acc[j][2 * q + 1]
-                                       : fmaf(acc[j][2 * q + 1], 1.f / 2048.f, acc[j][2 * q]) * 256.f;
-                    mine[(g + 8 * q) * M + m] = fmaf(w, v, mine[(g + 8 * q) * M + m]);
+            for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float hi, lo;
+                    int i;
+                    if (PH == 1) {
+                        hi = ch.sum(acc[j], 0, h), lo = ch.sum(acc[j], 1, h);
+                        i = j * 4 + t;
+                    } else {
+                        const int over = PH == 2 ? 1 : 2;   // the lane with the next token row
+                        hi = ch.sum(acc[j], 0, h);
+                        lo = __shfl_xor_sync(0xffffffffu, hi, over);
+                        i = PH == 2 ? ((t & 1) ? 16 : j * 2 + (t >> 1)) : (t ? 16 : j);
+                    }
+                    if (2 * i < R) {
+                        const int s = L.slot[li][i];
+                        const float v = BF ? hi + lo : fmaf(lo, 1.f / 2048.f, hi) * 256.f;
+                        float* to = mine + L.token_of[s] * 16 + g + 8 * h;
+                        *to = fmaf(L.wts[s], v, *to);
+                    }
                 }
             }
-            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
         }
-    }
-    cp_wait<0>();
-    __syncthreads();
-    for (int i = tid; i < 16 * M; i += blockDim.x) {
-        const int m = i >> 4, r = i & 15;
-        if (n0 + r >= op.K) continue;
-        float y = 0.f;
-        for (int w = 0; w < warps; ++w) y += sums[(w * 16 + r) * M + m];
-        const size_t at = (size_t)m * op.K + n0 + r;
-        if (op.residual) y += elem_f32<BF>(static_cast<const uint16_t*>(op.residual)[at]);
-        static_cast<uint16_t*>(op.y)[at] = elem_16<BF>(y);
+        __syncthreads();
+        for (int i = tid; i < 16 * M; i += blockDim.x) {
+            const int m = i >> 4, row = tile * 16 + (i & 15);
+            float y = 0.f;
+#pragma unroll
+            for (int w = 0; w < kMoeWarps; ++w) {
+                y += sums[w * 16 * M + i];
+                sums[w * 16 * M + i] = 0.f;
+            }
+            if (row >= op.K) continue;
+            const size_t at = (size_t)m * op.K + row;
+            if (op.residual) y += elem_f32<BF>(static_cast<const uint16_t*>(op.residual)[at]);
+            static_cast<uint16_t*>(op.y)[at] = elem_16<BF>(y);
+        }
+        __syncthreads();
     }
 }
 
@@ -587,50 +640,57 @@ size_t moe_ws_bytes(const dg_moe& op) {
     return place(op, nullptr, &w);
 }
 
+// Kernels of each format by their token blocks: NT blocks of 8 / PH token rows.
+template <int KIND>
+static const void* up_kernel(int M) {
+    if constexpr (KIND == DG_LINEAR_W4A16) {
+        if (M == 1) return (const void*)k_moe_up<KIND, 4, 1>;
+        return M <= 4   ? (const void*)k_moe_up<KIND, 2, 1>
+               : M <= 8 ? (const void*)k_moe_up<KIND, 2, 2> : (const void*)k_moe_up<KIND, 2, 4>;
+    } else {
+        return M <= 8 ? (const void*)k_moe_up<KIND, 1, 1> : (const void*)k_moe_up<KIND, 1, 2>;
+    }
+}
+template <int KIND>
+static const void* down_kernel(int M) {
+    if constexpr (KIND == DG_LINEAR_W4A16) {
+        if (M == 1) return (const void*)k_moe_down<KIND, 4, 1>;
+        return M <= 2   ? (const void*)k_moe_down<KIND, 2, 1>
+               : M <= 4 ? (const void*)k_moe_down<KIND, 2, 2>
+               : M <= 8 ? (const void*)k_moe_down<KIND, 2, 4> : (const void*)k_moe_down<KIND, 2, 8>;
+    } else {
+        return M <= 4   ? (const void*)k_moe_down<KIND, 1, 1>
+               : M <= 8 ? (const void*)k_moe_down<KIND, 1, 2> : (const void*)k_moe_down<KIND, 1, 4>;
+    }
+}
+
 template <int KIND>
 static cudaError_t launch_moe_kind(const dg_moe& op, void* ws, cudaStream_t s) {
-    using St = Stage<KIND>;
-    constexpr int kList = sizeof(Lists);
     MoeParams p;
     p.op = op;
     place(op, ws, &p.ws);
-    const int g = op.group_size;
-    auto vec16 = [](const void* q) { return ((uintptr_t)q & 15u) == 0; };
+    const bool g32 = KIND == DG_LINEAR_W4A16 && op.group_size == 32;
+    auto al4 = [](const void* q) { return ((uintptr_t)q & 3u) == 0; };
     void* args[] = {&p};
-
-    p.slot_bytes = p.vec_scales = 0;
-    cudaError_t e = launch_pdl((const void*)k_moe_scores<KIND == DG_LINEAR_BF16>, dim3(op.E), dim3(256), 0, s, args);
+    p.pair_scales = 0;
+    cudaError_t e = launch_pdl((const void*)k_moe_scores<KIND == DG_LINEAR_BF16>,
+                               dim3(op.E, (op.M + kScoreTokens - 1) / kScoreTokens), dim3(256), 0, s, args);
     if (e != cudaSuccess) return e;
 
-    auto stage_for = [](int most) {   // the largest stage of 1..most token rows
-        int b = 0;
-        for (int r = 1; r <= most; ++r) b = St::bytes(r) > b ? St::bytes(r) : b;
-        return b;
-    };
-    // up: one CTA per SM, as many warps as their rings fit
-    const int sms = sm_count();
-    p.slot_bytes = stage_for(op.M);
-    int warps = (int)((smem_optin_limit() - kList - 1024) / (kMoeStages * p.slot_bytes));
-    if (warps > kMoeMaxWarps) warps = kMoeMaxWarps;
-    if (warps < 1) return cudaErrorInvalidConfiguration;
-    size_t smem = (size_t)warps * kMoeStages * p.slot_bytes;
-    if (smem < (size_t)warps * op.E * 4) smem = (size_t)warps * op.E * 4;
-    p.vec_scales = St::kInt4 && g == 32 && op.K % 256 == 0 && vec16(op.gate_scale) && vec16(op.up_scale);
-    const void* fn = op.M <= 8 ? (const void*)k_moe_up<KIND, 1> : (const void*)k_moe_up<KIND, 2>;
+    // two CTAs per SM
+    p.pair_scales = g32 && op.K % 64 == 0 && al4(op.gate_scale) && al4(op.up_scale);
+    const int tok = op.M <= 8 ? 8 : 16;
+    size_t smem = (size_t)2 * kMoeWarps * tok * 16 * 4;
+    if (smem < (size_t)kMoeWarps * op.E * 4) smem = (size_t)kMoeWarps * op.E * 4;
+    const void* fn = up_kernel<KIND>(op.M);
     if ((e = tc::smem_attr_once(fn, smem)) != cudaSuccess) return e;
-    if ((e = launch_pdl(fn, dim3(sms), dim3(warps * 32), smem, s, args)) != cudaSuccess) return e;
+    const int ctas = 2 * sm_count();
+    if ((e = launch_pdl(fn, dim3(ctas), dim3(kMoeWarps * 32), smem, s, args)) != cudaSuccess) return e;
 
-    // down: two CTAs per SM (more row tiles than SMs then run side by side)
-    p.slot_bytes = stage_for(2 * op.M);
-    warps = (int)((114 * 1024 - kList - 2048) / (kMoeStages * p.slot_bytes + 64 * op.M));
-    if (warps > kMoeMaxWarps) warps = kMoeMaxWarps;
-    if (warps < 1) return cudaErrorInvalidConfiguration;
-    smem = (size_t)warps * (kMoeStages * p.slot_bytes + 64 * op.M);
-    p.vec_scales = St::kInt4 && g == 32 && op.I % 256 == 0 && vec16(op.down_scale);
-    fn = op.M <= 4 ? (const void*)k_moe_down<KIND, 1>
-         : op.M <= 8 ? (const void*)k_moe_down<KIND, 2> : (const void*)k_moe_down<KIND, 4>;
-    if ((e = tc::smem_attr_once(fn, smem)) != cudaSuccess) return e;
-    return launch_pdl(fn, dim3((op.K + 15) / 16), dim3(warps * 32), smem, s, args);
+    p.pair_scales = g32 && op.I % 64 == 0 && al4(op.down_scale);
+    const int tiles = (op.K + 15) / 16;
+    return launch_pdl(down_kernel<KIND>(op.M), dim3(tiles < ctas ? tiles : ctas), dim3(kMoeWarps * 32),
+                      (size_t)kMoeWarps * 16 * op.M * 4, s, args);
 }
 
 cudaError_t launch_moe(const dg_moe& op, void* ws, cudaStream_t s) {
