@@ -9,13 +9,17 @@
 // than for one.  Weights go from global memory straight into the
 // instruction's registers: a lane's 16 bytes are 8 columns of its row, and
 // the order of columns inside an instruction is free as long as the tokens'
-// values follow it.  A warp keeps one chunk (16 rows x 256 columns, 8 KB at
-// 16 bits) in flight and reloads each register as soon as it is used.
+// values follow it.  A warp loads one chunk (16 rows x 128 columns, 4 KB at 16
+// bits) with its tokens' values at once, then computes it; what keeps HBM busy
+// meanwhile are the SM's other warps (32 where registers allow).  A copy of
+// 1 GB in this pattern reads 6.7 TB/s with 32 warps of 4 KB per SM and 6.0 with
+// 16 of 8 KB; rows brought by the bulk copy engine (256 or 512 bytes each)
+// reached 2.9, cp.async rings of 8 warps 4.6.
 //
-//   up:   a CTA takes 8 gate and the same 8 up rows of an expert at a time, so
-//         that silu(gate) * up meets in one thread; its warps deal the row
-//         tile's chunks along K among themselves, without a break from one
-//         tile to the next, and their sums are added in warp order.
+//   up:   one, two, four or eight warps take 8 gate and the same 8 up rows of
+//         an expert at a time, so that silu(gate) * up meets in one thread;
+//         they deal the row tile's chunks along K among themselves and their
+//         sums are added in warp order.
 //   down: a CTA takes 16 output rows at a time; its warps deal the chunks of
 //         all chosen experts, each adding weight * sum into its own fp32 rows
 //         [token], which are summed in warp order.
@@ -29,6 +33,8 @@
 // token gets PH columns, column f carrying the token's values for the lanes
 // whose codes belong to group f and zero for the others, so that one
 // instruction sums the groups apart.
+#include <algorithm>
+
 #include "mma16.cuh"
 #include "tc_common.cuh"
 
@@ -50,7 +56,8 @@ struct MoeWs {
 struct MoeParams {
     dg_moe op;
     MoeWs ws;
-    int pair_scales;  // int4: two groups' scales are one aligned 4-byte load
+    int wide_scales;  // int4: a lane's scales of a chunk are one aligned load
+    int split;        // up: warps sharing a row tile's columns (1, 2, 4 or 8)
 };
 
 // ---- router scores ------------------------------------------------------------------------
@@ -105,12 +112,12 @@ __global__ void __launch_bounds__(256) k_moe_scores(const MoeParams p) {
         p.ws.scores[(size_t)(m0 + tid) * op.E + e] = v;
     }
     if (op.kind == DG_LINEAR_W4A16 && m0 == 0) {
-        const int n8 = op.M * K8;
-        for (int i = e * 256 + tid; i < n8; i += gridDim.x * 256) {
+        const int n8 = op.M * K8, first = e * 256 + tid, stride = gridDim.x * 256;
+        uint4* xp = reinterpret_cast<uint4*>(p.ws.xp);
+        for (int i = first; i < n8; i += stride) {
             const uint4 v = __ldcg(x + i);
-            reinterpret_cast<uint4*>(p.ws.xp)[i] =
-                make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                           __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+            xp[i] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                               __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
         }
     }
 }
@@ -236,124 +243,190 @@ struct Shape {
     static constexpr bool kInt4 = KIND == DG_LINEAR_W4A16;
     static constexpr int kLane = kInt4 ? (PH == 4 ? 32 : 16) : 8;
     static constexpr int kStep = 4 * kLane;
-    static constexpr int kCols = kInt4 ? 512 : 256;
+    static constexpr int kCols = PH == 4 ? 512 : kInt4 ? 256 : 128;
     static constexpr int kSteps = kCols / kStep;
     static constexpr int kWords = kInt4 ? kLane / 8 : 4;   // 32-bit registers of a row and step
     static constexpr int kTokens = 8 / PH;                 // token rows of 8 columns
+    static constexpr int kGroups = kCols / 128;            // int4: scale groups of a lane and row
 };
+
+// Streaming loads; the predicated forms give zero where `in` is false.
+__device__ __forceinline__ void ld_weights(uint32_t (&v)[4], const void* p) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "l"(p));
+}
+__device__ __forceinline__ void ld_weights(uint32_t (&v)[2], const void* p) {
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "l"(p));
+}
+__device__ __forceinline__ void ld_weights(uint32_t& v, const void* p) {
+    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+}
+__device__ __forceinline__ void ld_weights(uint32_t (&v)[4], const void* p, bool in) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+        "mov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=&r"(v[0]), "=&r"(v[1]), "=&r"(v[2]), "=&r"(v[3])
+        : "l"(p), "r"((int)in));
+}
+__device__ __forceinline__ void ld_weights(uint32_t (&v)[2], const void* p, bool in) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n\t}"
+        : "=&r"(v[0]), "=&r"(v[1])
+        : "l"(p), "r"((int)in));
+}
+__device__ __forceinline__ void ld_weights(uint32_t& v, const void* p, bool in) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.u32 %0, [%1];\n\t}"
+        : "=&r"(v)
+        : "l"(p), "r"((int)in));
+}
+// Eight values of a token row (kept in L1: other row tiles want them too).
+__device__ __forceinline__ uint4 ld_token(const uint16_t* p, bool in) {
+    uint4 v;
+    asm(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+        "mov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t@p ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((int)in));
+    return v;
+}
 
 // Rows g and g + 8 of a row tile at this lane's first column, and their scales.
 struct Src {
     const char* w[2];
     const uint16_t* s[2];
-    int k0;   // first column of the chunk
 };
 
 template <int KIND, int PH>
 struct Chunk {
     using S = Shape<KIND, PH>;
-    uint32_t v[S::kSteps][2][S::kWords];
-    uint32_t sc[S::kInt4 ? S::kSteps : 1][2];   // this thread's two columns' scales
 
-    __device__ __forceinline__ void load_step(const MoeParams& p, const Src& q, int i, int Kd) {
-        const int t = threadIdx.x & 3;
-        const bool in = q.k0 + i * S::kStep + t * S::kLane < Kd;
-        const size_t at = S::kInt4 ? (q.k0 + i * S::kStep) / 2 : (size_t)(q.k0 + i * S::kStep) * 2;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            if (S::kWords == 4) {
-                const uint4 x = in ? ld_stream16(q.w[r] + at) : make_uint4(0, 0, 0, 0);
-                v[i][r][0] = x.x, v[i][r][1] = x.y;
-                v[i][r][S::kWords - 2] = x.z, v[i][r][S::kWords - 1] = x.w;
-            } else {
-                uint2 x = make_uint2(0, 0);
-                if (in)
-                    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-                                 : "=r"(x.x), "=r"(x.y)
-                                 : "l"(q.w[r] + at));
-                v[i][r][0] = x.x, v[i][r][1] = x.y;
-            }
-            if (S::kInt4) {
-                // columns 2 t and 2 t + 1: groups f and f + 1 of the step's PH
-                const int grp = (q.k0 + i * S::kStep) / 32 + (PH == 4 ? (t & 1) * 2 : 0);
-                uint32_t two = 0;
-                if (p.pair_scales) {
-                    if (grp * 32 < Kd)
-                        asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];"
-                                     : "=r"(two)
-                                     : "l"(q.s[r] + grp));
-                } else {
-                    // any group size, count or alignment
-                    if (grp * 32 < Kd) two = ld_stream_u16(q.s[r] + grp * 32 / p.op.group_size);
-                    if (grp * 32 + 32 < Kd)
-                        two |= (uint32_t)ld_stream_u16(q.s[r] + (grp * 32 + 32) / p.op.group_size) << 16;
-                }
-                sc[i][r] = two;
-            }
-        }
-    }
-
-    __device__ __forceinline__ void load(const MoeParams& p, const Src& q, int Kd) {
-#pragma unroll
-        for (int i = 0; i < S::kSteps; ++i) load_step(p, q, i, Kd);
-    }
-
-    // acc[j] += (16 weight rows) x (token rows j * kTokens ..), the chunk's
-    // columns; each step's registers are then reloaded from `next` (if any).
-    // x[j]: the token row of this lane's column of block j, from column 0 on.
-    template <int NT>
-    __device__ __forceinline__ void mma(const MoeParams& p, const uint16_t* const (&x)[NT], int R, int k0,
-                                        int Kd, float (&acc)[NT][4], const Src& next, bool more) {
+    // acc[j] += (16 weight rows) x (token rows j * kTokens ..), columns [k0,
+    // k0 + kCols) of Kd.  x[j]: the token row of this lane's column of block j.
+    // FULL: all of the chunk's columns exist and int4 scales are wide_scales.
+    template <bool FULL, int NT>
+    __device__ __forceinline__ static void add_cols(const MoeParams& p, const Src& q, const uint16_t* const (&x)[NT],
+                                               int R, int k0, int Kd, float (&acc)[NT][4]) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const bool mine = PH == 1 || (PH == 2 ? (g & 1) == (t >> 1) : (g & 3) == t);
+        uint32_t v[S::kSteps][2][S::kWords], sc[2][2];
+        const size_t at = S::kInt4 ? k0 / 2 : (size_t)k0 * 2;
 #pragma unroll
         for (int i = 0; i < S::kSteps; ++i) {
-            const int k = k0 + i * S::kStep + t * S::kLane;
-            const bool in = mine && k < Kd;
-            if (S::kInt4) {
-                uint32_t lo[S::kWords][4], hi[S::kWords][4];
+            const bool in = k0 + i * S::kStep + t * S::kLane < Kd;
 #pragma unroll
-                for (int w = 0; w < S::kWords; ++w) {
-                    int4_pairs(v[i][0][w], lo[w]);
-                    int4_pairs(v[i][1][w], hi[w]);
-                }
-                const float2 f0 = __half22float2(u32_as_h2(sc[i][0])), f1 = __half22float2(u32_as_h2(sc[i][1]));
+            for (int r = 0; r < 2; ++r) {
+                const char* w = q.w[r] + at + (S::kInt4 ? i * S::kStep / 2 : i * S::kStep * 2);
+                if (FULL)
+                    ld_weights(v[i][r], w);
+                else
+                    ld_weights(v[i][r], w, in);
+            }
+        }
+        if constexpr (S::kInt4) {
+            // the chunk's scales of a row, in order over the quad's lanes: lane t
+            // holds groups t * kGroups .. + kGroups - 1 of the chunk
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    if (j * S::kTokens < R) {
-                        float c[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < 2; ++r) {
+                if (FULL) {
+                    if constexpr (S::kGroups == 4)
+                        ld_weights(sc[r], q.s[r] + k0 / 32 + t * 4);
+                    else
+                        ld_weights(sc[r][0], q.s[r] + k0 / 32 + t * 2);
+                } else {
+                    // any group size, count or alignment
 #pragma unroll
-                        for (int w = 0; w < S::kWords; ++w) {
-                            uint4 b = make_uint4(0, 0, 0, 0);
-                            if (in) b = __ldg(reinterpret_cast<const uint4*>(x[j] + k + w * 8));
-                            const uint32_t a0[4] = {lo[w][0], hi[w][0], lo[w][1], hi[w][1]};
-                            const uint32_t a1[4] = {lo[w][2], hi[w][2], lo[w][3], hi[w][3]};
-                            mma16816<false>(c, a0, b.x, b.y);
-                            mma16816<false>(c, a1, b.z, b.w);
-                        }
-                        acc[j][0] = fmaf(f0.x, c[0], acc[j][0]);
-                        acc[j][1] = fmaf(f0.y, c[1], acc[j][1]);
-                        acc[j][2] = fmaf(f1.x, c[2], acc[j][2]);
-                        acc[j][3] = fmaf(f1.y, c[3], acc[j][3]);
-                    }
-                }
-            } else {
-                constexpr bool BF = KIND == DG_LINEAR_BF16;
-                const uint32_t a0[4] = {v[i][0][0], v[i][1][0], v[i][0][1], v[i][1][1]};
-                const uint32_t a1[4] = {v[i][0][S::kWords - 2], v[i][1][S::kWords - 2],
-                                        v[i][0][S::kWords - 1], v[i][1][S::kWords - 1]};
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    if (j * S::kTokens < R) {
-                        uint4 b = make_uint4(0, 0, 0, 0);
-                        if (in) b = __ldg(reinterpret_cast<const uint4*>(x[j] + k));
-                        mma16816<BF>(acc[j], a0, b.x, b.y);
-                        mma16816<BF>(acc[j], a1, b.z, b.w);
+                    for (int w = 0; w < S::kGroups / 2; ++w) {
+                        const int k = k0 + (t * S::kGroups + 2 * w) * 32;
+                        uint32_t two = 0;
+                        if (k < Kd) two = ld_stream_u16(q.s[r] + k / p.op.group_size);
+                        if (k + 32 < Kd) two |= (uint32_t)ld_stream_u16(q.s[r] + (k + 32) / p.op.group_size) << 16;
+                        sc[r][w] = two;
                     }
                 }
             }
-            if (more) load_step(p, next, i, Kd);
         }
+        if constexpr (S::kInt4) {
+            // columns of other groups than this lane's codes are zero
+            const bool mine = PH == 2 ? (g & 1) == (t >> 1) : (g & 3) == t;
+#pragma unroll
+            for (int i = 0; i < S::kSteps; ++i) {
+                const int k = k0 + i * S::kStep + t * S::kLane;
+                const bool in = mine && (FULL || k < Kd);
+                float c[NT][4];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
+#pragma unroll
+                for (int w = 0; w < S::kWords; ++w) {
+                    uint32_t lo[4], hi[4];
+                    int4_pairs(v[i][0][w], lo);
+                    int4_pairs(v[i][1][w], hi);
+                    const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
+                    const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        if (j == 0 || j * S::kTokens < R) {
+                            const uint4 b = ld_token(x[j] + k + w * 8, in);
+                            mma16816<false>(c[j], a0, b.x, b.y);
+                            mma16816<false>(c[j], a1, b.z, b.w);
+                        }
+                    }
+                }
+                // columns 2 t and 2 t + 1: groups f and f + 1 of the step's PH
+                float2 f[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    uint32_t two;
+                    if (PH == 4) {   // step i's four groups are lane i's
+                        const uint32_t lo = __shfl_sync(0xffffffffu, sc[r][0], i, 4);
+                        const uint32_t hi = __shfl_sync(0xffffffffu, sc[r][1], i, 4);
+                        two = (t & 1) ? hi : lo;
+                    } else {         // step i's two groups are lane i's
+                        two = __shfl_sync(0xffffffffu, sc[r][0], i, 4);
+                    }
+                    f[r] = __half22float2(u32_as_h2(two));
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    acc[j][0] = fmaf(f[0].x, c[j][0], acc[j][0]);
+                    acc[j][1] = fmaf(f[0].y, c[j][1], acc[j][1]);
+                    acc[j][2] = fmaf(f[1].x, c[j][2], acc[j][2]);
+                    acc[j][3] = fmaf(f[1].y, c[j][3], acc[j][3]);
+                }
+            }
+        } else {
+            constexpr bool BF = KIND == DG_LINEAR_BF16;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                if (j == 0 || j * S::kTokens < R) {
+                    uint4 b[S::kSteps];
+#pragma unroll
+                    for (int i = 0; i < S::kSteps; ++i) {
+                        const int k = k0 + i * S::kStep + t * S::kLane;
+                        b[i] = FULL ? __ldg(reinterpret_cast<const uint4*>(x[j] + k)) : ld_token(x[j] + k, k < Kd);
+                    }
+#pragma unroll
+                    for (int i = 0; i < S::kSteps; ++i) {
+                        const uint32_t a0[4] = {v[i][0][0], v[i][1][0], v[i][0][1], v[i][1][1]};
+                        const uint32_t a1[4] = {v[i][0][2], v[i][1][2], v[i][0][3], v[i][1][3]};
+                        mma16816<BF>(acc[j], a0, b[i].x, b[i].y);
+                        mma16816<BF>(acc[j], a1, b[i].z, b[i].w);
+                    }
+                }
+            }
+        }
+    }
+
+    template <int NT>
+    __device__ __forceinline__ static void add(const MoeParams& p, const Src& q, const uint16_t* const (&x)[NT],
+                                               int R, int k0, int Kd, float (&acc)[NT][4]) {
+        if (k0 + S::kCols <= Kd && (!S::kInt4 || p.wide_scales))
+            add_cols<true>(p, q, x, R, k0, Kd, acc);
+        else
+            add_cols<false>(p, q, x, R, k0, Kd, acc);
     }
 
     // The sums of token row n of block j in acc, after all chunks: for 16-bit
@@ -367,11 +440,14 @@ struct Chunk {
     }
 };
 
-// The token row behind column g of block j (what a lane loads), and behind
-// this thread's accumulators.
+// The token row behind column g of block j.
 template <int PH>
 __device__ __forceinline__ int column_row(int j) {
     return j * (8 / PH) + ((threadIdx.x & 31) >> 2) / PH;
+}
+// Warps per SM that the kernels' registers are held to.
+__host__ __device__ constexpr int moe_warps(int KIND, int NT) {
+    return NT == 1 ? (KIND == DG_LINEAR_W4A16 ? 24 : 32) : NT == 2 ? 24 : NT == 4 ? 16 : 8;
 }
 
 // ---- gate and up ----------------------------------------------------------------------------
@@ -382,7 +458,7 @@ __device__ __forceinline__ size_t row_bytes_of(int cols) {
 }
 
 template <int KIND, int PH, int NT>
-__global__ void __launch_bounds__(kMoeWarps * 32, NT >= 8 ? 1 : 2) k_moe_up(const MoeParams p) {
+__global__ void __launch_bounds__(kMoeWarps * 32, moe_warps(KIND, NT) / kMoeWarps) k_moe_up(const MoeParams p) {
     using S = Shape<KIND, PH>;
     constexpr bool BF = KIND == DG_LINEAR_BF16;
     constexpr int kTok = NT * S::kTokens;   // token rows of the accumulators
@@ -405,42 +481,28 @@ __global__ void __launch_bounds__(kMoeWarps * 32, NT >= 8 ? 1 : 2) k_moe_up(cons
             if (op.weights) op.weights[s] = L.wts[s];
         }
 
-    // the warps' sums of a row tile, [2 tiles in turn][warps][kTok][16 rows]
-    float* part = dyn;
+    // warps [team * split, ..) share a row tile; their sums of it lie in part
+    // [2 tiles in turn][kTok][16 rows] of each warp
+    const int split = p.split, team = warp / split, first = team * split, teams = kMoeWarps / split;
+    constexpr int kPart = kTok * 16;
+    float* part = dyn + first * 2 * kPart;
     const int tiles = op.I / 8, total = L.count * tiles, n = (op.K + S::kCols - 1) / S::kCols;
     const size_t rb = row_bytes_of<KIND>(op.K);
     const uint16_t* x = S::kInt4 ? p.ws.xp : static_cast<const uint16_t*>(op.x);
-
-    // the next chunk to load: chunk fk of the n of row tile `fi`
-    int fi = blockIdx.x, fk = warp;
-    auto settle = [&] {
-        while (fk >= n) {
-            fk -= n;
-            fi += gridDim.x;
-        }
-    };
-    Src src{};
-    auto find = [&] {
-        const int li = fi / tiles, tile = fi - li * tiles;
-        const size_t row = (size_t)L.expert[li] * op.I + tile * 8 + g;
-        src.k0 = fk * S::kCols;
-        src.w[0] = static_cast<const char*>(op.W_gate) + row * rb + (S::kInt4 ? t * S::kLane / 2 : t * S::kLane * 2);
-        src.w[1] = static_cast<const char*>(op.W_up) + row * rb + (S::kInt4 ? t * S::kLane / 2 : t * S::kLane * 2);
-        if (S::kInt4) {
-            const size_t at = row * (op.K / op.group_size);
-            src.s[0] = static_cast<const uint16_t*>(op.gate_scale) + at;
-            src.s[1] = static_cast<const uint16_t*>(op.up_scale) + at;
-        }
-    };
-    Chunk<KIND, PH> ch;
-    settle();
-    if (fi < total) {
-        find();
-        ch.load(p, src, op.K);
-    }
-    int k = warp, turn = 0;
-    for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    int k = warp - first, turn = 0;   // this warp's next chunk of the row tile
+    for (int item = blockIdx.x + team * gridDim.x; item < total; item += teams * gridDim.x) {
         const int li = item / tiles, tile = item - li * tiles, R = L.tokens[li];
+        const size_t row = (size_t)L.expert[li] * op.I + tile * 8 + g;
+        Src src{};
+        {
+            const size_t at = row * rb + (S::kInt4 ? t * S::kLane / 2 : t * S::kLane * 2);
+            src.w[0] = static_cast<const char*>(op.W_gate) + at;
+            src.w[1] = static_cast<const char*>(op.W_up) + at;
+            if (S::kInt4) {
+                src.s[0] = static_cast<const uint16_t*>(op.gate_scale) + row * (op.K / op.group_size);
+                src.s[1] = static_cast<const uint16_t*>(op.up_scale) + row * (op.K / op.group_size);
+            }
+        }
         const uint16_t* xr[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -448,37 +510,33 @@ __global__ void __launch_bounds__(kMoeWarps * 32, NT >= 8 ? 1 : 2) k_moe_up(cons
         float acc[NT][4];
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-        for (; k < n; k += kMoeWarps) {
-            fk += kMoeWarps;
-            settle();
-            const bool more = fi < total;
-            if (more) find();
-            ch.mma(p, xr, R, k * S::kCols, op.K, acc, src, more);
-        }
+        for (; k < n; k += split) Chunk<KIND, PH>::add(p, src, xr, R, k * S::kCols, op.K, acc);
         k -= n;
-        float* mine = part + (size_t)(turn * kMoeWarps + warp) * kTok * 16;
+        float* mine = part + ((warp - first) * 2 + turn) * kPart;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (PH == 1) {
-                    mine[(j * 8 + t * 2) * 16 + g + 8 * h] = ch.sum(acc[j], 0, h);
-                    mine[(j * 8 + t * 2 + 1) * 16 + g + 8 * h] = ch.sum(acc[j], 1, h);
+                    mine[(j * 8 + t * 2) * 16 + g + 8 * h] = Chunk<KIND, PH>::sum(acc[j], 0, h);
+                    mine[(j * 8 + t * 2 + 1) * 16 + g + 8 * h] = Chunk<KIND, PH>::sum(acc[j], 1, h);
                 } else {
-                    const float v = ch.sum(acc[j], 0, h);
+                    const float v = Chunk<KIND, PH>::sum(acc[j], 0, h);
                     if (PH == 2 || (t & 1) == 0)
                         mine[(j * S::kTokens + (PH == 2 ? t : t >> 1)) * 16 + g + 8 * h] = v;
                 }
             }
-        __syncthreads();
-        for (int i = tid; i < R * 8; i += kMoeWarps * 32) {
+        if (split == 1)
+            __syncwarp();
+        else
+            tc::named_sync(1 + team, split * 32);
+        for (int i = tid - first * 32; i < R * 8; i += split * 32) {
             const int tok = i >> 3, r = i & 7;
-            const float* q = part + (size_t)turn * kMoeWarps * kTok * 16 + tok * 16 + r;
+            const float* q = part + turn * kPart + tok * 16 + r;
             float gate = 0.f, up = 0.f;
-#pragma unroll
-            for (int w = 0; w < kMoeWarps; ++w) {
-                gate += q[w * kTok * 16];
-                up += q[w * kTok * 16 + 8];
+            for (int w = 0; w < split; ++w) {
+                gate += q[w * 2 * kPart];
+                up += q[w * 2 * kPart + 8];
             }
             const float v = silu_f32(gate) * up;
             uint16_t* h = p.ws.h + (size_t)L.slot[li][tok] * 2 * op.I + tile * 8 +
@@ -495,17 +553,18 @@ __global__ void __launch_bounds__(kMoeWarps * 32, NT >= 8 ? 1 : 2) k_moe_up(cons
 // ---- down and the weighted sum ----------------------------------------------------------------
 
 template <int KIND, int PH, int NT>
-__global__ void __launch_bounds__(kMoeWarps * 32, NT >= 8 ? 1 : 2) k_moe_down(const MoeParams p) {
+__global__ void __launch_bounds__(moe_warps(KIND, NT) * 32) k_moe_down(const MoeParams p) {
     using S = Shape<KIND, PH>;
     constexpr bool BF = KIND == DG_LINEAR_BF16;
     extern __shared__ __align__(16) float dyn[];
     __shared__ Lists L;
     const dg_moe& op = p.op;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int warps = blockDim.x >> 5;
     const int M = op.M, tiles = (op.K + 15) / 16, n = (op.I + S::kCols - 1) / S::kCols;
     float* sums = dyn;   // [warps][M][16]
     griddep_launch_dependents();
-    for (int i = tid; i < kMoeWarps * 16 * M; i += blockDim.x) sums[i] = 0.f;
+    for (int i = tid; i < warps * 16 * M; i += blockDim.x) sums[i] = 0.f;
     griddep_wait();
     for (int s = tid; s < M * op.top_k; s += blockDim.x) {
         L.ids[s] = __ldcg(p.ws.ids + s);
@@ -516,45 +575,25 @@ __global__ void __launch_bounds__(kMoeWarps * 32, NT >= 8 ? 1 : 2) k_moe_down(co
     const size_t rb = row_bytes_of<KIND>(op.I);
     float* mine = sums + warp * 16 * M;
 
-    // the next chunk to load: chunk fk of the n of expert fl in row tile ft
-    int ft = blockIdx.x, fl = 0, fk = warp;
-    auto settle = [&] {
-        while (fk >= n) {
-            fk -= n;
-            if (++fl == L.count) {
-                fl = 0;
-                ft += gridDim.x;
-            }
-        }
-    };
-    Src src{};
-    auto find = [&] {
-        // op.K is a multiple of 8: a last tile may lack its second half
-        const size_t row = (size_t)L.expert[fl] * op.K + ft * 16 + g;
-        const int half = ft * 16 + 8 < op.K ? 8 : 0;
-        src.k0 = fk * S::kCols;
-        src.w[0] = static_cast<const char*>(op.W_down) + row * rb + (S::kInt4 ? t * S::kLane / 2 : t * S::kLane * 2);
-        src.w[1] = src.w[0] + half * rb;
-        if (S::kInt4) {
-            const int srow = op.I / op.group_size;
-            src.s[0] = static_cast<const uint16_t*>(op.down_scale) + row * srow;
-            src.s[1] = src.s[0] + half * srow;
-        }
-    };
-    Chunk<KIND, PH> ch;
-    settle();
-    if (ft < tiles) {
-        find();
-        ch.load(p, src, op.I);
-    }
-    int k = warp;
+    int k = warp;   // this warp's next chunk of the expert
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        // op.K is a multiple of 8: a last tile may lack its second half
+        const int half = tile * 16 + 8 < op.K ? 8 : 0;
         for (int li = 0; li < L.count; ++li) {
             if (k >= n) {   // nothing of this expert is this warp's
                 k -= n;
                 continue;
             }
             const int R = 2 * L.tokens[li];
+            const size_t row = (size_t)L.expert[li] * op.K + tile * 16 + g;
+            Src src{};
+            src.w[0] = static_cast<const char*>(op.W_down) + row * rb + (S::kInt4 ? t * S::kLane / 2 : t * S::kLane * 2);
+            src.w[1] = src.w[0] + half * rb;
+            if (S::kInt4) {
+                const int srow = op.I / op.group_size;
+                src.s[0] = static_cast<const uint16_t*>(op.down_scale) + row * srow;
+                src.s[1] = src.s[0] + half * srow;
+            }
             const uint16_t* xr[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -564,13 +603,7 @@ __global__ void __launch_bounds__(kMoeWarps * 32, NT >= 8 ? 1 : 2) k_moe_down(co
             float acc[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-            for (; k < n; k += kMoeWarps) {
-                fk += kMoeWarps;
-                settle();
-                const bool more = ft < tiles;
-                if (more) find();
-                ch.mma(p, xr, R, k * S::kCols, op.I, acc, src, more);
-            }
+            for (; k < n; k += warps) Chunk<KIND, PH>::add(p, src, xr, R, k * S::kCols, op.I, acc);
             k -= n;
             // token rows 2 i and 2 i + 1 are hi and lo of the expert's token i
 #pragma unroll
@@ -580,11 +613,11 @@ __global__ void __launch_bounds__(kMoeWarps * 32, NT >= 8 ? 1 : 2) k_moe_down(co
                     float hi, lo;
                     int i;
                     if (PH == 1) {
-                        hi = ch.sum(acc[j], 0, h), lo = ch.sum(acc[j], 1, h);
+                        hi = Chunk<KIND, PH>::sum(acc[j], 0, h), lo = Chunk<KIND, PH>::sum(acc[j], 1, h);
                         i = j * 4 + t;
                     } else {
                         const int over = PH == 2 ? 1 : 2;   // the lane with the next token row
-                        hi = ch.sum(acc[j], 0, h);
+                        hi = Chunk<KIND, PH>::sum(acc[j], 0, h);
                         lo = __shfl_xor_sync(0xffffffffu, hi, over);
                         i = PH == 2 ? ((t & 1) ? 16 : j * 2 + (t >> 1)) : (t ? 16 : j);
                     }
@@ -601,8 +634,7 @@ __global__ void __launch_bounds__(kMoeWarps * 32, NT >= 8 ? 1 : 2) k_moe_down(co
         for (int i = tid; i < 16 * M; i += blockDim.x) {
             const int m = i >> 4, row = tile * 16 + (i & 15);
             float y = 0.f;
-#pragma unroll
-            for (int w = 0; w < kMoeWarps; ++w) {
+            for (int w = 0; w < warps; ++w) {
                 y += sums[w * 16 * M + i];
                 sums[w * 16 * M + i] = 0.f;
             }
@@ -640,27 +672,35 @@ size_t moe_ws_bytes(const dg_moe& op) {
     return place(op, nullptr, &w);
 }
 
-// Kernels of each format by their token blocks: NT blocks of 8 / PH token rows.
+// Token blocks of the kernels: NT blocks of 8 / PH token rows, enough for all
+// of an expert's tokens (twice that in down: hi and lo).
+template <int KIND>
+static int token_blocks(int rows) {
+    const int per = KIND == DG_LINEAR_W4A16 ? 4 : 8, nt = (rows + per - 1) / per;
+    return nt <= 2 ? nt : nt <= 4 ? 4 : 8;
+}
 template <int KIND>
 static const void* up_kernel(int M) {
+    const int nt = token_blocks<KIND>(M);
     if constexpr (KIND == DG_LINEAR_W4A16) {
         if (M == 1) return (const void*)k_moe_up<KIND, 4, 1>;
-        return M <= 4   ? (const void*)k_moe_up<KIND, 2, 1>
-               : M <= 8 ? (const void*)k_moe_up<KIND, 2, 2> : (const void*)k_moe_up<KIND, 2, 4>;
+        return nt == 1   ? (const void*)k_moe_up<KIND, 2, 1>
+               : nt == 2 ? (const void*)k_moe_up<KIND, 2, 2> : (const void*)k_moe_up<KIND, 2, 4>;
     } else {
-        return M <= 8 ? (const void*)k_moe_up<KIND, 1, 1> : (const void*)k_moe_up<KIND, 1, 2>;
+        return nt == 1 ? (const void*)k_moe_up<KIND, 1, 1> : (const void*)k_moe_up<KIND, 1, 2>;
     }
 }
 template <int KIND>
 static const void* down_kernel(int M) {
+    const int nt = token_blocks<KIND>(2 * M);
     if constexpr (KIND == DG_LINEAR_W4A16) {
         if (M == 1) return (const void*)k_moe_down<KIND, 4, 1>;
-        return M <= 2   ? (const void*)k_moe_down<KIND, 2, 1>
-               : M <= 4 ? (const void*)k_moe_down<KIND, 2, 2>
-               : M <= 8 ? (const void*)k_moe_down<KIND, 2, 4> : (const void*)k_moe_down<KIND, 2, 8>;
+        return nt == 1   ? (const void*)k_moe_down<KIND, 2, 1>
+               : nt == 2 ? (const void*)k_moe_down<KIND, 2, 2>
+               : nt == 4 ? (const void*)k_moe_down<KIND, 2, 4> : (const void*)k_moe_down<KIND, 2, 8>;
     } else {
-        return M <= 4   ? (const void*)k_moe_down<KIND, 1, 1>
-               : M <= 8 ? (const void*)k_moe_down<KIND, 1, 2> : (const void*)k_moe_down<KIND, 1, 4>;
+        return nt == 1   ? (const void*)k_moe_down<KIND, 1, 1>
+               : nt == 2 ? (const void*)k_moe_down<KIND, 1, 2> : (const void*)k_moe_down<KIND, 1, 4>;
     }
 }
 
@@ -670,27 +710,38 @@ static cudaError_t launch_moe_kind(const dg_moe& op, void* ws, cudaStream_t s) {
     p.op = op;
     place(op, ws, &p.ws);
     const bool g32 = KIND == DG_LINEAR_W4A16 && op.group_size == 32;
-    auto al4 = [](const void* q) { return ((uintptr_t)q & 3u) == 0; };
+    auto al8 = [](const void* q) { return ((uintptr_t)q & 7u) == 0; };
     void* args[] = {&p};
-    p.pair_scales = 0;
+    p.wide_scales = 0;
     cudaError_t e = launch_pdl((const void*)k_moe_scores<KIND == DG_LINEAR_BF16>,
                                dim3(op.E, (op.M + kScoreTokens - 1) / kScoreTokens), dim3(256), 0, s, args);
     if (e != cudaSuccess) return e;
 
-    // two CTAs per SM
-    p.pair_scales = g32 && op.K % 64 == 0 && al4(op.gate_scale) && al4(op.up_scale);
-    const int tok = op.M <= 8 ? 8 : 16;
-    size_t smem = (size_t)2 * kMoeWarps * tok * 16 * 4;
+    p.wide_scales = g32 && op.K % 128 == 0 && al8(op.gate_scale) && al8(op.up_scale);
+    const int nt = token_blocks<KIND>(op.M), ctas = sm_count() * (moe_warps(KIND, nt) / kMoeWarps);
+    // as few warps to a row tile as leave no SM without work: each split costs a
+    // meeting per tile
+    const int chunk = KIND != DG_LINEAR_W4A16 ? 128 : op.M == 1 ? 512 : 256, experts = std::min(op.E, op.M * op.top_k);
+    p.split = 1;
+    while (p.split < kMoeWarps && (long long)experts * (op.I / 8) * p.split < 3ll * ctas * kMoeWarps &&
+           p.split * chunk < op.K)
+        p.split *= 2;
+    size_t smem = (size_t)2 * kMoeWarps * (op.M <= 8 ? 8 : 16) * 16 * 4;
     if (smem < (size_t)kMoeWarps * op.E * 4) smem = (size_t)kMoeWarps * op.E * 4;
     const void* fn = up_kernel<KIND>(op.M);
     if ((e = tc::smem_attr_once(fn, smem)) != cudaSuccess) return e;
-    const int ctas = 2 * sm_count();
     if ((e = launch_pdl(fn, dim3(ctas), dim3(kMoeWarps * 32), smem, s, args)) != cudaSuccess) return e;
 
-    p.pair_scales = g32 && op.I % 64 == 0 && al4(op.down_scale);
-    const int tiles = (op.K + 15) / 16;
-    return launch_pdl(down_kernel<KIND>(op.M), dim3(tiles < ctas ? tiles : ctas), dim3(kMoeWarps * 32),
-                      (size_t)kMoeWarps * 16 * op.M * 4, s, args);
+    // down: one CTA a row tile and the SM's warps divided among its CTAs, down
+    // to 8 warps; more tiles than that gives follow one another
+    p.wide_scales = g32 && op.I % 128 == 0 && al8(op.down_scale);
+    const int tiles = (op.K + 15) / 16, sms = sm_count(), most = moe_warps(KIND, token_blocks<KIND>(2 * op.M));
+    const int per_sm = std::min((tiles + sms - 1) / sms, most / kMoeWarps), warps = most / per_sm;
+    const int grid = std::min(tiles, sms * per_sm);
+    smem = (size_t)warps * 16 * op.M * 4;
+    fn = down_kernel<KIND>(op.M);
+    if ((e = tc::smem_attr_once(fn, smem)) != cudaSuccess) return e;
+    return launch_pdl(fn, dim3(grid), dim3(warps * 32), smem, s, args);
 }
 
 cudaError_t launch_moe(const dg_moe& op, void* ws, cudaStream_t s) {
