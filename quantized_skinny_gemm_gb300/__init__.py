@@ -180,11 +180,21 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_current = None
+
+
 def _stream(stream):
+    """The handle of a stream, or of the current one.  Asking torch for the raw
+    handle takes 0.4 us, building its Stream object 3 us: half of a small call."""
+    global _current
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    if _current is None:
+        import torch
+        torch.cuda.init()
+        _current = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    raw, device = _current
+    return raw(device())
 
 
 def _call(name, *args):
