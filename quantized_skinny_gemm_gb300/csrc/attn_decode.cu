@@ -5,7 +5,7 @@
 // few dozen rows per key / value head (query heads of the group x new tokens)
 // the kernel is bound by HBM as long as the rows share each key they read.
 // Rows therefore form 16-row tiles of mma.sync (m16n8k16, fp32 accumulators);
-// one stage of a warp is 16 keys and their values, copied into the warp's own
+// one stage of a warp is 16 keys (32 of up to 64 dims) and their values, copied into the warp's own
 // ring of shared memory by cp.async (16 bytes a lane: any page size, stride
 // and head size), so warps never wait for one another while they stream.
 //
@@ -20,6 +20,7 @@
 // Softmax is one pass: each warp keeps the running maximum m and sum l of its
 // own positions and rescales its output when m grows; scores are kept in
 // units of log2(e), so that e^z = 2^z'.
+#include <algorithm>
 #include <climits>
 
 #include "mma16.cuh"
@@ -29,9 +30,8 @@ namespace dg {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kStageKeys = 16;
-constexpr int kBlockKeys = 2 * kAttnWarps * kStageKeys;  // 128
-constexpr int kAttnMaxCtas = 512;
+constexpr int kBlockKeys = 128;
+constexpr int kAttnMaxCtas = 640;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
@@ -40,7 +40,19 @@ struct AttnParams {
     int rows;            // q_len * heads / kv_heads
     long long* prefix;   // [batch + 1] blocks of one head before each sequence
     float* part;         // [grid][2] parts of RT * 16 rows
+    uint32_t page_mul;   // j / page_size = mulhi(j, page_mul) >> page_shift, or j for 0
+    int page_shift;
 };
+
+// The page of position j of sequence b and its slot there; page -1: none.
+__device__ __forceinline__ int page_slot(const AttnParams& p, int b, int j, int& slot) {
+    const dg_paged_kv& kv = p.op.kv;
+    const int at = p.page_mul ? (int)(__umulhi((uint32_t)j, p.page_mul) >> p.page_shift) : j;
+    slot = j - at * kv.page_size;
+    if (at >= kv.max_pages) return -1;
+    const int page = __ldg(kv.block_table + (long long)b * kv.table_stride + at);
+    return page >= 0 && page < kv.num_pages ? page : -1;
+}
 
 __device__ __forceinline__ float exp2_fast(float v) {
     float r;
@@ -48,12 +60,16 @@ __device__ __forceinline__ float exp2_fast(float v) {
     return r;
 }
 
-// The positions some token of sequence b sees: [0, sinks) and [lo, end).
+// The positions some token of sequence b sees: [0, seen_sinks) and [seen_lo,
+// end).  They are walked in two pieces that start and end at multiples of 16,
+// [0, sinks) and [lo, end), so that with pages of a multiple of 16 positions a
+// stage lies in one page.
 struct Span {
     int first;   // position of the step's first token (negative: before the start)
-    int sinks, lo, end;
+    int sinks, lo, end, seen_sinks, seen_lo;
     __device__ __forceinline__ int count() const { return sinks + end - lo; }
     __device__ __forceinline__ int position(int c) const { return c < sinks ? c : c - sinks + lo; }
+    __device__ __forceinline__ bool seen(int j) const { return j >= seen_lo || j < seen_sinks; }
 };
 __device__ __forceinline__ Span span_of(const dg_attn& op, int b) {
     const int len = max(0, __ldg(op.kv.seq_lens + b));
@@ -62,24 +78,33 @@ __device__ __forceinline__ Span span_of(const dg_attn& op, int b) {
     s.first = len - op.q_len;
     s.end = (int)min((long long)len, cap);
     const long long lo = op.window ? (long long)s.first - op.window + 1 : 0;
-    s.lo = (int)max(0ll, min(lo, (long long)s.end));
-    s.sinks = min(op.sinks, s.lo);
+    s.seen_lo = (int)max(0ll, min(lo, (long long)s.end));
+    s.lo = s.seen_lo & ~15;
+    s.seen_sinks = min(op.sinks, s.seen_lo);
+    s.sinks = min((s.seen_sinks + 15) & ~15, s.lo);
     return s;
 }
 __device__ __forceinline__ int blocks_of(const Span& s) {
     return max(1, (int)(((long long)s.count() + kBlockKeys - 1) / kBlockKeys));
 }
 
-// First block of CTA c's range.
+// First block of CTA c's range: floor(c * total / ctas).
 __device__ __forceinline__ long long range_at(long long c, long long total, int ctas) {
+    if (total < (1 << 22)) return (unsigned)c * (unsigned)total / (unsigned)ctas;
     return c * total / ctas;
+}
+__device__ __forceinline__ int quotient(long long a, int b) {
+    return (unsigned long long)a >> 32 ? (int)(a / b) : (int)((unsigned)a / (unsigned)b);
 }
 
 template <int DP, int RT>
 struct AttnShape {
+    static constexpr int kSub = DP <= 64 ? 2 : 1;           // 16-key pieces of a stage
+    static constexpr int kKeys = 16 * kSub;
     static constexpr int kPitch = DP * 2 + 16;              // bytes; rows 16 bytes apart in banks
-    static constexpr int kStage = 2 * kStageKeys * kPitch;  // keys, then values
-    static constexpr int kStages = DP <= 64 ? 5 : DP <= 128 ? 3 : DP <= 192 ? 2 : 3;
+    static constexpr int kStage = 2 * kKeys * kPitch;       // keys, then values
+    static constexpr int kCtas = DP <= 192 ? 2 : 1;  // per SM
+    static constexpr int kStages = DP <= 64 ? (RT == 1 ? 3 : 2) : DP <= 128 ? 3 : DP <= 192 ? 2 : 3;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kRows = RT * 16;
     static constexpr int kQ = kRows * kPitch;
@@ -87,13 +112,14 @@ struct AttnShape {
     static constexpr int kOutPitch = DP + 8;                // floats of a merged row
     static constexpr int kPart = kRows * (DP + 2);          // floats of a part: m, l, then rows
     static_assert(kRows * kOutPitch * 4 <= kRing, "a warp's output fits its ring");
+    static_assert(kCtas * (kSmem + 2048) <= 228 * 1024, "an SM holds its CTAs");
 };
 
 template <bool BF16, int DP, int RT>
-__global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn(const AttnParams p) {
     using S = AttnShape<DP, RT>;
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ long long scan[kAttnThreads], found[4];
+    __shared__ long long scan[kAttnWarps], found[2];
     const dg_attn& op = p.op;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = op.kv.head_dim, G = op.heads / op.kv.kv_heads, B = op.kv.batch;
@@ -112,9 +138,27 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
     griddep_wait();
 
     // ---- this CTA's range of blocks -----------------------------------------------------
-    // Pass 0 counts all blocks; pass 1 finds the sequence of the range's first.
+    // The blocks of one head are counted over the sequences, 128 at a time; a
+    // second pass over more than 128 finds the sequence of the range's first.
     long long total = 0, begin = 0, end = 0;
-    for (int pass = 0; pass < 2; ++pass) {
+    auto take_range = [&] {
+        const int ctas = (int)min((long long)gridDim.x, total);
+        begin = range_at(blockIdx.x, total, ctas);
+        end = blockIdx.x < ctas ? range_at(blockIdx.x + 1, total, ctas) : begin;
+    };
+    int b = 0;
+    long long seq_at = 0;   // first block of sequence b
+    const int passes = B == 1 ? 0 : B <= kAttnThreads ? 1 : 2;
+    if (B == 1) {
+        const int n = blocks_of(span_of(op, 0));
+        total = (long long)n * heads;
+        take_range();
+        if (blockIdx.x == 0 && tid == 0) {
+            p.prefix[0] = 0;
+            p.prefix[1] = n;
+        }
+    }
+    for (int pass = 0; pass < passes; ++pass) {
         long long carry = 0;
         for (int b0 = 0; b0 < B; b0 += kAttnThreads) {
             const int b = b0 + tid;
@@ -134,7 +178,12 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
                 sum += scan[w];
             }
             const long long at = before + inc - n;
-            if (pass == 1 && b < B) {
+            carry += sum;
+            if (pass == 0 && b0 + kAttnThreads >= B) {
+                total = carry * heads;
+                take_range();
+            }
+            if (pass == passes - 1 && b < B) {
                 if (blockIdx.x == 0) {
                     p.prefix[b] = at;
                     if (b == B - 1) p.prefix[B] = at + n;
@@ -144,19 +193,14 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
                     found[1] = at;
                 }
             }
-            carry += sum;
             __syncthreads();
-        }
-        if (pass == 0) {
-            total = carry * heads;
-            const int ctas = (int)min((long long)gridDim.x, total);
-            begin = range_at(blockIdx.x, total, ctas);
-            end = blockIdx.x < ctas ? range_at(blockIdx.x + 1, total, ctas) : begin;
         }
     }
     if (begin >= end) return;
-    int b = (int)found[0];
-    long long seq_at = found[1] * heads;     // first block of sequence b
+    if (passes) {
+        b = (int)found[0];
+        seq_at = found[1] * heads;
+    }
 
     const float c2 = op.scale * kLog2e;
     const int g = lane >> 2, t4 = lane & 3;
@@ -171,32 +215,34 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
             sp = span_of(op, ++b);
             nb = blocks_of(sp);
         }
-        const int unit = (int)((blk - seq_at) / nb);          // head and row group
+        const int unit = quotient(blk - seq_at, nb);            // head and row group
         const int kb = (int)(blk - seq_at - (long long)unit * nb);
         const int ke = (int)min((long long)nb, kb + (end - blk));
         const int hk = unit / p.groups, row0 = (unit - hk * p.groups) * S::kRows;
         const int count = sp.count();
         const int last = sp.first + op.q_len - 1;
 
-        // this warp's stages: keys kb * 128 + 64 i + 16 warp on
-        const int key0 = kb * kBlockKeys + warp * kStageKeys;
+        // this warp's stages: kKeys keys from kb * 128 + warp * kKeys on, then every
+        // kStep further
+        constexpr int kKeys = S::kKeys;
+        const int key0 = kb * kBlockKeys + warp * kKeys;
         const int lim = min(count, ke * kBlockKeys);
-        constexpr int kStep = kAttnWarps * kStageKeys;
+        constexpr int kStep = kAttnWarps * kKeys;
         const int n = key0 < lim ? (lim - key0 + kStep - 1) / kStep : 0;
 
-        // Position and cache offset (elements; -1: nothing there) of key `lane` (lanes
-        // 0..15) of stage i.
+        // Position and cache offset (elements; -1: nothing there) of key `lane` (lane
+        // mod kKeys) of stage i.
         auto locate = [&](int i, int& pos, long long& off) {
-            const int c = key0 + i * kStep + (lane & 15);
+            const int c = key0 + i * kStep + (lane & (kKeys - 1));
             pos = INT_MAX;
             off = -1;
             if (i < n && c < lim) {
                 const int j = sp.position(c);
-                const int page = page_of(op.kv, b, j);
+                int slot = 0;
+                const int page = sp.seen(j) ? page_slot(p, b, j, slot) : -1;
                 if (page >= 0) {
                     pos = j;
-                    off = page * op.kv.page_stride + (j % op.kv.page_size) * op.kv.token_stride +
-                          hk * op.kv.head_stride;
+                    off = page * op.kv.page_stride + slot * op.kv.token_stride + hk * op.kv.head_stride;
                 }
             }
         };
@@ -204,16 +250,38 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
             if (i < n) {
                 const uint32_t dst = ring_a + (i % S::kStages) * S::kStage;
                 constexpr int kChunks = DP / 8;
-#pragma unroll
-                for (int it = 0; it < kStageKeys * kChunks / 32; ++it) {
-                    const int idx = it * 32 + lane, row = idx / kChunks, ch = idx % kChunks;
-                    const long long o = __shfl_sync(0xffffffffu, off, row);
+                // keys in a row in one page: addresses without exchanges
+                const long long o0 = __shfl_sync(0xffffffffu, off, 0);
+                const bool run = off >= 0 && off == o0 + (lane & (kKeys - 1)) * op.kv.token_stride;
+                if (32 % kChunks == 0 && __all_sync(0xffffffffu, run)) {
+                    constexpr int kRows = 32 % kChunks == 0 ? 32 / kChunks : 1;   // rows of an instruction
+                    const int row = lane / kChunks, ch = lane % kChunks;
                     if (ch * 8 < D) {
-                        const long long at = o < 0 ? 0 : o + ch * 8;
+                        const long long at = o0 + row * op.kv.token_stride + ch * 8;
+                        const uint16_t* k = static_cast<const uint16_t*>(op.kv.k) + at;
+                        const uint16_t* v = static_cast<const uint16_t*>(op.kv.v) + at;
                         const uint32_t d = dst + row * S::kPitch + ch * 16;
-                        cp_async16(d, static_cast<const uint16_t*>(op.kv.k) + at, o >= 0);
-                        cp_async16(d + kStageKeys * S::kPitch,
-                                   static_cast<const uint16_t*>(op.kv.v) + at, o >= 0);
+                        const long long step = kRows * op.kv.token_stride;
+#pragma unroll
+                        for (int it = 0; it < kKeys / kRows; ++it) {
+                            cp_async16(d + it * kRows * S::kPitch, k);
+                            cp_async16(d + (kKeys + it * kRows) * S::kPitch, v);
+                            k += step;
+                            v += step;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int it = 0; it < kKeys * kChunks / 32; ++it) {
+                        const int idx = it * 32 + lane, row = idx / kChunks, ch = idx % kChunks;
+                        const long long o = __shfl_sync(0xffffffffu, off, row);
+                        if (ch * 8 < D) {
+                            const long long at = o < 0 ? 0 : o + ch * 8;
+                            const uint32_t d = dst + row * S::kPitch + ch * 16;
+                            cp_async16(d, static_cast<const uint16_t*>(op.kv.k) + at, o >= 0);
+                            cp_async16(d + kKeys * S::kPitch,
+                                       static_cast<const uint16_t*>(op.kv.v) + at, o >= 0);
+                        }
                     }
                 }
             }
@@ -253,12 +321,15 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
             m[r][0] = m[r][1] = -INFINITY;
             l[r][0] = l[r][1] = 0.f;
         }
-        // one tile: q stays in registers; several tiles read it again for every stage
-        uint32_t qf[RT == 1 ? DP / 16 : 1][4];
+        // q stays in registers where they suffice, else it is read again for every stage
+        constexpr bool kKeepQ = RT == 1 || RT * DP <= 128;
+        uint32_t qf[kKeepQ ? RT : 1][kKeepQ ? DP / 16 : 1][4];
         const uint32_t qa = qs_a + ((lane & 7) + ((lane >> 3) & 1) * 8) * S::kPitch + (lane >> 4) * 16;
-        if (RT == 1) {
+        if constexpr (kKeepQ) {
 #pragma unroll
-            for (int k = 0; k < DP / 16; ++k) ldsm4(qf[RT == 1 ? k : 0], qa + k * 32);
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) ldsm4(qf[r][k], qa + r * 16 * S::kPitch + k * 32);
         }
 
 #pragma unroll 1
@@ -266,7 +337,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
             cp_wait<S::kStages - 2>();
             __syncwarp();
             const int slot = i % S::kStages;
-            const uint32_t ka = ring_a + slot * S::kStage, va = ka + kStageKeys * S::kPitch;
+            const uint32_t ka = ring_a + slot * S::kStage, va = ka + kKeys * S::kPitch;
             int my_pos = pos[0];
 #pragma unroll
             for (int q = 1; q < S::kStages; ++q)
@@ -279,40 +350,45 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
             issue(ni, off_next);
             locate(ni + 1, pos_next, off_next);
 
-            // scores of 16 keys
-            float s[RT][2][4];
+            // scores of the stage's keys, 8 to a block
+            constexpr int kBlk = 2 * S::kSub;
+            float s[RT][kBlk][4];
 #pragma unroll
             for (int r = 0; r < RT; ++r)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) s[r][j][0] = s[r][j][1] = s[r][j][2] = s[r][j][3] = 0.f;
+                for (int j = 0; j < kBlk; ++j) s[r][j][0] = s[r][j][1] = s[r][j][2] = s[r][j][3] = 0.f;
             const uint32_t kl = ka + ((lane & 7) + (lane >> 4) * 8) * S::kPitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k) {
-                uint32_t kf[4];
-                ldsm4(kf, kl + k * 32);
+                uint32_t kf[S::kSub][4];
+#pragma unroll
+                for (int u = 0; u < S::kSub; ++u) ldsm4(kf[u], kl + u * 16 * S::kPitch + k * 32);
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     uint32_t qr[4];
-                    if (RT > 1) ldsm4(qr, qa + r * 16 * S::kPitch + k * 32);
-                    const uint32_t(&a)[4] = RT == 1 ? qf[RT == 1 ? k : 0] : qr;
-                    mma16816<BF16>(s[r][0], a, kf[0], kf[1]);
-                    mma16816<BF16>(s[r][1], a, kf[2], kf[3]);
+                    if (!kKeepQ) ldsm4(qr, qa + r * 16 * S::kPitch + k * 32);
+                    const uint32_t(&a)[4] = kKeepQ ? qf[kKeepQ ? r : 0][kKeepQ ? k : 0] : qr;
+#pragma unroll
+                    for (int u = 0; u < S::kSub; ++u) {
+                        mma16816<BF16>(s[r][2 * u], a, kf[u][0], kf[u][1]);
+                        mma16816<BF16>(s[r][2 * u + 1], a, kf[u][2], kf[u][3]);
+                    }
                 }
             }
 #pragma unroll
             for (int r = 0; r < RT; ++r)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < kBlk; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[r][j][e] *= c2;
 
             // masks, where some row does not see some key of the stage
             const bool all = my_pos <= sp.first &&
                              (!op.window || last - my_pos < op.window || my_pos < op.sinks);
-            unsigned poison = 0;
+            unsigned poison = 0;   // keys whose values are not finite
             if (!__all_sync(0xffffffffu, all)) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < kBlk; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int kp = __shfl_sync(0xffffffffu, my_pos, j * 8 + t4 * 2 + e);
@@ -328,13 +404,14 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
                     }
                 if (op.q_len > 1) {
                     // a value that only some rows see must not meet the others' zero
-                    // weights if it is not finite: lanes 2k and 2k + 1 look at key k
+                    // weights if it is not finite: 32 / kKeys lanes look at each key
+                    constexpr int kPer = 32 / kKeys, kBytes = DP * 2 / kPer;
                     bool bad = false;
-                    const unsigned char* vr =
-                        ring + slot * S::kStage + (kStageKeys + (lane >> 1)) * S::kPitch + (lane & 1) * DP;
+                    const unsigned char* vr = ring + slot * S::kStage +
+                                              (kKeys + (lane & (kKeys - 1))) * S::kPitch + lane / kKeys * kBytes;
                     constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
 #pragma unroll 4
-                    for (int q = 0; q < DP / 16; ++q) {
+                    for (int q = 0; q < kBytes / 16; ++q) {
                         const uint4 v = *reinterpret_cast<const uint4*>(vr + q * 16);
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -342,18 +419,20 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
                             bad = bad || (w[x] & kExp) == kExp || ((w[x] >> 16) & kExp) == kExp;
                     }
                     poison = __ballot_sync(0xffffffffu, bad);
+                    if (kPer == 2) poison = (poison | poison >> 16) & 0xFFFFu;
                 }
             }
 
             // running maximum, weights, rescaling
-            uint32_t pf[RT][4];
+            uint32_t pf[RT][S::kSub][4];
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 float nm[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float v = fmaxf(fmaxf(s[r][0][2 * h], s[r][0][2 * h + 1]),
-                                    fmaxf(s[r][1][2 * h], s[r][1][2 * h + 1]));
+                    float v = fmaxf(s[r][0][2 * h], s[r][0][2 * h + 1]);
+#pragma unroll
+                    for (int j = 1; j < kBlk; ++j) v = fmaxf(v, fmaxf(s[r][j][2 * h], s[r][j][2 * h + 1]));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
                     nm[h] = fmaxf(m[r][h], v);
@@ -375,34 +454,36 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
                 for (int h = 0; h < 2; ++h) {
                     const float base = m[r][h] == -INFINITY ? 0.f : m[r][h];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
+                    for (int j = 0; j < kBlk; ++j) {
                         const float a = exp2_fast(s[r][j][2 * h] - base);
                         const float c = exp2_fast(s[r][j][2 * h + 1] - base);
                         l[r][h] += a + c;
                         // weights in [0, 1] meet the values as 16-bit numbers: what
                         // the matrix instruction takes, 2^-12 (fp16) or 2^-9 (bf16) off
-                        pf[r][2 * j + h] = pair_16<BF16>(a, c);
+                        pf[r][j >> 1][2 * (j & 1) + h] = pair_16<BF16>(a, c);
                         s[r][j][2 * h] = a;
                         s[r][j][2 * h + 1] = c;
                     }
                 }
             }
             if (poison) {
-                unsigned char* vb = ring + slot * S::kStage + kStageKeys * S::kPitch;
+                unsigned char* vb = ring + slot * S::kStage + kKeys * S::kPitch;
 #pragma unroll 1
-                for (int k = 0; k < kStageKeys; ++k) {
-                    if (!((poison >> (2 * k)) & 3u)) continue;
+                for (int k = 0; k < kKeys; ++k) {
+                    if (!((poison >> k) & 1u)) continue;
                     const int kp = __shfl_sync(0xffffffffu, my_pos, k);
                     const int src = (lane & ~3) | ((k & 7) >> 1);
 #pragma unroll
                     for (int r = 0; r < RT; ++r)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const float w00 = __shfl_sync(0xffffffffu, s[r][0][2 * h], src);
-                            const float w01 = __shfl_sync(0xffffffffu, s[r][0][2 * h + 1], src);
-                            const float w10 = __shfl_sync(0xffffffffu, s[r][1][2 * h], src);
-                            const float w11 = __shfl_sync(0xffffffffu, s[r][1][2 * h + 1], src);
-                            const float w = k < 8 ? ((k & 1) ? w01 : w00) : ((k & 1) ? w11 : w10);
+                            float w = 0.f;
+#pragma unroll
+                            for (int j = 0; j < kBlk; ++j) {
+                                const float w0 = __shfl_sync(0xffffffffu, s[r][j][2 * h], src);
+                                const float w1 = __shfl_sync(0xffffffffu, s[r][j][2 * h + 1], src);
+                                if (j == k >> 3) w = (k & 1) ? w1 : w0;
+                            }
                             const int pr = sp.first + (row0 + r * 16 + g + h * 8) / G;
                             const bool see = kp <= pr && (!op.window || pr - kp < op.window ||
                                                           kp < op.sinks);
@@ -426,15 +507,17 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
             // output += weights x values
             const uint32_t vl = va + ((lane & 7) + ((lane >> 3) & 1) * 8) * S::kPitch + (lane >> 4) * 16;
 #pragma unroll
-            for (int d = 0; d < DP / 16; ++d) {
-                uint32_t vf[4];
-                ldsm4_t(vf, vl + d * 32);
+            for (int u = 0; u < S::kSub; ++u)
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    mma16816<BF16>(o[r][2 * d], pf[r], vf[0], vf[1]);
-                    mma16816<BF16>(o[r][2 * d + 1], pf[r], vf[2], vf[3]);
+                for (int d = 0; d < DP / 16; ++d) {
+                    uint32_t vf[4];
+                    ldsm4_t(vf, vl + u * 16 * S::kPitch + d * 32);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        mma16816<BF16>(o[r][2 * d], pf[r][u], vf[0], vf[1]);
+                        mma16816<BF16>(o[r][2 * d + 1], pf[r][u], vf[2], vf[3]);
+                    }
                 }
-            }
         }
         cp_wait<0>();
         __syncwarp();
@@ -507,73 +590,96 @@ __global__ void __launch_bounds__(kAttnThreads) k_attn(const AttnParams p) {
     }
 }
 
-// One CTA per query row: the parts of its unit, where that was cut between
-// CTAs, added in CTA order (eight interleaved sequences, then those in order).
+// One CTA per row of a unit that was cut between CTAs: its parts joined in CTA
+// order, each warp every eighth part and then the warps' in order.  Where parts
+// are few (8 or less) every eighth CTA does eight rows, one warp each.
+constexpr int kJoinWarps = 8;
 template <bool BF16, int DP, int RT>
-__global__ void __launch_bounds__(256) k_attn_join(const AttnParams p, int ctas_max) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams p, int ctas_max) {
     using S = AttnShape<DP, RT>;
-    __shared__ float wgt[kAttnMaxCtas + 1], red[8], acc[8][DP];
+    constexpr int kPairs = DP / 64;   // pairs of output values of a lane, 64 apart
+    __shared__ float2 acc[kJoinWarps][kPairs][32];
+    __shared__ float tops[kJoinWarps], sums[kJoinWarps];
     griddep_launch_dependents();
     griddep_wait();
     const dg_attn& op = p.op;
-    const int t = blockIdx.x, h = blockIdx.y, D = op.kv.head_dim;
-    const int b = t / op.q_len, G = op.heads / op.kv.kv_heads;
-    const int hk = h / G, row = (t - b * op.q_len) * G + h - hk * G;
-    const int grp = row / S::kRows, r = row - grp * S::kRows;
-    const int heads = op.kv.kv_heads * p.groups;
-    const long long total = p.prefix[op.kv.batch] * heads;
-    const int ctas = (int)min((long long)ctas_max, total);
-    const long long nb = p.prefix[b + 1] - p.prefix[b];
-    const long long u0 = p.prefix[b] * heads + (hk * p.groups + grp) * nb, u1 = u0 + nb;
-    // the CTAs whose ranges hold the unit's first and last block
-    int c0 = (int)(u0 * ctas / total), c1 = (int)((u1 - 1) * ctas / total);
-    while (range_at(c0 + 1, total, ctas) <= u0) ++c0;
-    while (range_at(c1 + 1, total, ctas) <= u1 - 1) ++c1;
-    if (c0 == c1) return;  // finished in place
-    const int n = c1 - c0 + 1;
-    auto part_of = [&](int i) {
-        const int second = i == 0 && range_at(c0, total, ctas) < u0;
-        return p.part + ((size_t)(c0 + i) * 2 + second) * S::kPart;
+    const int G = op.heads / op.kv.kv_heads, heads = op.kv.kv_heads * p.groups;
+    const int b = blockIdx.x / heads, hg = blockIdx.x - b * heads, D = op.kv.head_dim;
+    const int hk = hg / p.groups, base_row = (hg - hk * p.groups) * S::kRows;
+    const long long total = __ldg(p.prefix + op.kv.batch) * heads, first = __ldg(p.prefix + b);
+    const int ctas = (int)min((long long)ctas_max, total), nb = (int)(__ldg(p.prefix + b + 1) - first);
+    const long long u0 = first * heads + (long long)hg * nb, u1 = u0 + nb - 1;
+    // the CTAs whose ranges hold the unit's first and last block: the largest c
+    // with floor(c * total / ctas) <= u, that is c * total < (u + 1) * ctas
+    auto cta_of = [&](long long u) {
+        const long long top = (u + 1) * ctas;
+        int c = min(ctas - 1, __float2int_rz(__fdividef((float)top, (float)total)));
+        while (c * total >= top) --c;
+        while ((c + 1) * total < top) ++c;
+        return c;
     };
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    float top = -INFINITY;
-    for (int i = tid; i < n; i += 256) top = fmaxf(top, wgt[i] = part_of(i)[r]);
+    const int c0 = cta_of(u0), c1 = cta_of(u1);
+    if (c0 == c1) return;  // finished in place
+    const int n = c1 - c0 + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool few = n <= kJoinWarps;
+    if (few && blockIdx.y % kJoinWarps) return;
+    const int r = blockIdx.y + (few ? warp : 0);
+    if (few && (r >= S::kRows || base_row + r >= p.rows)) return;
+    // a CTA's first segment is in its first part, its last one in the second
+    const float* parts = p.part + (size_t)c0 * 2 * S::kPart;
+    const int skip = c0 * total < u0 * ctas ? S::kPart : 0;
+
+    float top = -INFINITY, sum = 0.f;
+    float2 v[kPairs];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) red[warp] = top;
-    __syncthreads();
+    for (int x = 0; x < kPairs; ++x) v[x] = make_float2(0.f, 0.f);
+    auto add = [&](float m, float l, const float2 (&w)[kPairs]) {
+        const float nt = fmaxf(top, m), base = nt == -INFINITY ? 0.f : nt;
+        const float f = exp2_fast(top - base), k = exp2_fast(m - base);
+        top = nt;
+        sum = sum * f + l * k;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, v[DP / 32];
-#pragma unroll
-    for (int x = 0; x < DP / 32; ++x) v[x] = 0.f;
+        for (int x = 0; x < kPairs; ++x) {
+            v[x].x = v[x].x * f + w[x].x * k;
+            v[x].y = v[x].y * f + w[x].y * k;
+        }
+    };
 #pragma unroll 4
-    for (int i = warp; i < n; i += 8) {
-        const float* q = part_of(i);
-        const float f = exp2_fast(wgt[i] - base);
-        sum = fmaf(f, q[S::kRows + r], sum);
+    for (int i = few ? 0 : warp; i < n; i += few ? 1 : kJoinWarps) {
+        const float* q = parts + (size_t)i * 2 * S::kPart + (i == 0 ? skip : 0);
+        const float2* o = reinterpret_cast<const float2*>(q + 2 * S::kRows + r * DP) + lane;
+        float2 w[kPairs];
 #pragma unroll
-        for (int x = 0; x < DP / 32; ++x)
-            if (x * 32 + lane < D) v[x] = fmaf(f, q[2 * S::kRows + r * DP + x * 32 + lane], v[x]);
+        for (int x = 0; x < kPairs; ++x)
+            w[x] = x * 64 + lane * 2 < D ? __ldg(o + x * 32) : make_float2(0.f, 0.f);
+        add(__ldg(q + r), __ldg(q + S::kRows + r), w);
     }
-    __syncthreads();
-    if (lane == 0) red[warp] = sum;
+    if (!few) {
+        if (lane == 0) {
+            tops[warp] = top;
+            sums[warp] = sum;
+        }
 #pragma unroll
-    for (int x = 0; x < DP / 32; ++x) acc[warp][x * 32 + lane] = v[x];
-    __syncthreads();
-    sum = 0.f;
+        for (int x = 0; x < kPairs; ++x) acc[warp][x][lane] = v[x];
+        __syncthreads();
+        if (warp) return;
+        for (int w = 1; w < kJoinWarps; ++w) {
+            float2 o[kPairs];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) sum += red[w];
-    if (tid < D) {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) s += acc[w][tid];
-        static_cast<uint16_t*>(op.out)[(long long)t * op.out_stride + (long long)h * D + tid] =
-            elem_16<BF16>(sum == 0.f ? 0.f : s / sum);
+            for (int x = 0; x < kPairs; ++x) o[x] = acc[w][x][lane];
+            add(tops[w], sums[w], o);
+        }
     }
-    if (tid == 0 && op.lse)
-        op.lse[(long long)t * op.heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    const int row = base_row + r, tok = row / G, h = hk * G + row - tok * G;
+    const long long t = (long long)b * op.q_len + tok;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(op.out) + t * op.out_stride +
+                                                (long long)h * D);
+#pragma unroll
+    for (int x = 0; x < kPairs; ++x)
+        if (x * 64 + lane * 2 < D) out[x * 32 + lane] = pair_16<BF16>(v[x].x * inv, v[x].y * inv);
+    if (lane == 0 && op.lse)
+        op.lse[t * op.heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // Row tiles of a CTA: as many as share its keys with 128 output registers.
@@ -610,20 +716,30 @@ static cudaError_t launch_attn_t(const dg_attn& op, void* ws, cudaStream_t s) {
     p.groups = (p.rows + S::kRows - 1) / S::kRows;
     p.prefix = static_cast<long long*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + prefix_bytes(op));
+    // with s = ceil(log2(page_size)): exact for every j < 2^31
+    const uint32_t ps = (uint32_t)op.kv.page_size;
+    p.page_mul = 0;
+    p.page_shift = 0;
+    if (ps > 1) {
+        int log = 1;
+        while ((1ull << log) < ps) ++log;
+        p.page_mul = (uint32_t)((1ull << (31 + log)) / ps + 1);
+        p.page_shift = log - 1;
+    }
     const void* fn = (const void*)k_attn<BF16, DP, RT>;
     cudaError_t e = tc::smem_attr_once(fn, S::kSmem);
     if (e != cudaSuccess) return e;
-    const int per_sm = S::kSmem <= 112 * 1024 ? 2 : 1;
     const long long blocks = max_blocks(op, p.groups);
-    int grid = sm_count() * per_sm;
+    int grid = sm_count() * S::kCtas;
     if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
     if (grid > blocks) grid = (int)blocks;
     void* args[] = {&p};
     e = launch_pdl(fn, dim3(grid), dim3(kAttnThreads), S::kSmem, s, args);
     if (e != cudaSuccess || never_split(op)) return e;
     void* jargs[] = {&p, &grid};
-    return launch_pdl((const void*)k_attn_join<BF16, DP, RT>, dim3(op.kv.batch * op.q_len, op.heads),
-                      dim3(256), 0, s, jargs);
+    return launch_pdl((const void*)k_attn_join<BF16, DP, RT>,
+                      dim3(op.kv.batch * op.kv.kv_heads * p.groups, std::min(p.rows, S::kRows)),
+                      dim3(kJoinWarps * 32), 0, s, jargs);
 }
 
 template <bool BF16>
