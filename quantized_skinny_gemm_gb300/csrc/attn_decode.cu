@@ -18,8 +18,9 @@
 // load every SM alike, and no sum depends on timing.
 //
 // Softmax is one pass: each warp keeps the running maximum m and sum l of its
-// own positions and rescales its output when m grows; scores are kept in
-// units of log2(e), so that e^z = 2^z'.
+// own positions and rescales its output only when m has grown by more than
+// 2^8 since (weights then stay below 256, far inside the 16-bit types' range);
+// scores are turned to units of log2(e) inside the exponent.
 #include <algorithm>
 #include <climits>
 
@@ -101,16 +102,19 @@ template <int DP, int RT>
 struct AttnShape {
     static constexpr int kSub = DP <= 64 ? 2 : 1;           // 16-key pieces of a stage
     static constexpr int kKeys = 16 * kSub;
-    static constexpr int kPitch = DP * 2 + 16;              // bytes; rows 16 bytes apart in banks
+    static constexpr int kPitch = DP * 2;                   // bytes; see piece()
     static constexpr int kStage = 2 * kKeys * kPitch;       // keys, then values
     static constexpr int kCtas = DP <= 192 ? 2 : 1;  // per SM
-    static constexpr int kStages = DP <= 64 ? (RT == 1 ? 3 : 2) : DP <= 128 ? 3 : DP <= 192 ? 2 : 3;
+    static constexpr int kStages = DP <= 64 ? 3 : DP <= 128 ? 3 : DP <= 192 ? 2 : 3;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kRows = RT * 16;
     static constexpr int kQ = kRows * kPitch;
     static constexpr size_t kSmem = (size_t)kAttnWarps * kRing + kQ + 2 * kAttnWarps * kRows * 4;
     static constexpr int kOutPitch = DP + 8;                // floats of a merged row
     static constexpr int kPart = kRows * (DP + 2);          // floats of a part: m, l, then rows
+    // Byte of 16-byte piece c of row r: the pieces of 128 bytes change places by
+    // the row's low bits, so that eight rows' same piece lie in different banks.
+    __device__ static constexpr int piece(int r, int c) { return r * kPitch + ((c ^ (r & 7)) << 4); }
     static_assert(kRows * kOutPitch * 4 <= kRing, "a warp's output fits its ring");
     static_assert(kCtas * (kSmem + 2048) <= 228 * 1024, "an SM holds its CTAs");
 };
@@ -118,7 +122,7 @@ struct AttnShape {
 template <bool BF16, int DP, int RT>
 __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn(const AttnParams p) {
     using S = AttnShape<DP, RT>;
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long scan[kAttnWarps], found[2];
     const dg_attn& op = p.op;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -202,7 +206,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
         seq_at = found[1] * heads;
     }
 
-    const float c2 = op.scale * kLog2e;
+    // e^(scale q.k) = 2^(c2 (q'.k)) with c2 > 0: the sign, and a scale of zero, go into q'
+    const float c2 = op.scale == 0.f ? 1.f : fabsf(op.scale) * kLog2e;
+    const uint32_t q_flip = op.scale < 0.f ? 0x80008000u : 0u, q_keep = op.scale == 0.f ? 0u : 0xFFFFFFFFu;
+    const float grow = 8.f / c2;
     const int g = lane >> 2, t4 = lane & 3;
     bool first_segment = true;
 
@@ -260,12 +267,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                         const long long at = o0 + row * op.kv.token_stride + ch * 8;
                         const uint16_t* k = static_cast<const uint16_t*>(op.kv.k) + at;
                         const uint16_t* v = static_cast<const uint16_t*>(op.kv.v) + at;
-                        const uint32_t d = dst + row * S::kPitch + ch * 16;
                         const long long step = kRows * op.kv.token_stride;
 #pragma unroll
                         for (int it = 0; it < kKeys / kRows; ++it) {
-                            cp_async16(d + it * kRows * S::kPitch, k);
-                            cp_async16(d + (kKeys + it * kRows) * S::kPitch, v);
+                            const uint32_t d = dst + S::piece(it * kRows + row, ch);
+                            cp_async16(d, k);
+                            cp_async16(d + kKeys * S::kPitch, v);
                             k += step;
                             v += step;
                         }
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                         const long long o = __shfl_sync(0xffffffffu, off, row);
                         if (ch * 8 < D) {
                             const long long at = o < 0 ? 0 : o + ch * 8;
-                            const uint32_t d = dst + row * S::kPitch + ch * 16;
+                            const uint32_t d = dst + S::piece(row, ch);
                             cp_async16(d, static_cast<const uint16_t*>(op.kv.k) + at, o >= 0);
                             cp_async16(d + kKeys * S::kPitch,
                                        static_cast<const uint16_t*>(op.kv.v) + at, o >= 0);
@@ -308,8 +315,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                 v = ld_cg16(static_cast<const uint16_t*>(op.q) +
                             ((long long)b * op.q_len + tok) * op.q_stride +
                             (long long)(hk * G + row - tok * G) * D + ch * 8);
+                v.x = (v.x ^ q_flip) & q_keep, v.y = (v.y ^ q_flip) & q_keep;
+                v.z = (v.z ^ q_flip) & q_keep, v.w = (v.w ^ q_flip) & q_keep;
             }
-            *reinterpret_cast<uint4*>(qs + r * S::kPitch + ch * 16) = v;
+            *reinterpret_cast<uint4*>(qs + S::piece(r, ch)) = v;
         }
         __syncthreads();
 
@@ -324,12 +333,15 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
         // q stays in registers where they suffice, else it is read again for every stage
         constexpr bool kKeepQ = RT == 1 || RT * DP <= 128;
         uint32_t qf[kKeepQ ? RT : 1][kKeepQ ? DP / 16 : 1][4];
-        const uint32_t qa = qs_a + ((lane & 7) + ((lane >> 3) & 1) * 8) * S::kPitch + (lane >> 4) * 16;
+        // ldmatrix: this lane's row and first piece; piece 2 k further is 32 k bytes on,
+        // xor-ed inside 128 bytes
+        const uint32_t qa = qs_a + S::piece((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+        auto on = [](uint32_t at, int k) { return (at ^ (k * 32 & 127)) + (k * 32 & ~127); };
         if constexpr (kKeepQ) {
 #pragma unroll
             for (int r = 0; r < RT; ++r)
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k) ldsm4(qf[r][k], qa + r * 16 * S::kPitch + k * 32);
+                for (int k = 0; k < DP / 16; ++k) ldsm4(qf[r][k], on(qa, k) + r * 16 * S::kPitch);
         }
 
 #pragma unroll 1
@@ -357,16 +369,16 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
             for (int r = 0; r < RT; ++r)
 #pragma unroll
                 for (int j = 0; j < kBlk; ++j) s[r][j][0] = s[r][j][1] = s[r][j][2] = s[r][j][3] = 0.f;
-            const uint32_t kl = ka + ((lane & 7) + (lane >> 4) * 8) * S::kPitch + ((lane >> 3) & 1) * 16;
+            const uint32_t kl = ka + S::piece((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k) {
                 uint32_t kf[S::kSub][4];
 #pragma unroll
-                for (int u = 0; u < S::kSub; ++u) ldsm4(kf[u], kl + u * 16 * S::kPitch + k * 32);
+                for (int u = 0; u < S::kSub; ++u) ldsm4(kf[u], on(kl, k) + u * 16 * S::kPitch);
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     uint32_t qr[4];
-                    if (!kKeepQ) ldsm4(qr, qa + r * 16 * S::kPitch + k * 32);
+                    if (!kKeepQ) ldsm4(qr, on(qa, k) + r * 16 * S::kPitch);
                     const uint32_t(&a)[4] = kKeepQ ? qf[kKeepQ ? r : 0][kKeepQ ? k : 0] : qr;
 #pragma unroll
                     for (int u = 0; u < S::kSub; ++u) {
@@ -375,13 +387,6 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                     }
                 }
             }
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int j = 0; j < kBlk; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[r][j][e] *= c2;
-
             // masks, where some row does not see some key of the stage
             const bool all = my_pos <= sp.first &&
                              (!op.window || last - my_pos < op.window || my_pos < op.sinks);
@@ -437,10 +442,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
                     nm[h] = fmaxf(m[r][h], v);
                 }
-                if (__any_sync(0xffffffffu, nm[0] != m[r][0] || nm[1] != m[r][1])) {
+                if (__any_sync(0xffffffffu, nm[0] > m[r][0] + grow || nm[1] > m[r][1] + grow)) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float f = nm[h] == m[r][h] ? 1.f : exp2_fast(m[r][h] - nm[h]);
+                        const float f = nm[h] == m[r][h] ? 1.f : exp2_fast((m[r][h] - nm[h]) * c2);
                         m[r][h] = nm[h];
                         l[r][h] *= f;
 #pragma unroll
@@ -452,14 +457,15 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float base = m[r][h] == -INFINITY ? 0.f : m[r][h];
+                    const float base = m[r][h] == -INFINITY ? 0.f : -m[r][h] * c2;
 #pragma unroll
                     for (int j = 0; j < kBlk; ++j) {
-                        const float a = exp2_fast(s[r][j][2 * h] - base);
-                        const float c = exp2_fast(s[r][j][2 * h + 1] - base);
+                        const float a = exp2_fast(fmaf(s[r][j][2 * h], c2, base));
+                        const float c = exp2_fast(fmaf(s[r][j][2 * h + 1], c2, base));
                         l[r][h] += a + c;
-                        // weights in [0, 1] meet the values as 16-bit numbers: what
-                        // the matrix instruction takes, 2^-12 (fp16) or 2^-9 (bf16) off
+                        // weights meet the values as 16-bit numbers: what the matrix
+                        // instruction takes, 2^-12 (fp16) or 2^-9 (bf16) off (their fp32
+                        // sum is of the weights before that: lse is an fp32 result)
                         pf[r][j >> 1][2 * (j & 1) + h] = pair_16<BF16>(a, c);
                         s[r][j][2 * h] = a;
                         s[r][j][2 * h + 1] = c;
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
 #pragma unroll
                                 for (int d = 0; d < DP / 8; ++d) {
                                     const float2 v = pair_f32<BF16>(*reinterpret_cast<const uint32_t*>(
-                                        vb + k * S::kPitch + d * 16 + t4 * 4));
+                                        vb + S::piece(k, d) + t4 * 4));
                                     o[r][d][2 * h] = fmaf(w, v.x, o[r][d][2 * h]);
                                     o[r][d][2 * h + 1] = fmaf(w, v.y, o[r][d][2 * h + 1]);
                                 }
@@ -505,13 +511,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
             }
 
             // output += weights x values
-            const uint32_t vl = va + ((lane & 7) + ((lane >> 3) & 1) * 8) * S::kPitch + (lane >> 4) * 16;
+            const uint32_t vl = va + S::piece((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
 #pragma unroll
             for (int u = 0; u < S::kSub; ++u)
 #pragma unroll
                 for (int d = 0; d < DP / 16; ++d) {
                     uint32_t vf[4];
-                    ldsm4_t(vf, vl + u * 16 * S::kPitch + d * 32);
+                    ldsm4_t(vf, on(vl, d) + u * 16 * S::kPitch);
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
                         mma16816<BF16>(o[r][2 * d], pf[r][u], vf[0], vf[1]);
@@ -532,7 +538,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                 l[r][h] += __shfl_xor_sync(0xffffffffu, l[r][h], 2);
                 const int row = r * 16 + g + h * 8;
                 if (t4 == 0) {
-                    sm_m[warp * S::kRows + row] = m[r][h];
+                    sm_m[warp * S::kRows + row] = m[r][h] * c2;
                     sm_l[warp * S::kRows + row] = l[r][h];
                 }
 #pragma unroll
@@ -590,12 +596,14 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
     }
 }
 
-// One CTA per row of a unit that was cut between CTAs: its parts joined in CTA
-// order, each warp every eighth part and then the warps' in order.  Where parts
-// are few (8 or less) every eighth CTA does eight rows, one warp each.
+// The parts of a unit that was cut between CTAs, joined in CTA order.  A CTA has
+// `per` rows of the unit: its eight warps share them where the parts are few (8
+// or less), else they share each row, every eighth part a warp and then the
+// warps' in order.  per is 8 where the call has about as many units as CTAs, and
+// 1 where few units have many parts.
 constexpr int kJoinWarps = 8;
 template <bool BF16, int DP, int RT>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams p, int ctas_max) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams p, int ctas_max, int per) {
     using S = AttnShape<DP, RT>;
     constexpr int kPairs = DP / 64;   // pairs of output values of a lane, 64 apart
     __shared__ float2 acc[kJoinWarps][kPairs][32];
@@ -621,65 +629,68 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
     const int c0 = cta_of(u0), c1 = cta_of(u1);
     if (c0 == c1) return;  // finished in place
     const int n = c1 - c0 + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool few = n <= kJoinWarps;
-    if (few && blockIdx.y % kJoinWarps) return;
-    const int r = blockIdx.y + (few ? warp : 0);
-    if (few && (r >= S::kRows || base_row + r >= p.rows)) return;
     // a CTA's first segment is in its first part, its last one in the second
     const float* parts = p.part + (size_t)c0 * 2 * S::kPart;
     const int skip = c0 * total < u0 * ctas ? S::kPart : 0;
-
-    float top = -INFINITY, sum = 0.f;
-    float2 v[kPairs];
+    const bool few = per > 1 && n <= kJoinWarps;
+    const int last = min(min(S::kRows, p.rows - base_row), (int)(blockIdx.y + 1) * per);
+    for (int r = blockIdx.y * per + (few ? warp : 0); r < last; r += few ? kJoinWarps : 1) {
+        float top = -INFINITY, sum = 0.f;
+        float2 v[kPairs];
 #pragma unroll
-    for (int x = 0; x < kPairs; ++x) v[x] = make_float2(0.f, 0.f);
-    auto add = [&](float m, float l, const float2 (&w)[kPairs]) {
-        const float nt = fmaxf(top, m), base = nt == -INFINITY ? 0.f : nt;
-        const float f = exp2_fast(top - base), k = exp2_fast(m - base);
-        top = nt;
-        sum = sum * f + l * k;
+        for (int x = 0; x < kPairs; ++x) v[x] = make_float2(0.f, 0.f);
+        auto add = [&](float m, float l, const float2 (&w)[kPairs]) {
+            const float nt = fmaxf(top, m), base = nt == -INFINITY ? 0.f : nt;
+            const float f = exp2_fast(top - base), k = exp2_fast(m - base);
+            top = nt;
+            sum = sum * f + l * k;
 #pragma unroll
-        for (int x = 0; x < kPairs; ++x) {
-            v[x].x = v[x].x * f + w[x].x * k;
-            v[x].y = v[x].y * f + w[x].y * k;
-        }
-    };
+            for (int x = 0; x < kPairs; ++x) {
+                v[x].x = v[x].x * f + w[x].x * k;
+                v[x].y = v[x].y * f + w[x].y * k;
+            }
+        };
 #pragma unroll 4
-    for (int i = few ? 0 : warp; i < n; i += few ? 1 : kJoinWarps) {
-        const float* q = parts + (size_t)i * 2 * S::kPart + (i == 0 ? skip : 0);
-        const float2* o = reinterpret_cast<const float2*>(q + 2 * S::kRows + r * DP) + lane;
-        float2 w[kPairs];
+        for (int i = few ? 0 : warp; i < n; i += few ? 1 : kJoinWarps) {
+            const float* q = parts + (size_t)i * 2 * S::kPart + (i == 0 ? skip : 0);
+            const float2* o = reinterpret_cast<const float2*>(q + 2 * S::kRows + r * DP) + lane;
+            float2 w[kPairs];
 #pragma unroll
-        for (int x = 0; x < kPairs; ++x)
-            w[x] = x * 64 + lane * 2 < D ? __ldg(o + x * 32) : make_float2(0.f, 0.f);
-        add(__ldg(q + r), __ldg(q + S::kRows + r), w);
-    }
-    if (!few) {
-        if (lane == 0) {
-            tops[warp] = top;
-            sums[warp] = sum;
+            for (int x = 0; x < kPairs; ++x)
+                w[x] = x * 64 + lane * 2 < D ? __ldg(o + x * 32) : make_float2(0.f, 0.f);
+            add(__ldg(q + r), __ldg(q + S::kRows + r), w);
         }
+        if (!few) {
+            if (lane == 0) {
+                tops[warp] = top;
+                sums[warp] = sum;
+            }
 #pragma unroll
-        for (int x = 0; x < kPairs; ++x) acc[warp][x][lane] = v[x];
-        __syncthreads();
-        if (warp) return;
-        for (int w = 1; w < kJoinWarps; ++w) {
-            float2 o[kPairs];
+            for (int x = 0; x < kPairs; ++x) acc[warp][x][lane] = v[x];
+            __syncthreads();
+            if (warp == 0) {
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    float2 o[kPairs];
 #pragma unroll
-            for (int x = 0; x < kPairs; ++x) o[x] = acc[w][x][lane];
-            add(tops[w], sums[w], o);
+                    for (int x = 0; x < kPairs; ++x) o[x] = acc[w][x][lane];
+                    add(tops[w], sums[w], o);
+                }
+            }
         }
-    }
-    const int row = base_row + r, tok = row / G, h = hk * G + row - tok * G;
-    const long long t = (long long)b * op.q_len + tok;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(op.out) + t * op.out_stride +
-                                                (long long)h * D);
+        if (few || warp == 0) {
+            const int row = base_row + r, tok = row / G, h = hk * G + row - tok * G;
+            const long long t = (long long)b * op.q_len + tok;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(op.out) + t * op.out_stride +
+                                                        (long long)h * D);
 #pragma unroll
-    for (int x = 0; x < kPairs; ++x)
-        if (x * 64 + lane * 2 < D) out[x * 32 + lane] = pair_16<BF16>(v[x].x * inv, v[x].y * inv);
-    if (lane == 0 && op.lse)
-        op.lse[t * op.heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            for (int x = 0; x < kPairs; ++x)
+                if (x * 64 + lane * 2 < D) out[x * 32 + lane] = pair_16<BF16>(v[x].x * inv, v[x].y * inv);
+            if (lane == 0 && op.lse)
+                op.lse[t * op.heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        }
+        if (!few) __syncthreads();
+    }
 }
 
 // Row tiles of a CTA: as many as share its keys with 128 output registers.
@@ -736,9 +747,11 @@ static cudaError_t launch_attn_t(const dg_attn& op, void* ws, cudaStream_t s) {
     void* args[] = {&p};
     e = launch_pdl(fn, dim3(grid), dim3(kAttnThreads), S::kSmem, s, args);
     if (e != cudaSuccess || never_split(op)) return e;
-    void* jargs[] = {&p, &grid};
+    const long long units = (long long)op.kv.batch * op.kv.kv_heads * p.groups;
+    int per = units * kJoinWarps >= grid ? kJoinWarps : 1;
+    void* jargs[] = {&p, &grid, &per};
     return launch_pdl((const void*)k_attn_join<BF16, DP, RT>,
-                      dim3(op.kv.batch * op.kv.kv_heads * p.groups, std::min(p.rows, S::kRows)),
+                      dim3((unsigned)units, (std::min(p.rows, S::kRows) + per - 1) / per),
                       dim3(kJoinWarps * 32), 0, s, jargs);
 }
 
