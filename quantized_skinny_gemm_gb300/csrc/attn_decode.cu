@@ -39,7 +39,7 @@ struct AttnParams {
     dg_attn op;
     int groups;          // row groups of RT * 16 rows per (sequence, head)
     int rows;            // q_len * heads / kv_heads
-    long long* prefix;   // [batch + 1] blocks of one head before each sequence
+    int2* info;          // [units] a unit's first part and the number of its parts
     float* part;         // [grid][2] parts of RT * 16 rows
     uint32_t page_mul;   // j / page_size = mulhi(j, page_mul) >> page_shift, or j for 0
     int page_shift;
@@ -100,22 +100,23 @@ __device__ __forceinline__ int quotient(long long a, int b) {
 
 template <int DP, int RT>
 struct AttnShape {
-    static constexpr int kSub = DP <= 64 ? 2 : 1;           // 16-key pieces of a stage
+    static constexpr int kSub = DP <= 64 && RT < 4 ? 2 : 1;  // 16-key pieces of a stage
     static constexpr int kKeys = 16 * kSub;
     static constexpr int kPitch = DP * 2;                   // bytes; see piece()
     static constexpr int kStage = 2 * kKeys * kPitch;       // keys, then values
     static constexpr int kCtas = DP <= 192 ? 2 : 1;  // per SM
-    static constexpr int kStages = DP <= 64 ? 3 : DP <= 128 ? 3 : DP <= 192 ? 2 : 3;
+    static constexpr int kStages = RT == 4 ? 5 : DP <= 128 ? 3 : DP <= 192 ? 2 : 3;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kRows = RT * 16;
     static constexpr int kQ = kRows * kPitch;
     static constexpr size_t kSmem = (size_t)kAttnWarps * kRing + kQ + 2 * kAttnWarps * kRows * 4;
-    static constexpr int kOutPitch = DP + 8;                // floats of a merged row
     static constexpr int kPart = kRows * (DP + 2);          // floats of a part: m, l, then rows
     // Byte of 16-byte piece c of row r: the pieces of 128 bytes change places by
     // the row's low bits, so that eight rows' same piece lie in different banks.
     __device__ static constexpr int piece(int r, int c) { return r * kPitch + ((c ^ (r & 7)) << 4); }
-    static_assert(kRows * kOutPitch * 4 <= kRing, "a warp's output fits its ring");
+    // Value group d (8 floats) of row r of a warp's output, in place of stages.
+    __device__ static constexpr int out_at(int r, int d) { return r * DP + ((d ^ (r & 3)) << 3); }
+    static_assert(kRows * DP * 4 <= (kStages - 1) * kStage, "a warp's output leaves a stage free");
     static_assert(kCtas * (kSmem + 2048) <= 228 * 1024, "an SM holds its CTAs");
 };
 
@@ -136,191 +137,224 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
     float* sm_l = sm_m + kAttnWarps * S::kRows;
 
     griddep_launch_dependents();
-    if (D < DP)  // dims past the head's read as zero, in q and in the ring
-        for (int i = tid; i < (kAttnWarps * S::kRing + S::kQ) / 16; i += kAttnThreads)
-            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     griddep_wait();
 
     // ---- this CTA's range of blocks -----------------------------------------------------
-    // The blocks of one head are counted over the sequences, 128 at a time; a
-    // second pass over more than 128 finds the sequence of the range's first.
+    // The blocks of one head are counted over the sequences: by every warp for
+    // itself up to 32, else 128 at a time by the CTA, in two passes past 128 (the
+    // second finds the sequence of the range's first block).
     long long total = 0, begin = 0, end = 0;
+    int ctas = 0;
     auto take_range = [&] {
-        const int ctas = (int)min((long long)gridDim.x, total);
+        ctas = (int)min((long long)gridDim.x, total);
         begin = range_at(blockIdx.x, total, ctas);
         end = blockIdx.x < ctas ? range_at(blockIdx.x + 1, total, ctas) : begin;
     };
     int b = 0;
     long long seq_at = 0;   // first block of sequence b
-    const int passes = B == 1 ? 0 : B <= kAttnThreads ? 1 : 2;
-    if (B == 1) {
-        const int n = blocks_of(span_of(op, 0));
-        total = (long long)n * heads;
-        take_range();
-        if (blockIdx.x == 0 && tid == 0) {
-            p.prefix[0] = 0;
-            p.prefix[1] = n;
+    if (B <= 32) {
+        const int n = lane < B ? blocks_of(span_of(op, lane)) : 0;
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += t;
         }
-    }
-    for (int pass = 0; pass < passes; ++pass) {
-        long long carry = 0;
-        for (int b0 = 0; b0 < B; b0 += kAttnThreads) {
-            const int b = b0 + tid;
-            const int n = b < B ? blocks_of(span_of(op, b)) : 0;
-            long long inc = n;
+        total = (long long)__shfl_sync(0xffffffffu, inc, 31) * heads;
+        take_range();
+        const long long lo = (long long)(inc - n) * heads, hi = (long long)inc * heads;
+        const unsigned here = __ballot_sync(0xffffffffu, begin >= lo && begin < hi);
+        b = max(0, __ffs(here) - 1);
+        seq_at = __shfl_sync(0xffffffffu, lo, b);
+    } else {
+        const int passes = B <= kAttnThreads ? 1 : 2;
+        for (int pass = 0; pass < passes; ++pass) {
+            long long carry = 0;
+            for (int b0 = 0; b0 < B; b0 += kAttnThreads) {
+                const int n = b0 + tid < B ? blocks_of(span_of(op, b0 + tid)) : 0;
+                long long inc = n;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += t;
-            }
-            if (lane == 31) scan[warp] = inc;
-            __syncthreads();
-            long long before = carry, sum = 0;
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
-                if (w < warp) before += scan[w];
-                sum += scan[w];
-            }
-            const long long at = before + inc - n;
-            carry += sum;
-            if (pass == 0 && b0 + kAttnThreads >= B) {
-                total = carry * heads;
-                take_range();
-            }
-            if (pass == passes - 1 && b < B) {
-                if (blockIdx.x == 0) {
-                    p.prefix[b] = at;
-                    if (b == B - 1) p.prefix[B] = at + n;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += t;
                 }
-                if (begin >= at * heads && begin < (at + n) * heads) {
-                    found[0] = b;
+                if (lane == 31) scan[warp] = inc;
+                __syncthreads();
+                long long before = carry, sum = 0;
+#pragma unroll
+                for (int w = 0; w < kAttnWarps; ++w) {
+                    if (w < warp) before += scan[w];
+                    sum += scan[w];
+                }
+                const long long at = before + inc - n;
+                carry += sum;
+                if (pass == 0 && b0 + kAttnThreads >= B) {
+                    total = carry * heads;
+                    take_range();
+                }
+                if (pass == passes - 1 && n && begin >= at * heads && begin < (at + n) * heads) {
+                    found[0] = b0 + tid;
                     found[1] = at;
                 }
+                __syncthreads();
             }
-            __syncthreads();
         }
-    }
-    if (begin >= end) return;
-    if (passes) {
         b = (int)found[0];
         seq_at = found[1] * heads;
     }
+    if (begin >= end) return;
 
     // e^(scale q.k) = 2^(c2 (q'.k)) with c2 > 0: the sign, and a scale of zero, go into q'
     const float c2 = op.scale == 0.f ? 1.f : fabsf(op.scale) * kLog2e;
     const uint32_t q_flip = op.scale < 0.f ? 0x80008000u : 0u, q_keep = op.scale == 0.f ? 0u : 0xFFFFFFFFu;
     const float grow = 8.f / c2;
     const int g = lane >> 2, t4 = lane & 3;
-    bool first_segment = true;
 
-    // ---- one segment (the range's part of one unit) after another ------------------------
-    for (long long blk = begin; blk < end;) {
-        Span sp = span_of(op, b);
-        int nb = blocks_of(sp);
-        while (blk >= seq_at + (long long)nb * heads) {
-            seq_at += (long long)nb * heads;
-            sp = span_of(op, ++b);
-            nb = blocks_of(sp);
+    // ---- the range's part of one unit after another ---------------------------------------
+    struct Segment {
+        int b, hk, row0;   // sequence, key / value head, first row
+        int kb, ke, nb;    // blocks [kb, ke) of nb
+        Span sp;
+        int key0, lim, n;  // this warp's n stages: kKeys keys from key0 on, then every
+                           // kStep further, up to lim
+    } sg;
+    constexpr int kKeys = S::kKeys, kStep = kAttnWarps * kKeys, kStages = S::kStages;
+    auto enter = [&](long long blk, bool first) {
+        sg.sp = span_of(op, b);
+        sg.nb = blocks_of(sg.sp);
+        while (blk >= seq_at + (long long)sg.nb * heads) {
+            seq_at += (long long)sg.nb * heads;
+            sg.sp = span_of(op, ++b);
+            sg.nb = blocks_of(sg.sp);
         }
-        const int unit = quotient(blk - seq_at, nb);            // head and row group
-        const int kb = (int)(blk - seq_at - (long long)unit * nb);
-        const int ke = (int)min((long long)nb, kb + (end - blk));
-        const int hk = unit / p.groups, row0 = (unit - hk * p.groups) * S::kRows;
-        const int count = sp.count();
-        const int last = sp.first + op.q_len - 1;
-
-        // this warp's stages: kKeys keys from kb * 128 + warp * kKeys on, then every
-        // kStep further
-        constexpr int kKeys = S::kKeys;
-        const int key0 = kb * kBlockKeys + warp * kKeys;
-        const int lim = min(count, ke * kBlockKeys);
-        constexpr int kStep = kAttnWarps * kKeys;
-        const int n = key0 < lim ? (lim - key0 + kStep - 1) / kStep : 0;
-
-        // Position and cache offset (elements; -1: nothing there) of key `lane` (lane
-        // mod kKeys) of stage i.
-        auto locate = [&](int i, int& pos, long long& off) {
-            const int c = key0 + i * kStep + (lane & (kKeys - 1));
-            pos = INT_MAX;
-            off = -1;
-            if (i < n && c < lim) {
-                const int j = sp.position(c);
-                int slot = 0;
-                const int page = sp.seen(j) ? page_slot(p, b, j, slot) : -1;
-                if (page >= 0) {
-                    pos = j;
-                    off = page * op.kv.page_stride + slot * op.kv.token_stride + hk * op.kv.head_stride;
+        const int unit = quotient(blk - seq_at, sg.nb);
+        sg.b = b;
+        sg.kb = (int)(blk - seq_at - (long long)unit * sg.nb);
+        sg.ke = (int)min((long long)sg.nb, sg.kb + (end - blk));
+        sg.hk = unit / p.groups;
+        sg.row0 = (unit - sg.hk * p.groups) * S::kRows;
+        sg.key0 = sg.kb * kBlockKeys + warp * kKeys;
+        sg.lim = min(sg.sp.count(), sg.ke * kBlockKeys);
+        sg.n = sg.key0 < sg.lim ? (sg.lim - sg.key0 + kStep - 1) / kStep : 0;
+        if (sg.kb == 0 && tid == 0 && p.info) {
+            // the unit's parts lie in this CTA's first or second part and the first
+            // ones of the following CTAs; the last is the largest c with
+            // floor(c * total / ctas) <= u1, that is c * total < (u1 + 1) * ctas
+            int c = blockIdx.x;
+            if (sg.ke < sg.nb) {
+                const long long top = (blk + sg.nb) * ctas;
+                c = max(c, min(ctas - 1, __float2int_rz(__fdividef((float)top, (float)total))));
+                while (c * total >= top) --c;
+                while ((c + 1) * total < top) ++c;
+            }
+            p.info[(long long)b * heads + unit] =
+                make_int2(blockIdx.x * 2 + (first ? 0 : 1), c - (int)blockIdx.x + 1);
+        }
+    };
+    // Position and cache offset (elements; -1: nothing there) of key `lane` (lane
+    // mod kKeys) of stage i.
+    auto locate = [&](int i, int& pos, long long& off) {
+        const int c = sg.key0 + i * kStep + (lane & (kKeys - 1));
+        pos = INT_MAX;
+        off = -1;
+        if (i < sg.n && c < sg.lim) {
+            const int j = sg.sp.position(c);
+            int slot = 0;
+            const int page = sg.sp.seen(j) ? page_slot(p, sg.b, j, slot) : -1;
+            if (page >= 0) {
+                pos = j;
+                off = page * op.kv.page_stride + slot * op.kv.token_stride + sg.hk * op.kv.head_stride;
+            }
+        }
+    };
+    // Stage i lies in ring place (i - 1) mod kStages, so that the first one's is
+    // not in the way of the last segment's output.
+    auto place = [](int i) { return (i + kStages - 1) % kStages; };
+    auto issue = [&](int i, long long off) {
+        if (i < sg.n) {
+            const uint32_t dst = ring_a + place(i) * S::kStage;
+            constexpr int kChunks = DP / 8;
+            // keys in a row in one page: addresses without exchanges
+            const long long o0 = __shfl_sync(0xffffffffu, off, 0);
+            const bool run = off >= 0 && off == o0 + (lane & (kKeys - 1)) * op.kv.token_stride;
+            if (32 % kChunks == 0 && __all_sync(0xffffffffu, run)) {
+                constexpr int kRows = 32 % kChunks == 0 ? 32 / kChunks : 1;   // rows of an instruction
+                const int row = lane / kChunks, ch = lane % kChunks;
+                const bool in = ch * 8 < D;   // dims past the head's read as zero
+                const long long at = o0 + row * op.kv.token_stride + (in ? ch * 8 : 0);
+                const uint16_t* k = static_cast<const uint16_t*>(op.kv.k) + at;
+                const uint16_t* v = static_cast<const uint16_t*>(op.kv.v) + at;
+                const long long step = kRows * op.kv.token_stride;
+#pragma unroll
+                for (int it = 0; it < kKeys / kRows; ++it) {
+                    const uint32_t d = dst + S::piece(it * kRows + row, ch);
+                    cp_async16(d, k, in);
+                    cp_async16(d + kKeys * S::kPitch, v, in);
+                    k += step;
+                    v += step;
+                }
+            } else {
+#pragma unroll
+                for (int it = 0; it < kKeys * kChunks / 32; ++it) {
+                    const int idx = it * 32 + lane, row = idx / kChunks, ch = idx % kChunks;
+                    const long long o = __shfl_sync(0xffffffffu, off, row);
+                    const bool in = o >= 0 && ch * 8 < D;
+                    const long long at = in ? o + ch * 8 : 0;
+                    const uint32_t d = dst + S::piece(row, ch);
+                    cp_async16(d, static_cast<const uint16_t*>(op.kv.k) + at, in);
+                    cp_async16(d + kKeys * S::kPitch, static_cast<const uint16_t*>(op.kv.v) + at, in);
                 }
             }
-        };
-        auto issue = [&](int i, long long off) {
-            if (i < n) {
-                const uint32_t dst = ring_a + (i % S::kStages) * S::kStage;
-                constexpr int kChunks = DP / 8;
-                // keys in a row in one page: addresses without exchanges
-                const long long o0 = __shfl_sync(0xffffffffu, off, 0);
-                const bool run = off >= 0 && off == o0 + (lane & (kKeys - 1)) * op.kv.token_stride;
-                if (32 % kChunks == 0 && __all_sync(0xffffffffu, run)) {
-                    constexpr int kRows = 32 % kChunks == 0 ? 32 / kChunks : 1;   // rows of an instruction
-                    const int row = lane / kChunks, ch = lane % kChunks;
-                    if (ch * 8 < D) {
-                        const long long at = o0 + row * op.kv.token_stride + ch * 8;
-                        const uint16_t* k = static_cast<const uint16_t*>(op.kv.k) + at;
-                        const uint16_t* v = static_cast<const uint16_t*>(op.kv.v) + at;
-                        const long long step = kRows * op.kv.token_stride;
-#pragma unroll
-                        for (int it = 0; it < kKeys / kRows; ++it) {
-                            const uint32_t d = dst + S::piece(it * kRows + row, ch);
-                            cp_async16(d, k);
-                            cp_async16(d + kKeys * S::kPitch, v);
-                            k += step;
-                            v += step;
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int it = 0; it < kKeys * kChunks / 32; ++it) {
-                        const int idx = it * 32 + lane, row = idx / kChunks, ch = idx % kChunks;
-                        const long long o = __shfl_sync(0xffffffffu, off, row);
-                        if (ch * 8 < D) {
-                            const long long at = o < 0 ? 0 : o + ch * 8;
-                            const uint32_t d = dst + S::piece(row, ch);
-                            cp_async16(d, static_cast<const uint16_t*>(op.kv.k) + at, o >= 0);
-                            cp_async16(d + kKeys * S::kPitch,
-                                       static_cast<const uint16_t*>(op.kv.v) + at, o >= 0);
-                        }
-                    }
-                }
-            }
-            cp_commit();
-        };
-
-        int pos[S::kStages];          // positions of the stages in flight, by ring slot
-        long long off_next;
-        int pos_next;
-#pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) {
-            long long off;
-            locate(i, pos[i], off);
-            issue(i, off);
         }
-        locate(S::kStages - 1, pos_next, off_next);
-
-        // q rows of the unit, zero past the last
-        for (int i = tid; i < S::kRows * (DP / 8); i += kAttnThreads) {
-            const int r = i / (DP / 8), ch = i % (DP / 8), row = row0 + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < p.rows && ch * 8 < D) {
+        cp_commit();
+    };
+    // q rows of the unit, zero past the last and past the head's dims
+    constexpr int kQv = (S::kRows * (DP / 8) + kAttnThreads - 1) / kAttnThreads;
+    uint4 qv[kQv];
+    auto load_q = [&] {
+#pragma unroll
+        for (int x = 0; x < kQv; ++x) {
+            const int i = x * kAttnThreads + tid, r = i / (DP / 8), ch = i % (DP / 8), row = sg.row0 + r;
+            qv[x] = make_uint4(0, 0, 0, 0);
+            if (r < S::kRows && row < p.rows && ch * 8 < D) {
                 const int tok = row / G;
-                v = ld_cg16(static_cast<const uint16_t*>(op.q) +
-                            ((long long)b * op.q_len + tok) * op.q_stride +
-                            (long long)(hk * G + row - tok * G) * D + ch * 8);
-                v.x = (v.x ^ q_flip) & q_keep, v.y = (v.y ^ q_flip) & q_keep;
-                v.z = (v.z ^ q_flip) & q_keep, v.w = (v.w ^ q_flip) & q_keep;
+                qv[x] = __ldcg(reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(op.q) + ((long long)sg.b * op.q_len + tok) * op.q_stride +
+                    (long long)(sg.hk * G + row - tok * G) * D + ch * 8));
             }
-            *reinterpret_cast<uint4*>(qs + S::piece(r, ch)) = v;
         }
+    };
+    auto store_q = [&] {
+#pragma unroll
+        for (int x = 0; x < kQv; ++x) {
+            const int i = x * kAttnThreads + tid, r = i / (DP / 8), ch = i % (DP / 8);
+            if (r >= S::kRows) continue;
+            const uint4 v = qv[x];
+            *reinterpret_cast<uint4*>(qs + S::piece(r, ch)) =
+                make_uint4((v.x ^ q_flip) & q_keep, (v.y ^ q_flip) & q_keep, (v.z ^ q_flip) & q_keep,
+                           (v.w ^ q_flip) & q_keep);
+        }
+    };
+
+    int pos[kStages];              // positions of the stages in flight, by stage mod kStages
+    long long offs[kStages];
+    int pos_next;
+    long long off_next;
+    long long blk = begin;
+    enter(blk, true);
+    load_q();
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) locate(i, pos[i], offs[i]);
+    issue(0, offs[0]);
+    for (bool first_segment = true;; first_segment = false) {
+#pragma unroll
+        for (int i = 1; i < kStages - 1; ++i) issue(i, offs[i]);
+        pos_next = pos[kStages - 1];
+        off_next = offs[kStages - 1];
+        store_q();
         __syncthreads();
+        const Span sp = sg.sp;
+        const int row0 = sg.row0, n = sg.n, last = sp.first + op.q_len - 1;
 
         float o[RT][DP / 8][4], m[RT][2], l[RT][2];
 #pragma unroll
@@ -346,19 +380,19 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
 
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-            cp_wait<S::kStages - 2>();
+            cp_wait<kStages - 2>();
             __syncwarp();
-            const int slot = i % S::kStages;
+            const int slot = place(i);
             const uint32_t ka = ring_a + slot * S::kStage, va = ka + kKeys * S::kPitch;
             int my_pos = pos[0];
 #pragma unroll
-            for (int q = 1; q < S::kStages; ++q)
-                if (slot == q) my_pos = pos[q];
-            // the slot that the last stage left is free: refill it
-            const int ni = i + S::kStages - 1, nslot = ni % S::kStages;
+            for (int q = 1; q < kStages; ++q)
+                if (i % kStages == q) my_pos = pos[q];
+            // the place that the last stage left is free: refill it
+            const int ni = i + kStages - 1;
 #pragma unroll
-            for (int q = 0; q < S::kStages; ++q)
-                if (nslot == q) pos[q] = pos_next;
+            for (int q = 0; q < kStages; ++q)
+                if (ni % kStages == q) pos[q] = pos_next;
             issue(ni, off_next);
             locate(ni + 1, pos_next, off_next);
 
@@ -528,6 +562,19 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
         cp_wait<0>();
         __syncwarp();
 
+        // the next segment's first copies start before this one's output is written
+        const int cur_b = sg.b, hk = sg.hk;
+        const bool whole = sg.kb == 0 && sg.ke == sg.nb;
+        blk += sg.ke - sg.kb;
+        const bool more = blk < end;
+        if (more) {
+            enter(blk, false);
+            load_q();
+#pragma unroll
+            for (int i = 0; i < kStages; ++i) locate(i, pos[i], offs[i]);
+            issue(0, offs[0]);
+        }
+
         // ---- the four warps' parts, through shared memory ---------------------------------
         float* wo = reinterpret_cast<float*>(ring);
 #pragma unroll
@@ -543,12 +590,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                 }
 #pragma unroll
                 for (int d = 0; d < DP / 8; ++d)
-                    *reinterpret_cast<float2*>(wo + row * S::kOutPitch + d * 8 + t4 * 2) =
+                    *reinterpret_cast<float2*>(wo + S::out_at(row, d) + t4 * 2) =
                         make_float2(o[r][d][2 * h], o[r][d][2 * h + 1]);
             }
         }
         __syncthreads();
-        const bool whole = kb == 0 && ke == nb;
         float* part = p.part + ((size_t)blockIdx.x * 2 + (first_segment ? 0 : 1)) * S::kPart;
         for (int i = tid; i < S::kRows * (DP / 8); i += kAttnThreads) {
             const int r = i / (DP / 8), d = i % (DP / 8) * 8, row = row0 + r;
@@ -561,16 +607,20 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
             for (int w = 0; w < kAttnWarps; ++w) {
                 const float f = exp2_fast(sm_m[w * S::kRows + r] - base);
                 sum = fmaf(f, sm_l[w * S::kRows + r], sum);
-                const float* src = reinterpret_cast<const float*>(smem + w * S::kRing) + r * S::kOutPitch + d;
-#pragma unroll
-                for (int x = 0; x < 8; ++x) v[x] = fmaf(f, src[x], v[x]);
+                const float4* src = reinterpret_cast<const float4*>(
+                    reinterpret_cast<const float*>(smem + w * S::kRing) + S::out_at(r, d >> 3));
+                const float4 x = src[0], y = src[1];
+                v[0] = fmaf(f, x.x, v[0]), v[1] = fmaf(f, x.y, v[1]);
+                v[2] = fmaf(f, x.z, v[2]), v[3] = fmaf(f, x.w, v[3]);
+                v[4] = fmaf(f, y.x, v[4]), v[5] = fmaf(f, y.y, v[5]);
+                v[6] = fmaf(f, y.z, v[6]), v[7] = fmaf(f, y.w, v[7]);
             }
             if (whole) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
                 for (int x = 0; x < 8; ++x) v[x] *= inv;
                 const int tok = row / G, h = hk * G + row - tok * G;
-                const long long t = (long long)b * op.q_len + tok;
+                const long long t = (long long)cur_b * op.q_len + tok;
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(op.out) + t * op.out_stride +
                                           (long long)h * D + d) = pack8<BF16>(v);
                 if (d == 0 && op.lse)
@@ -585,25 +635,19 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                 dst[1] = make_float4(v[4], v[5], v[6], v[7]);
             }
         }
+        if (!more) return;
         __syncthreads();
-        if (D < DP) {  // the merge used the ring: its padding is zero again
-            for (int i = tid; i < kAttnWarps * S::kRing / 16; i += kAttnThreads)
-                reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-            __syncthreads();
-        }
-        first_segment = false;
-        blk += ke - kb;
     }
 }
 
 // The parts of a unit that was cut between CTAs, joined in CTA order.  A CTA has
-// `per` rows of the unit: its eight warps share them where the parts are few (8
+// `per` rows of the unit: its eight warps share them where the parts are few (32
 // or less), else they share each row, every eighth part a warp and then the
 // warps' in order.  per is 8 where the call has about as many units as CTAs, and
 // 1 where few units have many parts.
 constexpr int kJoinWarps = 8;
 template <bool BF16, int DP, int RT>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams p, int ctas_max, int per) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams p, int per) {
     using S = AttnShape<DP, RT>;
     constexpr int kPairs = DP / 64;   // pairs of output values of a lane, 64 apart
     __shared__ float2 acc[kJoinWarps][kPairs][32];
@@ -611,28 +655,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
     griddep_launch_dependents();
     griddep_wait();
     const dg_attn& op = p.op;
+    const int2 info = __ldg(p.info + blockIdx.x);
+    const int n = info.y;
+    if (n == 1) return;  // finished in place
     const int G = op.heads / op.kv.kv_heads, heads = op.kv.kv_heads * p.groups;
     const int b = blockIdx.x / heads, hg = blockIdx.x - b * heads, D = op.kv.head_dim;
     const int hk = hg / p.groups, base_row = (hg - hk * p.groups) * S::kRows;
-    const long long total = __ldg(p.prefix + op.kv.batch) * heads, first = __ldg(p.prefix + b);
-    const int ctas = (int)min((long long)ctas_max, total), nb = (int)(__ldg(p.prefix + b + 1) - first);
-    const long long u0 = first * heads + (long long)hg * nb, u1 = u0 + nb - 1;
-    // the CTAs whose ranges hold the unit's first and last block: the largest c
-    // with floor(c * total / ctas) <= u, that is c * total < (u + 1) * ctas
-    auto cta_of = [&](long long u) {
-        const long long top = (u + 1) * ctas;
-        int c = min(ctas - 1, __float2int_rz(__fdividef((float)top, (float)total)));
-        while (c * total >= top) --c;
-        while ((c + 1) * total < top) ++c;
-        return c;
-    };
-    const int c0 = cta_of(u0), c1 = cta_of(u1);
-    if (c0 == c1) return;  // finished in place
-    const int n = c1 - c0 + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // a CTA's first segment is in its first part, its last one in the second
-    const float* parts = p.part + (size_t)c0 * 2 * S::kPart;
-    const int skip = c0 * total < u0 * ctas ? S::kPart : 0;
-    const bool few = per > 1 && n <= kJoinWarps;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float* parts = p.part + (size_t)(info.x >> 1) * 2 * S::kPart;
+    const int skip = (info.x & 1) * S::kPart;
+    const bool few = per > 1 && n <= 32;
     const int last = min(min(S::kRows, p.rows - base_row), (int)(blockIdx.y + 1) * per);
     for (int r = blockIdx.y * per + (few ? warp : 0); r < last; r += few ? kJoinWarps : 1) {
         float top = -INFINITY, sum = 0.f;
@@ -708,14 +740,16 @@ static long long max_blocks(const dg_attn& op, int groups) {
 static bool never_split(const dg_attn& op) {
     return (long long)op.kv.max_pages * op.kv.page_size <= kBlockKeys;
 }
-static size_t prefix_bytes(const dg_attn& op) { return ((size_t)(op.kv.batch + 1) * 8 + 255) & ~(size_t)255; }
+static size_t info_bytes(const dg_attn& op, int groups) {
+    return ((size_t)op.kv.batch * op.kv.kv_heads * groups * 8 + 255) & ~(size_t)255;
+}
 
 size_t attn_ws_bytes(const dg_attn& op) {
     const int tiles = attn_tiles(op), dp = attn_dp(op.kv.head_dim);
     const int rows = op.q_len * (op.heads / op.kv.kv_heads), groups = (rows + tiles * 16 - 1) / (tiles * 16);
-    if (never_split(op)) return prefix_bytes(op);
+    if (never_split(op)) return 16;
     const long long ctas = max_blocks(op, groups) < kAttnMaxCtas ? max_blocks(op, groups) : kAttnMaxCtas;
-    return prefix_bytes(op) + (size_t)ctas * 2 * tiles * 16 * (dp + 2) * 4;
+    return info_bytes(op, groups) + (size_t)ctas * 2 * tiles * 16 * (dp + 2) * 4;
 }
 
 template <bool BF16, int DP, int RT>
@@ -725,8 +759,8 @@ static cudaError_t launch_attn_t(const dg_attn& op, void* ws, cudaStream_t s) {
     p.op = op;
     p.rows = op.q_len * (op.heads / op.kv.kv_heads);
     p.groups = (p.rows + S::kRows - 1) / S::kRows;
-    p.prefix = static_cast<long long*>(ws);
-    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + prefix_bytes(op));
+    p.info = never_split(op) ? nullptr : static_cast<int2*>(ws);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + info_bytes(op, p.groups));
     // with s = ceil(log2(page_size)): exact for every j < 2^31
     const uint32_t ps = (uint32_t)op.kv.page_size;
     p.page_mul = 0;
@@ -749,7 +783,7 @@ static cudaError_t launch_attn_t(const dg_attn& op, void* ws, cudaStream_t s) {
     if (e != cudaSuccess || never_split(op)) return e;
     const long long units = (long long)op.kv.batch * op.kv.kv_heads * p.groups;
     int per = units * kJoinWarps >= grid ? kJoinWarps : 1;
-    void* jargs[] = {&p, &grid, &per};
+    void* jargs[] = {&p, &per};
     return launch_pdl((const void*)k_attn_join<BF16, DP, RT>,
                       dim3((unsigned)units, (std::min(p.rows, S::kRows) + per - 1) / per),
                       dim3(kJoinWarps * 32), 0, s, jargs);

@@ -58,6 +58,7 @@ static dg_status check_attn(const dg_attn& op) {
     if (op.reserved || op.heads < 1 || !op.q || !op.out) return DG_ERR_INVALID_ARG;
     if (op.heads % op.kv.kv_heads || op.window < 0 || op.sinks < 0 || !std::isfinite(op.scale))
         return DG_ERR_INVALID_ARG;
+    if ((int64_t)op.kv.batch * op.q_len * op.heads > 0x7fffffff) return DG_ERR_UNSUPPORTED;
     const int64_t row = (int64_t)op.heads * op.kv.head_dim;
     if (op.q_stride < 0 || op.out_stride < row) return DG_ERR_INVALID_ARG;
     if (!aligned(op.q, 16) || !aligned(op.out, 16) || !aligned(op.kv.k, 16) || !aligned(op.kv.v, 16))
