@@ -41,19 +41,8 @@ struct AttnParams {
     int rows;            // q_len * heads / kv_heads
     int2* info;          // [units] a unit's first part and the number of its parts
     float* part;         // [grid][2] parts of RT * 16 rows
-    uint32_t page_mul;   // j / page_size = mulhi(j, page_mul) >> page_shift, or j for 0
-    int page_shift;
+    FastDiv page_size;
 };
-
-// The page of position j of sequence b and its slot there; page -1: none.
-__device__ __forceinline__ int page_slot(const AttnParams& p, int b, int j, int& slot) {
-    const dg_paged_kv& kv = p.op.kv;
-    const int at = p.page_mul ? (int)(__umulhi((uint32_t)j, p.page_mul) >> p.page_shift) : j;
-    slot = j - at * kv.page_size;
-    if (at >= kv.max_pages) return -1;
-    const int page = __ldg(kv.block_table + (long long)b * kv.table_stride + at);
-    return page >= 0 && page < kv.num_pages ? page : -1;
-}
 
 __device__ __forceinline__ float exp2_fast(float v) {
     float r;
@@ -260,7 +249,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
         if (i < sg.n && c < sg.lim) {
             const int j = sg.sp.position(c);
             int slot = 0;
-            const int page = sg.sp.seen(j) ? page_slot(p, sg.b, j, slot) : -1;
+            const int page = sg.sp.seen(j) ? page_slot(op.kv, p.page_size, sg.b, j, slot) : -1;
             if (page >= 0) {
                 pos = j;
                 off = page * op.kv.page_stride + slot * op.kv.token_stride + sg.hk * op.kv.head_stride;
@@ -761,16 +750,7 @@ static cudaError_t launch_attn_t(const dg_attn& op, void* ws, cudaStream_t s) {
     p.groups = (p.rows + S::kRows - 1) / S::kRows;
     p.info = never_split(op) ? nullptr : static_cast<int2*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + info_bytes(op, p.groups));
-    // with s = ceil(log2(page_size)): exact for every j < 2^31
-    const uint32_t ps = (uint32_t)op.kv.page_size;
-    p.page_mul = 0;
-    p.page_shift = 0;
-    if (ps > 1) {
-        int log = 1;
-        while ((1ull << log) < ps) ++log;
-        p.page_mul = (uint32_t)((1ull << (31 + log)) / ps + 1);
-        p.page_shift = log - 1;
-    }
+    p.page_size = fast_div((uint32_t)op.kv.page_size);
     const void* fn = (const void*)k_attn<BF16, DP, RT>;
     cudaError_t e = tc::smem_attr_once(fn, S::kSmem);
     if (e != cudaSuccess) return e;

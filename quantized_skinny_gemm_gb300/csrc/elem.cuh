@@ -53,10 +53,29 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pair_16<BF16>(f[4], f[5]), pair_16<BF16>(f[6], f[7]));
 }
 
-// The page of position j of sequence b, or -1 where the cache has none.
-__device__ __forceinline__ int page_of(const dg_paged_kv& kv, int b, int j) {
-    const int at = j / kv.page_size;
-    if (j < 0 || at >= kv.max_pages) return -1;
+// Division of 0 <= j < 2^31 by a fixed d >= 1: with s = ceil(log2 d) and mul =
+// floor(2^(31 + s) / d) + 1 < 2^32, the high word of j * mul shifted by s - 1 is
+// floor(j / d) exactly: mul is 2^(31 + s) / d + e with 0 < e <= 1, so j mul / 2^(31 + s)
+// = j / d + j e / 2^(31 + s), and the last term is below 2^-s <= 1 / d.  mul 0: d = 1.
+struct FastDiv {
+    uint32_t mul;
+    int shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+    if (d <= 1) return {0, 0};
+    int log = 1;
+    while ((1ull << log) < d) ++log;
+    return {(uint32_t)((1ull << (31 + log)) / d + 1), log - 1};
+}
+__device__ __forceinline__ int operator/(int j, FastDiv f) {
+    return f.mul ? (int)(__umulhi((uint32_t)j, f.mul) >> f.shift) : j;
+}
+
+// The page of position j >= 0 of sequence b and its slot there; page -1: none.
+__device__ __forceinline__ int page_slot(const dg_paged_kv& kv, FastDiv page_size, int b, int j, int& slot) {
+    const int at = j / page_size;
+    slot = j - at * kv.page_size;
+    if (at >= kv.max_pages) return -1;
     const int page = __ldg(kv.block_table + (long long)b * kv.table_stride + at);
     return page >= 0 && page < kv.num_pages ? page : -1;
 }

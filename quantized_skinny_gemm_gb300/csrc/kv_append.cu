@@ -3,99 +3,135 @@
 
 namespace dg {
 
-// One token per grid row.  Its heads (q, then k, then v) are cut into units of
-// U = 8 or 1 values: in the rotated part a unit is U pairs (U values and their
-// U partners), elsewhere U plain values.  Each unit is one thread's, which
-// reads all of it before it writes, so q_out may be q.
+// One token per CTA.  Its values are cut into pieces of U = 8 or 1: first those
+// that are copied, four at a time, from the last thread down, then the pairs of
+// pieces of q and k that rotate, from the first thread up (so that hardly a
+// warp does both).  A thread reads all of a pair before it writes any, so q_out
+// may be q.
 //
 // Bound by latency at decode sizes (one token: a few KB, two dependent reads,
 // length -> page id) and by HBM at large ones.
+constexpr int kAppendThreads = 128;
+template <int U>
+struct PieceOf {
+    using type = uint16_t;
+};
+template <>
+struct PieceOf<8> {
+    using type = uint4;
+};
+struct AppendParams {
+    dg_append op;
+    FastDiv q_len, page_size, pairs, plain, whole;
+};
 template <bool BF16, int U>
-__global__ void __launch_bounds__(256) k_kv_append(const dg_append op) {
+__global__ void __launch_bounds__(kAppendThreads) k_kv_append(const AppendParams prm) {
     griddep_launch_dependents();
     griddep_wait();
-    const int t = blockIdx.x;
-    const int b = t / op.q_len;
-    const int D = op.kv.head_dim, half = op.rot_dim / 2;
-    const int rot_units = half / U, units = rot_units + (D - op.rot_dim) / U;
-    const int heads = op.heads + 2 * op.kv.kv_heads;
-    const int at = blockIdx.y * blockDim.x + threadIdx.x;
-    if (at >= heads * units) return;
-    const int h = at / units, u = at - h * units;
-    const int p = op.kv.seq_lens[b] - op.q_len + t % op.q_len;
+    const dg_append& op = prm.op;
+    const int t = blockIdx.x, b = t / prm.q_len;
+    const int D = op.kv.head_dim, half = op.rot_dim / 2, kvh = op.kv.kv_heads;
+    const int p = op.kv.seq_lens[b] - op.q_len + (t - b * op.q_len);
     const bool live = p >= 0 && (op.rot_dim == 0 || p < op.max_pos);
-    const bool is_q = h < op.heads, is_v = h >= op.heads + op.kv.kv_heads;
-    const uint16_t* src;
-    uint16_t* dst;
-    if (is_q) {
-        src = static_cast<const uint16_t*>(op.q) + t * op.q_stride + (long long)h * D;
-        dst = static_cast<uint16_t*>(op.q_out) + t * op.q_out_stride + (long long)h * D;
-    } else {
-        const int page = live ? page_of(op.kv, b, p) : -1;
-        if (page < 0) return;
-        const int hk = h - op.heads - (is_v ? op.kv.kv_heads : 0);
-        src = is_v ? static_cast<const uint16_t*>(op.v) + t * op.v_stride + (long long)hk * D
-                   : static_cast<const uint16_t*>(op.k) + t * op.k_stride + (long long)hk * D;
-        dst = static_cast<uint16_t*>(is_v ? op.kv.v : op.kv.k) + page * op.kv.page_stride +
-              (p % op.kv.page_size) * op.kv.token_stride + hk * op.kv.head_stride;
-    }
-    // where this unit's values lie: first[i] at d0 + i, or (a pair) also at d1 + i
-    const bool pair = u < rot_units;
-    int d0, d1;
-    if (!pair) {
-        d0 = d1 = op.rot_dim + (u - rot_units) * U;
-    } else if (op.interleaved) {
-        d0 = 2 * u * U;
-        d1 = d0 + U;
-    } else {
-        d0 = u * U;
-        d1 = d0 + half;
-    }
-    if (U == 8) {
-        const uint4 a = *reinterpret_cast<const uint4*>(src + d0);
-        if (!pair) {
-            *reinterpret_cast<uint4*>(dst + d0) = live ? a : make_uint4(0, 0, 0, 0);
-            return;
-        }
-        const uint4 c = *reinterpret_cast<const uint4*>(src + d1);
-        if (!live || is_v) {
-            const uint4 z = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(dst + d0) = live ? a : z;
-            *reinterpret_cast<uint4*>(dst + d1) = live ? c : z;
-            return;
-        }
-        float f[2][8], cs[8], sn[8];
-        unpack8<BF16>(a, f[0]);
-        unpack8<BF16>(c, f[1]);
-        const float* cp = op.cos + (long long)p * half + u * 8;
-        const float* sp = op.sin + (long long)p * half + u * 8;
+    int at = 0;
+    const int page = live ? page_slot(op.kv, prm.page_size, b, p, at) : -1;
+    const long long slot = page < 0 ? 0 : page * op.kv.page_stride + at * op.kv.token_stride;
+    const uint16_t* q = static_cast<const uint16_t*>(op.q) + t * op.q_stride;
+    const uint16_t* k = static_cast<const uint16_t*>(op.k) + t * op.k_stride;
+    const uint16_t* v = static_cast<const uint16_t*>(op.v) + t * op.v_stride;
+    uint16_t* qo = static_cast<uint16_t*>(op.q_out) + t * op.q_out_stride;
+    uint16_t* ko = static_cast<uint16_t*>(op.kv.k) + slot;
+    uint16_t* vo = static_cast<uint16_t*>(op.kv.v) + slot;
+    const int turned = op.heads + kvh, pairs = half / U, plain = (D - op.rot_dim) / U, whole = D / U;
+    const int n_pair = turned * pairs, n_copy = turned * plain + kvh * whole;
+    using Piece = typename PieceOf<U>::type;
+    for (int i0 = blockDim.x - 1 - threadIdx.x; i0 < n_copy; i0 += 4 * blockDim.x) {
+        Piece x[4];
+        uint16_t* dst[4];
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-            *reinterpret_cast<float4*>(cs + i) = __ldg(reinterpret_cast<const float4*>(cp + i));
-            *reinterpret_cast<float4*>(sn + i) = __ldg(reinterpret_cast<const float4*>(sp + i));
+        for (int w = 0; w < 4; ++w) {
+            int j = i0 + w * blockDim.x;
+            dst[w] = nullptr;
+            if (j >= n_copy) continue;
+            const uint16_t* src;
+            bool is_q = false;
+            if (j < turned * plain) {
+                const int h = j / prm.plain, d = op.rot_dim + (j - h * plain) * U;
+                is_q = h < op.heads;
+                src = is_q ? q + h * D + d : k + (h - op.heads) * D + d;
+                dst[w] = is_q ? qo + h * D + d : ko + (h - op.heads) * op.kv.head_stride + d;
+            } else {
+                j -= turned * plain;
+                const int h = j / prm.whole, d = (j - h * whole) * U;
+                src = v + h * D + d;
+                dst[w] = vo + h * op.kv.head_stride + d;
+            }
+            if (!is_q && page < 0) dst[w] = nullptr;   // nowhere to put it
+            if (live)
+                x[w] = *reinterpret_cast<const Piece*>(src);
+            else
+                memset(&x[w], 0, sizeof(Piece));
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // interleaved: the 16 values in order are 8 neighbouring pairs
-            float& x = op.interleaved ? f[i >> 2][2 * (i & 3)] : f[0][i];
-            float& y = op.interleaved ? f[i >> 2][2 * (i & 3) + 1] : f[1][i];
-            const float x0 = x, y0 = y;
-            x = x0 * cs[i] - y0 * sn[i];
-            y = y0 * cs[i] + x0 * sn[i];
+        for (int w = 0; w < 4; ++w)
+            if (dst[w]) *reinterpret_cast<Piece*>(dst[w]) = x[w];
+    }
+    for (int i = threadIdx.x; i < n_pair; i += blockDim.x) {
+        const int h = i / prm.pairs, u = i - h * pairs;
+        const bool is_q = h < op.heads;
+        if (!is_q && page < 0) continue;   // nowhere to put it
+        const uint16_t* src = is_q ? q + h * D : k + (h - op.heads) * D;
+        uint16_t* dst = is_q ? qo + h * D : ko + (h - op.heads) * op.kv.head_stride;
+        const int d0 = op.interleaved ? 2 * u * U : u * U, d1 = d0 + (op.interleaved ? U : half);
+        const float* cp = op.cos + (long long)p * half + u * U;
+        const float* sp = op.sin + (long long)p * half + u * U;
+        if constexpr (U == 8) {
+            uint4 a = make_uint4(0, 0, 0, 0), c = a;
+            if (live) {
+                a = *reinterpret_cast<const uint4*>(src + d0);
+                c = *reinterpret_cast<const uint4*>(src + d1);
+                float x[8], y[8], cs[8], sn[8];
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    *reinterpret_cast<float4*>(cs + j) = __ldg(reinterpret_cast<const float4*>(cp + j));
+                    *reinterpret_cast<float4*>(sn + j) = __ldg(reinterpret_cast<const float4*>(sp + j));
+                }
+                if (op.interleaved) {   // pairs (x, y) lie side by side
+                    const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 f = pair_f32<BF16>(w[j]);
+                        o[j] = pair_16<BF16>(f.x * cs[j] - f.y * sn[j], f.y * cs[j] + f.x * sn[j]);
+                    }
+                    a = make_uint4(o[0], o[1], o[2], o[3]);
+                    c = make_uint4(o[4], o[5], o[6], o[7]);
+                } else {
+                    unpack8<BF16>(a, x);
+                    unpack8<BF16>(c, y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float x0 = x[j];
+                        x[j] = x0 * cs[j] - y[j] * sn[j];
+                        y[j] = y[j] * cs[j] + x0 * sn[j];
+                    }
+                    a = pack8<BF16>(x);
+                    c = pack8<BF16>(y);
+                }
+            }
+            *reinterpret_cast<uint4*>(dst + d0) = a;
+            *reinterpret_cast<uint4*>(dst + d1) = c;
+        } else {
+            uint16_t a = 0, c = 0;
+            if (live) {
+                const float x = elem_f32<BF16>(src[d0]), y = elem_f32<BF16>(src[d1]);
+                const float cs = __ldg(cp), sn = __ldg(sp);
+                a = elem_16<BF16>(x * cs - y * sn);
+                c = elem_16<BF16>(y * cs + x * sn);
+            }
+            dst[d0] = a;
+            dst[d1] = c;
         }
-        *reinterpret_cast<uint4*>(dst + d0) = pack8<BF16>(f[0]);
-        *reinterpret_cast<uint4*>(dst + d1) = pack8<BF16>(f[1]);
-    } else {
-        const uint16_t a = src[d0], c = src[d1];
-        if (!pair || !live || is_v) {
-            dst[d0] = live ? a : (uint16_t)0;
-            if (pair) dst[d1] = live ? c : (uint16_t)0;
-            return;
-        }
-        const float x = elem_f32<BF16>(a), y = elem_f32<BF16>(c);
-        const float cs = op.cos[(long long)p * half + u], sn = op.sin[(long long)p * half + u];
-        dst[d0] = elem_16<BF16>(x * cs - y * sn);
-        dst[d1] = elem_16<BF16>(y * cs + x * sn);
     }
 }
 
@@ -110,14 +146,22 @@ cudaError_t launch_kv_append(const dg_append& op, cudaStream_t s) {
                      vec_ok(kv.v, kv.token_stride) && kv.head_stride % 8 == 0 &&
                      (!op.heads || (vec_ok(op.q, op.q_stride) && vec_ok(op.q_out, op.q_out_stride))) &&
                      (!op.rot_dim || (vec_ok(op.cos, 0) && vec_ok(op.sin, 0)));
-    const int U = vec ? 8 : 1, half = op.rot_dim / 2;
-    const int units = (half + kv.head_dim - op.rot_dim) / U * (op.heads + 2 * kv.kv_heads);
-    const dim3 grid(kv.batch * op.q_len, (units + 255) / 256);
-    const int threads = units < 256 ? (units + 31) / 32 * 32 : 256;
+    const int U = vec ? 8 : 1;
+    const int turned = op.heads + kv.kv_heads;
+    const int units = turned * (op.rot_dim / 2 / U) + turned * ((kv.head_dim - op.rot_dim) / U) +
+                      kv.kv_heads * (kv.head_dim / U);
+    const dim3 grid(kv.batch * op.q_len);
+    const int threads = units < kAppendThreads ? (units + 31) / 32 * 32 : kAppendThreads;
+    AppendParams p{op,
+                   fast_div(op.q_len),
+                   fast_div(kv.page_size),
+                   fast_div(op.rot_dim / 2 / U),
+                   fast_div((kv.head_dim - op.rot_dim) / U),
+                   fast_div(kv.head_dim / U)};
     const bool bf = kv.type == DG_BF16;
     const void* fn = vec ? (bf ? (const void*)k_kv_append<true, 8> : (const void*)k_kv_append<false, 8>)
                          : (bf ? (const void*)k_kv_append<true, 1> : (const void*)k_kv_append<false, 1>);
-    void* args[] = {const_cast<dg_append*>(&op)};
+    void* args[] = {&p};
     return launch_pdl(fn, grid, dim3(threads), 0, s, args);
 }
 

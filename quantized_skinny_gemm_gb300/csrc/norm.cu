@@ -22,40 +22,37 @@ struct RowRegs {
     float v[C][U];
 };
 
-template <bool BF16, int U, int C>
-__device__ __forceinline__ void load_row(const void* p, int N, RowRegs<U, C>& r) {
+// Vector c of a row, zero past its end.
+template <bool BF16, int U>
+__device__ __forceinline__ void load_part(const void* p, int N, int c, float (&f)[U]) {
     const uint16_t* e = static_cast<const uint16_t*>(p);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int n = (c * blockDim.x + threadIdx.x) * U;
-        if (U == 8) {
-            float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (n < N) unpack8<BF16>(*reinterpret_cast<const uint4*>(e + n), f);
-#pragma unroll
-            for (int j = 0; j < U; ++j) r.v[c][j] = f[j];
-        } else {
-            r.v[c][0] = n < N ? elem_f32<BF16>(e[n]) : 0.f;
-        }
+    const int n = (c * blockDim.x + threadIdx.x) * U;
+    if constexpr (U == 8) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (n < N) v = *reinterpret_cast<const uint4*>(e + n);
+        unpack8<BF16>(v, f);
+    } else if constexpr (U == 2) {
+        const uint32_t v = n < N ? *reinterpret_cast<const uint32_t*>(e + n) : 0u;
+        const float2 x = pair_f32<BF16>(v);
+        f[0] = x.x, f[1] = x.y;
+    } else {
+        f[0] = n < N ? elem_f32<BF16>(e[n]) : 0.f;
     }
 }
-
-template <int U, int C>
-__device__ __forceinline__ void load_row_f32(const float* p, int N, RowRegs<U, C>& r) {
+template <int U>
+__device__ __forceinline__ void load_part_f32(const float* p, int N, int c, float (&f)[U]) {
+    const int n = (c * blockDim.x + threadIdx.x) * U;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int n = (c * blockDim.x + threadIdx.x) * U;
-        if (U == 8) {
-            float4 a = make_float4(0, 0, 0, 0), b = a;
-            if (n < N) {
-                a = *reinterpret_cast<const float4*>(p + n);
-                b = *reinterpret_cast<const float4*>(p + n + 4);
-            }
-            const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int j = 0; j < U; ++j) r.v[c][j] = f[j];
-        } else {
-            r.v[c][0] = n < N ? p[n] : 0.f;
-        }
+    for (int j = 0; j < U; ++j) f[j] = 0.f;
+    if (n >= N) return;
+    if constexpr (U == 8) {
+        const float4 a = *reinterpret_cast<const float4*>(p + n), b = *reinterpret_cast<const float4*>(p + n + 4);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    } else if constexpr (U == 2) {
+        const float2 a = *reinterpret_cast<const float2*>(p + n);
+        f[0] = a.x, f[1] = a.y;
+    } else {
+        f[0] = p[n];
     }
 }
 
@@ -66,14 +63,12 @@ __device__ __forceinline__ void store_row(void* p, int N, const RowRegs<U, C>& r
     for (int c = 0; c < C; ++c) {
         const int n = (c * blockDim.x + threadIdx.x) * U;
         if (n >= N) continue;
-        if (U == 8) {
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = r.v[c][j % U];
-            *reinterpret_cast<uint4*>(e + n) = pack8<BF16>(f);
-        } else {
+        if constexpr (U == 8)
+            *reinterpret_cast<uint4*>(e + n) = pack8<BF16>(r.v[c]);
+        else if constexpr (U == 2)
+            *reinterpret_cast<uint32_t*>(e + n) = pair_16<BF16>(r.v[c][0], r.v[c][1]);
+        else
             e[n] = elem_16<BF16>(r.v[c][0]);
-        }
     }
 }
 
@@ -83,11 +78,11 @@ __device__ __forceinline__ void store_row_f32(float* p, int N, const RowRegs<U, 
     for (int c = 0; c < C; ++c) {
         const int n = (c * blockDim.x + threadIdx.x) * U;
         if (n >= N) continue;
-        if (U == 8) {
-            *reinterpret_cast<float4*>(p + n) =
-                make_float4(r.v[c][0], r.v[c][1 % U], r.v[c][2 % U], r.v[c][3 % U]);
-            *reinterpret_cast<float4*>(p + n + 4) =
-                make_float4(r.v[c][4 % U], r.v[c][5 % U], r.v[c][6 % U], r.v[c][7 % U]);
+        if constexpr (U == 8) {
+            *reinterpret_cast<float4*>(p + n) = make_float4(r.v[c][0], r.v[c][1], r.v[c][2], r.v[c][3]);
+            *reinterpret_cast<float4*>(p + n + 4) = make_float4(r.v[c][4], r.v[c][5], r.v[c][6], r.v[c][7]);
+        } else if constexpr (U == 2) {
+            *reinterpret_cast<float2*>(p + n) = make_float2(r.v[c][0], r.v[c][1]);
         } else {
             p[n] = r.v[c][0];
         }
@@ -119,18 +114,17 @@ __device__ __forceinline__ void norm_row(const dg_norm& op, const void* w, const
 #pragma unroll
         for (int j = 0; j < U; ++j) q = fmaf(r.v[c][j], r.v[c][j], q);
     const float k = 1.f / sqrtf(cta_sum(q, red, turn) / (float)N + op.eps);
-    RowRegs<U, C> g;
-    load_row<BF16>(w, N, g);
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+        float g[U];
+        load_part<BF16>(w, N, c, g);
 #pragma unroll
-        for (int j = 0; j < U; ++j) r.v[c][j] = r.v[c][j] * k * (op.w_offset + g.v[c][j]);
-    if (b) {
-        load_row<BF16>(b, N, g);
+        for (int j = 0; j < U; ++j) r.v[c][j] = r.v[c][j] * k * (op.w_offset + g[j]);
+        if (b) {
+            load_part<BF16>(b, N, c, g);
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int j = 0; j < U; ++j) r.v[c][j] += g.v[c][j];
+            for (int j = 0; j < U; ++j) r.v[c][j] += g[j];
+        }
     }
 }
 
@@ -144,35 +138,31 @@ __global__ void __launch_bounds__(1024) k_norm(const dg_norm op) {
     griddep_wait();
     const int N = op.N;
     const size_t at = (size_t)blockIdx.x * N;
-    RowRegs<U, C> hr, r;
-    if (op.h) {
-        if (op.h_f32)
-            load_row_f32(static_cast<const float*>(op.h) + at, N, hr);
-        else
-            load_row<BF16>(static_cast<const uint16_t*>(op.h) + at, N, hr);
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int j = 0; j < U; ++j) hr.v[c][j] *= op.alpha;
-    }
+    RowRegs<U, C> r;
+    const uint16_t* y = static_cast<const uint16_t*>(op.y) + at;
+    const uint16_t* gate = static_cast<const uint16_t*>(op.gate) + (op.gate_rows == 1 ? 0 : at);
     if (op.y) {
-        load_row<BF16>(static_cast<const uint16_t*>(op.y) + at, N, r);
+#pragma unroll
+        for (int c = 0; c < C; ++c) load_part<BF16>(y, N, c, r.v[c]);
         if (op.w_post) norm_row<BF16>(op, op.w_post, op.b_post, r, red, turn);
-        if (op.gate) {
-            RowRegs<U, C> g;
-            load_row<BF16>(static_cast<const uint16_t*>(op.gate) + (op.gate_rows == 1 ? 0 : at), N, g);
+    }
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int j = 0; j < U; ++j) r.v[c][j] *= g.v[c][j];
+    for (int c = 0; c < C; ++c) {
+        float h[U], g[U];
+        if (op.h) {
+            if (op.h_f32)
+                load_part_f32(static_cast<const float*>(op.h) + at, N, c, h);
+            else
+                load_part<BF16>(static_cast<const uint16_t*>(op.h) + at, N, c, h);
         }
+        if (op.gate) load_part<BF16>(gate, N, c, g);
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int j = 0; j < U; ++j)
-                r.v[c][j] = op.h ? fmaf(op.beta, r.v[c][j], hr.v[c][j]) : op.beta * r.v[c][j];
-    } else {
-        r = hr;
+        for (int j = 0; j < U; ++j) {
+            float v = r.v[c][j];
+            if (op.gate) v *= g[j];
+            const float a = h[j] * op.alpha;
+            r.v[c][j] = !op.y ? a : op.h ? fmaf(op.beta, v, a) : op.beta * v;
+        }
     }
     if (op.h_out) {
         if (op.h_f32)
@@ -262,32 +252,40 @@ __global__ void __launch_bounds__(1024) k_norm_rows(const dg_norm op) {
     }
 }
 
+// Vectors of U values, C of them a thread.
 template <bool BF16, int U>
 static const void* norm_fn(int C) {
     if (C <= 1) return (const void*)k_norm<BF16, U, 1>;
     if (C <= 2) return (const void*)k_norm<BF16, U, 2>;
-    if (U == 8) return (const void*)k_norm<BF16, U, 4>;
-    if (C <= 4) return (const void*)k_norm<BF16, U == 8 ? 1 : U, 4>;
-    if (C <= 8) return (const void*)k_norm<BF16, U == 8 ? 1 : U, 8>;
-    return (const void*)k_norm<BF16, U == 8 ? 1 : U, 32>;
+    if (C <= 4) return (const void*)k_norm<BF16, U, 4>;
+    if constexpr (U < 8) {
+        if (C <= 8) return (const void*)k_norm<BF16, U, 8>;
+        if (C <= 16) return (const void*)k_norm<BF16, U, 16>;
+    }
+    if constexpr (U < 2) return (const void*)k_norm<BF16, U, 32>;
+    return nullptr;
 }
 
 cudaError_t launch_norm(const dg_norm& op, cudaStream_t s) {
-    bool vec = op.N % 8 == 0;
-    const void* ptrs[] = {op.y, op.w_post, op.b_post, op.gate, op.h, op.w_pre, op.b_pre, op.h_out, op.x_out};
-    for (const void* p : ptrs) vec = vec && ((uintptr_t)p & 15u) == 0;
-    const int U = vec ? 8 : 1;
+    // 16-byte vectors where rows and pointers allow, pairs for even widths, else
+    // single values
+    const void* p16[] = {op.y, op.w_post, op.b_post, op.gate, op.w_pre, op.b_pre, op.x_out};
+    uintptr_t low = (uintptr_t)op.N * 2, wide = 0;
+    for (const void* p : p16) low |= (uintptr_t)p;
+    wide = (uintptr_t)op.h | (uintptr_t)op.h_out;
+    const int U = (low | wide) % 16 == 0 ? 8 : low % 4 == 0 && wide % (op.h_f32 ? 8 : 4) == 0 ? 2 : 1;
     const int vecs = (op.N + U - 1) / U;
     int threads = (vecs + 31) / 32 * 32;
     if (threads > 1024) threads = 1024;
     const int C = (vecs + threads - 1) / threads;
     const bool bf = op.type == DG_BF16;
-    const void* fn = vec ? (bf ? norm_fn<true, 8>(C) : norm_fn<false, 8>(C))
-                         : (bf ? norm_fn<true, 1>(C) : norm_fn<false, 1>(C));
+    const void* fn = U == 8   ? (bf ? norm_fn<true, 8>(C) : norm_fn<false, 8>(C))
+                     : U == 2 ? (bf ? norm_fn<true, 2>(C) : norm_fn<false, 2>(C))
+                              : (bf ? norm_fn<true, 1>(C) : norm_fn<false, 1>(C));
     void* args[] = {const_cast<dg_norm*>(&op)};
     // 64 registers a thread: as many CTAs as an SM's 65536 hold
     const int resident = sm_count() * (1024 / threads);
-    if (vec && C == 1 && op.rows > resident)
+    if (U == 8 && C == 1 && op.rows > resident)
         return launch_pdl(bf ? (const void*)k_norm_rows<true> : (const void*)k_norm_rows<false>,
                           dim3(resident), dim3(threads), 0, s, args);
     return launch_pdl(fn, dim3(op.rows), dim3(threads), 0, s, args);
