@@ -124,46 +124,71 @@ __global__ void __launch_bounds__(256) k_moe_scores(const MoeParams p) {
 
 // ---- routing ------------------------------------------------------------------------------
 
-// One warp: a token's probabilities from its scores (prob: E floats of shared
-// memory), its top_k experts and their weights.  Selection compares integers:
-// 0 nothing, 1 NaN, then the probability's bits (it is not negative).
-__device__ void route_token(const dg_moe& op, const float* scores, float* prob, int* ids, float* wts) {
+// One warp: a token's probabilities from its scores, its top_k experts and
+// their weights.  Selection compares integers: 0 nothing, 1 NaN, otherwise the
+// probability's bits + 2 (it is not negative).  A lane keeps the experts lane,
+// lane + 32, .. of up to 256 in registers, more in `more` (E words of shared
+// memory).
+__device__ __forceinline__ unsigned route_key(float v) { return v != v ? 1u : __float_as_uint(v) + 2u; }
+__device__ void route_token(const dg_moe& op, const float* scores, unsigned* more, int* ids, float* wts) {
+    constexpr int kReg = 8;
     const int lane = threadIdx.x & 31, E = op.E;
+    float v[kReg];
+    unsigned key[kReg];
+#pragma unroll
+    for (int j = 0; j < kReg; ++j) v[j] = lane + 32 * j < E ? __ldcg(scores + lane + 32 * j) : -INFINITY;
     if (op.score == DG_MOE_SOFTMAX) {
         float top = -INFINITY, sum = 0.f;
-        for (int e = lane; e < E; e += 32) top = fmaxf(top, prob[e] = __ldcg(scores + e));
+#pragma unroll
+        for (int j = 0; j < kReg; ++j) top = fmaxf(top, v[j]);
+        for (int e = lane + 32 * kReg; e < E; e += 32) top = fmaxf(top, __ldcg(scores + e));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        for (int e = lane; e < E; e += 32) sum += prob[e] = expf(prob[e] - top);
+#pragma unroll
+        for (int j = 0; j < kReg; ++j) {
+            v[j] = lane + 32 * j < E ? expf(v[j] - top) : 0.f;
+            sum += v[j];
+        }
+        for (int e = lane + 32 * kReg; e < E; e += 32) sum += expf(__ldcg(scores + e) - top);
         sum = warp_sum(sum);
-        for (int e = lane; e < E; e += 32) prob[e] = prob[e] / sum;
+#pragma unroll
+        for (int j = 0; j < kReg; ++j) key[j] = lane + 32 * j < E ? route_key(v[j] / sum) : 0u;
+        for (int e = lane + 32 * kReg; e < E; e += 32) more[e] = route_key(expf(__ldcg(scores + e) - top) / sum);
     } else {
-        for (int e = lane; e < E; e += 32) prob[e] = 1.f / (1.f + expf(-__ldcg(scores + e)));
+#pragma unroll
+        for (int j = 0; j < kReg; ++j) key[j] = lane + 32 * j < E ? route_key(1.f / (1.f + expf(-v[j]))) : 0u;
+        for (int e = lane + 32 * kReg; e < E; e += 32) more[e] = route_key(1.f / (1.f + expf(-__ldcg(scores + e))));
     }
     float mine = 0.f, total = 0.f;   // lane c holds choice c
     int id = 0;
     for (int c = 0; c < op.top_k; ++c) {
         unsigned best = 0;
         int at = 0x7fffffff;
-        for (int e = lane; e < E; e += 32) {
-            const float v = prob[e];
-            const unsigned key = v != v ? 1u : v < 0.f ? 0u : __float_as_uint(v) + 2u;
-            if (key > best) {
-                best = key;
+#pragma unroll
+        for (int j = 0; j < kReg; ++j)
+            if (key[j] > best) {
+                best = key[j];
+                at = lane + 32 * j;
+            }
+        for (int e = lane + 32 * kReg; e < E; e += 32)
+            if (more[e] > best) {
+                best = more[e];
                 at = e;
             }
-        }
         const unsigned top = __reduce_max_sync(0xffffffffu, best);
         const int e = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7fffffff);
-        const float v = prob[e];   // this lane's or another's: nobody has changed it yet
-        __syncwarp();
-        if (lane == (e & 31)) prob[e] = -1.f;
+        if (at == e) {   // this lane's: taken
+#pragma unroll
+            for (int j = 0; j < kReg; ++j)
+                if (e == lane + 32 * j) key[j] = 0;
+            if (e >= 32 * kReg) more[e] = 0;
+        }
+        const float prob = top == 1u ? NAN : __uint_as_float(top - 2u);
         if (lane == c) {
-            mine = v;
+            mine = prob;
             id = e;
         }
-        total += v;
-        __syncwarp();
+        total += prob;
     }
     if (lane < op.top_k) {
         ids[lane] = id;
@@ -188,6 +213,27 @@ struct Lists {
 // From L.ids (filled, synchronized) by all threads of the CTA.
 __device__ void build_lists(const dg_moe& op, Lists& L) {
     const int tid = threadIdx.x, slots = op.M * op.top_k;
+    if (slots <= 32) {   // one warp's lanes: a slot each
+        if (tid < 32) {
+            const int e = tid < slots ? L.ids[tid] : -1 - tid;
+            const unsigned same = __match_any_sync(0xffffffffu, e), below = (1u << tid) - 1;
+            const bool first = e >= 0 && !(same & below);
+            const unsigned firsts = __ballot_sync(0xffffffffu, first);
+            int at = 0;
+            for (unsigned f = firsts; f; f &= f - 1) at += __shfl_sync(0xffffffffu, e, __ffs(f) - 1) < e;
+            if (e >= 0) {
+                L.token_of[tid] = (uint8_t)(tid / op.top_k);
+                L.slot[at][__popc(same & below)] = (uint8_t)tid;
+                if (first) {
+                    L.expert[at] = (uint16_t)e;
+                    L.tokens[at] = (uint8_t)__popc(same);
+                }
+            }
+            if (tid == 0) L.count = __popc(firsts);
+        }
+        __syncthreads();
+        return;
+    }
     for (int e = tid; e < op.E; e += blockDim.x) L.mask[e] = 0;
     __syncthreads();
     for (int s = tid; s < slots; s += blockDim.x) {
@@ -295,6 +341,13 @@ __device__ __forceinline__ uint4 ld_token(const uint16_t* p, bool in) {
     return v;
 }
 
+// The same, leaving v as it is where `in` is false.
+__device__ __forceinline__ void ld_token_keep(uint4& v, const uint16_t* p, bool in) {
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+        : "l"(p), "r"((int)in));
+}
+
 // Rows g and g + 8 of a row tile at this lane's first column, and their scales.
 struct Src {
     const char* w[2];
@@ -352,10 +405,12 @@ struct Chunk {
         if constexpr (S::kInt4) {
             // columns of other groups than this lane's codes are zero
             const bool mine = PH == 2 ? (g & 1) == (t >> 1) : (g & 3) == t;
+            uint4 b[2][S::kWords];   // stays zero in lanes that load nothing
+#pragma unroll
+            for (int w = 0; w < 2 * S::kWords; ++w) b[w / S::kWords][w % S::kWords] = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < S::kSteps; ++i) {
                 const int k = k0 + i * S::kStep + t * S::kLane;
-                const bool in = mine && (FULL || k < Kd);
                 float c[NT][4];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
@@ -369,9 +424,13 @@ struct Chunk {
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         if (j == 0 || j * S::kTokens < R) {
-                            const uint4 b = ld_token(x[j] + k + w * 8, in);
-                            mma16816<false>(c[j], a0, b.x, b.y);
-                            mma16816<false>(c[j], a1, b.z, b.w);
+                            uint4& q = b[NT == 1 ? i & 1 : j & 1][w];
+                            if (FULL)
+                                ld_token_keep(q, x[j] + k + w * 8, mine);
+                            else
+                                q = ld_token(x[j] + k + w * 8, mine && k < Kd);
+                            mma16816<false>(c[j], a0, q.x, q.y);
+                            mma16816<false>(c[j], a1, q.z, q.w);
                         }
                     }
                 }
@@ -445,9 +504,10 @@ template <int PH>
 __device__ __forceinline__ int column_row(int j) {
     return j * (8 / PH) + ((threadIdx.x & 31) >> 2) / PH;
 }
-// Warps per SM that the kernels' registers are held to.
+// Warps per SM that the kernels' registers are held to.  NT 0 (int4, one token):
+// four phases only.
 __host__ __device__ constexpr int moe_warps(int KIND, int NT) {
-    return NT == 1 ? (KIND == DG_LINEAR_W4A16 ? 24 : 32) : NT == 2 ? 24 : NT == 4 ? 16 : 8;
+    return NT <= 1 ? (KIND == DG_LINEAR_W4A16 ? 16 : 32) : NT == 2 ? (KIND == DG_LINEAR_W4A16 ? 16 : 24) : NT == 4 ? 16 : 8;
 }
 
 // ---- gate and up ----------------------------------------------------------------------------
@@ -457,19 +517,64 @@ __device__ __forceinline__ size_t row_bytes_of(int cols) {
     return KIND == DG_LINEAR_W4A16 ? (size_t)cols / 2 : (size_t)cols * 2;
 }
 
+// This warp's chunks k, k + split, .. of row tile `tile` of expert li: its sums
+// to mine [token][16 rows].
 template <int KIND, int PH, int NT>
-__global__ void __launch_bounds__(kMoeWarps * 32, moe_warps(KIND, NT) / kMoeWarps) k_moe_up(const MoeParams p) {
+__device__ __forceinline__ void up_tile(const MoeParams& p, const Lists& L, int li, int tile, int& k, int split,
+                                        float* mine) {
     using S = Shape<KIND, PH>;
-    constexpr bool BF = KIND == DG_LINEAR_BF16;
-    constexpr int kTok = NT * S::kTokens;   // token rows of the accumulators
+    using C = Chunk<KIND, PH>;
+    const dg_moe& op = p.op;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, R = L.tokens[li];
+    const int n = (op.K + S::kCols - 1) / S::kCols;
+    const size_t row = (size_t)L.expert[li] * op.I + tile * 8 + g;
+    const size_t at = row * row_bytes_of<KIND>(op.K) + (S::kInt4 ? t * S::kLane / 2 : t * S::kLane * 2);
+    Src src{};
+    src.w[0] = static_cast<const char*>(op.W_gate) + at;
+    src.w[1] = static_cast<const char*>(op.W_up) + at;
+    if (S::kInt4) {
+        src.s[0] = static_cast<const uint16_t*>(op.gate_scale) + row * (op.K / op.group_size);
+        src.s[1] = static_cast<const uint16_t*>(op.up_scale) + row * (op.K / op.group_size);
+    }
+    const uint16_t* x = S::kInt4 ? p.ws.xp : static_cast<const uint16_t*>(op.x);
+    const uint16_t* xr[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+        xr[j] = x + (size_t)L.token_of[L.slot[li][min(column_row<PH>(j), R - 1)]] * op.K;
+    float acc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+    for (; k < n; k += split) C::add(p, src, xr, R, k * S::kCols, op.K, acc);
+    k -= n;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (PH == 1) {
+                mine[(j * 8 + t * 2) * 16 + g + 8 * h] = C::sum(acc[j], 0, h);
+                mine[(j * 8 + t * 2 + 1) * 16 + g + 8 * h] = C::sum(acc[j], 1, h);
+            } else {
+                const float v = C::sum(acc[j], 0, h);
+                if (PH == 2 || (t & 1) == 0)
+                    mine[(j * S::kTokens + (PH == 2 ? t : t >> 1)) * 16 + g + 8 * h] = v;
+            }
+        }
+}
+
+// NT: blocks of eight columns for all of an expert's token rows (int4: two
+// phases; experts with one or two token rows take four).
+template <int KIND, int NT>
+__global__ void __launch_bounds__(kMoeWarps * 32, moe_warps(KIND, NT) / kMoeWarps) k_moe_up(const MoeParams p) {
+    constexpr bool BF = KIND == DG_LINEAR_BF16, kInt4 = KIND == DG_LINEAR_W4A16;
+    constexpr int kTok = !kInt4 ? NT * 8 : NT ? NT * 4 : 2;   // token rows of the sums
     extern __shared__ __align__(16) float dyn[];
     __shared__ Lists L;
     const dg_moe& op = p.op;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, warp = tid >> 5;
     griddep_launch_dependents();
     griddep_wait();
     for (int m = warp; m < op.M; m += kMoeWarps)
-        route_token(op, p.ws.scores + (size_t)m * op.E, dyn + (size_t)warp * op.E, L.ids + m * op.top_k,
+        route_token(op, p.ws.scores + (size_t)m * op.E, reinterpret_cast<unsigned*>(dyn) + (size_t)warp * op.E, L.ids + m * op.top_k,
                     L.wts + m * op.top_k);
     __syncthreads();
     build_lists(op, L);
@@ -486,46 +591,19 @@ __global__ void __launch_bounds__(kMoeWarps * 32, moe_warps(KIND, NT) / kMoeWarp
     const int split = p.split, team = warp / split, first = team * split, teams = kMoeWarps / split;
     constexpr int kPart = kTok * 16;
     float* part = dyn + first * 2 * kPart;
-    const int tiles = op.I / 8, total = L.count * tiles, n = (op.K + S::kCols - 1) / S::kCols;
-    const size_t rb = row_bytes_of<KIND>(op.K);
-    const uint16_t* x = S::kInt4 ? p.ws.xp : static_cast<const uint16_t*>(op.x);
+    const int tiles = op.I / 8, total = L.count * tiles;
     int k = warp - first, turn = 0;   // this warp's next chunk of the row tile
     for (int item = blockIdx.x + team * gridDim.x; item < total; item += teams * gridDim.x) {
         const int li = item / tiles, tile = item - li * tiles, R = L.tokens[li];
-        const size_t row = (size_t)L.expert[li] * op.I + tile * 8 + g;
-        Src src{};
-        {
-            const size_t at = row * rb + (S::kInt4 ? t * S::kLane / 2 : t * S::kLane * 2);
-            src.w[0] = static_cast<const char*>(op.W_gate) + at;
-            src.w[1] = static_cast<const char*>(op.W_up) + at;
-            if (S::kInt4) {
-                src.s[0] = static_cast<const uint16_t*>(op.gate_scale) + row * (op.K / op.group_size);
-                src.s[1] = static_cast<const uint16_t*>(op.up_scale) + row * (op.K / op.group_size);
-            }
-        }
-        const uint16_t* xr[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            xr[j] = x + (size_t)L.token_of[L.slot[li][min(column_row<PH>(j), R - 1)]] * op.K;
-        float acc[NT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-        for (; k < n; k += split) Chunk<KIND, PH>::add(p, src, xr, R, k * S::kCols, op.K, acc);
-        k -= n;
         float* mine = part + ((warp - first) * 2 + turn) * kPart;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (PH == 1) {
-                    mine[(j * 8 + t * 2) * 16 + g + 8 * h] = Chunk<KIND, PH>::sum(acc[j], 0, h);
-                    mine[(j * 8 + t * 2 + 1) * 16 + g + 8 * h] = Chunk<KIND, PH>::sum(acc[j], 1, h);
-                } else {
-                    const float v = Chunk<KIND, PH>::sum(acc[j], 0, h);
-                    if (PH == 2 || (t & 1) == 0)
-                        mine[(j * S::kTokens + (PH == 2 ? t : t >> 1)) * 16 + g + 8 * h] = v;
-                }
-            }
+        if constexpr (kInt4) {
+            if (R <= 2)
+                up_tile<KIND, 4, 1>(p, L, li, tile, k, split, mine);
+            else if constexpr (NT > 0)
+                up_tile<KIND, 2, NT>(p, L, li, tile, k, split, mine);
+        } else {
+            up_tile<KIND, 1, NT>(p, L, li, tile, k, split, mine);
+        }
         if (split == 1)
             __syncwarp();
         else
@@ -540,7 +618,7 @@ __global__ void __launch_bounds__(kMoeWarps * 32, moe_warps(KIND, NT) / kMoeWarp
             }
             const float v = silu_f32(gate) * up;
             uint16_t* h = p.ws.h + (size_t)L.slot[li][tok] * 2 * op.I + tile * 8 +
-                          (S::kInt4 ? int4_place(r) : r);
+                          (kInt4 ? int4_place(r) : r);
             const float s = BF ? v : v * 0.00390625f;
             const uint16_t hi = elem_16<BF>(s);
             h[0] = hi;
@@ -552,16 +630,77 @@ __global__ void __launch_bounds__(kMoeWarps * 32, moe_warps(KIND, NT) / kMoeWarp
 
 // ---- down and the weighted sum ----------------------------------------------------------------
 
+// This warp's chunks k, k + warps, .. of expert li for output rows tile * 16 ..:
+// weight * sum added to mine [token][16 rows].
 template <int KIND, int PH, int NT>
-__global__ void __launch_bounds__(moe_warps(KIND, NT) * 32) k_moe_down(const MoeParams p) {
+__device__ __forceinline__ void down_expert(const MoeParams& p, const Lists& L, int li, int tile, int& k, int warps,
+                                            float* mine) {
     using S = Shape<KIND, PH>;
+    using C = Chunk<KIND, PH>;
+    constexpr bool BF = KIND == DG_LINEAR_BF16;
+    const dg_moe& op = p.op;
+    const int n = (op.I + S::kCols - 1) / S::kCols;
+    if (k >= n) {   // nothing of this expert is this warp's
+        k -= n;
+        return;
+    }
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, R = 2 * L.tokens[li];
+    // op.K is a multiple of 8: a last tile may lack its second half
+    const int half = tile * 16 + 8 < op.K ? 8 : 0;
+    const size_t row = (size_t)L.expert[li] * op.K + tile * 16 + g, rb = row_bytes_of<KIND>(op.I);
+    Src src{};
+    src.w[0] = static_cast<const char*>(op.W_down) + row * rb + (S::kInt4 ? t * S::kLane / 2 : t * S::kLane * 2);
+    src.w[1] = src.w[0] + half * rb;
+    if (S::kInt4) {
+        const int srow = op.I / op.group_size;
+        src.s[0] = static_cast<const uint16_t*>(op.down_scale) + row * srow;
+        src.s[1] = src.s[0] + half * srow;
+    }
+    const uint16_t* xr[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int r = min(column_row<PH>(j), R - 1);
+        xr[j] = p.ws.h + ((size_t)L.slot[li][r >> 1] * 2 + (r & 1)) * op.I;
+    }
+    float acc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+    for (; k < n; k += warps) C::add(p, src, xr, R, k * S::kCols, op.I, acc);
+    k -= n;
+    // token rows 2 i and 2 i + 1 are hi and lo of the expert's token i
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float hi, lo;
+            int i;
+            if (PH == 1) {
+                hi = C::sum(acc[j], 0, h), lo = C::sum(acc[j], 1, h);
+                i = j * 4 + t;
+            } else {
+                const int over = PH == 2 ? 1 : 2;   // the lane with the next token row
+                hi = C::sum(acc[j], 0, h);
+                lo = __shfl_xor_sync(0xffffffffu, hi, over);
+                i = PH == 2 ? ((t & 1) ? 16 : j * 2 + (t >> 1)) : (t ? 16 : j);
+            }
+            if (2 * i < R) {
+                const int s = L.slot[li][i];
+                const float v = BF ? hi + lo : fmaf(lo, 1.f / 2048.f, hi) * 256.f;
+                float* to = mine + L.token_of[s] * 16 + g + 8 * h;
+                *to = fmaf(L.wts[s], v, *to);
+            }
+        }
+    }
+}
+
+template <int KIND, int NT>
+__global__ void __launch_bounds__(moe_warps(KIND, NT) * 32) k_moe_down(const MoeParams p) {
     constexpr bool BF = KIND == DG_LINEAR_BF16;
     extern __shared__ __align__(16) float dyn[];
     __shared__ Lists L;
     const dg_moe& op = p.op;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int warps = blockDim.x >> 5;
-    const int M = op.M, tiles = (op.K + 15) / 16, n = (op.I + S::kCols - 1) / S::kCols;
+    const int tid = threadIdx.x, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int M = op.M, tiles = (op.K + 15) / 16;
     float* sums = dyn;   // [warps][M][16]
     griddep_launch_dependents();
     for (int i = tid; i < warps * 16 * M; i += blockDim.x) sums[i] = 0.f;
@@ -572,62 +711,18 @@ __global__ void __launch_bounds__(moe_warps(KIND, NT) * 32) k_moe_down(const Moe
     }
     __syncthreads();
     build_lists(op, L);
-    const size_t rb = row_bytes_of<KIND>(op.I);
     float* mine = sums + warp * 16 * M;
 
     int k = warp;   // this warp's next chunk of the expert
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        // op.K is a multiple of 8: a last tile may lack its second half
-        const int half = tile * 16 + 8 < op.K ? 8 : 0;
         for (int li = 0; li < L.count; ++li) {
-            if (k >= n) {   // nothing of this expert is this warp's
-                k -= n;
-                continue;
-            }
-            const int R = 2 * L.tokens[li];
-            const size_t row = (size_t)L.expert[li] * op.K + tile * 16 + g;
-            Src src{};
-            src.w[0] = static_cast<const char*>(op.W_down) + row * rb + (S::kInt4 ? t * S::kLane / 2 : t * S::kLane * 2);
-            src.w[1] = src.w[0] + half * rb;
-            if (S::kInt4) {
-                const int srow = op.I / op.group_size;
-                src.s[0] = static_cast<const uint16_t*>(op.down_scale) + row * srow;
-                src.s[1] = src.s[0] + half * srow;
-            }
-            const uint16_t* xr[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int r = min(column_row<PH>(j), R - 1);
-                xr[j] = p.ws.h + ((size_t)L.slot[li][r >> 1] * 2 + (r & 1)) * op.I;
-            }
-            float acc[NT][4];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-            for (; k < n; k += warps) Chunk<KIND, PH>::add(p, src, xr, R, k * S::kCols, op.I, acc);
-            k -= n;
-            // token rows 2 i and 2 i + 1 are hi and lo of the expert's token i
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float hi, lo;
-                    int i;
-                    if (PH == 1) {
-                        hi = Chunk<KIND, PH>::sum(acc[j], 0, h), lo = Chunk<KIND, PH>::sum(acc[j], 1, h);
-                        i = j * 4 + t;
-                    } else {
-                        const int over = PH == 2 ? 1 : 2;   // the lane with the next token row
-                        hi = Chunk<KIND, PH>::sum(acc[j], 0, h);
-                        lo = __shfl_xor_sync(0xffffffffu, hi, over);
-                        i = PH == 2 ? ((t & 1) ? 16 : j * 2 + (t >> 1)) : (t ? 16 : j);
-                    }
-                    if (2 * i < R) {
-                        const int s = L.slot[li][i];
-                        const float v = BF ? hi + lo : fmaf(lo, 1.f / 2048.f, hi) * 256.f;
-                        float* to = mine + L.token_of[s] * 16 + g + 8 * h;
-                        *to = fmaf(L.wts[s], v, *to);
-                    }
-                }
+            if constexpr (KIND == DG_LINEAR_W4A16) {
+                if (L.tokens[li] == 1)
+                    down_expert<KIND, 4, 1>(p, L, li, tile, k, warps, mine);
+                else if constexpr (NT > 0)
+                    down_expert<KIND, 2, NT>(p, L, li, tile, k, warps, mine);
+            } else {
+                down_expert<KIND, 1, NT>(p, L, li, tile, k, warps, mine);
             }
         }
         __syncthreads();
@@ -672,36 +767,33 @@ size_t moe_ws_bytes(const dg_moe& op) {
     return place(op, nullptr, &w);
 }
 
-// Token blocks of the kernels: NT blocks of 8 / PH token rows, enough for all
-// of an expert's tokens (twice that in down: hi and lo).
+// Token blocks of the kernels, enough for all of an expert's token rows (M in up,
+// hi and lo of M in down).
 template <int KIND>
-static int token_blocks(int rows) {
+static int token_blocks(int M, int rows) {
+    if (KIND == DG_LINEAR_W4A16 && M == 1) return 0;
     const int per = KIND == DG_LINEAR_W4A16 ? 4 : 8, nt = (rows + per - 1) / per;
     return nt <= 2 ? nt : nt <= 4 ? 4 : 8;
 }
 template <int KIND>
-static const void* up_kernel(int M) {
-    const int nt = token_blocks<KIND>(M);
-    if constexpr (KIND == DG_LINEAR_W4A16) {
-        if (M == 1) return (const void*)k_moe_up<KIND, 4, 1>;
-        return nt == 1   ? (const void*)k_moe_up<KIND, 2, 1>
-               : nt == 2 ? (const void*)k_moe_up<KIND, 2, 2> : (const void*)k_moe_up<KIND, 2, 4>;
-    } else {
-        return nt == 1 ? (const void*)k_moe_up<KIND, 1, 1> : (const void*)k_moe_up<KIND, 1, 2>;
-    }
+static const void* up_kernel(int nt) {
+    if constexpr (KIND == DG_LINEAR_W4A16)
+        return nt == 0   ? (const void*)k_moe_up<KIND, 0>
+               : nt == 1 ? (const void*)k_moe_up<KIND, 1>
+               : nt == 2 ? (const void*)k_moe_up<KIND, 2> : (const void*)k_moe_up<KIND, 4>;
+    else
+        return nt == 1 ? (const void*)k_moe_up<KIND, 1> : (const void*)k_moe_up<KIND, 2>;
 }
 template <int KIND>
-static const void* down_kernel(int M) {
-    const int nt = token_blocks<KIND>(2 * M);
-    if constexpr (KIND == DG_LINEAR_W4A16) {
-        if (M == 1) return (const void*)k_moe_down<KIND, 4, 1>;
-        return nt == 1   ? (const void*)k_moe_down<KIND, 2, 1>
-               : nt == 2 ? (const void*)k_moe_down<KIND, 2, 2>
-               : nt == 4 ? (const void*)k_moe_down<KIND, 2, 4> : (const void*)k_moe_down<KIND, 2, 8>;
-    } else {
-        return nt == 1   ? (const void*)k_moe_down<KIND, 1, 1>
-               : nt == 2 ? (const void*)k_moe_down<KIND, 1, 2> : (const void*)k_moe_down<KIND, 1, 4>;
-    }
+static const void* down_kernel(int nt) {
+    if constexpr (KIND == DG_LINEAR_W4A16)
+        return nt == 0   ? (const void*)k_moe_down<KIND, 0>
+               : nt == 1 ? (const void*)k_moe_down<KIND, 1>
+               : nt == 2 ? (const void*)k_moe_down<KIND, 2>
+               : nt == 4 ? (const void*)k_moe_down<KIND, 4> : (const void*)k_moe_down<KIND, 8>;
+    else
+        return nt == 1   ? (const void*)k_moe_down<KIND, 1>
+               : nt == 2 ? (const void*)k_moe_down<KIND, 2> : (const void*)k_moe_down<KIND, 4>;
 }
 
 template <int KIND>
@@ -718,28 +810,29 @@ static cudaError_t launch_moe_kind(const dg_moe& op, void* ws, cudaStream_t s) {
     if (e != cudaSuccess) return e;
 
     p.wide_scales = g32 && op.K % 128 == 0 && al8(op.gate_scale) && al8(op.up_scale);
-    const int nt = token_blocks<KIND>(op.M), ctas = sm_count() * (moe_warps(KIND, nt) / kMoeWarps);
+    const int nt = token_blocks<KIND>(op.M, op.M), ctas = sm_count() * (moe_warps(KIND, nt) / kMoeWarps);
     // as few warps to a row tile as leave no SM without work: each split costs a
     // meeting per tile
-    const int chunk = KIND != DG_LINEAR_W4A16 ? 128 : op.M == 1 ? 512 : 256, experts = std::min(op.E, op.M * op.top_k);
+    const int chunk = KIND == DG_LINEAR_W4A16 ? 512 : 128, experts = std::min(op.E, op.M * op.top_k);
     p.split = 1;
     while (p.split < kMoeWarps && (long long)experts * (op.I / 8) * p.split < 3ll * ctas * kMoeWarps &&
            p.split * chunk < op.K)
         p.split *= 2;
     size_t smem = (size_t)2 * kMoeWarps * (op.M <= 8 ? 8 : 16) * 16 * 4;
     if (smem < (size_t)kMoeWarps * op.E * 4) smem = (size_t)kMoeWarps * op.E * 4;
-    const void* fn = up_kernel<KIND>(op.M);
+    const void* fn = up_kernel<KIND>(nt);
     if ((e = tc::smem_attr_once(fn, smem)) != cudaSuccess) return e;
     if ((e = launch_pdl(fn, dim3(ctas), dim3(kMoeWarps * 32), smem, s, args)) != cudaSuccess) return e;
 
     // down: one CTA a row tile and the SM's warps divided among its CTAs, down
     // to 8 warps; more tiles than that gives follow one another
     p.wide_scales = g32 && op.I % 128 == 0 && al8(op.down_scale);
-    const int tiles = (op.K + 15) / 16, sms = sm_count(), most = moe_warps(KIND, token_blocks<KIND>(2 * op.M));
+    const int tiles = (op.K + 15) / 16, sms = sm_count(), dt = token_blocks<KIND>(op.M, 2 * op.M);
+    const int most = moe_warps(KIND, dt);
     const int per_sm = std::min((tiles + sms - 1) / sms, most / kMoeWarps), warps = most / per_sm;
     const int grid = std::min(tiles, sms * per_sm);
     smem = (size_t)warps * 16 * op.M * 4;
-    fn = down_kernel<KIND>(op.M);
+    fn = down_kernel<KIND>(dt);
     if ((e = tc::smem_attr_once(fn, smem)) != cudaSuccess) return e;
     return launch_pdl(fn, dim3(grid), dim3(warps * 32), smem, s, args);
 }
