@@ -424,7 +424,8 @@ size_t dg_attn_workspace_bytes(const dg_attn* op);
  * given), h_out or x_out (not both; w_pre is needed only with x_out).  h_out
  * may be h or (same type) y, x_out may be y or (same type) h; other overlaps
  * are not allowed.  1 <= N <= 32768; any 2-byte (fp32: 4-byte) alignment
- * works, 16-byte aligned pointers and N a multiple of 8 take the vector path. */
+ * works; the fastest path wants the row tensors 16-byte aligned (any N), for a
+ * few rows the weights too and N a multiple of 8. */
 typedef enum { DG_NORM_RMS = 0, DG_NORM_LAYER = 1 } dg_norm_kind;
 typedef struct {
     int32_t type; /* dg_ftype */

@@ -133,3 +133,37 @@ def test_zero_constant_and_non_finite_rows(kind):
     _, rx, _, bx = ref.norm(f, None, np.ones(300), None, None, None, None, 1.0, 1.0,
                             float(np.float32(1e-5)), 0.0, kind == dg.NORM_LAYER, "f16", 0)
     ref.check(ref.f64(xo)[keep], rx, bx, "rows")
+
+
+@pytest.mark.parametrize("N", [1, 5, 8, 113, 114, 121, 128, 129, 242, 243, 256, 263, 1537, 2056])
+@pytest.mark.parametrize("ftype,kind,h32,gate", [("f16", 0, 0, 2), ("bf16", 1, 1, 1), ("bf16", 1, 0, 0)])
+def test_many_rows(N, ftype, kind, h32, gate):
+    """More rows than run at once, so that each team takes several."""
+    need_gpu()
+    t = _case(20011 if N < 300 else 2003, N, ftype, h32, gate, N)
+    _run_and_check(t, ftype, h32, kind, alpha=0.9, beta=0.5, what="many N=%d" % N)
+
+
+@pytest.mark.parametrize("rows,N", [(331, 8185), (331, 8186), (331, 8193), (317, 8192), (160, 16371), (9, 16371),
+                                    (157, 32749), (157, 32752), (3, 32753)])
+@pytest.mark.parametrize("bare", [False, True])
+def test_wide_rows(rows, N, bare):
+    """Few and many rows of widths around the vectors a thread holds; with all
+    weights and with one alone, which shared memory holds."""
+    need_gpu()
+    t = _case(rows, N, "bf16", 0, 1, N)
+    if bare:
+        t["w_post"] = t["b_post"] = t["b_pre"] = None
+    _run_and_check(t, "bf16", 0, 1, alpha=0.9, beta=0.5, what="wide N=%d" % N)
+
+
+def test_rows_in_place():
+    """h' over h, x over y: odd rows share 16-byte vectors with their neighbours."""
+    need_gpu()
+    t = _case(5003, 333, "f16", 0, 0, 3)
+    d = {k: None if v is None else v.to(DEV) for k, v in t.items()}
+    dg.norm_residual(dg.norm(d["h"], d["h"], d["y"], d["w_pre"], b_pre=d["b_pre"], y=d["y"], w_post=d["w_post"],
+                             b_post=d["b_post"]))
+    sync()
+    ho, xo = _run_and_check(t, "f16", 0, 0, eps=1e-6, w_offset=0.0)
+    assert torch.equal(d["h"], ho) and torch.equal(d["y"], xo)
