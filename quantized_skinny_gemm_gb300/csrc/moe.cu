@@ -56,8 +56,9 @@ struct MoeWs {
 struct MoeParams {
     dg_moe op;
     MoeWs ws;
-    int wide_scales;  // int4: a lane's scales of a chunk are one aligned load
-    int split;        // up: warps sharing a row tile's columns (1, 2, 4 or 8)
+    int scale_pairs;    // int4: groups of 32 whose scales can be loaded two at a time
+    FastDiv group_32s;  // int4: group_size / 32
+    int split;          // up: warps sharing a row tile's columns (1, 2, 4 or 8)
 };
 
 // ---- router scores ------------------------------------------------------------------------
@@ -360,7 +361,7 @@ struct Chunk {
 
     // acc[j] += (16 weight rows) x (token rows j * kTokens ..), columns [k0,
     // k0 + kCols) of Kd.  x[j]: the token row of this lane's column of block j.
-    // FULL: all of the chunk's columns exist and int4 scales are wide_scales.
+    // FULL: all of the chunk's columns exist and int4 scales come in pairs.
     template <bool FULL, int NT>
     __device__ __forceinline__ static void add_cols(const MoeParams& p, const Src& q, const uint16_t* const (&x)[NT],
                                                int R, int k0, int Kd, float (&acc)[NT][4]) {
@@ -383,24 +384,21 @@ struct Chunk {
             // the chunk's scales of a row, in order over the quad's lanes: lane t
             // holds groups t * kGroups .. + kGroups - 1 of the chunk
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                if (FULL) {
-                    if constexpr (S::kGroups == 4)
-                        ld_weights(sc[r], q.s[r] + k0 / 32 + t * 4);
-                    else
-                        ld_weights(sc[r][0], q.s[r] + k0 / 32 + t * 2);
-                } else {
-                    // any group size, count or alignment
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int w = 0; w < S::kGroups / 2; ++w) {
-                        const int k = k0 + (t * S::kGroups + 2 * w) * 32;
+                for (int w = 0; w < S::kGroups / 2; ++w) {
+                    const int j = k0 / 32 + t * S::kGroups + 2 * w;   // which 32 columns
+                    if (FULL) {
+                        ld_weights(sc[r][w], q.s[r] + j);
+                    } else if (p.scale_pairs) {
+                        ld_weights(sc[r][w], q.s[r] + j, j * 32 < Kd);
+                    } else {   // any group size, count or alignment
                         uint32_t two = 0;
-                        if (k < Kd) two = ld_stream_u16(q.s[r] + k / p.op.group_size);
-                        if (k + 32 < Kd) two |= (uint32_t)ld_stream_u16(q.s[r] + (k + 32) / p.op.group_size) << 16;
+                        if (j * 32 < Kd) two = ld_stream_u16(q.s[r] + j / p.group_32s);
+                        if (j * 32 + 32 < Kd) two |= (uint32_t)ld_stream_u16(q.s[r] + (j + 1) / p.group_32s) << 16;
                         sc[r][w] = two;
                     }
                 }
-            }
         }
         if constexpr (S::kInt4) {
             // columns of other groups than this lane's codes are zero
@@ -482,7 +480,7 @@ struct Chunk {
     template <int NT>
     __device__ __forceinline__ static void add(const MoeParams& p, const Src& q, const uint16_t* const (&x)[NT],
                                                int R, int k0, int Kd, float (&acc)[NT][4]) {
-        if (k0 + S::kCols <= Kd && (!S::kInt4 || p.wide_scales))
+        if (k0 + S::kCols <= Kd && (!S::kInt4 || p.scale_pairs))
             add_cols<true>(p, q, x, R, k0, Kd, acc);
         else
             add_cols<false>(p, q, x, R, k0, Kd, acc);
@@ -802,14 +800,14 @@ static cudaError_t launch_moe_kind(const dg_moe& op, void* ws, cudaStream_t s) {
     p.op = op;
     place(op, ws, &p.ws);
     const bool g32 = KIND == DG_LINEAR_W4A16 && op.group_size == 32;
-    auto al8 = [](const void* q) { return ((uintptr_t)q & 7u) == 0; };
+    auto al4 = [](const void* q) { return ((uintptr_t)q & 3u) == 0; };
     void* args[] = {&p};
-    p.wide_scales = 0;
+    p.group_32s = fast_div(KIND == DG_LINEAR_W4A16 ? op.group_size / 32 : 1);
     cudaError_t e = launch_pdl((const void*)k_moe_scores<KIND == DG_LINEAR_BF16>,
                                dim3(op.E, (op.M + kScoreTokens - 1) / kScoreTokens), dim3(256), 0, s, args);
     if (e != cudaSuccess) return e;
 
-    p.wide_scales = g32 && op.K % 128 == 0 && al8(op.gate_scale) && al8(op.up_scale);
+    p.scale_pairs = g32 && op.K % 64 == 0 && al4(op.gate_scale) && al4(op.up_scale);
     const int nt = token_blocks<KIND>(op.M, op.M), ctas = sm_count() * (moe_warps(KIND, nt) / kMoeWarps);
     // as few warps to a row tile as leave no SM without work: each split costs a
     // meeting per tile
@@ -826,7 +824,7 @@ static cudaError_t launch_moe_kind(const dg_moe& op, void* ws, cudaStream_t s) {
 
     // down: one CTA a row tile and the SM's warps divided among its CTAs, down
     // to 8 warps; more tiles than that gives follow one another
-    p.wide_scales = g32 && op.I % 128 == 0 && al8(op.down_scale);
+    p.scale_pairs = g32 && op.I % 64 == 0 && al4(op.down_scale);
     const int tiles = (op.K + 15) / 16, sms = sm_count(), dt = token_blocks<KIND>(op.M, 2 * op.M);
     const int most = moe_warps(KIND, dt);
     const int per_sm = std::min((tiles + sms - 1) / sms, most / kMoeWarps), warps = most / per_sm;
