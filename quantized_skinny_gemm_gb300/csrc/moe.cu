@@ -198,7 +198,8 @@ __device__ void route_token(const dg_moe& op, const float* scores, unsigned* mor
 }
 
 // The chosen experts in ascending order and each one's slots (token * top_k +
-// choice) in token order.
+// choice) in token order.  An expert of more tokens than the kernel takes at a
+// time (CAP) is listed twice.
 struct Lists {
     int count;
     uint16_t expert[kMoeMaxSlots];
@@ -212,22 +213,25 @@ struct Lists {
 };
 
 // From L.ids (filled, synchronized) by all threads of the CTA.
+template <int CAP>
 __device__ void build_lists(const dg_moe& op, Lists& L) {
+    static_assert(CAP >= 8, "16 tokens make two parts at most");
     const int tid = threadIdx.x, slots = op.M * op.top_k;
     if (slots <= 32) {   // one warp's lanes: a slot each
         if (tid < 32) {
             const int e = tid < slots ? L.ids[tid] : -1 - tid;
-            const unsigned same = __match_any_sync(0xffffffffu, e), below = (1u << tid) - 1;
-            const bool first = e >= 0 && !(same & below);
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            const int rank = __popc(same & ((1u << tid) - 1)), key = e * 2 + rank / CAP;
+            const bool first = e >= 0 && rank % CAP == 0;
             const unsigned firsts = __ballot_sync(0xffffffffu, first);
             int at = 0;
-            for (unsigned f = firsts; f; f &= f - 1) at += __shfl_sync(0xffffffffu, e, __ffs(f) - 1) < e;
+            for (unsigned f = firsts; f; f &= f - 1) at += __shfl_sync(0xffffffffu, key, __ffs(f) - 1) < key;
             if (e >= 0) {
                 L.token_of[tid] = (uint8_t)(tid / op.top_k);
-                L.slot[at][__popc(same & below)] = (uint8_t)tid;
+                L.slot[at][rank % CAP] = (uint8_t)tid;
                 if (first) {
                     L.expert[at] = (uint16_t)e;
-                    L.tokens[at] = (uint8_t)__popc(same);
+                    L.tokens[at] = (uint8_t)min(__popc(same) - rank, CAP);
                 }
             }
             if (tid == 0) L.count = __popc(firsts);
@@ -246,23 +250,27 @@ __device__ void build_lists(const dg_moe& op, Lists& L) {
     if (tid < 32) {
         int n = 0;
         for (int e0 = 0; e0 < op.E; e0 += 32) {
-            const int e = e0 + tid;
-            const unsigned mk = e < op.E ? L.mask[e] : 0u;
-            const unsigned b = __ballot_sync(0xffffffffu, mk != 0);
-            if (mk) {
-                const int at = n + __popc(b & ((1u << tid) - 1));
-                L.expert[at] = (uint16_t)e;
-                L.tokens[at] = (uint8_t)__popc(mk);
+            const int e = e0 + tid, tokens = e < op.E ? __popc(L.mask[e]) : 0;
+            const unsigned one = __ballot_sync(0xffffffffu, tokens > 0), two = __ballot_sync(0xffffffffu, tokens > CAP);
+            if (tokens) {
+                const unsigned below = (1u << tid) - 1;
+                const int at = n + __popc(one & below) + __popc(two & below);
                 L.at[e] = (uint16_t)at;
+                L.expert[at] = (uint16_t)e;
+                L.tokens[at] = (uint8_t)min(tokens, CAP);
+                if (tokens > CAP) {
+                    L.expert[at + 1] = (uint16_t)e;
+                    L.tokens[at + 1] = (uint8_t)(tokens - CAP);
+                }
             }
-            n += __popc(b);
+            n += __popc(one) + __popc(two);
         }
         if (tid == 0) L.count = n;
     }
     __syncthreads();
     for (int s = tid; s < slots; s += blockDim.x) {
-        const int e = L.ids[s], m = L.token_of[s];
-        L.slot[L.at[e]][__popc(L.mask[e] & ((1u << m) - 1))] = (uint8_t)s;
+        const int e = L.ids[s], m = L.token_of[s], rank = __popc(L.mask[e] & ((1u << m) - 1));
+        L.slot[L.at[e] + rank / CAP][rank % CAP] = (uint8_t)s;
     }
     __syncthreads();
 }
@@ -505,7 +513,7 @@ __device__ __forceinline__ int column_row(int j) {
 // Warps per SM that the kernels' registers are held to.  NT 0 (int4, one token):
 // four phases only.
 __host__ __device__ constexpr int moe_warps(int KIND, int NT) {
-    return NT <= 1 ? (KIND == DG_LINEAR_W4A16 ? 16 : 32) : NT == 2 ? (KIND == DG_LINEAR_W4A16 ? 16 : 24) : NT == 4 ? 16 : 8;
+    return KIND == DG_LINEAR_W4A16 ? 16 : NT <= 1 ? 32 : NT == 2 ? 24 : 16;
 }
 
 // ---- gate and up ----------------------------------------------------------------------------
@@ -564,7 +572,7 @@ __device__ __forceinline__ void up_tile(const MoeParams& p, const Lists& L, int 
 template <int KIND, int NT>
 __global__ void __launch_bounds__(kMoeWarps * 32, moe_warps(KIND, NT) / kMoeWarps) k_moe_up(const MoeParams p) {
     constexpr bool BF = KIND == DG_LINEAR_BF16, kInt4 = KIND == DG_LINEAR_W4A16;
-    constexpr int kTok = !kInt4 ? NT * 8 : NT ? NT * 4 : 2;   // token rows of the sums
+    constexpr int kTok = !kInt4 ? NT * 8 : NT ? NT * 4 : 2;   // token rows at a time
     extern __shared__ __align__(16) float dyn[];
     __shared__ Lists L;
     const dg_moe& op = p.op;
@@ -575,7 +583,7 @@ __global__ void __launch_bounds__(kMoeWarps * 32, moe_warps(KIND, NT) / kMoeWarp
         route_token(op, p.ws.scores + (size_t)m * op.E, reinterpret_cast<unsigned*>(dyn) + (size_t)warp * op.E, L.ids + m * op.top_k,
                     L.wts + m * op.top_k);
     __syncthreads();
-    build_lists(op, L);
+    build_lists<kTok < 8 ? 16 : kTok>(op, L);   // fewer than 8: so are the tokens
     if (blockIdx.x == 0)
         for (int s = tid; s < op.M * op.top_k; s += blockDim.x) {
             p.ws.ids[s] = L.ids[s];
@@ -694,6 +702,7 @@ __device__ __forceinline__ void down_expert(const MoeParams& p, const Lists& L, 
 template <int KIND, int NT>
 __global__ void __launch_bounds__(moe_warps(KIND, NT) * 32) k_moe_down(const MoeParams p) {
     constexpr bool BF = KIND == DG_LINEAR_BF16;
+    constexpr int kTok = KIND == DG_LINEAR_W4A16 ? NT * 2 : NT * 4;   // tokens at a time
     extern __shared__ __align__(16) float dyn[];
     __shared__ Lists L;
     const dg_moe& op = p.op;
@@ -708,7 +717,7 @@ __global__ void __launch_bounds__(moe_warps(KIND, NT) * 32) k_moe_down(const Moe
         L.wts[s] = __ldcg(p.ws.wts + s);
     }
     __syncthreads();
-    build_lists(op, L);
+    build_lists<kTok < 8 ? 16 : kTok>(op, L);   // fewer than 8: so are the tokens
     float* mine = sums + warp * 16 * M;
 
     int k = warp;   // this warp's next chunk of the expert
@@ -765,20 +774,19 @@ size_t moe_ws_bytes(const dg_moe& op) {
     return place(op, nullptr, &w);
 }
 
-// Token blocks of the kernels, enough for all of an expert's token rows (M in up,
-// hi and lo of M in down).
+// Token blocks of the kernels, enough for `tokens` of `rows` token rows each (up:
+// one; down: hi and lo).
 template <int KIND>
-static int token_blocks(int M, int rows) {
-    if (KIND == DG_LINEAR_W4A16 && M == 1) return 0;
-    const int per = KIND == DG_LINEAR_W4A16 ? 4 : 8, nt = (rows + per - 1) / per;
-    return nt <= 2 ? nt : nt <= 4 ? 4 : 8;
+static int token_blocks(int tokens, int rows) {
+    if (KIND == DG_LINEAR_W4A16 && tokens == 1) return 0;
+    const int per = KIND == DG_LINEAR_W4A16 ? 4 : 8, nt = (tokens * rows + per - 1) / per;
+    return nt <= 2 ? nt : 4;
 }
 template <int KIND>
 static const void* up_kernel(int nt) {
     if constexpr (KIND == DG_LINEAR_W4A16)
         return nt == 0   ? (const void*)k_moe_up<KIND, 0>
-               : nt == 1 ? (const void*)k_moe_up<KIND, 1>
-               : nt == 2 ? (const void*)k_moe_up<KIND, 2> : (const void*)k_moe_up<KIND, 4>;
+               : nt == 1 ? (const void*)k_moe_up<KIND, 1> : (const void*)k_moe_up<KIND, 2>;
     else
         return nt == 1 ? (const void*)k_moe_up<KIND, 1> : (const void*)k_moe_up<KIND, 2>;
 }
@@ -787,8 +795,7 @@ static const void* down_kernel(int nt) {
     if constexpr (KIND == DG_LINEAR_W4A16)
         return nt == 0   ? (const void*)k_moe_down<KIND, 0>
                : nt == 1 ? (const void*)k_moe_down<KIND, 1>
-               : nt == 2 ? (const void*)k_moe_down<KIND, 2>
-               : nt == 4 ? (const void*)k_moe_down<KIND, 4> : (const void*)k_moe_down<KIND, 8>;
+               : nt == 2 ? (const void*)k_moe_down<KIND, 2> : (const void*)k_moe_down<KIND, 4>;
     else
         return nt == 1   ? (const void*)k_moe_down<KIND, 1>
                : nt == 2 ? (const void*)k_moe_down<KIND, 2> : (const void*)k_moe_down<KIND, 4>;
@@ -808,7 +815,15 @@ static cudaError_t launch_moe_kind(const dg_moe& op, void* ws, cudaStream_t s) {
     if (e != cudaSuccess) return e;
 
     p.scale_pairs = g32 && op.K % 64 == 0 && al4(op.gate_scale) && al4(op.up_scale);
-    const int nt = token_blocks<KIND>(op.M, op.M), ctas = sm_count() * (moe_warps(KIND, nt) / kMoeWarps);
+    // Tokens of an expert at a time: registers for sixteen cost warps, a second
+    // part reads the expert's weights again (mostly from L2).  int4 always takes
+    // eight (16 tokens, 4096 x 2048, 2 of 8 experts: 94 us, sixteen 142; all 16 on
+    // one expert of 2048 x 2048: 29, 44), 16-bit weights where experts of more are
+    // rare (12 tokens, 2048 x 1024, 8 of 64: 125, 134; but 16 tokens, 4096 x
+    // 14336, 2 of 8: 572, 480).
+    const bool few = KIND == DG_LINEAR_W4A16 || op.M * op.top_k <= 2 * op.E;
+    const int tokens = few ? std::min(op.M, 8) : op.M;
+    const int nt = token_blocks<KIND>(tokens, 1), ctas = sm_count() * (moe_warps(KIND, nt) / kMoeWarps);
     // as few warps to a row tile as leave no SM without work: each split costs a
     // meeting per tile
     const int chunk = KIND == DG_LINEAR_W4A16 ? 512 : 128, experts = std::min(op.E, op.M * op.top_k);
@@ -816,7 +831,7 @@ static cudaError_t launch_moe_kind(const dg_moe& op, void* ws, cudaStream_t s) {
     while (p.split < kMoeWarps && (long long)experts * (op.I / 8) * p.split < 3ll * ctas * kMoeWarps &&
            p.split * chunk < op.K)
         p.split *= 2;
-    size_t smem = (size_t)2 * kMoeWarps * (op.M <= 8 ? 8 : 16) * 16 * 4;
+    size_t smem = (size_t)2 * kMoeWarps * (tokens <= 8 ? 8 : 16) * 16 * 4;
     if (smem < (size_t)kMoeWarps * op.E * 4) smem = (size_t)kMoeWarps * op.E * 4;
     const void* fn = up_kernel<KIND>(nt);
     if ((e = tc::smem_attr_once(fn, smem)) != cudaSuccess) return e;
@@ -825,7 +840,7 @@ static cudaError_t launch_moe_kind(const dg_moe& op, void* ws, cudaStream_t s) {
     // down: one CTA a row tile and the SM's warps divided among its CTAs, down
     // to 8 warps; more tiles than that gives follow one another
     p.scale_pairs = g32 && op.I % 64 == 0 && al4(op.down_scale);
-    const int tiles = (op.K + 15) / 16, sms = sm_count(), dt = token_blocks<KIND>(op.M, 2 * op.M);
+    const int tiles = (op.K + 15) / 16, sms = sm_count(), dt = token_blocks<KIND>(tokens, 2);
     const int most = moe_warps(KIND, dt);
     const int per_sm = std::min((tiles + sms - 1) / sms, most / kMoeWarps), warps = most / per_sm;
     const int grid = std::min(tiles, sms * per_sm);

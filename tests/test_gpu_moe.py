@@ -171,3 +171,23 @@ def test_y_may_be_x_and_the_residual():
     dg.moe_forward(op, ws)
     sync()
     assert torch.equal(d["x"], want)
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16", "w4"])
+@pytest.mark.parametrize("M,top_k", [(16, 1), (9, 3), (13, 4), (16, 4)])
+def test_crowded_experts_among_many(fmt, M, top_k):
+    """All tokens but one on the same experts, more than are taken at a time."""
+    need_gpu()
+    t = _case(fmt, M, 256, 96, 64, 67)
+    keep = t["x"][1].clone()
+    t["x"][:] = t["x"][0]
+    t["x"][1] = keep
+    y, _, _ = _check(t, fmt, top_k, residual=False, what="crowded")
+    assert all(torch.equal(y[0], y[i]) for i in range(2, min(M, 8)))
+
+
+@pytest.mark.parametrize("K,I", [(576, 192), (1088, 320), (96, 704), (544, 1120)])
+def test_int4_sizes_between_chunks(K, I):
+    need_gpu()
+    _check(_case("w4", 3, K, I, 9, 68), "w4", 2, what="K=%d I=%d" % (K, I))
+    _check(_case("w4", 12, K, I, 9, 69), "w4", 3, what="K=%d I=%d, twelve" % (K, I))
