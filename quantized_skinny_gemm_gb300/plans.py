@@ -16,7 +16,9 @@ from typing import Dict, List, Optional
 import torch
 
 from . import (EPI_RESIDUAL, EPI_SWIGLU, LINEAR_F16, LINEAR_W4A16, LINEAR_W4A8, LINEAR_W8A8,
-               StepPlan, decode_step_weights, linear, residual_add, swiglu)
+               StepPlan, append, attention, attn_decode, attn_workspace_bytes, decode_step_weights,
+               kv_append, linear, moe, moe_forward, moe_workspace_bytes, norm, norm_residual,
+               paged_kv, residual_add, swiglu)
 
 
 class Arena:
@@ -310,3 +312,93 @@ def fp16_block_step(layers, hs, device, fused=True) -> BlockStep:
             residual_add(ys["h1"], ys["y_down"], ys["h2"], stream=stream)
     keep.append(per_layer)
     return BlockStep(run, ins, outs, ain.buf, aout.buf, wbytes, 5 * len(per_layer), None, ws, keep)
+
+
+@dataclass
+class SparseStep:
+    """A sparse decoder's whole step for the q_len new tokens of each sequence.
+    run() enqueues one step: h in, h_out and x_out (normed) out, and the new
+    tokens' keys and values into the caches.  Before each run seq_lens must
+    count the new tokens and block_table must name the pages they fall in; both
+    are read on the device, so a captured graph follows them."""
+    run: object
+    h: torch.Tensor                            # fp32 [batch * q_len][hidden]
+    h_out: torch.Tensor                        # fp32
+    x_out: torch.Tensor                        # fp16
+    seq_lens: torch.Tensor                     # int32 [batch]
+    block_table: torch.Tensor                  # int32 [batch][max_pages]
+    caches: List[tuple]                        # per layer: k, v [pages][page_size][kv_heads][head_dim]
+    layers: List[Dict[str, torch.Tensor]]      # per layer: q, k, v, q_rot, att, o, x, h_mid, x_mid, y, ids, weights
+    keep: list = field(default_factory=list)
+
+
+def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None, batch=1, q_len=1,
+                        page_size=64, max_pages=16, window=0, sinks=0, group=32, rope=None,
+                        share=None) -> SparseStep:
+    """layers: synth.sparse_decoder_workload(...) output; rope: (cos, sin) fp32
+    [max_pos][rot / 2] or None; share: another SparseStep of the same layers
+    (a different q_len or batch) whose weights, caches, table and lengths this
+    one uses.  Per layer
+      h += y (of the layer before); x = norm_attn(h); q, k, v = W x;
+      rotate q and k, k and v into the cache; att = attention; o = W_o att;
+      h += o; x = norm_mlp(h); y = experts(x)
+    and last h += y; x_out = final_norm(h).  The residual stream stays fp32; the
+    adds are part of the norms."""
+    M, f16, f32, i32 = batch * q_len, torch.float16, torch.float32, torch.int32
+    if share is not None and share.block_table.shape[0] != batch:
+        raise ValueError("share: another batch")
+    hidden = layers[0].q.shape[1]
+    dim = layers[0].q.shape[0] // heads
+    new = lambda *shape, dtype=f16: torch.zeros(shape, dtype=dtype, device=device)
+    if share is None:
+        pages = batch * max_pages
+        lens = new(batch, dtype=i32)
+        table = torch.arange(pages, dtype=i32, device=device).view(batch, max_pages)
+        weights = [{k: v.to(device) for k, v in vars(L).items() if torch.is_tensor(v)} for L in layers]
+        scales = [{k: v.to(device) for k, v in L.scales.items()} for L in layers]
+        caches = [(new(pages, page_size, kv_heads, dim), new(pages, page_size, kv_heads, dim)) for _ in layers]
+        final = (torch.ones(hidden, dtype=f16) if final_norm is None else final_norm).to(device)
+        cos, sin = (None, None) if rope is None else (t.to(device) for t in rope)
+    else:
+        lens, table, caches = share.seq_lens, share.block_table, share.caches
+        weights, scales, final, cos, sin = share.keep[0]
+    first = h = new(M, hidden, dtype=f32)
+    y, ops, views, attn_ws, moe_ws, lin_ws = None, [], [], 0, 0, 0
+    for W, S, (kc, vc) in zip(weights, scales, caches):
+        kv = paged_kv(kc, vc, table, lens)
+        t = {"x": new(M, hidden), "q": new(M, heads * dim), "k": new(M, kv_heads * dim), "v": new(M, kv_heads * dim),
+             "q_rot": new(M, heads * dim), "att": new(M, heads * dim), "o": new(M, hidden),
+             "h": new(M, hidden, dtype=f32), "h_mid": new(M, hidden, dtype=f32), "x_mid": new(M, hidden),
+             "y": new(M, hidden), "ids": new(M, top_k, dtype=i32), "weights": new(M, top_k, dtype=f32)}
+        lin = lambda w, a, b: linear(LINEAR_F16, W[w], M, b.shape[1], a.shape[1], x=a, y=b)
+        qkv = StepPlan([lin(n, t["x"], t[n]) for n in ("q", "k", "v")])
+        out = StepPlan([lin("o", t["att"], t["o"])])
+        att = attention(kv, t["q_rot"], t["att"], q_len=q_len, window=window, sinks=sinks)
+        kind = LINEAR_W4A16 if S else LINEAR_F16
+        experts = moe(kind, t["x_mid"], t["y"], W["router"], W["gate"], W["up"], W["down"], top_k,
+                      gate_scale=S.get("gate"), up_scale=S.get("up"), down_scale=S.get("down"), ids=t["ids"],
+                      weights=t["weights"], group_size=group, renormalize=True)
+        ops.append((norm(h, t["h"], t["x"], W["norm_attn"], y=y), qkv,
+                    append(kv, t["q"], t["k"], t["v"], q_out=t["q_rot"], q_len=q_len, cos=cos, sin=sin), att, out,
+                    norm(t["h"], t["h_mid"], t["x_mid"], W["norm_mlp"], y=t["o"]), experts))
+        attn_ws = max(attn_ws, attn_workspace_bytes(att))
+        moe_ws = max(moe_ws, moe_workspace_bytes(experts))
+        lin_ws = max(lin_ws, qkv.workspace_bytes(), out.workspace_bytes())
+        h, y = t["h_mid"], t["y"]
+        views.append(t)
+    h_out, x_out = new(M, hidden, dtype=f32), new(M, hidden)
+    last = norm(h, h_out, x_out, final, y=y)
+    ws_a, ws_m, ws_l = (new(max(n, 16), dtype=torch.uint8) for n in (attn_ws, moe_ws, lin_ws))
+
+    def run(stream=None):
+        for pre, qkv, app, att, out, mid, experts in ops:
+            norm_residual(pre, stream=stream)
+            decode_step_weights(qkv, ws_l, stream=stream)
+            kv_append(app, stream=stream)
+            attn_decode(att, ws_a, stream=stream)
+            decode_step_weights(out, ws_l, stream=stream)
+            norm_residual(mid, stream=stream)
+            moe_forward(experts, ws_m, stream=stream)
+        norm_residual(last, stream=stream)
+    return SparseStep(run, first, h_out, x_out, lens, table, caches, views,
+                      [(weights, scales, final, cos, sin), ws_a, ws_m, ws_l, share])

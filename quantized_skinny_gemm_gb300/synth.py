@@ -28,6 +28,9 @@ Workloads (the shapes of the decoders the pages run single-request decode on):
   down 4096x14336, plus lm_head 128256x4096; int4 codes uniform in [-7, 7],
   group 32 along K, fp16 scales ~U(1e-3, 1e-2); per layer x_attn, x_o, x_mlp
   [4096], x_down [14336] and the lm_head input [4096], fp16 ~N(0, 1).
+* ``sparse_decoder`` -- layers of a sparse decoder of any size: norms, q, k, v,
+  o, router and experts (fp16 or int4), every matrix ~N(0, 1 / K) (the residual
+  stream keeps its scale through the layers).
 """
 from dataclasses import dataclass, field
 from typing import Dict, List, Optional
@@ -199,3 +202,48 @@ def fp16_head(vocab, hidden, seed=0):
     generator, so the int4 workload's draws are unchanged)."""
     g = generator(seed + 104729)
     return Linear("lm_head", vocab, hidden, normal((vocab, hidden), W_STD, g), None, "x_head")
+
+
+# ---- a sparse decoder ---------------------------------------------------------
+
+@dataclass
+class SparseLayer:
+    norm_attn: torch.Tensor                 # [hidden]
+    norm_mlp: torch.Tensor
+    q: torch.Tensor                         # [heads * head_dim][hidden]
+    k: torch.Tensor                         # [kv_heads * head_dim][hidden]
+    v: torch.Tensor
+    o: torch.Tensor                         # [hidden][heads * head_dim]
+    router: torch.Tensor                    # [experts][hidden]
+    gate: torch.Tensor                      # [experts][inter][hidden] (int4: packed)
+    up: torch.Tensor
+    down: torch.Tensor                      # [experts][hidden][inter]
+    scales: Dict[str, torch.Tensor] = field(default_factory=dict)   # int4: gate, up, down
+
+
+def sparse_decoder_workload(seed=0, layers=2, hidden=1536, heads=12, kv_heads=2, head_dim=128, inter=512,
+                            experts=16, int4=False, group=32):
+    g = generator(seed)
+    fan = lambda *shape: normal(shape, shape[-1] ** -0.5, g)
+    out = []
+    for _ in range(layers):
+        L = SparseLayer(1 + normal((hidden,), 0.1, g), 1 + normal((hidden,), 0.1, g), fan(heads * head_dim, hidden),
+                        fan(kv_heads * head_dim, hidden), fan(kv_heads * head_dim, hidden),
+                        fan(hidden, heads * head_dim), fan(experts, hidden), None, None, None)
+        for name, rows, cols in (("gate", inter, hidden), ("up", inter, hidden), ("down", hidden, inter)):
+            if int4:   # codes of variance 18.7
+                w = int4_packed(experts * rows, cols, g).view(experts, rows, cols // 2)
+                L.scales[name] = uniform((experts, rows, cols // group), 0.1 * cols ** -0.5, 0.36 * cols ** -0.5, g,
+                                         torch.float16)
+            else:
+                w = fan(experts, rows, cols)
+            setattr(L, name, w)
+        out.append(L)
+    return out
+
+
+def rotary_tables(max_pos, rot_dim, base=10000.0):
+    """cos and sin fp32 [max_pos][rot_dim / 2] of a rotary embedding's angles."""
+    j = torch.arange(rot_dim // 2, dtype=torch.float64)
+    angle = torch.arange(max_pos, dtype=torch.float64)[:, None] * base ** (-2.0 * j / rot_dim)
+    return angle.cos().float(), angle.sin().float()
