@@ -17,20 +17,20 @@ from quantized_skinny_gemm_gb300 import plans, synth  # noqa: E402
 WINDOW = 16
 
 
-def decode(layers, embed, prompt, tokens, heads, kv_heads, top_k, device, graph=True):
-    """prompt: int64 [P] on the host; embed [vocab][hidden] fp16 (also the
-    lm_head).  Returns the `tokens` greedy continuations and the microseconds of
-    a step."""
+def decode(layers, embed, lm_head, prompt, tokens, heads, kv_heads, top_k, device, graph=True):
+    """prompt: int64 [P] on the host; embed and lm_head [vocab][hidden]
+    fp16.  Returns the `tokens` greedy continuations and the microseconds of a
+    step."""
     vocab, hidden = embed.shape
     dim = layers[0].q.shape[0] // heads
     total = len(prompt) + tokens
     pages = (total + 63) // 64
     rope = synth.rotary_tables(total, dim)
-    E = embed.to(device)
+    E, W = embed.to(device), lm_head.to(device)
     one = plans.sparse_decoder_step(layers, device, heads, kv_heads, top_k, max_pages=pages, rope=rope)
     logits = torch.empty(vocab, dtype=torch.float32, device=device)
     token = torch.empty(1, dtype=torch.int32, device=device)
-    head = dg.linear(dg.LINEAR_F16, E, 1, vocab, hidden, x=one.x_out, logits=logits, token=token)
+    head = dg.linear(dg.LINEAR_F16, W, 1, vocab, hidden, x=one.x_out, logits=logits, token=token)
     ws = torch.empty(dg.workspace_bytes([head]), dtype=torch.uint8, device=device)
 
     window = plans.sparse_decoder_step(layers, device, heads, kv_heads, top_k, q_len=WINDOW, rope=rope, share=one)
@@ -75,7 +75,7 @@ def decode(layers, embed, prompt, tokens, heads, kv_heads, top_k, device, graph=
 
 def main():
     a = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
-    for name, value in (("layers", 8), ("hidden", 2048), ("heads", 16), ("kv-heads", 4), ("head-dim", 128),
+    for name, value in (("layers", 8), ("hidden", 2048), ("heads", 16), ("kv-heads", 2), ("head-dim", 128),
                         ("inter", 1024), ("experts", 64), ("top-k", 6), ("vocab", 32768), ("prompt", 200),
                         ("tokens", 64)):
         a.add_argument("--" + name, type=int, default=value)
@@ -84,9 +84,10 @@ def main():
     layers = synth.sparse_decoder_workload(0, a.layers, a.hidden, a.heads, a.kv_heads, a.head_dim, a.inter,
                                            a.experts, a.int4)
     g = synth.generator(1)
-    embed = synth.normal((a.vocab, a.hidden), 0.05, g)
+    embed = synth.normal((a.vocab, a.hidden), 1.0, g)
+    lm_head = synth.normal((a.vocab, a.hidden), a.hidden ** -0.5, g)
     prompt = torch.randint(0, a.vocab, (a.prompt,), generator=g)
-    tokens, us = decode(layers, embed, prompt, a.tokens, a.heads, a.kv_heads, a.top_k, torch.device("cuda"))
+    tokens, us = decode(layers, embed, lm_head, prompt, a.tokens, a.heads, a.kv_heads, a.top_k, torch.device("cuda"))
     print("%d layers, %d of %d experts (%s): %.1f us a token" %
           (a.layers, a.top_k, a.experts, "int4" if a.int4 else "fp16", us))
     print("tokens:", " ".join(str(t) for t in tokens.tolist()[:16]), "...")

@@ -120,9 +120,9 @@ def test_the_example_decodes_the_same_in_a_graph(int4, prompt):
     import sparse_decode
     layers = _layers(int4, 3)
     g = torch.Generator().manual_seed(11)
-    embed = synth.normal((512, HIDDEN), 0.05, g)
+    embed, lm_head = synth.normal((512, HIDDEN), 1.0, g), synth.normal((512, HIDDEN), HIDDEN ** -0.5, g)
     words = torch.randint(0, 512, (prompt,), generator=g)
-    runs = [sparse_decode.decode(layers, embed, words, 20, HEADS, KV_HEADS, TOP_K, DEV, graph)[0]
+    runs = [sparse_decode.decode(layers, embed, lm_head, words, 20, HEADS, KV_HEADS, TOP_K, DEV, graph)[0]
             for graph in (True, False, True)]
     assert torch.equal(runs[0], runs[1]) and torch.equal(runs[0], runs[2])
     assert (runs[0] >= 0).all() and (runs[0] < 512).all()
