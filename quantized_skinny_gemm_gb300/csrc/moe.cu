@@ -59,6 +59,7 @@ struct MoeParams {
     int scale_pairs;    // int4: groups of 32 whose scales can be loaded two at a time
     FastDiv group_32s;  // int4: group_size / 32
     int split;          // up: warps sharing a row tile's columns (1, 2, 4 or 8)
+    int stage;          // byte of dynamic shared memory where the warps' token rows are staged
 };
 
 // ---- router scores ------------------------------------------------------------------------
@@ -303,6 +304,8 @@ struct Shape {
     static constexpr int kWords = kInt4 ? kLane / 8 : 4;   // 32-bit registers of a row and step
     static constexpr int kTokens = 8 / PH;                 // token rows of 8 columns
     static constexpr int kGroups = kCols / 128;            // int4: scale groups of a lane and row
+    static constexpr bool kStaged = PH == 2;               // token rows through shared memory
+    static constexpr int kPitch = kCols * 2;               // bytes of a staged token row
 };
 
 // Streaming loads; the predicated forms give zero where `in` is false.
@@ -356,6 +359,12 @@ __device__ __forceinline__ void ld_token_keep(uint4& v, const uint16_t* p, bool 
         : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
         : "l"(p), "r"((int)in));
 }
+// Eight values from shared memory, likewise.
+__device__ __forceinline__ void lds_token_keep(uint4& v, uint32_t at, bool in) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+                 : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+                 : "r"(at), "r"((int)in));
+}
 
 // Rows g and g + 8 of a row tile at this lane's first column, and their scales.
 struct Src {
@@ -363,18 +372,40 @@ struct Src {
     const uint16_t* s[2];
 };
 
+// The token row behind column g of block j.
+template <int PH>
+__device__ __forceinline__ int column_row(int j) {
+    return j * (8 / PH) + ((threadIdx.x & 31) >> 2) / PH;
+}
+
 template <int KIND, int PH>
 struct Chunk {
     using S = Shape<KIND, PH>;
 
     // acc[j] += (16 weight rows) x (token rows j * kTokens ..), columns [k0,
     // k0 + kCols) of Kd.  x[j]: the token row of this lane's column of block j.
+    // Two phases (experts of three tokens or more) have the warp copy the chunk of
+    // their R token rows row(r) to shared memory at xs beside the weight loads,
+    // so that they are not fetched step by step (16 tokens, 4096 x 2048, 2 of 8
+    // experts: 93 -> 82 us); one or two rows are faster from L1 (one token, 4096
+    // x 14336, 2 of 8: 56 us, staged 66).
     // FULL: all of the chunk's columns exist and int4 scales come in pairs.
-    template <bool FULL, int NT>
+    template <bool FULL, int NT, class Row>
     __device__ __forceinline__ static void add_cols(const MoeParams& p, const Src& q, const uint16_t* const (&x)[NT],
-                                               int R, int k0, int Kd, float (&acc)[NT][4]) {
+                                                    const Row& row, uint32_t xs, int R, int k0, int Kd,
+                                                    float (&acc)[NT][4]) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         uint32_t v[S::kSteps][2][S::kWords], sc[2][2];
+        if constexpr (S::kStaged) {
+            __syncwarp();   // the last chunk's values have been read
+            for (int r = 0; r < R; ++r) {
+                const uint16_t* from = row(r) + k0;
+#pragma unroll
+                for (int c = lane * 8; c < S::kCols; c += 256)
+                    cp_async16(xs + r * S::kPitch + c * 2, from + (FULL || k0 + c < Kd ? c : 0), FULL || k0 + c < Kd);
+            }
+            cp_commit();
+        }
         const size_t at = S::kInt4 ? k0 / 2 : (size_t)k0 * 2;
 #pragma unroll
         for (int i = 0; i < S::kSteps; ++i) {
@@ -409,8 +440,15 @@ struct Chunk {
                 }
         }
         if constexpr (S::kInt4) {
+            if constexpr (S::kStaged) {
+                cp_wait<0>();
+                __syncwarp();
+            }
             // columns of other groups than this lane's codes are zero
             const bool mine = PH == 2 ? (g & 1) == (t >> 1) : (g & 3) == t;
+            uint32_t xl[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) xl[j] = xs + min(column_row<PH>(j), R - 1) * S::kPitch + t * S::kLane * 2;
             uint4 b[2][S::kWords];   // stays zero in lanes that load nothing
 #pragma unroll
             for (int w = 0; w < 2 * S::kWords; ++w) b[w / S::kWords][w % S::kWords] = make_uint4(0, 0, 0, 0);
@@ -431,7 +469,9 @@ struct Chunk {
                     for (int j = 0; j < NT; ++j) {
                         if (j == 0 || j * S::kTokens < R) {
                             uint4& q = b[NT == 1 ? i & 1 : j & 1][w];
-                            if (FULL)
+                            if (S::kStaged)
+                                lds_token_keep(q, xl[j] + (i * S::kStep + w * 8) * 2, mine);
+                            else if (FULL)
                                 ld_token_keep(q, x[j] + k + w * 8, mine);
                             else
                                 q = ld_token(x[j] + k + w * 8, mine && k < Kd);
@@ -485,13 +525,14 @@ struct Chunk {
         }
     }
 
-    template <int NT>
+    template <int NT, class Row>
     __device__ __forceinline__ static void add(const MoeParams& p, const Src& q, const uint16_t* const (&x)[NT],
-                                               int R, int k0, int Kd, float (&acc)[NT][4]) {
+                                               const Row& row, uint32_t xs, int R, int k0, int Kd,
+                                               float (&acc)[NT][4]) {
         if (k0 + S::kCols <= Kd && (!S::kInt4 || p.scale_pairs))
-            add_cols<true>(p, q, x, R, k0, Kd, acc);
+            add_cols<true>(p, q, x, row, xs, R, k0, Kd, acc);
         else
-            add_cols<false>(p, q, x, R, k0, Kd, acc);
+            add_cols<false>(p, q, x, row, xs, R, k0, Kd, acc);
     }
 
     // The sums of token row n of block j in acc, after all chunks: for 16-bit
@@ -505,15 +546,15 @@ struct Chunk {
     }
 };
 
-// The token row behind column g of block j.
-template <int PH>
-__device__ __forceinline__ int column_row(int j) {
-    return j * (8 / PH) + ((threadIdx.x & 31) >> 2) / PH;
-}
 // Warps per SM that the kernels' registers are held to.  NT 0 (int4, one token):
 // four phases only.
 __host__ __device__ constexpr int moe_warps(int KIND, int NT) {
     return KIND == DG_LINEAR_W4A16 ? 16 : NT <= 1 ? 32 : NT == 2 ? 24 : 16;
+}
+
+// Bytes of a warp's staged token rows.
+__host__ __device__ constexpr int moe_stage(int KIND, int NT) {
+    return KIND == DG_LINEAR_W4A16 ? NT * Shape<DG_LINEAR_W4A16, 2>::kTokens * Shape<DG_LINEAR_W4A16, 2>::kPitch : 0;
 }
 
 // ---- gate and up ----------------------------------------------------------------------------
@@ -527,7 +568,7 @@ __device__ __forceinline__ size_t row_bytes_of(int cols) {
 // to mine [token][16 rows].
 template <int KIND, int PH, int NT>
 __device__ __forceinline__ void up_tile(const MoeParams& p, const Lists& L, int li, int tile, int& k, int split,
-                                        float* mine) {
+                                        uint32_t xs, float* mine) {
     using S = Shape<KIND, PH>;
     using C = Chunk<KIND, PH>;
     const dg_moe& op = p.op;
@@ -543,14 +584,14 @@ __device__ __forceinline__ void up_tile(const MoeParams& p, const Lists& L, int 
         src.s[1] = static_cast<const uint16_t*>(op.up_scale) + row * (op.K / op.group_size);
     }
     const uint16_t* x = S::kInt4 ? p.ws.xp : static_cast<const uint16_t*>(op.x);
+    auto token = [&](int r) { return x + (size_t)L.token_of[L.slot[li][r]] * op.K; };
     const uint16_t* xr[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-        xr[j] = x + (size_t)L.token_of[L.slot[li][min(column_row<PH>(j), R - 1)]] * op.K;
+    for (int j = 0; j < NT; ++j) xr[j] = token(min(column_row<PH>(j), R - 1));
     float acc[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-    for (; k < n; k += split) C::add(p, src, xr, R, k * S::kCols, op.K, acc);
+    for (; k < n; k += split) C::add(p, src, xr, token, xs, R, k * S::kCols, op.K, acc);
     k -= n;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -597,6 +638,7 @@ __global__ void __launch_bounds__(kMoeWarps * 32, moe_warps(KIND, NT) / kMoeWarp
     const int split = p.split, team = warp / split, first = team * split, teams = kMoeWarps / split;
     constexpr int kPart = kTok * 16;
     float* part = dyn + first * 2 * kPart;
+    const uint32_t xs = (uint32_t)__cvta_generic_to_shared(dyn) + p.stage + warp * moe_stage(KIND, NT);
     const int tiles = op.I / 8, total = L.count * tiles;
     int k = warp - first, turn = 0;   // this warp's next chunk of the row tile
     for (int item = blockIdx.x + team * gridDim.x; item < total; item += teams * gridDim.x) {
@@ -604,11 +646,11 @@ __global__ void __launch_bounds__(kMoeWarps * 32, moe_warps(KIND, NT) / kMoeWarp
         float* mine = part + ((warp - first) * 2 + turn) * kPart;
         if constexpr (kInt4) {
             if (R <= 2)
-                up_tile<KIND, 4, 1>(p, L, li, tile, k, split, mine);
+                up_tile<KIND, 4, 1>(p, L, li, tile, k, split, xs, mine);
             else if constexpr (NT > 0)
-                up_tile<KIND, 2, NT>(p, L, li, tile, k, split, mine);
+                up_tile<KIND, 2, NT>(p, L, li, tile, k, split, xs, mine);
         } else {
-            up_tile<KIND, 1, NT>(p, L, li, tile, k, split, mine);
+            up_tile<KIND, 1, NT>(p, L, li, tile, k, split, xs, mine);
         }
         if (split == 1)
             __syncwarp();
@@ -640,7 +682,7 @@ __global__ void __launch_bounds__(kMoeWarps * 32, moe_warps(KIND, NT) / kMoeWarp
 // weight * sum added to mine [token][16 rows].
 template <int KIND, int PH, int NT>
 __device__ __forceinline__ void down_expert(const MoeParams& p, const Lists& L, int li, int tile, int& k, int warps,
-                                            float* mine) {
+                                            uint32_t xs, float* mine) {
     using S = Shape<KIND, PH>;
     using C = Chunk<KIND, PH>;
     constexpr bool BF = KIND == DG_LINEAR_BF16;
@@ -662,16 +704,14 @@ __device__ __forceinline__ void down_expert(const MoeParams& p, const Lists& L, 
         src.s[0] = static_cast<const uint16_t*>(op.down_scale) + row * srow;
         src.s[1] = src.s[0] + half * srow;
     }
+    auto token = [&](int r) { return p.ws.h + ((size_t)L.slot[li][r >> 1] * 2 + (r & 1)) * op.I; };
     const uint16_t* xr[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int r = min(column_row<PH>(j), R - 1);
-        xr[j] = p.ws.h + ((size_t)L.slot[li][r >> 1] * 2 + (r & 1)) * op.I;
-    }
+    for (int j = 0; j < NT; ++j) xr[j] = token(min(column_row<PH>(j), R - 1));
     float acc[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-    for (; k < n; k += warps) C::add(p, src, xr, R, k * S::kCols, op.I, acc);
+    for (; k < n; k += warps) C::add(p, src, xr, token, xs, R, k * S::kCols, op.I, acc);
     k -= n;
     // token rows 2 i and 2 i + 1 are hi and lo of the expert's token i
 #pragma unroll
@@ -719,17 +759,18 @@ __global__ void __launch_bounds__(moe_warps(KIND, NT) * 32) k_moe_down(const Moe
     __syncthreads();
     build_lists<kTok < 8 ? 16 : kTok>(op, L);   // fewer than 8: so are the tokens
     float* mine = sums + warp * 16 * M;
+    const uint32_t xs = (uint32_t)__cvta_generic_to_shared(dyn) + p.stage + warp * moe_stage(KIND, NT);
 
     int k = warp;   // this warp's next chunk of the expert
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         for (int li = 0; li < L.count; ++li) {
             if constexpr (KIND == DG_LINEAR_W4A16) {
                 if (L.tokens[li] == 1)
-                    down_expert<KIND, 4, 1>(p, L, li, tile, k, warps, mine);
+                    down_expert<KIND, 4, 1>(p, L, li, tile, k, warps, xs, mine);
                 else if constexpr (NT > 0)
-                    down_expert<KIND, 2, NT>(p, L, li, tile, k, warps, mine);
+                    down_expert<KIND, 2, NT>(p, L, li, tile, k, warps, xs, mine);
             } else {
-                down_expert<KIND, 1, NT>(p, L, li, tile, k, warps, mine);
+                down_expert<KIND, 1, NT>(p, L, li, tile, k, warps, xs, mine);
             }
         }
         __syncthreads();
@@ -833,6 +874,8 @@ static cudaError_t launch_moe_kind(const dg_moe& op, void* ws, cudaStream_t s) {
         p.split *= 2;
     size_t smem = (size_t)2 * kMoeWarps * (tokens <= 8 ? 8 : 16) * 16 * 4;
     if (smem < (size_t)kMoeWarps * op.E * 4) smem = (size_t)kMoeWarps * op.E * 4;
+    p.stage = (int)((smem + 15) & ~(size_t)15);
+    smem = p.stage + (size_t)kMoeWarps * moe_stage(KIND, nt);
     const void* fn = up_kernel<KIND>(nt);
     if ((e = tc::smem_attr_once(fn, smem)) != cudaSuccess) return e;
     if ((e = launch_pdl(fn, dim3(ctas), dim3(kMoeWarps * 32), smem, s, args)) != cudaSuccess) return e;
@@ -844,7 +887,8 @@ static cudaError_t launch_moe_kind(const dg_moe& op, void* ws, cudaStream_t s) {
     const int most = moe_warps(KIND, dt);
     const int per_sm = std::min((tiles + sms - 1) / sms, most / kMoeWarps), warps = most / per_sm;
     const int grid = std::min(tiles, sms * per_sm);
-    smem = (size_t)warps * 16 * op.M * 4;
+    p.stage = (int)((size_t)warps * 16 * op.M * 4);
+    smem = p.stage + (size_t)warps * moe_stage(KIND, dt);
     fn = down_kernel<KIND>(dt);
     if ((e = tc::smem_attr_once(fn, smem)) != cudaSuccess) return e;
     return launch_pdl(fn, dim3(grid), dim3(warps * 32), smem, s, args);
