@@ -5,9 +5,10 @@
 // few dozen rows per key / value head (query heads of the group x new tokens)
 // the kernel is bound by HBM as long as the rows share each key they read.
 // Rows therefore form 16-row tiles of mma.sync (m16n8k16, fp32 accumulators);
-// one stage of a warp is 16 keys (32 of up to 64 dims) and their values, copied into the warp's own
-// ring of shared memory by cp.async (16 bytes a lane: any page size, stride
-// and head size), so warps never wait for one another while they stream.
+// one stage of a warp is 16 keys (32 of up to 64 dims) and their values, copied
+// into the warp's own ring of shared memory by cp.async (16 bytes a lane: any
+// page size, stride and head size), so warps never wait for one another while
+// they stream.
 //
 // Work split.  The visible positions of one (sequence, key / value head, row
 // group) are a unit of blocks of kBlockKeys positions.  All blocks of the call,
@@ -21,6 +22,12 @@
 // own positions and rescales its output only when m has grown by more than
 // 2^8 since (weights then stay below 256, far inside the 16-bit types' range);
 // scores are turned to units of log2(e) inside the exponent.
+//
+// Measured: 200001 positions of 8 x 128 bf16, 32 heads: 126.6 us, 6.5 TB/s of the
+// copy's 6.8; 16 sequences of up to 8191, 12 heads on 2: 11.1 us; one of 100: 5.4
+// us, one launch where the table holds 128 positions at most, else two; 8 tokens
+// of 8 sequences on windows of 4096, 32 heads on 8 of 64: 31 us, bound by the
+// latency of a few stages per warp and of the join.
 #include <algorithm>
 #include <climits>
 
@@ -89,7 +96,10 @@ __device__ __forceinline__ int quotient(long long a, int b) {
 
 template <int DP, int RT>
 struct AttnShape {
-    static constexpr int kSub = DP <= 64 && RT < 4 ? 2 : 1;  // 16-key pieces of a stage
+    // 16-key pieces of a stage: two where they are small, for the bookkeeping of a
+    // stage (64 dims: 31 us on the windows above and 60 on 12 sequences of up to
+    // 84056 positions; stages of 16 keys with 3 CTAs per SM 42 and 85)
+    static constexpr int kSub = DP <= 64 && RT < 4 ? 2 : 1;
     static constexpr int kKeys = 16 * kSub;
     static constexpr int kPitch = DP * 2;                   // bytes; see piece()
     static constexpr int kStage = 2 * kKeys * kPitch;       // keys, then values
@@ -644,7 +654,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
     griddep_launch_dependents();
     griddep_wait();
     const dg_attn& op = p.op;
-    const int2 info = __ldg(p.info + blockIdx.x);
+    const int2 info = __ldcg(p.info + blockIdx.x);
     const int n = info.y;
     if (n == 1) return;  // finished in place
     const int G = op.heads / op.kv.kv_heads, heads = op.kv.kv_heads * p.groups;
@@ -678,8 +688,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
             float2 w[kPairs];
 #pragma unroll
             for (int x = 0; x < kPairs; ++x)
-                w[x] = x * 64 + lane * 2 < D ? __ldg(o + x * 32) : make_float2(0.f, 0.f);
-            add(__ldg(q + r), __ldg(q + S::kRows + r), w);
+                w[x] = x * 64 + lane * 2 < D ? __ldcg(o + x * 32) : make_float2(0.f, 0.f);
+            add(__ldcg(q + r), __ldcg(q + S::kRows + r), w);
         }
         if (!few) {
             if (lane == 0) {

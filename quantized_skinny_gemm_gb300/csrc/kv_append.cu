@@ -10,7 +10,9 @@ namespace dg {
 // may be q.
 //
 // Bound by latency at decode sizes (one token: a few KB, two dependent reads,
-// length -> page id) and by HBM at large ones.
+// length -> page id; 2.8 us back to back, 4.8 alone) and by HBM at large ones (8
+// tokens of 256 sequences, 32 + 2 x 8 heads of 128: 11.3 us, 4.5 TB/s; one piece
+// at a time 14.1).
 constexpr int kAppendThreads = 128;
 template <int U>
 struct PieceOf {
