@@ -8,6 +8,10 @@
  *   - a very wide lm_head + greedy argmax (dg_lm_head_argmax)
  *   - weight-quantized: W8A8 per-channel int8 (dg_gemv_w8a8) and groupwise
  *     int4 with fp16 or int8 activations (dg_gemv_w4), dequantized in registers.
+ * and what a decoder runs between those products for a step's new tokens: norms
+ * with the residual add (dg_norm_residual), rotary positions and the cache
+ * append (dg_kv_append), attention over a paged cache (dg_attn_decode) and an
+ * expert layer (dg_moe_forward).
  * Sources: the M=1 custom cube matmul, the 16-slice lm_head with a host reduce
  * and the weight-bandwidth floor of "MiniCPM-V on Orange Pi AIPro (Ascend 310B)";
  * single-request decode and graph-replayed decode steps of "EdgeFM: Efficient
@@ -323,7 +327,8 @@ size_t dg_workspace_bytes(const dg_linear* ops, int n_ops);
  * max_pages * page_size on and positions whose page id is outside
  * [0, num_pages) do not exist: the append writes nothing there and no token
  * sees them.  The table and the lengths are device memory, read when the
- * kernels run, so a captured graph follows them. */
+ * kernels run, so a captured graph follows them.  Up to 2^20 sequences and 1024
+ * heads; more return DG_ERR_UNSUPPORTED. */
 typedef struct {
     int32_t type;      /* dg_ftype of the cache and of q, k, v, out */
     int32_t batch;
@@ -456,10 +461,14 @@ dg_status dg_norm_residual(const dg_norm* op, dg_stream stream);
  * x, y, residual [M][K]; router [E][K] in x's type; W_gate, W_up [E][I][K] and
  * W_down [E][K][I] in the format `kind`: DG_LINEAR_F16, DG_LINEAR_BF16, or
  * DG_LINEAR_W4A16 (packed int4 [E][rows][cols / 2], fp16 scales
- * [E][rows][cols / group_size], x and y fp16).  h is kept in fp32.  ids int32 [M][top_k] and weights fp32
- * [M][top_k], both optional, receive the routing in descending order of prob.  Each expert's
- * weights are read once for all of its tokens.  K and I multiples of 8 (fp16,
- * bf16) or of group_size, itself a multiple of 32 (int4); 1 <= E <= 1024,
+ * [E][rows][cols / group_size], x and y fp16).  All sums are fp32.  h_e is held
+ * as the sum of two 16-bit numbers: 22 significant bits (fp16 x; |h_e| below
+ * 2^24, larger ones become infinite) or 16 (bf16 x).  ids int32 [M][top_k] and
+ * weights fp32 [M][top_k], both optional, receive the routing in descending
+ * order of prob.  Each expert's weights are read once for up to eight of its
+ * tokens, mostly for all sixteen.  A token's result does not depend on the order
+ * in which CTAs run.  K and I multiples of 8 (fp16,
+ * bf16) or of group_size, itself a multiple of 32 (int4), up to 65536; 1 <= E <= 1024,
  * 1 <= top_k <= min(E, 16); pointers 16-byte aligned (scales 2, residual 2,
  * ids and weights 4).  y may be residual or x.  ws: dg_moe_workspace_bytes(op)
  * bytes, 16-byte aligned, overwritten; a call that may overlap another needs

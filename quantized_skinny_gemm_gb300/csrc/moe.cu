@@ -34,8 +34,8 @@
 // whose codes belong to group f and zero for the others, so that one
 // instruction sums the groups apart.
 //
-// Measured: 16 tokens, 4096 x 14336 bf16, 2 of 8 experts: 477 us, 5.8 TB/s; one
-// token, fp16 (101 MB): 30 us, 3.4 TB/s, of which the scores and the routing at
+// Measured: 16 tokens, 4096 x 14336 bf16, 2 of 8 experts: 450 us, 6.2 TB/s; one
+// token, fp16 (101 MB): 29 us, 3.4 TB/s, of which the scores and the routing at
 // the head of `up` take 6; int4, one token, 4096 x 14336, 2 of 8: 56 us, 3.5
 // TB/s, bound by unpacking and by the latency of 16 warps' chunks.
 #include <algorithm>
