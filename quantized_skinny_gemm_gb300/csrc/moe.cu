@@ -35,8 +35,8 @@
 // instruction sums the groups apart.
 //
 // Measured: 16 tokens, 4096 x 14336 bf16, 2 of 8 experts: 450 us, 6.2 TB/s; one
-// token, fp16 (101 MB): 29 us, 3.4 TB/s, of which the scores and the routing at
-// the head of `up` take 6; int4, one token, 4096 x 14336, 2 of 8: 56 us, 3.5
+// token, fp16 (101 MB): 29 us, 3.5 TB/s, of which the scores and the routing at
+// the head of `up` take 6; int4, one token, 4096 x 14336, 2 of 8: 57 us, 3.5
 // TB/s, bound by unpacking and by the latency of 16 warps' chunks.
 #include <algorithm>
 
@@ -313,11 +313,20 @@ struct Shape {
     static constexpr int kPitch = kCols * 2;               // bytes of a staged token row
 };
 
-// Streaming loads; the predicated forms give zero where `in` is false.
-__device__ __forceinline__ void ld_weights(uint32_t (&v)[4], const void* p) {
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                 : "l"(p));
+// Streaming loads; the predicated forms give zero where `in` is false.  WIDE asks
+// L2 for the whole 256 bytes: better for long streams (16 tokens, 2.8 GB bf16: 451
+// us, 466 without; 8 tokens int4: 93.0, 94.6), worse for the short ones of one
+// block of tokens at 16 bits (one token, 101 MB: 29.4, 28.6 without).
+template <bool WIDE>
+__device__ __forceinline__ void ld_weights16(uint32_t (&v)[4], const void* p) {
+    if (WIDE)
+        asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "l"(p));
+    else
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "l"(p));
 }
 __device__ __forceinline__ void ld_weights(uint32_t (&v)[2], const void* p) {
     asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "l"(p));
@@ -415,15 +424,17 @@ struct Chunk {
         }
         const size_t at = S::kInt4 ? k0 / 2 : (size_t)k0 * 2;
 #pragma unroll
-        for (int i = 0; i < S::kSteps; ++i) {
-            const bool in = k0 + i * S::kStep + t * S::kLane < Kd;
+        for (int r = 0; r < 2; ++r) {   // a row's 256 bytes one after the other: whole lines
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int i = 0; i < S::kSteps; ++i) {
+                const bool in = k0 + i * S::kStep + t * S::kLane < Kd;
                 const char* w = q.w[r] + at + (S::kInt4 ? i * S::kStep / 2 : i * S::kStep * 2);
-                if (FULL)
-                    ld_weights(v[i][r], w);
-                else
+                if constexpr (!FULL)
                     ld_weights(v[i][r], w, in);
+                else if constexpr (S::kWords == 4)
+                    ld_weights16<S::kInt4 || (NT > 1)>(v[i][r], w);
+                else
+                    ld_weights(v[i][r], w);
             }
         }
         if constexpr (S::kInt4) {
