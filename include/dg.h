@@ -314,8 +314,9 @@ size_t dg_workspace_bytes(const dg_linear* ops, int n_ops);
  * append, attention over the cache, and (sparse decoders) an expert layer.
  * The pages name these steps without formulas (single-request decode over a
  * KV cache and draft / verify tokens: EdgeFM, sections 2.B and 2.C); each
- * declaration states the definition.  All arithmetic is fp32 or wider; each
- * 16-bit output is rounded to nearest even once. */
+ * declaration states the definition.  All arithmetic is fp32 or wider, but for
+ * what a declaration says of its weights or its hidden values; each 16-bit output
+ * is rounded to nearest even once. */
 
 /* A paged key / value cache of `batch` sequences.  Sequence b's position j lies
  * in page block_table[b * table_stride + j / page_size], slot j % page_size;
@@ -391,12 +392,13 @@ dg_status dg_kv_append(const dg_append* op, dg_stream stream);
  * A token that sees nothing (p < 0, no existing page), or whose visible scores
  * are all -infinity, gets out = 0 and lse = -infinity.  Values at positions a
  * token does not see never reach it, whatever they hold (NaN and infinity
- * too); visible ones follow IEEE.  q [batch * q_len][heads][head_dim] with
+ * too); visible ones follow IEEE.  Scores and sums are fp32; e^(z_j) meets v_j as
+ * the sum of two 16-bit numbers, 2^-21 (fp16) or 2^-16 (bf16) of itself off, and in
+ * fp16 up to 2^-32 of the strongest key's.  q [batch * q_len][heads][head_dim] with
  * q_stride elements between tokens, out likewise; lse fp32
  * [batch * q_len][heads].  heads is a multiple of kv_heads, 1 <= q_len <= 16.
- * q, out, k, v 16-byte aligned, strides multiples of 8.  Sums, the running
- * maximum and the joined parts are fp32; the result does not depend on the
- * order in which CTAs run.  ws: dg_attn_workspace_bytes(op) bytes, 16-byte
+ * q, out, k, v 16-byte aligned, strides multiples of 8.  The result does not
+ * depend on the order in which CTAs run.  ws: dg_attn_workspace_bytes(op) bytes, 16-byte
  * aligned, overwritten (nothing needs to be zeroed); a call that may overlap
  * another needs its own. */
 typedef struct {

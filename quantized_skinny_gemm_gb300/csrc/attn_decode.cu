@@ -20,13 +20,15 @@
 //
 // Softmax is one pass: each warp keeps the running maximum m and sum l of its
 // own positions and rescales its output only when m has grown by more than
-// 2^8 since (weights then stay below 256, far inside the 16-bit types' range);
-// scores are turned to units of log2(e) inside the exponent.
+// 2^8 since (weights then stay below 256); scores are turned to units of
+// log2(e) inside the exponent.  A weight meets the values as two 16-bit numbers
+// (split_pair), at half as many matrix instructions again: 0.4 % on the long
+// cache below, 4 to 5 % on the others, 19 % where 64 rows share a key.
 //
-// Measured: 200001 positions of 8 x 128 bf16, 32 heads: 126.6 us, 6.5 TB/s of the
-// copy's 6.8; 16 sequences of up to 8191, 12 heads on 2: 11.1 us; one of 100: 5.4
+// Measured: 200001 positions of 8 x 128 bf16, 32 heads: 127.3 us, 6.4 TB/s of the
+// copy's 6.8; 16 sequences of up to 8191, 12 heads on 2: 11.5 us; one of 100: 5.7
 // us, one launch where the table holds 128 positions at most, else two; 8 tokens
-// of 8 sequences on windows of 4096, 32 heads on 8 of 64: 31 us, bound by the
+// of 8 sequences on windows of 4096, 32 heads on 8 of 64: 33 us, bound by the
 // latency of a few stages per warp and of the join.
 #include <algorithm>
 #include <climits>
@@ -55,6 +57,27 @@ __device__ __forceinline__ float exp2_fast(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
+}
+
+// The matrix instruction takes weights of 16 bits; one would cost 2^-12 (fp16) or
+// 2^-9 (bf16) of a weight, as much as the output's own rounding.  Each weight is
+// therefore the sum of two, hi + lo, 2^-21 (fp16) or 2^-16 (bf16) off.  hi is cut
+// off below the weight, so that lo is above zero too and a value of infinity meets
+// no zero and no minus.  fp16 ends at 2^-24: weights are taken 2^kLift times, up to
+// 2^15, so that what is lost of one lies 2^-32 below the strongest key's.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
+template <bool BF16>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
+    constexpr float kBelow = 1.f - 1.f / 4096;
+    if (BF16) {
+        hi = __byte_perm(__float_as_uint(a * kBelow), __float_as_uint(b * kBelow), 0x7632);
+    } else {
+        constexpr float kStep = 5.9604645e-8f * kBelow;   // just below the smallest fp16 number
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(fmaf(b, kBelow, -kStep)), "f"(fmaf(a, kBelow, -kStep)));
+    }
+    const float2 h = pair_f32<BF16>(hi);
+    lo = pair_16<BF16>(a - h.x, b - h.y);
 }
 
 // The positions some token of sequence b sees: [0, seen_sinks) and [seen_lo,
@@ -97,8 +120,9 @@ __device__ __forceinline__ int quotient(long long a, int b) {
 template <int DP, int RT>
 struct AttnShape {
     // 16-key pieces of a stage: two where they are small, for the bookkeeping of a
-    // stage (64 dims: 31 us on the windows above and 60 on 12 sequences of up to
-    // 84056 positions; stages of 16 keys with 3 CTAs per SM 42 and 85)
+    // stage (64 dims, with weights of one 16-bit number: 31 us on the windows above
+    // and 60 on 12 sequences of up to 84056 positions; stages of 16 keys with 3 CTAs
+    // per SM 42 and 85)
     static constexpr int kSub = DP <= 64 && RT < 4 ? 2 : 1;
     static constexpr int kKeys = 16 * kSub;
     static constexpr int kPitch = DP * 2;                   // bytes; see piece()
@@ -462,7 +486,6 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
             }
 
             // running maximum, weights, rescaling
-            uint32_t pf[RT][S::kSub][4];
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 float nm[2];
@@ -490,16 +513,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float base = m[r][h] == -INFINITY ? 0.f : -m[r][h] * c2;
+                    const float base = m[r][h] == -INFINITY ? 0.f : kLift<BF16> - m[r][h] * c2;
 #pragma unroll
                     for (int j = 0; j < kBlk; ++j) {
                         const float a = exp2_fast(fmaf(s[r][j][2 * h], c2, base));
                         const float c = exp2_fast(fmaf(s[r][j][2 * h + 1], c2, base));
                         l[r][h] += a + c;
-                        // weights meet the values as 16-bit numbers: what the matrix
-                        // instruction takes, 2^-12 (fp16) or 2^-9 (bf16) off (their fp32
-                        // sum is of the weights before that: lse is an fp32 result)
-                        pf[r][j >> 1][2 * (j & 1) + h] = pair_16<BF16>(a, c);
                         s[r][j][2 * h] = a;
                         s[r][j][2 * h + 1] = c;
                     }
@@ -546,17 +565,27 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
             // output += weights x values
             const uint32_t vl = va + S::piece((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
 #pragma unroll
-            for (int u = 0; u < S::kSub; ++u)
+            for (int u = 0; u < S::kSub; ++u) {
+                uint32_t hi[RT][4], lo[RT][4];
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        split_pair<BF16>(s[r][2 * u + (x >> 1)][2 * (x & 1)], s[r][2 * u + (x >> 1)][2 * (x & 1) + 1],
+                                         hi[r][x], lo[r][x]);
 #pragma unroll
                 for (int d = 0; d < DP / 16; ++d) {
                     uint32_t vf[4];
                     ldsm4_t(vf, on(vl, d) + u * 16 * S::kPitch);
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
-                        mma16816<BF16>(o[r][2 * d], pf[r][u], vf[0], vf[1]);
-                        mma16816<BF16>(o[r][2 * d + 1], pf[r][u], vf[2], vf[3]);
+                        mma16816<BF16>(o[r][2 * d], hi[r], vf[0], vf[1]);
+                        mma16816<BF16>(o[r][2 * d + 1], hi[r], vf[2], vf[3]);
+                        mma16816<BF16>(o[r][2 * d], lo[r], vf[0], vf[1]);
+                        mma16816<BF16>(o[r][2 * d + 1], lo[r], vf[2], vf[3]);
                     }
                 }
+            }
         }
         cp_wait<0>();
         __syncwarp();
@@ -623,7 +652,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(op.out) + t * op.out_stride +
                                           (long long)h * D + d) = pack8<BF16>(v);
                 if (d == 0 && op.lse)
-                    op.lse[t * op.heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                    op.lse[t * op.heads + h] = sum == 0.f ? -INFINITY : (top + (log2f(sum) - kLift<BF16>)) * kLn2;
             } else {
                 if (d == 0) {
                     part[r] = top;
@@ -718,7 +747,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
             for (int x = 0; x < kPairs; ++x)
                 if (x * 64 + lane * 2 < D) out[x * 32 + lane] = pair_16<BF16>(v[x].x * inv, v[x].y * inv);
             if (lane == 0 && op.lse)
-                op.lse[t * op.heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                op.lse[t * op.heads + h] = sum == 0.f ? -INFINITY : (top + (log2f(sum) - kLift<BF16>)) * kLn2;
         }
         if (!few) __syncthreads();
     }

@@ -1,0 +1,118 @@
+"""Attention to the precision that the header states: fp32 scores and sums, weights
+2^-21 (fp16) or 2^-16 (bf16) off, one rounding into the output; infinities and NaN
+that a token does see follow IEEE."""
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as ref
+import quantized_skinny_gemm_gb300 as dg
+from gpu_util import DEV, need_gpu, sync
+
+pytestmark = pytest.mark.gpu
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+WEIGHT = {"f16": 2.0 ** -21, "bf16": 2.0 ** -16}   # of a weight, as the sum of two 16-bit numbers
+LEAST = {"f16": 2.0 ** -32, "bf16": 0.0}           # what may be lost of one, next to the strongest
+
+
+def _attention(q, k, v, lens, ftype, q_len=1, page=16, window=0, sinks=0):
+    """q [T][H][D]; k, v [n][G][D]: every sequence reads the same n positions.
+    Returns out and lse."""
+    n, G, D = k.shape
+    pages = -(-n // page)
+    pool = torch.zeros(2, pages * page, G, D, dtype=q.dtype)
+    pool[0, :n], pool[1, :n] = k, v
+    pool = pool.view(2, pages, page, G, D).to(DEV)
+    table = torch.arange(pages, dtype=torch.int32).repeat(len(lens), 1).to(DEV)
+    ld = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    qd = q.to(DEV)
+    out = torch.full_like(qd, float("nan"))
+    lse = torch.full(q.shape[:2], float("nan"), dtype=torch.float32, device=DEV)
+    op = dg.attention(dg.paged_kv(pool[0], pool[1], table, ld), qd, out, lse=lse, q_len=q_len, window=window,
+                      sinks=sinks)
+    ws = torch.full((dg.attn_workspace_bytes(op),), 255, dtype=torch.uint8, device=DEV)
+    dg.attn_decode(op, ws)
+    sync()
+    return ref.f64(out), ref.f64(lse)
+
+
+def _exact(q, k, v, keep, ftype):
+    """One row q [D] over the positions `keep` of k, v [n][D], in 64 bits: out, lse
+    and their bounds."""
+    q, k, v = ref.f64(q), ref.f64(k)[keep], ref.f64(v)[keep]
+    D, n, scale = q.size, len(keep), q.size ** -0.5
+    z = scale * (k @ q)
+    m = z.max()
+    e = np.exp(z - m)
+    l = e.sum()
+    with np.errstate(invalid="ignore"):
+        out = e @ v / l
+        A = e @ np.abs(v) / l
+        lost = LEAST[ftype] * np.abs(v).sum(0) / l
+    lse = m + np.log(l)
+    ez = ((D + 2) * ref.U32 * scale * (np.abs(k) @ np.abs(q)) + ref.U32 * np.abs(z)).max()
+    rel = ez + ref.FN + (n + 2) * ref.U32
+    bound = A * (2 * rel + WEIGHT[ftype]) + lost + ref.U16[ftype] * np.abs(out) + ref.TINY[ftype]
+    return out, lse, bound, rel + ref.FN + 2 * ref.U32 * (abs(m) + abs(lse))
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16"])
+@pytest.mark.parametrize("heads,kv_heads,dim,n,q_len", [(4, 2, 64, 40, 1), (32, 2, 64, 600, 4), (8, 2, 128, 333, 1),
+                                                        (40, 2, 128, 90, 2), (3, 1, 192, 257, 1), (5, 1, 256, 64, 2)])
+def test_weights_keep_more_than_one_rounding(ftype, heads, kv_heads, dim, n, q_len):
+    """Values in pairs of opposite sign under nearly equal weights: the output is a
+    small difference of large sums, where rounded weights would show."""
+    need_gpu()
+    g = torch.Generator().manual_seed(dim + n)
+    k = torch.randn(n, kv_heads, dim, generator=g).to(DT[ftype])
+    v = torch.randn(n, kv_heads, dim, generator=g).to(DT[ftype])
+    v[1::2] = -v[0:n - 1:2]
+    q = (torch.randn(q_len, heads, dim, generator=g) * 0.03).to(DT[ftype])
+    out, lse = _attention(q, k, v, [n], ftype, q_len)
+    for t in range(q_len):
+        for h in range(heads):
+            kv = h // (heads // kv_heads)
+            ro, rl, bo, bl = _exact(q[t, h], k[:, kv], v[:, kv], np.arange(n - q_len + t + 1), ftype)
+            ref.check(out[t, h], ro, bo, "out of token %d, head %d" % (t, h))
+            ref.check(lse[t, h], rl, bl, "lse of token %d, head %d" % (t, h))
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16"])
+def test_many_weak_keys_beside_a_strong_one(ftype):
+    """2048 keys of weight e^-17 beside one strong key whose value is zero: their sum
+    is the output.  64 sequences of 8 heads, so that one warp reads hundreds of them."""
+    need_gpu()
+    n, G, D, B = 2049, 8, 64, 64
+    k, v = torch.zeros(n, G, D, dtype=DT[ftype]), torch.full((n, G, D), 30000.0).to(DT[ftype])
+    k[5, :, 0], v[5] = 17.0 * 8, 0.0                     # 17 / scale / q
+    q = torch.zeros(B, G, D, dtype=DT[ftype])
+    q[:, :, 0] = 1.0
+    out, lse = _attention(q, k, v, [n] * B, ftype)
+    ro, rl, bo, bl = _exact(q[0, 0], k[:, 0], v[:, 0], np.arange(n), ftype)
+    ref.check(out, np.broadcast_to(ro, out.shape), bo, "out")
+    ref.check(lse, np.broadcast_to(rl, lse.shape), bl, "lse")
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16"])
+@pytest.mark.parametrize("q_len,window", [(1, 0), (3, 0), (2, 50)])
+def test_infinities_and_nan_that_a_token_sees(ftype, q_len, window):
+    """One visible value of each kind, in dims of its own: the output is that
+    infinity or NaN in the dim and unharmed beside it."""
+    need_gpu()
+    n, D, inf = 150, 64, float("inf")
+    g = torch.Generator().manual_seed(7)
+    k, v = (torch.randn(n, 1, D, generator=g).to(DT[ftype]) for _ in range(2))
+    q = (torch.randn(q_len, 4, D, generator=g) * 2).to(DT[ftype])
+    for j, d, x in ((120, 0, inf), (121, 1, -inf), (122, 2, float("nan")), (123, 3, inf), (n - 1, 3, inf),
+                    (130, 4, -inf), (131, 4, inf), (n - q_len, 5, -inf), (n - 1, 6, inf), (3, 7, inf)):
+        v[j, 0, d] = x
+    out, lse = _attention(q, k, v, [n], ftype, q_len, window=window)
+    for t in range(q_len):
+        p = n - q_len + t
+        keep = np.arange(max(0, p - window + 1) if window else 0, p + 1)
+        for h in range(4):
+            with np.errstate(invalid="ignore"):
+                ro, rl, bo, bl = _exact(q[t, h], k[:, 0], v[:, 0], keep, ftype)
+            assert np.isinf(ro).any() and np.isnan(ro).any() and np.isfinite(ro).any()
+            ref.check(out[t, h], ro, bo, "out of token %d, head %d" % (t, h))
+            ref.check(lse[t, h], rl, bl, "lse of token %d, head %d" % (t, h))
