@@ -345,7 +345,7 @@ typedef struct {
     int64_t token_stride;
     int64_t head_stride;
     const int32_t* block_table;
-    int64_t table_stride;
+    int64_t table_stride;    /* at least max_pages, or batch 1 */
     const int32_t* seq_lens; /* [batch] */
 } dg_paged_kv;
 

@@ -352,7 +352,8 @@ def paged_kv(k_cache, v_cache, block_table, seq_lens):
     """A paged cache: k_cache and v_cache [pages][page_size][kv_heads][head_dim]
     (any strides with the last dimension contiguous and both alike, so a
     [pages][kv_heads][page_size][head_dim] cache is passed transposed),
-    block_table int32 [batch][max_pages], seq_lens int32 [batch]."""
+    block_table int32 [batch][max_pages] with rows at least max_pages apart (no
+    expanded tables), seq_lens int32 [batch]."""
     import torch
     where = "paged_kv"
     kind = _ftype(k_cache, where)
@@ -364,7 +365,8 @@ def paged_kv(k_cache, v_cache, block_table, seq_lens):
     _fits(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and
           0 < seq_lens.numel() == block_table.shape[0], where)
     pages, page_size, heads, dim = k_cache.shape
-    table_stride = max(block_table.stride(0), block_table.shape[1])
+    table_stride = block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+    _fits(table_stride >= block_table.shape[1], where)
     return PagedKV(kind, block_table.shape[0], heads, dim, page_size, pages,
                    block_table.shape[1], 0, _ptr(k_cache), _ptr(v_cache), k_cache.stride(0),
                    k_cache.stride(1), k_cache.stride(2), _ptr(block_table), table_stride,

@@ -181,3 +181,18 @@ def test_builders_refuse_tensors_that_do_not_fit():
         dg.norm(h(2, 8).float(), h(2, 8), h(2, 8), w_pre=h(8))
     with pytest.raises(dg.DGError):
         dg.moe(dg.LINEAR_F16, h(1, 64), h(1, 64), h(4, 64), h(4, 32, 64), h(4, 32, 64), h(4, 64, 40), 2)
+
+
+def test_a_page_table_is_described_with_its_own_stride():
+    """Rows that overlap are refused: sequences would read past the table."""
+    k = torch.zeros(4, 16, 2, 64, dtype=torch.float16)
+    ids = torch.zeros(64, dtype=torch.int32)
+    lens = torch.zeros(2, dtype=torch.int32)
+    for rows, stride in ((2, 3), (2, 5), (1, 0), (1, 1)):
+        kv = dg.paged_kv(k, k, ids.as_strided((rows, 3), (stride, 1)), lens[:rows])
+        assert kv.max_pages == 3 and kv.table_stride == (stride if rows > 1 else 3)
+    assert dg.paged_kv(k, k, ids.as_strided((2, 1), (4, 9)), lens).table_stride == 4
+    for table in (ids[:3].expand(2, 3), ids.as_strided((2, 3), (1, 1)), ids.as_strided((2, 3), (2, 1)),
+                  ids[:1].expand(2, 1)):
+        with pytest.raises(dg.DGError):
+            dg.paged_kv(k, k, table, lens)
