@@ -392,7 +392,8 @@ dg_status dg_kv_append(const dg_append* op, dg_stream stream);
  * A token that sees nothing (p < 0, no existing page), or whose visible scores
  * are all -infinity, gets out = 0 and lse = -infinity.  Values at positions a
  * token does not see never reach it, whatever they hold (NaN and infinity
- * too); visible ones follow IEEE.  Scores and sums are fp32; e^(z_j) meets v_j as
+ * too); visible ones follow IEEE.  scale is any number with a finite
+ * scale * log2(e), zero and negative ones too.  Scores and sums are fp32; e^(z_j) meets v_j as
  * the sum of two 16-bit numbers, 2^-21 (fp16) or 2^-16 (bf16) of itself off, and in
  * fp16 up to 2^-32 of the strongest key's.  q [batch * q_len][heads][head_dim] with
  * q_stride elements between tokens, out likewise; lse fp32

@@ -31,6 +31,7 @@
 // of 8 sequences on windows of 4096, 32 heads on 8 of 64: 33 us, bound by the
 // latency of a few stages per warp and of the join.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 
 #include "mma16.cuh"
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
     // e^(scale q.k) = 2^(c2 (q'.k)) with c2 > 0: the sign, and a scale of zero, go into q'
     const float c2 = op.scale == 0.f ? 1.f : fabsf(op.scale) * kLog2e;
     const uint32_t q_flip = op.scale < 0.f ? 0x80008000u : 0u, q_keep = op.scale == 0.f ? 0u : 0xFFFFFFFFu;
-    const float grow = 8.f / c2;
+    const float grow = fminf(8.f / c2, FLT_MAX);   // finite: the first maximum is always taken
     const int g = lane >> 2, t4 = lane & 3;
 
     // ---- the range's part of one unit after another ---------------------------------------

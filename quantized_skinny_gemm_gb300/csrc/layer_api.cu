@@ -56,7 +56,8 @@ static dg_status check_attn(const dg_attn& op) {
     const dg_status st = check_kv(op.kv, op.q_len, op.heads);
     if (st != DG_OK) return st;
     if (op.reserved || op.heads < 1 || !op.q || !op.out) return DG_ERR_INVALID_ARG;
-    if (op.heads % op.kv.kv_heads || op.window < 0 || op.sinks < 0 || !std::isfinite(op.scale))
+    // scores are held in units of log2(e)
+    if (op.heads % op.kv.kv_heads || op.window < 0 || op.sinks < 0 || !std::isfinite(op.scale * 1.4426950408889634f))
         return DG_ERR_INVALID_ARG;
     if ((int64_t)op.kv.batch * op.q_len * op.heads > 0x7fffffff) return DG_ERR_UNSUPPORTED;
     const int64_t row = (int64_t)op.heads * op.kv.head_dim;

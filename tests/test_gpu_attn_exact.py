@@ -15,7 +15,7 @@ WEIGHT = {"f16": 2.0 ** -21, "bf16": 2.0 ** -16}   # of a weight, as the sum of 
 LEAST = {"f16": 2.0 ** -32, "bf16": 0.0}           # what may be lost of one, next to the strongest
 
 
-def _attention(q, k, v, lens, ftype, q_len=1, page=16, window=0, sinks=0):
+def _attention(q, k, v, lens, ftype, q_len=1, page=16, window=0, sinks=0, scale=None):
     """q [T][H][D]; k, v [n][G][D]: every sequence reads the same n positions.
     Returns out and lse."""
     n, G, D = k.shape
@@ -29,18 +29,18 @@ def _attention(q, k, v, lens, ftype, q_len=1, page=16, window=0, sinks=0):
     out = torch.full_like(qd, float("nan"))
     lse = torch.full(q.shape[:2], float("nan"), dtype=torch.float32, device=DEV)
     op = dg.attention(dg.paged_kv(pool[0], pool[1], table, ld), qd, out, lse=lse, q_len=q_len, window=window,
-                      sinks=sinks)
+                      sinks=sinks, scale=scale)
     ws = torch.full((dg.attn_workspace_bytes(op),), 255, dtype=torch.uint8, device=DEV)
     dg.attn_decode(op, ws)
     sync()
     return ref.f64(out), ref.f64(lse)
 
 
-def _exact(q, k, v, keep, ftype):
+def _exact(q, k, v, keep, ftype, scale=None):
     """One row q [D] over the positions `keep` of k, v [n][D], in 64 bits: out, lse
     and their bounds."""
     q, k, v = ref.f64(q), ref.f64(k)[keep], ref.f64(v)[keep]
-    D, n, scale = q.size, len(keep), q.size ** -0.5
+    D, n, scale = q.size, len(keep), q.size ** -0.5 if scale is None else float(np.float32(scale))
     z = scale * (k @ q)
     m = z.max()
     e = np.exp(z - m)
@@ -50,7 +50,7 @@ def _exact(q, k, v, keep, ftype):
         A = e @ np.abs(v) / l
         lost = LEAST[ftype] * np.abs(v).sum(0) / l
     lse = m + np.log(l)
-    ez = ((D + 2) * ref.U32 * scale * (np.abs(k) @ np.abs(q)) + ref.U32 * np.abs(z)).max()
+    ez = ((D + 2) * ref.U32 * abs(scale) * (np.abs(k) @ np.abs(q)) + ref.U32 * np.abs(z)).max()
     rel = ez + ref.FN + (n + 2) * ref.U32
     bound = A * (2 * rel + WEIGHT[ftype]) + lost + ref.U16[ftype] * np.abs(out) + ref.TINY[ftype]
     return out, lse, bound, rel + ref.FN + 2 * ref.U32 * (abs(m) + abs(lse))
@@ -116,3 +116,18 @@ def test_infinities_and_nan_that_a_token_sees(ftype, q_len, window):
             assert np.isinf(ro).any() and np.isnan(ro).any() and np.isfinite(ro).any()
             ref.check(out[t, h], ro, bo, "out of token %d, head %d" % (t, h))
             ref.check(lse[t, h], rl, bl, "lse of token %d, head %d" % (t, h))
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16"])
+@pytest.mark.parametrize("scale", [1e-45, 3e-39, -1e-38, 1.5e-38, 1e-30])
+def test_tiny_scales_weigh_all_positions_alike(ftype, scale):
+    need_gpu()
+    n, D = 300, 64
+    g = torch.Generator().manual_seed(8)
+    k, v = (torch.randn(n, 1, D, generator=g).to(DT[ftype]) for _ in range(2))
+    q = torch.randn(1, 2, D, generator=g).to(DT[ftype])
+    out, lse = _attention(q, k, v, [n], ftype, scale=scale)
+    for h in range(2):
+        ro, rl, bo, bl = _exact(q[0, h], k[:, 0], v[:, 0], np.arange(n), ftype, scale)
+        ref.check(out[0, h], ro, bo, "out of head %d" % h)
+        ref.check(lse[0, h], rl, bl, "lse of head %d" % h)

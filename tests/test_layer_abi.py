@@ -196,3 +196,12 @@ def test_a_page_table_is_described_with_its_own_stride():
                   ids[:1].expand(2, 1)):
         with pytest.raises(dg.DGError):
             dg.paged_kv(k, k, table, lens)
+
+
+def test_scales_that_overflow_are_refused(lib):
+    """Scores are held in units of log2(e)."""
+    f = lambda scale: lib.dg_attn_decode(ctypes.byref(_attn(scale=scale)), A, 0, None)
+    for scale in (2.5e38, -3.4e38):
+        assert f(scale) == INVALID
+    for scale in (2.3e38, -2.3e38, 0.0, 1e-45, -1e-39):
+        assert f(scale) == WORKSPACE      # taken, and refused for its workspace
