@@ -20,8 +20,8 @@
 //
 // Softmax is one pass: each warp keeps the running maximum m and sum l of its
 // own positions and rescales its output only when m has grown by more than
-// 2^8 since (weights then stay below 256); scores are turned to units of
-// log2(e) inside the exponent.  A weight meets the values as two 16-bit numbers
+// 2^8 since (weights then stay below 256); differences of scores are turned to
+// units of log2(e) inside the exponent.  A weight meets the values as two 16-bit numbers
 // (split_pair), at half as many matrix instructions again: 0.4 % on the long
 // cache below, 4 to 5 % on the others, 19 % where 64 rows share a key.
 //
@@ -71,14 +71,21 @@ constexpr float kLift = BF16 ? 0.f : 7.f;
 template <bool BF16>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
     constexpr float kBelow = 1.f - 1.f / 4096;
-    if (BF16) {
-        hi = __byte_perm(__float_as_uint(a * kBelow), __float_as_uint(b * kBelow), 0x7632);
-    } else {
-        constexpr float kStep = 5.9604645e-8f * kBelow;   // just below the smallest fp16 number
-        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(fmaf(b, kBelow, -kStep)), "f"(fmaf(a, kBelow, -kStep)));
-    }
-    const float2 h = pair_f32<BF16>(hi);
-    lo = pair_16<BF16>(a - h.x, b - h.y);
+    constexpr float kStep = BF16 ? 0.f : 5.9604645e-8f * kBelow;   // just below the smallest fp16 number
+    const float2 w = make_float2(a, b), c = fma2(w, make_float2(kBelow, kBelow), make_float2(-kStep, -kStep));
+    if (BF16)
+        hi = __byte_perm(__float_as_uint(c.x), __float_as_uint(c.y), 0x7632);
+    else
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(c.y), "f"(c.x));
+    const float2 l = fma2(pair_f32<BF16>(hi), make_float2(-1.f, -1.f), w);
+    lo = pair_16<BF16>(l.x, l.y);
+}
+
+// log sum e^z from the greatest score in units of log2(e) and the sum of the
+// weights 2^(kLift + ..).
+template <bool BF16>
+__device__ __forceinline__ float lse_of(float top, float sum) {
+    return sum == 0.f ? -INFINITY : (top + (log2f(sum) - kLift<BF16>)) * kLn2;
 }
 
 // The positions some token of sequence b sees: [0, seen_sinks) and [seen_lo,
@@ -228,7 +235,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
     }
     if (begin >= end) return;
 
-    // e^(scale q.k) = 2^(c2 (q'.k)) with c2 > 0: the sign, and a scale of zero, go into q'
+    // e^(scale q.k) = 2^(c2 (q'.k)) with c2 > 0: the sign, and a scale of zero, go into
+    // q'.  A weight's exponent is c2 times the difference to the maximum, not the
+    // difference of two products: past scores of 2^24 those are rounded by whole
+    // numbers, and a strongest key of weight 2^64 overflows.  (Parts are joined by
+    // products: there the greatest one's weight is 1 whatever the rounding.)
     const float c2 = op.scale == 0.f ? 1.f : fabsf(op.scale) * kLog2e;
     const uint32_t q_flip = op.scale < 0.f ? 0x80008000u : 0u, q_keep = op.scale == 0.f ? 0u : 0xFFFFFFFFu;
     const float grow = fminf(8.f / c2, FLT_MAX);   // finite: the first maximum is always taken
@@ -514,11 +525,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float base = m[r][h] == -INFINITY ? 0.f : kLift<BF16> - m[r][h] * c2;
+                    const float shift = m[r][h] == -INFINITY ? 0.f : -m[r][h];
 #pragma unroll
                     for (int j = 0; j < kBlk; ++j) {
-                        const float a = exp2_fast(fmaf(s[r][j][2 * h], c2, base));
-                        const float c = exp2_fast(fmaf(s[r][j][2 * h + 1], c2, base));
+                        const float2 d = fma2(make_float2(s[r][j][2 * h], s[r][j][2 * h + 1]), make_float2(1.f, 1.f),
+                                              make_float2(shift, shift));
+                        const float2 z = fma2(d, make_float2(c2, c2), make_float2(kLift<BF16>, kLift<BF16>));
+                        const float a = exp2_fast(z.x), c = exp2_fast(z.y);
                         l[r][h] += a + c;
                         s[r][j][2 * h] = a;
                         s[r][j][2 * h + 1] = c;
@@ -653,7 +666,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(op.out) + t * op.out_stride +
                                           (long long)h * D + d) = pack8<BF16>(v);
                 if (d == 0 && op.lse)
-                    op.lse[t * op.heads + h] = sum == 0.f ? -INFINITY : (top + (log2f(sum) - kLift<BF16>)) * kLn2;
+                    op.lse[t * op.heads + h] = lse_of<BF16>(top, sum);
             } else {
                 if (d == 0) {
                     part[r] = top;
@@ -748,7 +761,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
             for (int x = 0; x < kPairs; ++x)
                 if (x * 64 + lane * 2 < D) out[x * 32 + lane] = pair_16<BF16>(v[x].x * inv, v[x].y * inv);
             if (lane == 0 && op.lse)
-                op.lse[t * op.heads + h] = sum == 0.f ? -INFINITY : (top + (log2f(sum) - kLift<BF16>)) * kLn2;
+                op.lse[t * op.heads + h] = lse_of<BF16>(top, sum);
         }
         if (!few) __syncthreads();
     }

@@ -131,3 +131,25 @@ def test_tiny_scales_weigh_all_positions_alike(ftype, scale):
         ro, rl, bo, bl = _exact(q[0, h], k[:, 0], v[:, 0], np.arange(n), ftype, scale)
         ref.check(out[0, h], ro, bo, "out of head %d" % h)
         ref.check(lse[0, h], rl, bl, "lse of head %d" % h)
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16"])
+@pytest.mark.parametrize("n,scale,large", [(300, -1e30, 1.0), (300, 1e10, 1.0), (9000, 1e20, 1.0), (300, None, 3000.0),
+                                           (9000, None, 60000.0)])
+def test_large_scores_leave_the_strongest_position(ftype, n, scale, large):
+    """Scores far past 2^24, where fp32 holds them to whole numbers and worse, but the
+    strongest lies further from the rest than that."""
+    need_gpu()
+    D = 64
+    g = torch.Generator().manual_seed(8)
+    k, v = (torch.randn(n, 1, D, generator=g).to(DT[ftype]) for _ in range(2))
+    q = (torch.randn(1, 2, D, generator=g) * large).clamp(-60000, 60000).to(DT[ftype])
+    k = (k * large).clamp(-60000, 60000).to(DT[ftype])
+    out, lse = _attention(q, k, v, [n], ftype, scale=scale)
+    scale = D ** -0.5 if scale is None else float(np.float32(scale))
+    for h in range(2):
+        z = scale * (ref.f64(k[:, 0]) @ ref.f64(q[0, h]))
+        err = (D + 3) * ref.U32 * abs(scale) * (np.abs(ref.f64(k[:, 0])) @ np.abs(ref.f64(q[0, h]))).max()
+        assert np.sort(z)[-2] < z.max() - 2 * err - 200      # the others weigh nothing
+        assert np.array_equal(out[0, h], ref.f64(v[z.argmax(), 0]))
+        assert abs(lse[0, h] - z.max()) <= err + 4 * ref.U32 * abs(z.max())
