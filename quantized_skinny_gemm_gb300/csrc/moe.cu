@@ -687,8 +687,9 @@ __global__ void __launch_bounds__(kMoeWarps * 32, moe_warps(KIND, NT) / kMoeWarp
                           (kInt4 ? int4_place(r) : r);
             const float s = BF ? v : v * 0.00390625f;
             const uint16_t hi = elem_16<BF>(s);
+            const float rest = s - elem_f32<BF>(hi);   // not finite beside a hi that is not
             h[0] = hi;
-            h[op.I] = elem_16<BF>((s - elem_f32<BF>(hi)) * (BF ? 1.f : 2048.f));
+            h[op.I] = elem_16<BF>(fabsf(rest) < INFINITY ? rest * (BF ? 1.f : 2048.f) : 0.f);
         }
         turn ^= 1;
     }
