@@ -465,8 +465,9 @@ dg_status dg_norm_residual(const dg_norm* op, dg_stream stream);
  * W_down [E][K][I] in the format `kind`: DG_LINEAR_F16, DG_LINEAR_BF16, or
  * DG_LINEAR_W4A16 (packed int4 [E][rows][cols / 2], fp16 scales
  * [E][rows][cols / group_size], x and y fp16).  All sums are fp32.  h_e is held
- * as the sum of two 16-bit numbers: 22 significant bits (fp16 x; |h_e| from about
- * 2^24 on becomes infinite) or 16 (bf16 x).  ids int32 [M][top_k] and
+ * as the sum of two 16-bit numbers: 22 significant bits from |h_e| = 2^-6 up and
+ * steps of 2^-27 below (fp16 x, int4; from about 2^24 on it becomes infinite), or
+ * 16 significant bits (bf16 x).  ids int32 [M][top_k] and
  * weights fp32 [M][top_k], both optional, receive the routing in descending
  * order of prob.  Each expert's weights are read once for up to eight of its
  * tokens, mostly for all sixteen.  A token's result does not depend on the order

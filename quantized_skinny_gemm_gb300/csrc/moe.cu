@@ -26,8 +26,9 @@
 //
 // h goes from one to the other as two 16-bit values, hi + lo, that are two
 // columns of the matrix instruction: fp16 hi = h / 256 and lo = the rest x 2048
-// (22 bits, |h| up to 2^24), bf16 hi and lo (16 bits); the products keep fp32
-// sums.  int4 codes become fp16 by bit operations (exact).  A group of 32
+// (22 bits from 2^-6 to 2^24; below, where hi is subnormal, steps of 2^-27, an
+// eighth of an fp16 output's finest), bf16 hi and lo (16 bits); the products keep
+// fp32 sums.  int4 codes become fp16 by bit operations (exact).  A group of 32
 // codes must be summed on its own before its scale, but a quad's lanes hold
 // parts of several groups (PH = 2 of 8-byte pieces, or 4 of 16-byte ones): each
 // token gets PH columns, column f carrying the token's values for the lanes

@@ -109,3 +109,32 @@ def test_a_nan_hidden_value_is_its_tokens_alone(fmt):
     y = _run(fmt, *args)
     assert np.isnan(y[2]).all()
     assert np.array_equal(y[[0, 1, 3]], calm[[0, 1, 3]])
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 4, 12])
+@pytest.mark.parametrize("fmt", ["f16", "w4"])
+@pytest.mark.parametrize("size", [2.0 ** -6, 2.0 ** -10, 2.0 ** -14, 2.0 ** -18])
+def test_small_hidden_values_keep_the_stated_steps(fmt, tokens, size):
+    """Gate and up of `size` and large down weights: h is held to 22 bits, or to steps
+    of 2^-27."""
+    need_gpu()
+    K, I = 128, 160
+    g = torch.Generator().manual_seed(73)
+    x = torch.randn(tokens, K, generator=g).half()
+    if fmt == "w4":
+        gate, up, down = (torch.randint(-7, 8, (1, r, c), generator=g, dtype=torch.int8)
+                          for r, c in ((I, K), (I, K), (K, I)))
+        scales = tuple(float(np.float16(s)) for s in (0.25, size * K ** -0.5 / 4, 16.0))
+        real = [q[0].double().numpy() * s for q, s in zip((gate, up, down), scales)]
+    else:
+        gate, up, down = ((torch.randn(1, r, c, generator=g) * s).half()
+                          for r, c, s in ((I, K, 1.0), (I, K, size * K ** -0.5), (K, I, 64.0)))
+        scales, real = None, [ref.f64(w[0]) for w in (gate, up, down)]
+    y = _run(fmt, x, torch.zeros(1, K).half(), gate, up, down, scales)
+    for m in range(tokens):
+        h, eh = _h(ref.f64(x[m]), real[0], real[1])
+        A = np.abs(real[2]) @ np.abs(h)
+        ry = real[2] @ h
+        bound = (np.abs(real[2]) @ (eh + 2.0 ** -22 * np.abs(h) + 2.0 ** -28) + (I + 20) * ref.U32 * A
+                 + ref.U16["f16"] * np.abs(ry) + ref.TINY["f16"])
+        ref.check(y[m], ry, bound, "token %d" % m)
