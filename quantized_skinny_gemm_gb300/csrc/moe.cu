@@ -733,7 +733,9 @@ __device__ __forceinline__ void down_expert(const MoeParams& p, const Lists& L, 
     for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
     for (; k < n; k += warps) C::add(p, src, xr, token, xs, R, k * S::kCols, op.I, acc);
     k -= n;
-    // token rows 2 i and 2 i + 1 are hi and lo of the expert's token i
+    // token rows 2 i and 2 i + 1 are hi and lo of the expert's token i.  In the expert
+    // before, another lane may have held this token: its sums must have arrived.
+    __syncwarp();
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll

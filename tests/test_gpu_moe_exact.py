@@ -7,6 +7,7 @@ import torch
 import layer_ref as ref
 import quantized_skinny_gemm_gb300 as dg
 from gpu_util import DEV, need_gpu, sync
+from test_gpu_moe import _case, _check
 
 pytestmark = pytest.mark.gpu
 KIND = {"f16": dg.LINEAR_F16, "bf16": dg.LINEAR_BF16, "w4": dg.LINEAR_W4A16}
@@ -138,3 +139,20 @@ def test_small_hidden_values_keep_the_stated_steps(fmt, tokens, size):
         bound = (np.abs(real[2]) @ (eh + 2.0 ** -22 * np.abs(h) + 2.0 ** -28) + (I + 20) * ref.U32 * A
                  + ref.U16["f16"] * np.abs(ry) + ref.TINY["f16"])
         ref.check(y[m], ry, bound, "token %d" % m)
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16", "w4"])
+@pytest.mark.parametrize("M,top_k,E", [(8, 1, 8), (8, 3, 5), (16, 4, 7), (2, 2, 16)])
+def test_a_token_changes_its_place_from_expert_to_expert(fmt, M, top_k, E):
+    """Each expert's list of tokens differs, so that the sums of one token come from
+    other lanes of a warp expert by expert; short rows, so that a warp has the chunks
+    of many experts.  The same bits on every call."""
+    need_gpu()
+    t = _case(fmt, M, 512, 32, E, 74)
+    first, ids, _ = _check(t, fmt, top_k, residual=True, what="first")
+    lists = [np.argwhere((ids.cpu().numpy() == e).any(1))[:, 0].tolist() for e in range(E)]
+    places = {m: {held.index(m) for held in lists if m in held} for m in range(M)}
+    assert top_k == 1 or M == 2 or any(len(p) > 1 for p in places.values())
+    for _ in range(3):
+        again, _, _ = _check(t, fmt, top_k, residual=True, what="again")
+        assert torch.equal(again, first)
