@@ -100,7 +100,7 @@ struct Span {
     __device__ __forceinline__ bool seen(int j) const { return j >= seen_lo || j < seen_sinks; }
 };
 __device__ __forceinline__ Span span_of(const dg_attn& op, int b) {
-    const int len = max(0, __ldg(op.kv.seq_lens + b));
+    const int len = max(0, op.kv.seq_lens[b]);   // a step's own writes: no read-only loads
     const long long cap = (long long)op.kv.max_pages * op.kv.page_size;
     Span s;
     s.first = len - op.q_len;

@@ -71,12 +71,14 @@ __device__ __forceinline__ int operator/(int j, FastDiv f) {
     return f.mul ? (int)(__umulhi((uint32_t)j, f.mul) >> f.shift) : j;
 }
 
-// The page of position j >= 0 of sequence b and its slot there; page -1: none.
+// The page of position j >= 0 of sequence b and its slot there; page -1: none.  The
+// table may be the work of the kernel before, which ran while this one had already
+// started: no read-only load.
 __device__ __forceinline__ int page_slot(const dg_paged_kv& kv, FastDiv page_size, int b, int j, int& slot) {
     const int at = j / page_size;
     slot = j - at * kv.page_size;
     if (at >= kv.max_pages) return -1;
-    const int page = __ldg(kv.block_table + (long long)b * kv.table_stride + at);
+    const int page = kv.block_table[(long long)b * kv.table_stride + at];
     return page >= 0 && page < kv.num_pages ? page : -1;
 }
 

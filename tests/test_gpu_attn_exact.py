@@ -153,3 +153,58 @@ def test_large_scores_leave_the_strongest_position(ftype, n, scale, large):
         assert np.sort(z)[-2] < z.max() - 2 * err - 200      # the others weigh nothing
         assert np.array_equal(out[0, h], ref.f64(v[z.argmax(), 0]))
         assert abs(lse[0, h] - z.max()) <= err + 4 * ref.U32 * abs(z.max())
+
+
+def test_lengths_and_tables_that_the_kernel_before_writes():
+    """The length is a greedy token and the page table an expert layer's choice, each
+    written by the library's own kernel right before the append and the attention, which
+    start while it still runs: 64 different ones in a row, then compared."""
+    need_gpu()
+    g = torch.Generator().manual_seed(11)
+    steps, pages, page, G, D, K = 64, 12, 16, 2, 64, 64
+    f16 = lambda *s: torch.randn(*s, generator=g).half()
+    vocab = page * 8
+    lengths = 1 + torch.randperm(vocab - 1, generator=g)[:steps]                     # 1 .. 127
+    order = torch.stack([torch.randperm(pages, generator=g)[:8] for _ in range(steps)])
+    code = torch.linalg.qr(torch.randn(vocab, vocab, generator=g, dtype=torch.float64))[0]
+    head = code.half()                                                               # row j answers to column j
+    xs = head[lengths]
+    mark = torch.zeros(steps, K)                                                     # x picks its experts in order
+    mark.scatter_(1, order, torch.linspace(9, 2, 8).repeat(steps, 1))
+    router = torch.eye(pages, K).half()
+    k, v, q = f16(pages, page, G, D), f16(pages, page, G, D), f16(steps, 4, D)
+    kn, vn = f16(steps, G, D), f16(steps, G, D)
+
+    on = lambda t: t.contiguous().to(DEV)
+    kd, vd, qd, xd, md, hd, rd, knd, vnd = (on(t) for t in (k, v, q, xs, mark.half(), head, router, kn, vn))
+    length, table = (torch.zeros(n, dtype=torch.int32, device=DEV) for n in (1, 8))
+    out = torch.empty(steps, 4, D, dtype=torch.float16, device=DEV)
+    logits = torch.empty(vocab, dtype=torch.float32, device=DEV)
+    w = [on(f16(pages, 32, K)), on(f16(pages, 32, K)), on(f16(pages, K, 32))]
+    y = torch.empty(K, dtype=torch.float16, device=DEV)
+    kv = dg.paged_kv(kd, vd, table.view(1, 8), length)
+    ops = []
+    for i in range(steps):
+        ops.append((dg.moe(dg.LINEAR_F16, md[i], y, rd, *w, 8, ids=table),
+                    dg.linear(dg.LINEAR_F16, hd, 1, vocab, vocab, x=xd[i], logits=logits, token=length),
+                    dg.append(kv, None, knd[i:i + 1], vnd[i:i + 1]), dg.attention(kv, qd[i:i + 1], out[i:i + 1])))
+    new = lambda n: torch.empty(max(n, 16), dtype=torch.uint8, device=DEV)
+    ws_m, ws_h = new(dg.moe_workspace_bytes(ops[0][0])), new(dg.workspace_bytes([ops[0][1]]))
+    ws_a = new(dg.attn_workspace_bytes(ops[0][3]))
+    for experts, greedy, append, attend in ops:
+        dg.moe_forward(experts, ws_m)
+        dg.lm_head_argmax(greedy, ws_h)
+        dg.kv_append(append)
+        dg.attn_decode(attend, ws_a)
+    sync()
+    kh, vh = ref.f64(k), ref.f64(v)
+    for i in range(steps):
+        n, ids = int(lengths[i]), order[i].numpy()
+        _, kh, vh, _, _ = ref.append(np.zeros((1, 0, D)), ref.f64(kn[i:i + 1]), ref.f64(vn[i:i + 1]), kh, vh, ids[None],
+                                     [n], 1, None, None, False, "f16")
+        flat = kh[ids].reshape(-1, G, D), vh[ids].reshape(-1, G, D)
+        for h in range(4):
+            ro, _, bo, _ = _exact(q[i, h], torch.from_numpy(flat[0][:, h // 2]), torch.from_numpy(flat[1][:, h // 2]),
+                                  np.arange(n), "f16")
+            ref.check(ref.f64(out[i, h]), ro, bo, "step %d, head %d" % (i, h))
+    assert np.array_equal(ref.f64(kd), kh) and np.array_equal(ref.f64(vd), vh)
