@@ -10,9 +10,9 @@ namespace dg {
 
 // ---- elementwise epilogues ---------------------------------------------------------
 // Eight fp16 elements per thread (one 16-byte vector each way), fp32 arithmetic,
-// one rounding into fp16.
-__global__ void __launch_bounds__(256) k_swiglu(const uint4* __restrict__ g,
-                                                const uint4* __restrict__ u, uint4* h, int n8) {
+// one rounding into fp16.  Inputs are not __restrict__: the kernel before may still
+// write them when these start, and their loads must not become read-only ones.
+__global__ void __launch_bounds__(256) k_swiglu(const uint4* g, const uint4* u, uint4* h, int n8) {
     griddep_launch_dependents();
     griddep_wait();
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += gridDim.x * blockDim.x) {
@@ -28,9 +28,7 @@ __global__ void __launch_bounds__(256) k_swiglu(const uint4* __restrict__ g,
     }
 }
 
-__global__ void __launch_bounds__(256) k_residual_add(const uint4* __restrict__ a,
-                                                      const uint4* __restrict__ b, uint4* out,
-                                                      int n8) {
+__global__ void __launch_bounds__(256) k_residual_add(const uint4* a, const uint4* b, uint4* out, int n8) {
     griddep_launch_dependents();
     griddep_wait();
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += gridDim.x * blockDim.x) {
@@ -76,10 +74,10 @@ cudaError_t launch_residual_add(const void* a, const void* b, void* out, int n, 
 // fp16 products and one fp32 rounding per term, j ascending; the window then
 // shifts by one input.
 template <int W>
-__global__ void __launch_bounds__(256) k_conv1d_update(const __half* __restrict__ x, __half* state,
+__global__ void __launch_bounds__(256) k_conv1d_update(const __half* x, __half* state,
                                                        const __half* __restrict__ w,
                                                        const __half* __restrict__ bias,
-                                                       __half* __restrict__ y, int M, int C,
+                                                       __half* y, int M, int C,
                                                        int silu) {
     griddep_launch_dependents();
     griddep_wait();

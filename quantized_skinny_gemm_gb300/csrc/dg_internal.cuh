@@ -142,11 +142,13 @@ __device__ __forceinline__ void prefetch_line_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-// Activation loads: through the read-only path (L1-cached), or L2 only for
-// data written earlier in the same kernel (L1 is not kept coherent).
-__device__ __forceinline__ uint4 ld_nc16(const void* p) {
+// Activation loads: L1-cached, or L2 only for data written earlier in the same
+// kernel (L1 is not kept coherent).  Not the read-only path: the kernel before,
+// which wrote them, may still run when this one has started, and read-only memory
+// is what nobody writes in a kernel's lifetime.
+__device__ __forceinline__ uint4 ld_act16(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;

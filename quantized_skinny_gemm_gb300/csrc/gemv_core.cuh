@@ -171,7 +171,7 @@ struct PolicyFP {
     // chains of four, merged into the row sum once per chunk.
     __device__ __forceinline__ static uint4 load_x(const void* x, int c, bool coherent) {
         const unsigned char* p = static_cast<const unsigned char*>(x) + (size_t)c * 16;
-        return coherent ? ld_cg16(p) : ld_nc16(p);
+        return coherent ? ld_cg16(p) : ld_act16(p);
     }
     __device__ __forceinline__ static void mac_direct(Acc (&acc)[1], const Chunk& ch, const uint4& xv) {
         float s0 = mac2(ch.w.x, xv.x, 0.f);
@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(kThreads) k_gemv(const __grid_constant__ GemvP
             for (int r = 0; r < R; ++r) {
                 if (!rows[r].valid) continue;
                 if (ARGMAX) {
-                    const float sx = p.a.x_scale ? __ldg(p.a.x_scale) : 1.f;
+                    const float sx = p.a.x_scale ? *p.a.x_scale : 1.f;
                     const float v = P::finish(rows[r], acc[r][0], sx);
                     if (lane == 0) {
                         p.logits[rows[r].global] = v;
@@ -826,7 +826,7 @@ __global__ void __launch_bounds__(kThreads) k_gemv(const __grid_constant__ GemvP
                                 static_cast<int*>(p.kpart)[((size_t)sidx * p.a.M + m) * p.t.N +
                                                            rows[r].global] = to_bits(acc[r][m]);
                             } else {
-                                const float sx = p.a.x_scale ? __ldg(p.a.x_scale + m) : 1.f;
+                                const float sx = p.a.x_scale ? p.a.x_scale[m] : 1.f;
                                 const int ru = r + 1 < R ? r + 1 : r;  // (pairs: R is even)
                                 store_row<P>(rows[r], m, acc[r][m], sx, p.t.res, p.t.pair != 0,
                                              rows[ru], acc[ru][m]);
@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(256) k_split_finish(const __grid_constant__ Ge
         for (int s = 1; s < S; ++s) acc += from_bits<Acc>(part[((size_t)s * M + m) * N + row]);
         RowRef z{};
         const RowRef rr = locate(p.t, row, 0, z);
-        const float sx = p.a.x_scale ? __ldg(p.a.x_scale + m) : 1.f;
+        const float sx = p.a.x_scale ? p.a.x_scale[m] : 1.f;
         P::store(rr, m, acc, sx);
     }
 }

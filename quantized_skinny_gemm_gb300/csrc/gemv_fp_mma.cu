@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(kThreads) k_fp_mma(const __grid_constant__ Gem
                 if (kb + u < nblk) {
                     alo[u] = ld_stream16(wlo + (size_t)(kb + u) * 64);
                     ahi[u] = ld_stream16(whi + (size_t)(kb + u) * 64);
-                    blv[u] = has_lo ? ld_nc16(xlo + (size_t)(kb + u) * 64) : make_uint4(0, 0, 0, 0);
-                    bhv[u] = has_hi ? ld_nc16(xhi + (size_t)(kb + u) * 64) : make_uint4(0, 0, 0, 0);
+                    blv[u] = has_lo ? ld_act16(xlo + (size_t)(kb + u) * 64) : make_uint4(0, 0, 0, 0);
+                    bhv[u] = has_hi ? ld_act16(xhi + (size_t)(kb + u) * 64) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
             for (int u = 0; u < kFpMmaUnroll; ++u)

@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(kThreads) k_w8a8_mma(const __grid_constant__ G
                 if (kb + u < nblk) {
                     alo[u] = ld_stream16(wlo + (size_t)(kb + u) * 64);
                     ahi[u] = ld_stream16(whi + (size_t)(kb + u) * 64);
-                    blv[u] = has_lo ? ld_nc16(xlo + (size_t)(kb + u) * 64) : make_uint4(0, 0, 0, 0);
-                    bhv[u] = has_hi ? ld_nc16(xhi + (size_t)(kb + u) * 64) : make_uint4(0, 0, 0, 0);
+                    blv[u] = has_lo ? ld_act16(xlo + (size_t)(kb + u) * 64) : make_uint4(0, 0, 0, 0);
+                    bhv[u] = has_hi ? ld_act16(xhi + (size_t)(kb + u) * 64) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
             for (int u = 0; u < kMmaUnroll; ++u)
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) k_w8a8_mma(const __grid_constant__ G
         for (int j = 0; j < 4; ++j) {
             const int m = tok[j];
             if (m >= M) continue;
-            const float sx = __ldg(p.a.x_scale + m);
+            const float sx = p.a.x_scale[m];
             if (rlo.valid) PolicyI8::store(rlo, m, val_lo[j], sx);
             if (rhi.valid) PolicyI8::store(rhi, m, val_hi[j], sx);
         }
@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(kThreads) k_w8a8_mma_f16(const __grid_constant
                     if (kb + u < kb1) {
                         alo[u] = ld_stream16(wlo + (size_t)(kb + u) * 64);
                         ahi[u] = ld_stream16(whi + (size_t)(kb + u) * 64);
-                        blv[u] = has_lo ? ld_nc16(xlo + (size_t)(kb + u) * 64) : make_uint4(0, 0, 0, 0);
-                        bhv[u] = has_hi ? ld_nc16(xhi + (size_t)(kb + u) * 64) : make_uint4(0, 0, 0, 0);
+                        blv[u] = has_lo ? ld_act16(xlo + (size_t)(kb + u) * 64) : make_uint4(0, 0, 0, 0);
+                        bhv[u] = has_hi ? ld_act16(xhi + (size_t)(kb + u) * 64) : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
                 for (int u = 0; u < kMmaUnroll; ++u)
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) k_w8a8_mma_f16(const __grid_constant
         for (int j = 0; j < 4; ++j) {
             const int m = tok[j];
             if (m >= M) continue;
-            const float sx = __ldg(p.a.x_scale + m);
+            const float sx = p.a.x_scale[m];
             if (rlo.valid) PolicyI8::store(rlo, m, val_lo[j], sx);
             if (rhi.valid) PolicyI8::store(rhi, m, val_hi[j], sx);
         }

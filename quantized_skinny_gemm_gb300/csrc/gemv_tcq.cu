@@ -578,6 +578,9 @@ __global__ void __launch_bounds__(QTraits<F>::kThreads, 1) k_gemv_tcq(const __gr
             if (!live) continue;
             const size_t rows = (size_t)p.rows[g];
             __half* y = static_cast<__half*>(p.y[g]);
+            float sx[kTok];   // read before the stores, which could change them for all the compiler knows
+#pragma unroll
+            for (int m = 0; m < kTok; ++m) sx[m] = F != Q_W4A16 && m < p.M ? p.x_scale[m] : 1.f;
             if (F == Q_W8A8) {
                 const float sw = __ldg(static_cast<const float*>(p.scale[g]) + row);
                 int32_t* ao = p.acc_out[g];
@@ -585,14 +588,14 @@ __global__ void __launch_bounds__(QTraits<F>::kThreads, 1) k_gemv_tcq(const __gr
                 for (int m = 0; m < kTok; ++m) {
                     if (m >= p.M) break;
                     if (ao) ao[(size_t)m * rows + row] = ai[m];
-                    if (y) y[(size_t)m * rows + row] = __float2half_rn((float)ai[m] * sw * __ldg(p.x_scale + m));
+                    if (y) y[(size_t)m * rows + row] = __float2half_rn((float)ai[m] * sw * sx[m]);
                 }
             } else {
 #pragma unroll
                 for (int m = 0; m < kTok; ++m) {
                     if (m >= p.M) break;
                     y[(size_t)m * rows + row] =
-                        __float2half_rn(F == Q_W4A8 ? __ldg(p.x_scale + m) * a[m] : a[m]);
+                        __float2half_rn(F == Q_W4A8 ? sx[m] * a[m] : a[m]);
                 }
             }
         }

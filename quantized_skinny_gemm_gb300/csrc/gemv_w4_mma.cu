@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kW4MmaWarps * 32) k_w4_mma(const __grid_consta
         for (int j = 0; j < 4; ++j) {
             const int m = tok[j];
             if (m >= M) continue;
-            const float sx = A8 ? __ldg(p.a.x_scale + m) : 1.f;
+            const float sx = A8 ? p.a.x_scale[m] : 1.f;
             if (rlo.valid) write_out<false>(rlo, m, A8 ? sx * ylo[j] : ylo[j]);
             if (rhi.valid) write_out<false>(rhi, m, A8 ? sx * yhi[j] : yhi[j]);
         }

@@ -12,8 +12,7 @@ namespace dg {
 // under the total order of arg_better (larger value, then lower index).  The
 // maximum of a total order does not depend on the reduction tree, so any
 // fixed tree gives the same token.
-__global__ void __launch_bounds__(1024) k_argmax_pass2(const ArgPart* __restrict__ part,
-                                                       int nparts, int32_t* __restrict__ token) {
+__global__ void __launch_bounds__(1024) k_argmax_pass2(const ArgPart* part, int nparts, int32_t* token) {
     griddep_launch_dependents();
     griddep_wait();
     float bv = NAN;
@@ -60,9 +59,7 @@ cudaError_t launch_argmax_pass2(const ArgPart* part, int nparts, int32_t* token,
 // ---- per-token int8 activations -----------------------------------------------------
 // One CTA per token: amax = max |x|, s = amax / 127 (IEEE fp32 division),
 // q = clamp(rne(x / s), -127, 127); s = 1, q = 0 for an all-zero token.
-__global__ void __launch_bounds__(256) k_quant_act(const __half* __restrict__ x,
-                                                   int8_t* __restrict__ xq,
-                                                   float* __restrict__ xs, int K) {
+__global__ void __launch_bounds__(256) k_quant_act(const __half* x, int8_t* xq, float* xs, int K) {
     griddep_launch_dependents();
     griddep_wait();
     const __half* xr = x + (size_t)blockIdx.x * K;

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 } else {
                     // given codes, or codes the prologue wrote in this launch
                     // (read through L2: the prologue's writes are not in L1)
-                    sx = (ph.flags & kPhasePreQuant) ? __ldcg(ph.x_scale) : __ldg(ph.x_scale);
+                    sx = (ph.flags & kPhasePreQuant) ? __ldcg(ph.x_scale) : *ph.x_scale;
                 }
             }
             P::stage_x(a, xs, 1);
