@@ -335,8 +335,8 @@ class SparseStep:
 def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None, batch=1, q_len=1,
                         page_size=64, max_pages=16, window=0, sinks=0, group=32, rope=None,
                         share=None) -> SparseStep:
-    """layers: synth.sparse_decoder_workload(...) output; rope: (cos, sin) fp32
-    [max_pos][rot / 2] or None; share: another SparseStep of the same layers
+    """layers: synth.sparse_decoder_workload(...) output; batch * q_len from 1 to
+    16; rope: (cos, sin) fp32 [max_pos][rot / 2] or None; share: another SparseStep of the same layers
     (a different q_len or batch) whose weights, caches, table and lengths this
     one uses.  Per layer
       h += y (of the layer before); x = norm_attn(h); q, k, v = W x;
@@ -345,6 +345,8 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
     and last h += y; x_out = final_norm(h).  The residual stream stays fp32; the
     adds are part of the norms."""
     M, f16, f32, i32 = batch * q_len, torch.float16, torch.float32, torch.int32
+    if batch < 1 or q_len < 1 or M > 16:
+        raise ValueError("batch * q_len: the products and the experts take 1 to 16 rows")
     if share is not None and share.block_table.shape[0] != batch:
         raise ValueError("share: another batch")
     hidden = layers[0].q.shape[1]
@@ -381,6 +383,10 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
         ops.append((norm(h, t["h"], t["x"], W["norm_attn"], y=y), qkv,
                     append(kv, t["q"], t["k"], t["v"], q_out=t["q_rot"], q_len=q_len, cos=cos, sin=sin), att, out,
                     norm(t["h"], t["h_mid"], t["x_mid"], W["norm_mlp"], y=t["o"]), experts))
+        if not attn_workspace_bytes(att):
+            raise ValueError("the attention refuses these heads, window or strides")
+        if not moe_workspace_bytes(experts):
+            raise ValueError("the expert layer refuses these sizes")
         attn_ws = max(attn_ws, attn_workspace_bytes(att))
         moe_ws = max(moe_ws, moe_workspace_bytes(experts))
         lin_ws = max(lin_ws, qkv.workspace_bytes(), out.workspace_bytes())

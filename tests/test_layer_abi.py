@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import quantized_skinny_gemm_gb300 as dg
+from quantized_skinny_gemm_gb300 import plans, synth
 
 OK, INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE = range(5)
 A, B, C, D = 0x100000, 0x200000, 0x300000, 0x400000   # fake aligned addresses
@@ -205,3 +206,17 @@ def test_scales_that_overflow_are_refused(lib):
         assert f(scale) == INVALID
     for scale in (2.3e38, -2.3e38, 0.0, 1e-45, -1e-39):
         assert f(scale) == WORKSPACE      # taken, and refused for its workspace
+
+
+def test_a_sparse_plan_refuses_what_its_operators_would(lib):
+    """At the plan, not at run() behind the first norm."""
+    layers = synth.sparse_decoder_workload(1, 1, 64, 4, 2, 16, 32, 4)
+    plan = lambda heads=4, kv_heads=2, top_k=2, **kw: plans.sparse_decoder_step(
+        layers, torch.device("cpu"), heads, kv_heads, top_k, max_pages=2, **kw)
+    for kw in (dict(), dict(batch=4, q_len=4), dict(q_len=16), dict(batch=16), dict(window=9, sinks=2)):
+        step = plan(**kw)
+        assert step.h.shape == (kw.get("batch", 1) * kw.get("q_len", 1), 64)
+    for kw in (dict(batch=17), dict(q_len=17), dict(batch=3, q_len=6), dict(batch=0), dict(q_len=0), dict(top_k=5),
+               dict(window=-1)):
+        with pytest.raises((ValueError, dg.DGError)):
+            plan(**kw)
