@@ -351,6 +351,11 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
         raise ValueError("share: another batch")
     hidden = layers[0].q.shape[1]
     dim = layers[0].q.shape[0] // heads
+    for L in layers:
+        if any(tuple(w.shape) != (rows, cols) for w, rows, cols in (
+                (L.q, heads * dim, hidden), (L.k, kv_heads * dim, hidden), (L.v, kv_heads * dim, hidden),
+                (L.o, hidden, heads * dim))):
+            raise ValueError("heads, kv_heads: the layers' q, k, v, o have other sizes")
     new = lambda *shape, dtype=f16: torch.zeros(shape, dtype=dtype, device=device)
     if share is None:
         pages = batch * max_pages

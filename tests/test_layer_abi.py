@@ -217,6 +217,6 @@ def test_a_sparse_plan_refuses_what_its_operators_would(lib):
         step = plan(**kw)
         assert step.h.shape == (kw.get("batch", 1) * kw.get("q_len", 1), 64)
     for kw in (dict(batch=17), dict(q_len=17), dict(batch=3, q_len=6), dict(batch=0), dict(q_len=0), dict(top_k=5),
-               dict(window=-1)):
+               dict(window=-1), dict(heads=8)):
         with pytest.raises((ValueError, dg.DGError)):
             plan(**kw)
