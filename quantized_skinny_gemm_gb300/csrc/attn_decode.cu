@@ -95,7 +95,7 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
 struct Span {
     int first;   // position of the step's first token (negative: before the start)
     int sinks, lo, end, seen_sinks, seen_lo;
-    __device__ __forceinline__ int count() const { return sinks + end - lo; }
+    __device__ __forceinline__ int count() const { return end - lo + sinks; }
     __device__ __forceinline__ int position(int c) const { return c < sinks ? c : c - sinks + lo; }
     __device__ __forceinline__ bool seen(int j) const { return j >= seen_lo || j < seen_sinks; }
 };
@@ -109,7 +109,7 @@ __device__ __forceinline__ Span span_of(const dg_attn& op, int b) {
     s.seen_lo = (int)max(0ll, min(lo, (long long)s.end));
     s.lo = s.seen_lo & ~15;
     s.seen_sinks = min(op.sinks, s.seen_lo);
-    s.sinks = min((s.seen_sinks + 15) & ~15, s.lo);
+    s.sinks = (int)min(((unsigned)s.seen_sinks + 15u) & ~15u, (unsigned)s.lo);
     return s;
 }
 __device__ __forceinline__ int blocks_of(const Span& s) {
@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
         sg.hk = unit / p.groups;
         sg.row0 = (unit - sg.hk * p.groups) * S::kRows;
         sg.key0 = sg.kb * kBlockKeys + warp * kKeys;
-        sg.lim = min(sg.sp.count(), sg.ke * kBlockKeys);
-        sg.n = sg.key0 < sg.lim ? (sg.lim - sg.key0 + kStep - 1) / kStep : 0;
+        sg.lim = sg.ke == sg.nb ? sg.sp.count() : sg.ke * kBlockKeys;   // nb * kBlockKeys may be 2^31
+        sg.n = sg.key0 < sg.lim ? (int)((unsigned)(sg.lim - sg.key0 + kStep - 1) / kStep) : 0;
         if (sg.kb == 0 && tid == 0 && p.info) {
             // the unit's parts lie in this CTA's first or second part and the first
             // ones of the following CTAs; the last is the largest c with
@@ -289,11 +289,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
     // Position and cache offset (elements; -1: nothing there) of key `lane` (lane
     // mod kKeys) of stage i.
     auto locate = [&](int i, int& pos, long long& off) {
-        const int c = sg.key0 + i * kStep + (lane & (kKeys - 1));
+        const unsigned c = (unsigned)sg.key0 + (unsigned)i * kStep + (lane & (kKeys - 1));
         pos = INT_MAX;
         off = -1;
-        if (i < sg.n && c < sg.lim) {
-            const int j = sg.sp.position(c);
+        if (i < sg.n && c < (unsigned)sg.lim) {
+            const int j = sg.sp.position((int)c);
             int slot = 0;
             const int page = sg.sp.seen(j) ? page_slot(op.kv, p.page_size, sg.b, j, slot) : -1;
             if (page >= 0) {

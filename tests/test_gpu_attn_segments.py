@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import layer_ref as ref
-from gpu_util import need_gpu
+import quantized_skinny_gemm_gb300 as dg
+from gpu_util import DEV, need_gpu, sync
 from test_gpu_attn import DT, _q, _run
 
 pytestmark = pytest.mark.gpu
@@ -81,3 +82,35 @@ def test_batches_around_the_range_searches(batch):
     ro, rl, bo, bl = ref.attention(ref.f64(q), ref.f64(k), ref.f64(v), table.numpy(), lens, 2, 0.125)
     ref.check(ref.f64(out), ro, bo, "out")
     ref.check(ref.f64(lse), rl, bl, "lse")
+
+
+@pytest.mark.parametrize("q_len,window,sinks", [(1, 0, 0), (3, 0, 0), (2, 100, 50), (1, 2 ** 31 - 1, 7),
+                                                (2, 70, 2 ** 31 - 1)])
+def test_the_longest_length(q_len, window, sinks):
+    """2^31 - 1 positions, all but the last 63 in one page that the table names 2^25 - 1
+    times; the last ones' page holds the strongest key.  Every position is visited where
+    there is no window."""
+    need_gpu()
+    page, dim, n = 64, 8, 2 ** 31 - 1
+    g = torch.Generator().manual_seed(94)
+    k, v = (torch.randn(2, page, 1, dim, generator=g).half() for _ in range(2))
+    k[0] *= 0.1
+    q = torch.randn(q_len, 2, dim, generator=g).half().abs()
+    k[1, 50, 0] = 30.0                                     # z >= 30 * sum(q) / sqrt(8), far above 2^31 others
+    table = torch.zeros(1, 2 ** 25, dtype=torch.int32, device=DEV)
+    table[0, -1] = 1
+    kd, vd, qd = k.to(DEV), v.to(DEV), q.to(DEV)
+    out, lse = torch.full_like(qd, float("nan")), torch.zeros(q_len, 2, device=DEV)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    op = dg.attention(dg.paged_kv(kd, vd, table, lens), qd, out, lse=lse, q_len=q_len, window=window, sinks=sinks)
+    ws = torch.full((dg.attn_workspace_bytes(op),), 255, dtype=torch.uint8, device=DEV)
+    dg.attn_decode(op, ws)
+    sync()
+    z = 30.0 * ref.f64(q).sum(-1) * dim ** -0.5
+    others = np.abs(ref.f64(q)).sum(-1) * np.abs(ref.f64(k[0])).max() * dim ** -0.5 + np.log(2.0 ** 31)
+    near = np.abs(ref.f64(q)).sum(-1) * np.abs(ref.f64(k[1][torch.arange(page) != 50])).max() * dim ** -0.5
+    assert (z > others + 9).all() and (z > near + 9).all()  # together below 63 e^-9 of the strongest
+    want = ref.f64(v[1, 50, 0])
+    rest = 64 * np.exp(-9.0) * (np.abs(want) + max(np.abs(ref.f64(v[0])).max(), np.abs(ref.f64(v[1])).max()))
+    assert (np.abs(ref.f64(out) - want) <= rest + 2.0 ** -10 * np.abs(want)).all()
+    assert (np.abs(ref.f64(lse) - z) <= 64 * np.exp(-9.0) + 1e-5 * z).all()
