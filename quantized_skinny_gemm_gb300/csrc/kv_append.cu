@@ -33,7 +33,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(const AppendParams
     const dg_append& op = prm.op;
     const int t = blockIdx.x, b = t / prm.q_len;
     const int D = op.kv.head_dim, half = op.rot_dim / 2, kvh = op.kv.kv_heads;
-    const int p = op.kv.seq_lens[b] - op.q_len + (t - b * op.q_len);
+    // a length below zero is none: no position may wrap around
+    const int p = max(0, op.kv.seq_lens[b]) - op.q_len + (t - b * op.q_len);
     const bool live = p >= 0 && (op.rot_dim == 0 || p < op.max_pos);
     int at = 0;
     const int page = live ? page_slot(op.kv, prm.page_size, b, p, at) : -1;

@@ -208,3 +208,22 @@ def test_lengths_and_tables_that_the_kernel_before_writes():
                                   np.arange(n), "f16")
             ref.check(ref.f64(out[i, h]), ro, bo, "step %d, head %d" % (i, h))
     assert np.array_equal(ref.f64(kd), kh) and np.array_equal(ref.f64(vd), vh)
+
+
+@pytest.mark.parametrize("rot", [0, 32])
+def test_append_at_the_most_negative_length(rot):
+    """No token has a position: zeros in q_out, nothing in the cache."""
+    need_gpu()
+    g = torch.Generator().manual_seed(12)
+    f16 = lambda *s: torch.randn(*s, generator=g).half().to(DEV)
+    k_cache, v_cache, q, k, v = f16(4, 16, 2, 64), f16(4, 16, 2, 64), f16(6, 4, 64), f16(6, 2, 64), f16(6, 2, 64)
+    kh, vh = k_cache.clone(), v_cache.clone()
+    table = torch.arange(4, dtype=torch.int32, device=DEV).view(2, 2)
+    lens = torch.tensor([-2 ** 31, -2 ** 31 + 1], dtype=torch.int32, device=DEV)
+    cos = sin = None
+    if rot:
+        cos = sin = torch.ones(32, rot // 2, device=DEV)
+    q_out = torch.full_like(q, 7.0)
+    dg.kv_append(dg.append(dg.paged_kv(k_cache, v_cache, table, lens), q, k, v, q_out, q_len=3, cos=cos, sin=sin))
+    sync()
+    assert (q_out == 0).all() and torch.equal(k_cache, kh) and torch.equal(v_cache, vh)
