@@ -21,6 +21,8 @@ def decode(layers, embed, lm_head, prompt, tokens, heads, kv_heads, top_k, devic
     """prompt: int64 [P] on the host; embed and lm_head [vocab][hidden]
     fp16.  Returns the `tokens` greedy continuations and the microseconds of a
     step."""
+    if not len(prompt) or tokens < 1:
+        raise ValueError("a prompt of one token at least, and one token to decode")
     vocab, hidden = embed.shape
     dim = layers[0].q.shape[0] // heads
     total = len(prompt) + tokens
