@@ -457,7 +457,8 @@ def norm(h, h_out, x_out, w_pre=None, b_pre=None, y=None, w_post=None, b_post=No
         _fits(t is None or t.numel() == rows * N, where)
     for t in (w_pre, b_pre, w_post, b_post):
         _fits(t is None or t.numel() == N, where)
-    _fits(gate is None or gate.numel() in (N, rows * N), where)
+    _fits(gate is None or (gate.numel() in (N, rows * N) and
+                           (gate.dim() == 1 or gate.shape[-1] == N)), where)
     gate_rows = 0 if gate is None else gate.numel() // N
     return Norm(ftype, kind, rows, N, h_f32, gate_rows, alpha, beta, eps, w_offset, _ptr(y),
                 _ptr(w_post), _ptr(b_post), _ptr(gate), _ptr(h), _ptr(w_pre), _ptr(b_pre),

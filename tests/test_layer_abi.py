@@ -220,3 +220,14 @@ def test_a_sparse_plan_refuses_what_its_operators_would(lib):
                dict(window=-1), dict(heads=8)):
         with pytest.raises((ValueError, dg.DGError)):
             plan(**kw)
+
+
+def test_a_gate_of_one_value_a_row_is_refused():
+    """[rows][1] has as many values as a row [N] where rows == N."""
+    h = lambda *s: torch.zeros(*s, dtype=torch.float16)
+    op = lambda gate, rows=8: dg.norm(h(rows, 8), h(rows, 8), None, y=h(rows, 8), gate=gate)
+    assert op(h(8)).gate_rows == 1 and op(h(1, 8)).gate_rows == 1 and op(h(8, 8)).gate_rows == 8
+    assert op(h(64)).gate_rows == 8 and op(h(4, 2, 8)).gate_rows == 8
+    for gate in (h(8, 1), h(2, 4), h(16, 4), h(8, 8, 1)):
+        with pytest.raises(dg.DGError):
+            op(gate)
