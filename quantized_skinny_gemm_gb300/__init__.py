@@ -395,9 +395,10 @@ def append(kv, q, k, v, q_out=None, q_len=1, cos=None, sin=None, interleaved=Fal
     ks = _head_rows(k, tokens, kv.kv_heads, dim, dt, where)
     vs = _head_rows(v, tokens, kv.kv_heads, dim, dt, where)
     rot = max_pos = 0
+    _fits((cos is None) == (sin is None), where)
     if cos is not None:
         _contiguous(where, torch.float32, cos, sin)
-        _fits(sin is not None and cos.dim() == 2 and cos.shape == sin.shape, where)
+        _fits(cos.dim() == 2 and cos.shape == sin.shape, where)
         max_pos, rot = cos.shape[0], 2 * cos.shape[1]
     return Append(kv, q_len, heads, rot, int(interleaved), max_pos, 0, _ptr(q), _ptr(k), _ptr(v),
                   _ptr(q_out), qs, ks, vs, qos, _ptr(cos), _ptr(sin))

@@ -231,3 +231,15 @@ def test_a_gate_of_one_value_a_row_is_refused():
     for gate in (h(8, 1), h(2, 4), h(16, 4), h(8, 8, 1)):
         with pytest.raises(dg.DGError):
             op(gate)
+
+
+def test_half_a_rotation_is_refused():
+    h = lambda *s: torch.zeros(*s, dtype=torch.float16)
+    kv = dg.paged_kv(h(4, 16, 2, 64), h(4, 16, 2, 64), torch.zeros(2, 3, dtype=torch.int32),
+                     torch.zeros(2, dtype=torch.int32))
+    table = torch.zeros(9, 32)
+    op = lambda **kw: dg.append(kv, h(2, 4, 64), h(2, 2, 64), h(2, 2, 64), **kw)
+    assert op(cos=table, sin=table).rot_dim == 64 and op().rot_dim == 0
+    for kw in (dict(sin=table), dict(cos=table)):
+        with pytest.raises(dg.DGError):
+            op(**kw)
