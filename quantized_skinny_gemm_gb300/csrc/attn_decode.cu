@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
     // numbers, and a strongest key of weight 2^64 overflows.  (Parts are joined by
     // products: there the greatest one's weight is 1 whatever the rounding.)
     const float c2 = op.scale == 0.f ? 1.f : fabsf(op.scale) * kLog2e;
-    const uint32_t q_flip = op.scale < 0.f ? 0x80008000u : 0u, q_keep = op.scale == 0.f ? 0u : 0xFFFFFFFFu;
+    const float sign = op.scale > 0.f ? 1.f : op.scale < 0.f ? -1.f : 0.f;
+    const uint32_t sign2 = pair_16<BF16>(sign, sign);
     const float grow = fminf(8.f / c2, FLT_MAX);   // finite: the first maximum is always taken
     const int g = lane >> 2, t4 = lane & 3;
 
@@ -364,10 +365,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<DP, RT>::kCtas) k_attn
         for (int x = 0; x < kQv; ++x) {
             const int i = x * kAttnThreads + tid, r = i / (DP / 8), ch = i % (DP / 8);
             if (r >= S::kRows) continue;
-            const uint4 v = qv[x];
+            const uint4 v = qv[x];   // a product, so that zero times infinity is NaN
             *reinterpret_cast<uint4*>(qs + S::piece(r, ch)) =
-                make_uint4((v.x ^ q_flip) & q_keep, (v.y ^ q_flip) & q_keep, (v.z ^ q_flip) & q_keep,
-                           (v.w ^ q_flip) & q_keep);
+                make_uint4(mul_16<BF16>(v.x, sign2), mul_16<BF16>(v.y, sign2), mul_16<BF16>(v.z, sign2),
+                           mul_16<BF16>(v.w, sign2));
         }
     };
 

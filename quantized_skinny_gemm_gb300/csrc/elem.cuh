@@ -36,6 +36,17 @@ __device__ __forceinline__ uint32_t pair_16(float a, float b) {
     return h2_as_u32(__floats2half2_rn(a, b));
 }
 
+// Products of two pairs, each rounded to the 16-bit type.
+template <bool BF16>
+__device__ __forceinline__ uint32_t mul_16(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (BF16)
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 template <bool BF16>
 __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};

@@ -227,3 +227,40 @@ def test_append_at_the_most_negative_length(rot):
     dg.kv_append(dg.append(dg.paged_kv(k_cache, v_cache, table, lens), q, k, v, q_out, q_len=3, cos=cos, sin=sin))
     sync()
     assert (q_out == 0).all() and torch.equal(k_cache, kh) and torch.equal(v_cache, vh)
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, 0.125])
+def test_infinite_and_nan_queries_are_nan_at_any_scale(ftype, scale):
+    need_gpu()
+    n, D = 90, 64
+    g = torch.Generator().manual_seed(13)
+    k, v = (torch.randn(n, 1, D, generator=g).to(DT[ftype]) for _ in range(2))
+    q = torch.randn(1, 5, D, generator=g).to(DT[ftype])
+    q[0, 1, 7], q[0, 2, 7], q[0, 3, 7] = float("nan"), float("inf"), -float("inf")
+    out, lse = _attention(q, k, v, [n], ftype, scale=scale)
+    for h in (0, 4):
+        ro, rl, bo, bl = _exact(q[0, h], k[:, 0], v[:, 0], np.arange(n), ftype, scale)
+        ref.check(out[0, h], ro, bo, "out of head %d" % h)
+        ref.check(lse[0, h], rl, bl, "lse of head %d" % h)
+    assert np.isnan(out[0, 1]).all() and np.isnan(lse[0, 1])
+    for h in (2, 3):      # scores of +-infinity (their softmax: inf - inf), or 0 * inf
+        assert np.isnan(out[0, h]).all()
+
+
+@pytest.mark.parametrize("ftype,small", [("f16", 2.0 ** -24), ("bf16", 2.0 ** -133)])
+def test_subnormal_queries_count(ftype, small):
+    """The smallest numbers of the type, under a scale that makes them matter."""
+    need_gpu()
+    n, D, scale = 40, 64, -2.0 ** 14 if ftype == "f16" else -2.0 ** 100
+    g = torch.Generator().manual_seed(14)
+    k, v = (torch.randn(n, 1, D, generator=g) for _ in range(2))
+    k = (k * (1.0 if ftype == "f16" else 2.0 ** 30)).to(DT[ftype])
+    v = v.to(DT[ftype])
+    q = (torch.randint(-40, 41, (1, 3, D), generator=g) * small).to(DT[ftype])
+    out, lse = _attention(q, k, v, [n], ftype, scale=scale)
+    for h in range(3):
+        ro, rl, bo, bl = _exact(q[0, h], k[:, 0], v[:, 0], np.arange(n), ftype, scale)
+        assert np.abs(rl - np.log(n)) > 1e-3
+        ref.check(out[0, h], ro, bo, "out of head %d" % h)
+        ref.check(lse[0, h], rl, bl, "lse of head %d" % h)
