@@ -25,9 +25,10 @@
 // (split_pair), at half as many matrix instructions again: 0.4 % on the long
 // cache below, 4 to 5 % on the others, 19 % where 64 rows share a key.
 //
-// Measured: 200001 positions of 8 x 128 bf16, 32 heads: 127.3 us, 6.4 TB/s of the
-// copy's 6.8; 16 sequences of up to 8191, 12 heads on 2: 11.5 us; one of 100: 5.7
-// us, one launch where the table holds 128 positions at most, else two; 8 tokens
+// Measured: 200001 positions of 8 x 128 bf16, 32 heads: 127 us, 6.4 TB/s of the
+// copy's 6.8; 16 sequences of up to 8191, 12 heads on 2: 11.5 us; one of 100: 5.6
+// us, one launch where the table holds 128 positions at most, else two (in a graph
+// 5.1 and, in a table of 4096, 5.9); 8 tokens
 // of 8 sequences on windows of 4096, 32 heads on 8 of 64: 33 us, bound by the
 // latency of a few stages per warp and of the join.
 #include <algorithm>

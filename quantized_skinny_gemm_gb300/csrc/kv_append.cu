@@ -9,10 +9,11 @@ namespace dg {
 // warp does both).  A thread reads all of a pair before it writes any, so q_out
 // may be q.
 //
-// Bound by latency at decode sizes (one token: a few KB, two dependent reads,
-// length -> page id; 2.8 us back to back, 4.8 alone) and by HBM at large ones (8
-// tokens of 256 sequences, 32 + 2 x 8 heads of 128: 11.3 us, 4.5 TB/s; one piece
-// at a time 14.1).
+// Bound by latency: one token is a few KB behind two dependent reads, length ->
+// page id (2.8 us back to back); of many tokens each small CTA waits for length ->
+// page id -> copy in turn, with half of an SM's warps resident (8 tokens of 256
+// sequences, 32 + 2 x 8 heads of 128: 11.3 us, 4.5 TB/s of traffic that L2 mostly
+// holds, DRAM 26 %; one piece at a time 14.1).
 constexpr int kAppendThreads = 128;
 template <int U>
 struct PieceOf {

@@ -35,8 +35,8 @@
 // whose codes belong to group f and zero for the others, so that one
 // instruction sums the groups apart.
 //
-// Measured: 16 tokens, 4096 x 14336 bf16, 2 of 8 experts: 450 us, 6.2 TB/s; one
-// token, fp16 (101 MB): 29 us, 3.5 TB/s, of which the scores and the routing at
+// Measured: 16 tokens, 4096 x 14336 bf16, 2 of 8 experts: 436 to 449 us, 6.2 to 6.4
+// TB/s; one token, fp16 (101 MB): 28.4 us, 3.6 TB/s, of which the scores and the routing at
 // the head of `up` take 6; int4, one token, 4096 x 14336, 2 of 8: 57 us, 3.5
 // TB/s, bound by unpacking and by the latency of 16 warps' chunks.
 #include <algorithm>
@@ -315,9 +315,10 @@ struct Shape {
 };
 
 // Streaming loads; the predicated forms give zero where `in` is false.  WIDE asks
-// L2 for the whole 256 bytes: better for long streams (16 tokens, 2.8 GB bf16: 451
-// us, 466 without; 8 tokens int4: 93.0, 94.6), worse for the short ones of one
-// block of tokens at 16 bits (one token, 101 MB: 29.4, 28.6 without).
+// L2 for the whole 256 bytes: better for long streams (16 tokens, 2.8 GB bf16: 436 to
+// 449 us, 450 to 461 without; one token, 198 MB int4: 56.8, 57.6; 4 tokens, 310 MB
+// int4: 91 both), worse for the short ones of one block of tokens at 16 bits (one
+// token, 101 MB: 29.4, 28.6 without).
 template <bool WIDE>
 __device__ __forceinline__ void ld_weights16(uint32_t (&v)[4], const void* p) {
     if (WIDE)
@@ -883,7 +884,7 @@ static cudaError_t launch_moe_kind(const dg_moe& op, void* ws, cudaStream_t s) {
     // eight (16 tokens, 4096 x 2048, 2 of 8 experts: 94 us, sixteen 142; all 16 on
     // one expert of 2048 x 2048: 29, 44), 16-bit weights where experts of more are
     // rare (12 tokens, 2048 x 1024, 8 of 64: 125, 134; but 16 tokens, 4096 x
-    // 14336, 2 of 8: 572, 480).
+    // 14336, 2 of 8: 536 to 584, 436 to 449).
     const bool few = KIND == DG_LINEAR_W4A16 || op.M * op.top_k <= 2 * op.E;
     const int tokens = few ? std::min(op.M, 8) : op.M;
     const int nt = token_blocks<KIND>(tokens, 1), ctas = sm_count() * (moe_warps(KIND, nt) / kMoeWarps);

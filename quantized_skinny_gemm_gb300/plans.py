@@ -336,9 +336,9 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
                         page_size=64, max_pages=16, window=0, sinks=0, group=32, rope=None,
                         share=None) -> SparseStep:
     """layers: synth.sparse_decoder_workload(...) output; batch * q_len from 1 to
-    16; rope: (cos, sin) fp32 [max_pos][rot / 2] or None; share: another SparseStep of the same layers
-    (a different q_len or batch) whose weights, caches, table and lengths this
-    one uses.  Per layer
+    16; rope: (cos, sin) fp32 [max_pos][rot / 2] or None; share: another
+    SparseStep of the same layers and batch (with another q_len) whose weights,
+    tables, caches and lengths this one uses.  Per layer
       h += y (of the layer before); x = norm_attn(h); q, k, v = W x;
       rotate q and k, k and v into the cache; att = attention; o = W_o att;
       h += o; x = norm_mlp(h); y = experts(x)
