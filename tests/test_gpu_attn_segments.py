@@ -50,7 +50,7 @@ def _shared_pool(lens, heads, dim, dt, seed):
     ("bf16", 6, 2, 192, 3, 1, 120),      # 192 and 256 dims
     ("f16", 10, 2, 160, 4, 2, 50),
     ("f16", 4, 2, 256, 2, 1, 60),
-    ("bf16", 12, 2, 256, 4, 2, 40),
+    ("bf16", 14, 2, 256, 4, 2, 40),
 ])
 def test_many_units_a_cta(ftype, heads, kv_heads, dim, q_len, groups, batch, window, sinks):
     need_gpu()
