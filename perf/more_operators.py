@@ -471,7 +471,7 @@ def _pages(s):
     grown = served.view(-1, 1) & (col >= held.view(-1, 1)) & (col < need.view(-1, 1))
     number = (upto - more - held).view(-1, 1) + col
     rows = torch.where(grown, s["pool"][(first + number.clamp(min=0)) % N], table)
-    taken = torch.where(served, upto, torch.zeros_like(upto)).amax()
+    taken = torch.where(served & (more > 0), upto, torch.zeros_like(upto)).amax()
     back = torch.where(ended, held, torch.zeros_like(held))
     given = torch.cumsum(back, 0)
     gives = col < back.view(-1, 1)
