@@ -11,7 +11,10 @@
  * and what a decoder runs between those products for a step's new tokens: norms
  * with the residual add (dg_norm_residual), rotary positions and the cache
  * append (dg_kv_append), attention over a paged cache (dg_attn_decode) and an
- * expert layer (dg_moe_forward).
+ * expert layer (dg_moe_forward); and what a serving step runs around them: pages
+ * for the tokens to come (dg_assign_pages), head norms with the append, also to a
+ * cache held in 4 bits (dg_qkv_append, dg_kv4_read), attention over that cache
+ * (dg_attn4_decode) and log probabilities of tokens (dg_token_logprobs).
  * Sources: the M=1 custom cube matmul, the 16-slice lm_head with a host reduce
  * and the weight-bandwidth floor of "MiniCPM-V on Orange Pi AIPro (Ascend 310B)";
  * single-request decode and graph-replayed decode steps of "EdgeFM: Efficient
@@ -501,6 +504,219 @@ typedef struct {
 dg_status dg_moe_forward(const dg_moe* op, void* ws, size_t ws_bytes, dg_stream stream);
 /* Workspace of dg_moe_forward; 0 for an op that it would refuse. */
 size_t dg_moe_workspace_bytes(const dg_moe* op);
+
+/* ---- a serving step ------------------------------------------------------------------
+ * Pages for the tokens to come, head norms with the append, a cache held in 4 bits
+ * with the attention that reads it, and log probabilities of the answer.  The pages
+ * name none of these; each declaration states the definition.  Lengths, tables, maps
+ * and pools are device memory, read when the kernels run, so a captured graph follows
+ * them.  All arithmetic on values is fp32 or wider, and each 16-bit output is rounded to
+ * nearest even once. */
+
+/* A paged cache as dg_paged_kv, held in 4 bits: each 16 consecutive dims of a head
+ * are 16 codes c, 4-bit two's complement with dims 2j and 2j + 1 in bits 0-3 and 4-7
+ * of byte j, and one scale byte s, an e4m3 number (fn: 0x7F and 0xFF are NaN).  A
+ * value is factor * s * c, its factor k_factor or v_factor: 4.5 bits a value.  The
+ * codes of sequence b's position j, head g start at
+ *   k + page * page_stride + slot * token_stride + g * head_stride      (bytes)
+ * and its head_dim / 16 scales at k_scale with the scale_* strides; v and v_scale
+ * likewise.  [page][head][slot][..] reads each head's rows in one piece and is the
+ * faster order.  Codes of -8 are read as such (the append writes none).  k, v and
+ * the strides of codes are multiples of 8 bytes; scales may lie anywhere. */
+typedef struct {
+    int32_t type;      /* dg_ftype of q, k, v, out beside the cache */
+    int32_t batch;
+    int32_t kv_heads;
+    int32_t head_dim;  /* multiple of 16, at most 256 */
+    int32_t page_size;
+    int32_t num_pages;
+    int32_t max_pages; /* pages per sequence in block_table */
+    int32_t reserved;  /* must be 0 */
+    uint8_t* k;
+    uint8_t* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    int64_t page_stride, token_stride, head_stride;                   /* of codes */
+    int64_t scale_page_stride, scale_token_stride, scale_head_stride; /* of scales */
+    float k_factor;    /* above 0, finite; 1 / 7 of a group's largest value over it */
+    float v_factor;    /* should lie in 2^-6..448, where e4m3 has all of its bits */
+    const int32_t* block_table;
+    int64_t table_stride;    /* at least max_pages, or batch 1 */
+    const int32_t* seq_lens; /* [batch] */
+} dg_paged_kv4;
+
+/* Norms of queries and keys for each head, rotary positions, and the append, in one
+ * pass.  For a head's values x of one token (q with w_q, k with w_k; not normed
+ * where that is NULL, and v never):
+ *   x = u / sqrt(mean(u^2) + eps) * (w_offset + w),   u = x (DG_NORM_RMS) or
+ *       x - mean(x) (DG_NORM_LAYER), over the head's head_dim values
+ * then the rotation of dg_kv_append (pairs, dims from rot_dim on and tables as
+ * there), all in fp32.  q goes to q_out (which may be q), k and v to the cache:
+ *   bits 16 (kv):  rounded once
+ *   bits 4 (kv4):  per 16 dims s = e4m3(max |x| / (7 factor)), to nearest even and at
+ *       most 448, c = min(max(rne(x / (s factor)), -7), 7), 0 where s is 0; a group
+ *       that holds an infinity or a NaN gets s = NaN and c = 0.
+ * Without slots: token t = b * q_len + i of batch * q_len, 1 <= q_len <= 16, has
+ * position p = seq_lens[b] - q_len + i and its place by the block table.  With slots
+ * (int64 [tokens]; positions int32 [tokens], both needed): token t has position
+ * positions[t] and lies in slot slots[t] = page * page_size + place, wherever that
+ * is: prompts of any lengths in one call (the table and the lengths are not read, q_len is 0).
+ * A token with p < 0 or, when rotating, p >= max_pos writes zeros to q_out and
+ * nothing to the cache; one whose page or slot does not exist writes nothing to the
+ * cache.  Two tokens must not share a slot.  Any 2-byte alignment of q, k, v, q_out and
+ * a 16-bit cache works; 16-byte aligned pointers and strides, head_dim a
+ * multiple of 8 and rot_dim of 16 take the vector path.  q may be NULL (heads 0). */
+typedef struct {
+    dg_paged_kv kv;      /* bits 16 */
+    dg_paged_kv4 kv4;    /* bits 4 */
+    int32_t bits;        /* 16 or 4: which of the two is meant; the other is not read */
+    int32_t q_len;
+    int32_t tokens;      /* with slots, else 0 */
+    int32_t heads;
+    int32_t rot_dim;     /* even, at most head_dim */
+    int32_t interleaved; /* 0 or 1 */
+    int32_t max_pos;
+    int32_t norm;        /* dg_norm_kind */
+    float eps, w_offset;
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    const float* cos;
+    const float* sin;
+    const void* w_q;     /* [head_dim], the type of q */
+    const void* w_k;
+    const int64_t* slots;
+    const int32_t* positions;
+} dg_head_append;
+dg_status dg_qkv_append(const dg_head_append* op, dg_stream stream);
+
+/* Keys and values of a 4-bit cache back in 16 bits: k and v [tokens][kv_heads]
+ * [head_dim] of type kv.type, *_stride elements from one token to the next, rounded
+ * once; either may be NULL.  Without slots: the last q_len positions of each
+ * sequence, any q_len >= 1, tokens = batch * q_len; with slots (int64 [tokens],
+ * q_len 0): what lies there.  Zeros for what does not exist.  Any 2-byte alignment. */
+typedef struct {
+    dg_paged_kv4 kv;
+    int32_t q_len;
+    int32_t tokens;
+    void* k;
+    void* v;
+    int64_t k_stride, v_stride;
+    const int64_t* slots;
+} dg_kv4_rows;
+dg_status dg_kv4_read(const dg_kv4_rows* op, dg_stream stream);
+
+/* dg_attn_decode over a cache held in 4 bits: the same definition, masks, outputs
+ * and refusals, with the cache's values as dg_paged_kv4 states them.  They meet the
+ * matrix instruction as they are (a code times an e4m3 number is exact in fp16); scores and
+ * sums are fp32; e^(z_j) is the sum of two fp16 numbers, 2^-21 of itself off and up
+ * to 2^-32 of the strongest key's, for both types; a bf16 query is taken in fp16 times a power of two,
+ * exact but for values below 2^-30 of its row's largest.  A group whose scale is NaN makes
+ * the scores (k) or its 16 dims of the output (v) NaN for those that see it, and for
+ * nobody else.  scale * k_factor * log2(e) and 16 * v_factor must be finite.  q and out
+ * 16-byte aligned, strides multiples of 8.  ws: dg_attn4_workspace_bytes(op) bytes,
+ * 16-byte aligned, overwritten; a call that may overlap another needs its own. */
+typedef struct {
+    dg_paged_kv4 kv;
+    int32_t q_len;
+    int32_t heads;
+    int32_t window;
+    int32_t sinks;
+    float scale;
+    int32_t reserved; /* must be 0 */
+    const void* q;
+    void* out;
+    float* lse;
+    int64_t q_stride, out_stride;
+} dg_attn4;
+dg_status dg_attn4_decode(const dg_attn4* op, void* ws, size_t ws_bytes, dg_stream stream);
+/* Workspace of dg_attn4_decode; 0 for an op that it would refuse. */
+size_t dg_attn4_workspace_bytes(const dg_attn4* op);
+
+/* Pages for a step's tokens, and where each token goes.  Sequence b holds lens[b]
+ * tokens (below zero: none) in its first ceil(lens[b] / page_size) table entries and
+ * asks for n = new_lens[b] more (new_len for all where new_lens is NULL); n < 0: it
+ * ends.  Free pages wait in a queue, pool[(first + i) mod pool_size] for i < count,
+ * with pool_state = {first, count}.  In order of b:
+ *   - one that ends gives its pages back, behind the queue's end, to be taken by later
+ *     calls; its length becomes 0 and its table row stays as it is;
+ *   - one fits if its pages then fit the table (max_pages) and, with slots, its tokens
+ *     the map (max_tokens); of those that fit, `asked` is the running sum of pages
+ *     that they need beyond those held, and one is served if it needs none or
+ *     asked <= count.  Served: the next pages of the queue go into its row, its
+ *     length grows by n.  Not served: nothing of it changes.
+ * Token i of sequence b is number starts[b] + i of the map, starts the running sum of
+ * all n >= 0 (served or not; at most 2^31 - 1): slots[.] = page * page_size + place and
+ * positions[.] = lens[b] + i, both -1 for tokens that are not served and in the rest
+ * of the map (max_tokens); a slot whose table entry is below 0 is -1 too.  lens_out,
+ * pool_state_out may be lens, pool_state; other overlaps are not allowed.  Table
+ * entries and pool entries that no rule above names stay as they are.  May be NULL:
+ * new_lens, starts [batch + 1], slots (int64, max_tokens 0 without), positions.
+ * pool_size must be at least the number of pages there are.  ws:
+ * dg_pages_workspace_bytes(op) bytes (0 for small calls: ws may be NULL then), 16-byte
+ * aligned, overwritten; a call that may overlap another needs its own. */
+typedef struct {
+    int32_t batch;      /* up to 2^20 */
+    int32_t page_size;
+    int32_t max_pages;
+    int32_t pool_size;
+    int32_t new_len;
+    int32_t max_tokens;
+    int64_t table_stride; /* at least max_pages, or batch 1 */
+    const int32_t* lens;
+    const int32_t* new_lens;
+    int32_t* lens_out;
+    int32_t* block_table;
+    int32_t* pool;
+    const int32_t* pool_state;
+    int32_t* pool_state_out;
+    int32_t* starts;
+    int64_t* slots;
+    int32_t* positions;
+} dg_page_plan;
+dg_status dg_assign_pages(const dg_page_plan* op, void* ws, size_t ws_bytes, dg_stream stream);
+/* Workspace of dg_assign_pages; 0 where it needs none, or would refuse the op. */
+size_t dg_pages_workspace_bytes(const dg_page_plan* op);
+
+/* Log probabilities of given tokens, entropy and the best alternatives, from logits
+ * [rows][V] (type, or fp32 with logits_f32; `stride` elements between rows), with
+ * z = scale * logit (scale, 1 / temperature, above 0):
+ *   lse = log sum e^z,   logprob = z_token - lse,   entropy = lse - sum e^(z - lse) z
+ *   rank = how many tokens come before the given one
+ *   top_ids, top_logprobs [rows][top_k]: the first top_k tokens and their z - lse
+ * in the order of larger logit, then lower index; a NaN counts below every number.
+ * Logits of -infinity have no part in the sums; a row of nothing else has lse
+ * and logprobs of -infinity and entropy 0.  A row that holds NaN or +infinity has
+ * NaN for its numbers; order and ranks stay.  A token outside [0, V) has logprob
+ * -infinity (NaN in such a row) and rank V.  0 <= top_k <= min(V, 32); up to 2^22 rows and
+ * V up to 2^30.  May be NULL: tokens (with logprob and rank), logprob, rank, entropy,
+ * lse, and with top_k 0 top_ids and top_logprobs (else one of the two); one output at
+ * least.  Any alignment of the logits' own size works; 16 bytes and strides of
+ * whole 16 bytes take wider loads.  Results do not depend on the order in which CTAs run.  ws:
+ * dg_logprobs_workspace_bytes(op) bytes, 16-byte aligned, overwritten; a call that may overlap
+ * another needs its own. */
+typedef struct {
+    int32_t type;       /* dg_ftype of the logits, where logits_f32 is 0 */
+    int32_t logits_f32; /* 0 or 1 */
+    int32_t rows;
+    int32_t V;
+    int32_t top_k;
+    float scale;
+    int64_t stride;
+    const void* logits;
+    const int32_t* tokens;
+    float* logprob;
+    int32_t* rank;
+    float* entropy;
+    float* lse;
+    int32_t* top_ids;
+    float* top_logprobs;
+} dg_logprobs;
+dg_status dg_token_logprobs(const dg_logprobs* op, void* ws, size_t ws_bytes, dg_stream stream);
+/* Workspace of dg_token_logprobs (0 where it needs none); 0 for an op that it would refuse. */
+size_t dg_logprobs_workspace_bytes(const dg_logprobs* op);
 
 /* Synchronizes `stream`, then reports DG_ERR_CUDA for a sticky CUDA error or
  * DG_ERR_TIMEOUT if a bounded device-side wait gave up on the current device

@@ -19,6 +19,9 @@ __all__ = [
     "NORM_RMS", "NORM_LAYER", "MOE_SOFTMAX", "MOE_SIGMOID", "PagedKV", "Append", "Attention",
     "Norm", "Moe", "paged_kv", "append", "kv_append", "attention", "attn_decode",
     "attn_workspace_bytes", "norm", "norm_residual", "moe", "moe_forward", "moe_workspace_bytes",
+    "PagedKV4", "HeadAppend", "KV4Rows", "Attention4", "PagePlan", "Logprobs", "paged_kv4", "head_append",
+    "qkv_append", "kv4_rows", "kv4_read", "attention4", "attn4_decode", "attn4_workspace_bytes", "page_plan",
+    "assign_pages", "pages_workspace_bytes", "logprobs", "token_logprobs", "logprobs_workspace_bytes",
     "check_device_status", "selftest_wait_timeout", "status_string", "probe_copy", "probe_read", "version",
     "library_path", "load",
 ]
@@ -120,6 +123,80 @@ class Moe(ctypes.Structure):
     ]
 
 
+class PagedKV4(ctypes.Structure):
+    """Mirror of the C struct dg_paged_kv4."""
+    _fields_ = [
+        ("type", ctypes.c_int32), ("batch", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
+        ("scale_token_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+        ("k_factor", ctypes.c_float), ("v_factor", ctypes.c_float),
+        ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p),
+    ]
+
+
+class HeadAppend(ctypes.Structure):
+    """Mirror of the C struct dg_head_append."""
+    _fields_ = [
+        ("kv", PagedKV), ("kv4", PagedKV4), ("bits", ctypes.c_int32), ("q_len", ctypes.c_int32),
+        ("tokens", ctypes.c_int32), ("heads", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("max_pos", ctypes.c_int32), ("norm", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("w_offset", ctypes.c_float), ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64), ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+        ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+    ]
+
+
+class KV4Rows(ctypes.Structure):
+    """Mirror of the C struct dg_kv4_rows."""
+    _fields_ = [
+        ("kv", PagedKV4), ("q_len", ctypes.c_int32), ("tokens", ctypes.c_int32),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("slots", ctypes.c_void_p),
+    ]
+
+
+class Attention4(ctypes.Structure):
+    """Mirror of the C struct dg_attn4."""
+    _fields_ = [
+        ("kv", PagedKV4), ("q_len", ctypes.c_int32), ("heads", ctypes.c_int32),
+        ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32), ("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+    ]
+
+
+class PagePlan(ctypes.Structure):
+    """Mirror of the C struct dg_page_plan."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("pool_size", ctypes.c_int32), ("new_len", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+        ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p),
+        ("lens_out", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("pool", ctypes.c_void_p),
+        ("pool_state", ctypes.c_void_p), ("pool_state_out", ctypes.c_void_p),
+        ("starts", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+    ]
+
+
+class Logprobs(ctypes.Structure):
+    """Mirror of the C struct dg_logprobs."""
+    _fields_ = [
+        ("type", ctypes.c_int32), ("logits_f32", ctypes.c_int32), ("rows", ctypes.c_int32),
+        ("V", ctypes.c_int32), ("top_k", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("stride", ctypes.c_int64), ("logits", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+        ("logprob", ctypes.c_void_p), ("rank", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("top_ids", ctypes.c_void_p), ("top_logprobs", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -158,6 +235,11 @@ def load():
         "dg_attn_decode": [P, P, Z, P],
         "dg_norm_residual": [P, P],
         "dg_moe_forward": [P, P, Z, P],
+        "dg_qkv_append": [P, P],
+        "dg_kv4_read": [P, P],
+        "dg_attn4_decode": [P, P, Z, P],
+        "dg_assign_pages": [P, P, Z, P],
+        "dg_token_logprobs": [P, P, Z, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -165,7 +247,8 @@ def load():
         f.restype = ctypes.c_int
     lib.dg_workspace_bytes.argtypes = [P, I]
     lib.dg_workspace_bytes.restype = Z
-    for name in ("dg_attn_workspace_bytes", "dg_moe_workspace_bytes"):
+    for name in ("dg_attn_workspace_bytes", "dg_moe_workspace_bytes", "dg_attn4_workspace_bytes",
+                 "dg_pages_workspace_bytes", "dg_logprobs_workspace_bytes"):
         getattr(lib, name).argtypes = [P]
         getattr(lib, name).restype = Z
     lib.dg_status_string.argtypes = [I]
@@ -513,6 +596,203 @@ def moe_workspace_bytes(op):
 def moe_forward(op, ws, stream=None):
     """A mixture-of-experts layer for a few tokens."""
     _call("dg_moe_forward", ctypes.byref(op), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+# ---- a serving step -----------------------------------------------------------------
+
+def _paging(block_table, seq_lens, where):
+    """batch, max_pages and table stride of a block table int32 [batch][max_pages]."""
+    import torch
+    _fits(block_table.dim() == 2 and block_table.dtype == torch.int32 and
+          (block_table.shape[1] <= 1 or block_table.stride(1) == 1), where)
+    batch, pages = block_table.shape
+    _fits(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and
+          0 < seq_lens.numel() == batch, where)
+    stride = block_table.stride(0) if batch > 1 else pages
+    _fits(stride >= pages, where)
+    return batch, pages, stride
+
+
+def paged_kv4(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, dtype=None, k_factor=1.0,
+              v_factor=1.0):
+    """A paged cache held in 4 bits: codes uint8 [pages][page_size][kv_heads][head_dim / 2],
+    scales uint8 or float8_e4m3fn [pages][page_size][kv_heads][head_dim / 16] (any
+    strides with the last dimension contiguous, keys and values alike: a [pages][kv_heads]
+    [page_size][..] cache, the faster order, is passed transposed); block_table and seq_lens
+    as for paged_kv; dtype: of the q, k, v and out beside it (float16 by default)."""
+    import torch
+    where = "paged_kv4"
+    dtype = torch.float16 if dtype is None else dtype
+    _fits(dtype in (torch.float16, torch.bfloat16), where)
+    _fits(k_codes.dim() == 4 and k_codes.shape == v_codes.shape and k_codes.stride() == v_codes.stride() and
+          k_codes.stride(3) == 1 and k_codes.dtype == v_codes.dtype == torch.uint8, where)
+    _fits(k_scales.dim() == 4 and k_scales.shape == v_scales.shape and
+          k_scales.stride() == v_scales.stride() and (k_scales.shape[3] <= 1 or k_scales.stride(3) == 1) and
+          k_scales.dtype in (torch.uint8, torch.float8_e4m3fn) and v_scales.dtype == k_scales.dtype, where)
+    pages, page_size, heads, half = k_codes.shape
+    _fits(half % 8 == 0 and tuple(k_scales.shape) == (pages, page_size, heads, half // 8), where)
+    batch, max_pages, table_stride = _paging(block_table, seq_lens, where)
+    return PagedKV4(F16 if dtype == torch.float16 else BF16, batch, heads, 2 * half, page_size, pages, max_pages, 0,
+                    _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), *k_codes.stride()[:3],
+                    *k_scales.stride()[:3], k_factor, v_factor, _ptr(block_table), table_stride, _ptr(seq_lens))
+
+
+def head_append(kv, q, k, v, q_out=None, q_len=None, cos=None, sin=None, interleaved=False, w_q=None, w_k=None,
+                eps=1e-6, w_offset=0.0, kind=NORM_RMS, slots=None, positions=None):
+    """Describes qkv_append into kv, a paged_kv or a paged_kv4: q [tokens][heads][head_dim]
+    (or None), k and v with kv_heads heads; w_q and w_k [head_dim], or None for no norm;
+    cos, sin, interleaved and q_out as for append.  Tokens are the last q_len (1 by
+    default) of each sequence, or those of slots (int64) and positions (int32)."""
+    import torch
+    where, dt, dim = "head_append", _kv_dtype(kv), kv.head_dim
+    by_map = slots is not None
+    _fits(by_map == (positions is not None) and not (by_map and q_len is not None), where)
+    if by_map:
+        _contiguous(where, torch.int64, slots)
+        _contiguous(where, torch.int32, positions)
+        tokens, q_len = slots.numel(), 0
+        _fits(tokens > 0 and positions.numel() == tokens, where)
+    else:
+        q_len = 1 if q_len is None else q_len
+        _fits(q_len > 0, where)
+        tokens = kv.batch * q_len
+    heads = 0 if q is None else q.numel() // (tokens * dim)
+    q_out = q if q_out is None else q_out
+    qs = qos = 0
+    if q is not None:
+        qs = _head_rows(q, tokens, heads, dim, dt, where)
+        qos = _head_rows(q_out, tokens, heads, dim, dt, where)
+    ks = _head_rows(k, tokens, kv.kv_heads, dim, dt, where)
+    vs = _head_rows(v, tokens, kv.kv_heads, dim, dt, where)
+    rot = max_pos = 0
+    _fits((cos is None) == (sin is None), where)
+    if cos is not None:
+        _contiguous(where, torch.float32, cos, sin)
+        _fits(cos.dim() == 2 and cos.shape == sin.shape, where)
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    _contiguous(where, dt, w_q, w_k)
+    for w in (w_q, w_k):
+        _fits(w is None or w.numel() == dim, where)
+    four = isinstance(kv, PagedKV4)
+    return HeadAppend(PagedKV() if four else kv, kv if four else PagedKV4(), 4 if four else 16, q_len,
+                      tokens if by_map else 0, heads, rot, int(interleaved), max_pos, kind, eps, w_offset, _ptr(q),
+                      _ptr(k), _ptr(v), _ptr(q_out), qs, ks, vs, qos, _ptr(cos), _ptr(sin), _ptr(w_q), _ptr(w_k),
+                      _ptr(slots), _ptr(positions))
+
+
+def qkv_append(op, stream=None):
+    """Head norms, rotary positions and the append, to a 16-bit or a 4-bit cache."""
+    _call("dg_qkv_append", ctypes.byref(op), _stream(stream))
+
+
+def kv4_rows(kv, k=None, v=None, q_len=None, slots=None):
+    """Describes kv4_read: k and v [tokens][kv_heads][head_dim] of the cache's dtype (or
+    None) receive the last q_len positions of each sequence (1 by default), or what
+    lies in slots (int64)."""
+    import torch
+    where, dt = "kv4_rows", _kv_dtype(kv)
+    _fits(not (slots is not None and q_len is not None) and not (k is None and v is None), where)
+    _contiguous(where, torch.int64, slots)
+    if slots is None:
+        q_len = 1 if q_len is None else q_len
+    tokens = slots.numel() if slots is not None else kv.batch * q_len
+    _fits(tokens > 0, where)
+    row = kv.kv_heads * kv.head_dim
+    rows = lambda t: 0 if t is None else max(row, _head_rows(t, tokens, kv.kv_heads, kv.head_dim, dt, where))
+    return KV4Rows(kv, 0 if slots is not None else q_len, tokens, _ptr(k), _ptr(v), rows(k), rows(v), _ptr(slots))
+
+
+def kv4_read(op, stream=None):
+    """A 4-bit cache's keys and values back in 16 bits."""
+    _call("dg_kv4_read", ctypes.byref(op), _stream(stream))
+
+
+def attention4(kv, q, out, lse=None, q_len=1, scale=None, window=0, sinks=0):
+    """Describes attn4_decode over a paged_kv4; the rest as for attention."""
+    import torch
+    where, dt = "attention4", _kv_dtype(kv)
+    _fits(q_len > 0, where)
+    tokens, dim = kv.batch * q_len, kv.head_dim
+    heads = q.numel() // (tokens * dim)
+    qs = _head_rows(q, tokens, heads, dim, dt, where)
+    os_ = _head_rows(out, tokens, heads, dim, dt, where)
+    _contiguous(where, torch.float32, lse)
+    _fits(lse is None or lse.numel() == tokens * heads, where)
+    return Attention4(kv, q_len, heads, window, sinks, dim ** -0.5 if scale is None else scale, 0,
+                      _ptr(q), _ptr(out), _ptr(lse), qs, os_)
+
+
+def attn4_workspace_bytes(op):
+    return int(load().dg_attn4_workspace_bytes(ctypes.byref(op)))
+
+
+def attn4_decode(op, ws, stream=None):
+    """Attention of a step's new tokens over the paged 4-bit cache."""
+    _call("dg_attn4_decode", ctypes.byref(op), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def page_plan(lens, block_table, pool, pool_state, page_size, new_lens=None, new_len=1, lens_out=None,
+              pool_state_out=None, starts=None, slots=None, positions=None):
+    """Describes assign_pages: lens and new_lens int32 [batch] (new_len for every sequence
+    without), block_table int32 [batch][max_pages], pool int32 [..] with pool_state
+    int32 (first, count); lens and pool_state are updated in place unless given an
+    output; starts int32 [batch + 1], slots int64 and positions int32 [tokens] or None."""
+    import torch
+    where = "page_plan"
+    batch, max_pages, stride = _paging(block_table, lens, where)
+    lens_out = lens if lens_out is None else lens_out
+    pool_state_out = pool_state if pool_state_out is None else pool_state_out
+    _contiguous(where, torch.int32, new_lens, lens_out, pool, pool_state, pool_state_out, starts, positions)
+    _contiguous(where, torch.int64, slots)
+    for t, n in ((new_lens, batch), (lens_out, batch), (pool_state, 2), (pool_state_out, 2), (starts, batch + 1)):
+        _fits(t is None or t.numel() == n, where)
+    tokens = 0 if slots is None else slots.numel()
+    _fits(positions is None or positions.numel() == tokens, where)
+    return PagePlan(batch, page_size, max_pages, pool.numel(), new_len, tokens, stride, _ptr(lens), _ptr(new_lens),
+                    _ptr(lens_out), _ptr(block_table), _ptr(pool), _ptr(pool_state), _ptr(pool_state_out),
+                    _ptr(starts), _ptr(slots), _ptr(positions))
+
+
+def pages_workspace_bytes(op):
+    return int(load().dg_pages_workspace_bytes(ctypes.byref(op)))
+
+
+def assign_pages(op, ws=None, stream=None):
+    """Pages for a step's tokens, and the slots where they go."""
+    _call("dg_assign_pages", ctypes.byref(op), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def logprobs(logits, tokens=None, logprob=None, rank=None, entropy=None, lse=None, top_ids=None,
+             top_logprobs=None, scale=1.0):
+    """Describes token_logprobs: logits [rows][V] (or [V]) fp16, bf16 or fp32, rows any
+    stride apart; tokens int32 [rows]; outputs, each optional: logprob, entropy, lse
+    fp32 [rows], rank int32 [rows], top_ids int32 and top_logprobs fp32 [rows][top_k]."""
+    import torch
+    where = "logprobs"
+    f32 = logits.dtype == torch.float32
+    kind = F16 if f32 else _ftype(logits, where)
+    _fits(logits.dim() in (1, 2) and logits.numel() > 0 and (logits.shape[-1] == 1 or logits.stride(-1) == 1), where)
+    rows, V = (1, logits.shape[0]) if logits.dim() == 1 else logits.shape
+    stride = logits.stride(0) if rows > 1 else V
+    _contiguous(where, torch.int32, tokens, rank, top_ids)
+    _contiguous(where, torch.float32, logprob, entropy, lse, top_logprobs)
+    for t in (tokens, rank, logprob, entropy, lse):
+        _fits(t is None or t.numel() == rows, where)
+    top = top_ids if top_ids is not None else top_logprobs
+    top_k = 0 if top is None else top.numel() // rows
+    for t in (top_ids, top_logprobs):
+        _fits(t is None or t.numel() == rows * top_k, where)
+    return Logprobs(kind, int(f32), rows, V, top_k, scale, stride, _ptr(logits), _ptr(tokens), _ptr(logprob),
+                    _ptr(rank), _ptr(entropy), _ptr(lse), _ptr(top_ids), _ptr(top_logprobs))
+
+
+def logprobs_workspace_bytes(op):
+    return int(load().dg_logprobs_workspace_bytes(ctypes.byref(op)))
+
+
+def token_logprobs(op, ws=None, stream=None):
+    """Log probabilities of given tokens, entropy and the best alternatives."""
+    _call("dg_token_logprobs", ctypes.byref(op), _ptr(ws), _nbytes(ws), _stream(stream))
 
 
 def check_device_status(stream=None):

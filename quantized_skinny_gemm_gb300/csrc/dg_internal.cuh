@@ -366,6 +366,15 @@ size_t attn_ws_bytes(const dg_attn& op);
 cudaError_t launch_attn(const dg_attn& op, void* ws, cudaStream_t s);
 size_t moe_ws_bytes(const dg_moe& op);
 cudaError_t launch_moe(const dg_moe& op, void* ws, cudaStream_t s);
+// A serving step (arguments checked by layer_api.cu).
+cudaError_t launch_head_append(const dg_head_append& op, cudaStream_t s);
+cudaError_t launch_kv4_read(const dg_kv4_rows& op, cudaStream_t s);
+size_t attn4_ws_bytes(const dg_attn4& op);
+cudaError_t launch_attn4(const dg_attn4& op, void* ws, cudaStream_t s);
+size_t plan_ws_bytes(const dg_page_plan& op);
+cudaError_t launch_plan(const dg_page_plan& op, void* ws, cudaStream_t s);
+size_t lp_ws_bytes(const dg_logprobs& op);
+cudaError_t launch_logprobs(const dg_logprobs& op, void* ws, cudaStream_t s);
 cudaError_t launch_probe_read(const void* src, size_t bytes, uint32_t* sink, cudaStream_t s);
 
 }  // namespace dg

@@ -143,6 +143,143 @@ static dg_status check_moe(const dg_moe& op) {
     return DG_OK;
 }
 
+// ---- a serving step ---------------------------------------------------------------------
+
+// (table and lengths belong to a cache also where an op has slots)
+static dg_status check_kv4(const dg_paged_kv4& kv, int heads) {
+    if (kv.type != DG_F16 && kv.type != DG_BF16) return DG_ERR_INVALID_ARG;
+    if (kv.batch < 1 || kv.kv_heads < 1 || kv.head_dim < 1 || kv.page_size < 1 || kv.num_pages < 1 ||
+        kv.max_pages < 1 || kv.reserved)
+        return DG_ERR_INVALID_ARG;
+    if (!kv.k || !kv.v || !kv.k_scale || !kv.v_scale || !kv.block_table || !kv.seq_lens) return DG_ERR_INVALID_ARG;
+    if (kv.page_stride < 0 || kv.token_stride < 0 || kv.head_stride < 0 || kv.scale_page_stride < 0 ||
+        kv.scale_token_stride < 0 || kv.scale_head_stride < 0)
+        return DG_ERR_INVALID_ARG;
+    if (!(kv.k_factor > 0.f) || !(kv.v_factor > 0.f) || !std::isfinite(7.f * kv.k_factor) ||
+        !std::isfinite(16.f * kv.v_factor))
+        return DG_ERR_INVALID_ARG;
+    if (kv.table_stride < (kv.batch > 1 ? kv.max_pages : 0)) return DG_ERR_INVALID_ARG;
+    if (kv.batch > kMaxBatch || kv.kv_heads > kMaxHeads || heads > kMaxHeads) return DG_ERR_UNSUPPORTED;
+    if (kv.head_dim % 16 || kv.head_dim > 256) return DG_ERR_UNSUPPORTED;
+    if (!aligned(kv.block_table, 4) || !aligned(kv.seq_lens, 4) || !aligned(kv.k, 8) || !aligned(kv.v, 8) ||
+        kv.page_stride % 8 || kv.token_stride % 8 || kv.head_stride % 8)
+        return DG_ERR_MISALIGNED;
+    return DG_OK;
+}
+
+static dg_status check_head_append(const dg_head_append& op) {
+    if (op.bits != 16 && op.bits != 4) return DG_ERR_INVALID_ARG;
+    if (op.slots ? op.tokens < 1 || op.q_len || !op.positions : op.tokens || op.q_len < 1 || op.positions)
+        return DG_ERR_INVALID_ARG;
+    if (op.q_len > kMaxQLen) return DG_ERR_UNSUPPORTED;
+    const dg_status st = op.bits == 4 ? check_kv4(op.kv4, op.heads) : check_kv(op.kv, 1, op.heads);
+    if (st != DG_OK) return st;
+    const int D = op.bits == 4 ? op.kv4.head_dim : op.kv.head_dim, kvh = op.bits == 4 ? op.kv4.kv_heads : op.kv.kv_heads;
+    const int batch = op.bits == 4 ? op.kv4.batch : op.kv.batch;
+    if (op.heads < 0 || (op.heads > 0) != (op.q != nullptr) || (op.heads > 0) != (op.q_out != nullptr) || !op.k || !op.v)
+        return DG_ERR_INVALID_ARG;
+    if ((op.w_q && !op.q) || (op.norm != DG_NORM_RMS && op.norm != DG_NORM_LAYER) || !(op.eps >= 0.f) ||
+        !std::isfinite(op.eps) || !std::isfinite(op.w_offset))
+        return DG_ERR_INVALID_ARG;
+    if (op.interleaved != 0 && op.interleaved != 1) return DG_ERR_INVALID_ARG;
+    if (op.rot_dim < 0 || op.rot_dim % 2 || op.rot_dim > D) return DG_ERR_INVALID_ARG;
+    if (op.rot_dim && (!op.cos || !op.sin || op.max_pos < 1)) return DG_ERR_INVALID_ARG;
+    if (op.q_stride < 0 || op.k_stride < 0 || op.v_stride < 0) return DG_ERR_INVALID_ARG;
+    if (op.heads && op.q_out_stride < (int64_t)op.heads * D) return DG_ERR_INVALID_ARG;
+    if (op.heads && op.q_out == op.q && op.q_out_stride != op.q_stride) return DG_ERR_INVALID_ARG;
+    // a CTA takes four heads at least
+    const int64_t tokens = op.slots ? op.tokens : (int64_t)batch * op.q_len;
+    if (tokens * ((op.heads + 2 * kvh + 3) / 4) > 0x7fffffff) return DG_ERR_UNSUPPORTED;
+    const void* p2[] = {op.q, op.k, op.v, op.q_out, op.w_q, op.w_k, op.bits == 16 ? op.kv.k : nullptr,
+                        op.bits == 16 ? op.kv.v : nullptr};
+    for (const void* p : p2)
+        if (!aligned(p, 2)) return DG_ERR_MISALIGNED;
+    if (op.rot_dim && (!aligned(op.cos, 4) || !aligned(op.sin, 4))) return DG_ERR_MISALIGNED;
+    if (!aligned(op.slots, 8) || !aligned(op.positions, 4)) return DG_ERR_MISALIGNED;
+    return DG_OK;
+}
+
+static dg_status check_kv4_rows(const dg_kv4_rows& op) {
+    const dg_status st = check_kv4(op.kv, 0);
+    if (st != DG_OK) return st;
+    if (op.tokens < 1 || (!op.k && !op.v)) return DG_ERR_INVALID_ARG;
+    if (op.slots ? op.q_len != 0 : op.q_len < 1 || op.tokens != (int64_t)op.kv.batch * op.q_len)
+        return DG_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)op.kv.kv_heads * op.kv.head_dim;
+    if ((op.k && op.k_stride < row) || (op.v && op.v_stride < row)) return DG_ERR_INVALID_ARG;
+    if (!aligned(op.k, 2) || !aligned(op.v, 2) || !aligned(op.slots, 8)) return DG_ERR_MISALIGNED;
+    return DG_OK;
+}
+
+static dg_status check_attn4(const dg_attn4& op) {
+    const dg_status st = check_kv4(op.kv, op.heads);
+    if (st != DG_OK) return st;
+    if (op.reserved || op.q_len < 1 || op.heads < 1 || !op.q || !op.out) return DG_ERR_INVALID_ARG;
+    if (op.q_len > kMaxQLen) return DG_ERR_UNSUPPORTED;
+    if (op.heads % op.kv.kv_heads || op.window < 0 || op.sinks < 0 ||
+        !std::isfinite(op.scale * 1.4426950408889634f * 16.f) ||
+        !std::isfinite(op.scale * 1.4426950408889634f * 16.f * op.kv.k_factor))
+        return DG_ERR_INVALID_ARG;
+    if ((int64_t)op.kv.batch * op.q_len * op.heads > 0x7fffffff) return DG_ERR_UNSUPPORTED;
+    if (op.q_stride < 0 || op.out_stride < (int64_t)op.heads * op.kv.head_dim) return DG_ERR_INVALID_ARG;
+    if (!aligned(op.q, 16) || !aligned(op.out, 16) || op.q_stride % 8 || op.out_stride % 8 ||
+        (op.lse && !aligned(op.lse, 4)))
+        return DG_ERR_MISALIGNED;
+    return DG_OK;
+}
+
+static dg_status check_plan(const dg_page_plan& op) {
+    if (op.batch < 1 || op.page_size < 1 || op.max_pages < 1 || op.pool_size < 1 || op.max_tokens < 0)
+        return DG_ERR_INVALID_ARG;
+    if (!op.lens || !op.lens_out || !op.block_table || !op.pool || !op.pool_state || !op.pool_state_out)
+        return DG_ERR_INVALID_ARG;
+    if ((op.slots != nullptr) != (op.max_tokens > 0) || (op.positions && !op.slots)) return DG_ERR_INVALID_ARG;
+    if (op.table_stride < (op.batch > 1 ? op.max_pages : 0)) return DG_ERR_INVALID_ARG;
+    if (op.batch > kMaxBatch) return DG_ERR_UNSUPPORTED;
+    const void* p4[] = {op.lens, op.new_lens, op.lens_out, op.block_table, op.pool, op.pool_state, op.pool_state_out,
+                        op.starts, op.positions};
+    for (const void* p : p4)
+        if (!aligned(p, 4)) return DG_ERR_MISALIGNED;
+    if (!aligned(op.slots, 8)) return DG_ERR_MISALIGNED;
+    // what is written apart from what is read and from each other; lens_out may be lens
+    // and pool_state_out pool_state
+    const size_t B = (size_t)op.batch * 4,
+                 table = ((size_t)(op.batch - 1) * op.table_stride + op.max_pages) * 4;
+    struct Area {
+        const void* p;
+        size_t bytes;
+    };
+    const Area out[] = {{op.lens_out, B}, {op.pool_state_out, 8}, {op.block_table, table},
+                        {op.pool, (size_t)op.pool_size * 4}, {op.starts, B + 4},
+                        {op.slots, (size_t)op.max_tokens * 8}, {op.positions, (size_t)op.max_tokens * 4}};
+    const Area in[] = {{op.lens, B}, {op.pool_state, 8}, {op.new_lens, B}};
+    for (const Area& o : out) {
+        for (const Area& i : in)
+            if (overlap(o.p, o.bytes, i.p, i.bytes) && !(o.p == i.p && &o - out == &i - in)) return DG_ERR_INVALID_ARG;
+        for (const Area& x : out)
+            if (&x != &o && overlap(o.p, o.bytes, x.p, x.bytes)) return DG_ERR_INVALID_ARG;
+    }
+    return DG_OK;
+}
+
+static dg_status check_logprobs(const dg_logprobs& op) {
+    if (op.type != DG_F16 && op.type != DG_BF16) return DG_ERR_INVALID_ARG;
+    if ((op.logits_f32 != 0 && op.logits_f32 != 1) || op.rows < 1 || op.V < 1 || op.top_k < 0 || op.top_k > op.V)
+        return DG_ERR_INVALID_ARG;
+    if (!op.logits || op.stride < (op.rows > 1 ? op.V : 0) || !(op.scale > 0.f) ||
+        !std::isfinite(op.scale * 1.4426950408889634f))
+        return DG_ERR_INVALID_ARG;
+    if ((!op.tokens && (op.logprob || op.rank)) || (op.top_k > 0) != (op.top_ids || op.top_logprobs))
+        return DG_ERR_INVALID_ARG;
+    if (!op.logprob && !op.rank && !op.entropy && !op.lse && !op.top_k) return DG_ERR_INVALID_ARG;
+    if (op.top_k > 32 || op.rows > (1 << 22) || op.V > (1 << 30)) return DG_ERR_UNSUPPORTED;
+    if (!aligned(op.logits, op.logits_f32 ? 4 : 2)) return DG_ERR_MISALIGNED;
+    const void* p4[] = {op.tokens, op.logprob, op.rank, op.entropy, op.lse, op.top_ids, op.top_logprobs};
+    for (const void* p : p4)
+        if (!aligned(p, 4)) return DG_ERR_MISALIGNED;
+    return DG_OK;
+}
+
 static dg_status check_ws(const void* ws, size_t have, size_t need) {
     if (!ws || have < need) return DG_ERR_WORKSPACE;
     return aligned(ws, 16) ? DG_OK : DG_ERR_MISALIGNED;
@@ -188,6 +325,56 @@ dg_status dg_moe_forward(const dg_moe* op, void* ws, size_t ws_bytes, dg_stream 
     if (st != DG_OK) return st;
     if ((st = check_ws(ws, ws_bytes, moe_ws_bytes(*op))) != DG_OK) return st;
     return status_of(launch_moe(*op, ws, stream));
+}
+
+dg_status dg_qkv_append(const dg_head_append* op, dg_stream stream) {
+    if (!op) return DG_ERR_INVALID_ARG;
+    const dg_status st = check_head_append(*op);
+    return st != DG_OK ? st : status_of(launch_head_append(*op, stream));
+}
+
+dg_status dg_kv4_read(const dg_kv4_rows* op, dg_stream stream) {
+    if (!op) return DG_ERR_INVALID_ARG;
+    const dg_status st = check_kv4_rows(*op);
+    return st != DG_OK ? st : status_of(launch_kv4_read(*op, stream));
+}
+
+size_t dg_attn4_workspace_bytes(const dg_attn4* op) {
+    return op && check_attn4(*op) == DG_OK ? attn4_ws_bytes(*op) : 0;
+}
+
+dg_status dg_attn4_decode(const dg_attn4* op, void* ws, size_t ws_bytes, dg_stream stream) {
+    if (!op) return DG_ERR_INVALID_ARG;
+    dg_status st = check_attn4(*op);
+    if (st != DG_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, attn4_ws_bytes(*op))) != DG_OK) return st;
+    return status_of(launch_attn4(*op, ws, stream));
+}
+
+size_t dg_pages_workspace_bytes(const dg_page_plan* op) {
+    return op && check_plan(*op) == DG_OK ? plan_ws_bytes(*op) : 0;
+}
+
+dg_status dg_assign_pages(const dg_page_plan* op, void* ws, size_t ws_bytes, dg_stream stream) {
+    if (!op) return DG_ERR_INVALID_ARG;
+    dg_status st = check_plan(*op);
+    if (st != DG_OK) return st;
+    const size_t need = plan_ws_bytes(*op);
+    if (need && (st = check_ws(ws, ws_bytes, need)) != DG_OK) return st;
+    return status_of(launch_plan(*op, ws, stream));
+}
+
+size_t dg_logprobs_workspace_bytes(const dg_logprobs* op) {
+    return op && check_logprobs(*op) == DG_OK ? lp_ws_bytes(*op) : 0;
+}
+
+dg_status dg_token_logprobs(const dg_logprobs* op, void* ws, size_t ws_bytes, dg_stream stream) {
+    if (!op) return DG_ERR_INVALID_ARG;
+    dg_status st = check_logprobs(*op);
+    if (st != DG_OK) return st;
+    const size_t need = lp_ws_bytes(*op);
+    if (need && (st = check_ws(ws, ws_bytes, need)) != DG_OK) return st;
+    return status_of(launch_logprobs(*op, ws, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,259 @@
+// Pages and slots for the tokens of a step, from the sequences' lengths.
+//
+// Three running sums over the sequences say everything: of the tokens asked for
+// (where a sequence's tokens lie in the map, and whether they fit it), of the pages
+// that the fitting ones need beyond those held (who is served, and which pages of the
+// queue are whose), and of the pages given back.  One CTA takes the sums and leaves a
+// record for each sequence; then each token, page taken and page given back finds its
+// sequence by a search over the records and is written by a thread of its own.
+//
+// Bound by latency: small calls are one CTA that keeps the records in shared memory and
+// writes everything itself; others two launches, the sums by one CTA and the rest by
+// many.
+#include <climits>
+
+#include "elem.cuh"
+
+namespace dg {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanItems = 4;            // sequences of a thread in a round of the large form
+constexpr int kPlanSmallBatch = 1024, kPlanSmallTokens = 16384;
+
+struct PlanTotals {
+    int first, count, taken, given;
+};
+struct PlanParams {
+    dg_page_plan op;
+    FastDiv page;
+    PlanTotals* totals;   // large form: workspace
+    int4* rec;            // [batch + 1]
+};
+
+// A sequence's record: x its first token in the map, y its first page of those taken,
+// z its first page of those given back, w its length, or ~length where it is not
+// served.  Sums past 2^31 - 1 stay there.
+__device__ __forceinline__ int sat(long long v) { return v > INT_MAX ? INT_MAX : (int)v; }
+
+// Inclusive sums over the CTA's threads, and their totals.
+struct Pair {
+    long long a, b;
+};
+__device__ __forceinline__ Pair block_scan(Pair v, Pair* warps, Pair& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, v.a, o), b = __shfl_up_sync(0xffffffffu, v.b, o);
+        if (lane >= o) {
+            v.a += a;
+            v.b += b;
+        }
+    }
+    __syncthreads();   // the last call's sums have been read
+    if (lane == 31) warps[warp] = v;
+    __syncthreads();
+    Pair w = lane < n ? warps[lane] : Pair{0, 0};
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, w.a, o), b = __shfl_up_sync(0xffffffffu, w.b, o);
+        if (lane >= o) {
+            w.a += a;
+            w.b += b;
+        }
+    }
+    total = {__shfl_sync(0xffffffffu, w.a, 31), __shfl_sync(0xffffffffu, w.b, 31)};
+    const Pair before = {__shfl_sync(0xffffffffu, w.a, max(warp - 1, 0)),
+                         __shfl_sync(0xffffffffu, w.b, max(warp - 1, 0))};
+    if (warp) {
+        v.a += before.a;
+        v.b += before.b;
+    }
+    return v;
+}
+
+__device__ __forceinline__ long long pages_of(long long tokens, int page) { return (tokens + page - 1) / page; }
+
+// All running sums, by one CTA.  rec may be shared memory.
+template <int ITEMS>
+__device__ void plan_sums(const PlanParams& p, int4* rec, PlanTotals& out) {
+    __shared__ Pair warps[32];
+    __shared__ int most;
+    const dg_page_plan& op = p.op;
+    const int B = op.batch, N = op.pool_size;
+    int first = op.pool_state[0] % N;
+    if (first < 0) first += N;
+    const int count = min(max(op.pool_state[1], 0), N);
+    if (threadIdx.x == 0) most = 0;
+    __syncthreads();
+    Pair carry = {0, 0}, asked = {0, 0};   // tokens and pages given back; pages asked for
+    int taken = 0;
+    for (int b0 = 0; b0 < B; b0 += blockDim.x * ITEMS) {
+        const int mine = b0 + threadIdx.x * ITEMS;
+        int len[ITEMS], want[ITEMS], back[ITEMS];
+        long long more[ITEMS];
+        Pair sum = {0, 0};
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int b = mine + i;
+            len[i] = want[i] = back[i] = 0;
+            if (b < B) {
+                const int n = op.new_lens ? op.new_lens[b] : op.new_len;
+                len[i] = max(op.lens[b], 0);
+                want[i] = n;
+                if (n < 0) back[i] = (int)min(pages_of(len[i], op.page_size), (long long)op.max_pages);
+            }
+            sum.a += max(want[i], 0);
+            sum.b += back[i];
+        }
+        Pair total;
+        Pair at = block_scan(sum, warps, total);
+        at = {carry.a + at.a - sum.a, carry.b + at.b - sum.b};
+        carry = {carry.a + total.a, carry.b + total.b};
+        Pair need = {0, 0};
+        long long end = at.a;
+        bool fits[ITEMS];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int w = max(want[i], 0);
+            end += w;
+            const long long pages = pages_of((long long)len[i] + w, op.page_size);
+            fits[i] = mine + i < B && want[i] >= 0 && pages <= op.max_pages && (long long)len[i] + w <= INT_MAX &&
+                      (!op.slots || end <= op.max_tokens);
+            more[i] = fits[i] ? pages - pages_of(len[i], op.page_size) : 0;
+            need.a += more[i];
+        }
+        Pair all;
+        Pair pg = block_scan(need, warps, all);
+        long long upto = asked.a + pg.a - need.a;
+        asked.a += all.a;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int b = mine + i;
+            if (b >= B) break;
+            const long long from = upto;
+            upto += more[i];
+            const bool served = fits[i] && (more[i] == 0 || upto <= count);
+            if (served && more[i]) taken = (int)upto;
+            rec[b] = make_int4(sat(at.a), sat(from), sat(at.b), served ? len[i] : ~len[i]);
+            if (op.starts) op.starts[b] = sat(at.a);
+            op.lens_out[b] = want[i] < 0 ? 0 : served ? len[i] + want[i] : op.lens[b];
+            at.a += max(want[i], 0);
+            at.b += back[i];
+        }
+    }
+    if (taken) atomicMax(&most, taken);
+    __syncthreads();
+    out.first = first;
+    out.count = count;
+    out.taken = most;
+    out.given = (int)min(carry.b, (long long)N - count);   // the queue holds no more
+    if (threadIdx.x == 0) {
+        rec[B] = make_int4(sat(carry.a), INT_MAX, INT_MAX, 0);
+        if (op.starts) op.starts[B] = sat(carry.a);
+        op.pool_state_out[0] = (int)(((long long)first + out.taken) % N);
+        op.pool_state_out[1] = count - out.taken + out.given;
+    }
+}
+
+// The last record whose field F is at most v.
+template <int F>
+__device__ __forceinline__ int find(const int4* rec, int B, int v) {
+    int lo = 0, hi = B;   // rec[lo] <= v < rec[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        const int x = F == 0 ? rec[mid].x : F == 1 ? rec[mid].y : rec[mid].z;
+        if (x <= v) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Tokens, pages taken and pages given back, by all threads of the launch.
+__device__ __forceinline__ void plan_fill(const PlanParams& p, const int4* rec, const PlanTotals& t, unsigned id,
+                                          unsigned threads) {
+    const dg_page_plan& op = p.op;
+    const int N = op.pool_size;
+    auto queue = [&](int i) { return (int)(((long long)t.first + i) % N); };
+    const int tokens = min(rec[op.batch].x, op.max_tokens);
+    if (op.slots) {
+        for (long long i = id; i < op.max_tokens; i += threads) {
+            long long slot = -1;
+            int pos = -1;
+            if (i < tokens) {
+                const int b = find<0>(rec, op.batch, (int)i);
+                const int4 r = rec[b];
+                if (r.w >= 0) {
+                    pos = r.w + ((int)i - r.x);
+                    const int at = pos / p.page, held = (int)pages_of(r.w, op.page_size);
+                    const int page = at < held ? op.block_table[(long long)b * op.table_stride + at]
+                                               : op.pool[queue(r.y + at - held)];
+                    if (page >= 0) slot = (long long)page * op.page_size + (pos - at * op.page_size);
+                }
+            }
+            op.slots[i] = slot;
+            if (op.positions) op.positions[i] = pos;
+        }
+    }
+    for (long long i = id; i < t.taken; i += threads) {
+        const int b = find<1>(rec, op.batch, (int)i);
+        const int4 r = rec[b];
+        op.block_table[(long long)b * op.table_stride + pages_of(r.w, op.page_size) + ((int)i - r.y)] =
+            op.pool[queue((int)i)];
+    }
+    for (long long i = id; i < t.given; i += threads) {
+        const int b = find<2>(rec, op.batch, (int)i);
+        op.pool[(int)(((long long)t.first + t.count + i) % N)] =
+            op.block_table[(long long)b * op.table_stride + ((int)i - rec[b].z)];
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) k_plan_small(const PlanParams p) {
+    __shared__ int4 rec[kPlanSmallBatch + 1];
+    griddep_launch_dependents();
+    griddep_wait();
+    PlanTotals t;
+    plan_sums<1>(p, rec, t);
+    __syncthreads();
+    plan_fill(p, rec, t, threadIdx.x, blockDim.x);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) k_plan_sums(const PlanParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    PlanTotals t;
+    plan_sums<kPlanItems>(p, p.rec, t);
+    if (threadIdx.x == 0) *p.totals = t;
+}
+
+__global__ void __launch_bounds__(256) k_plan_fill(const PlanParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const PlanTotals t = *p.totals;
+    plan_fill(p, p.rec, t, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+}
+
+static bool plan_small(const dg_page_plan& op) {
+    return op.batch <= kPlanSmallBatch && op.max_tokens <= kPlanSmallTokens;
+}
+
+size_t plan_ws_bytes(const dg_page_plan& op) {
+    return plan_small(op) ? 0 : sizeof(PlanTotals) + ((size_t)op.batch + 1) * sizeof(int4);
+}
+
+cudaError_t launch_plan(const dg_page_plan& op, void* ws, cudaStream_t s) {
+    PlanParams p{op, fast_div((uint32_t)op.page_size), static_cast<PlanTotals*>(ws),
+                 reinterpret_cast<int4*>(static_cast<char*>(ws) + sizeof(PlanTotals))};
+    void* args[] = {&p};
+    if (plan_small(op)) {
+        const int work = op.batch > op.max_tokens ? op.batch : op.max_tokens;
+        const int threads = work <= 128 ? 128 : work <= 256 ? 256 : kPlanThreads;
+        return launch_pdl((const void*)k_plan_small, dim3(1),
+                          dim3(op.batch > threads ? kPlanThreads : threads), 0, s, args);
+    }
+    const cudaError_t e = launch_pdl((const void*)k_plan_sums, dim3(1), dim3(kPlanThreads), 0, s, args);
+    if (e != cudaSuccess) return e;
+    const long long want = ((long long)op.max_tokens + 4ll * op.batch + 255) / 256, most = sm_count() * 8ll;
+    return launch_pdl((const void*)k_plan_fill, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, s, args);
+}
+
+}  // namespace dg

@@ -1,0 +1,179 @@
+"""dg_token_logprobs against the definition in 64 bits: rows of every length around a vector
+and a tile, ties, masked words, infinities and NaN, odd alignment, parts, graphs."""
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as ref
+import quantized_skinny_gemm_gb300 as dg
+import serve_ref
+from gpu_util import DEV, need_gpu, sync
+
+pytestmark = pytest.mark.gpu
+DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def run(x, tokens, top_k, scale=1.0, stream=None):
+    """x on the device.  logprob, rank, entropy, lse, top_ids, top_logprobs on the host."""
+    R = x.shape[0]
+    f = lambda *s: torch.full(s, 77.0, dtype=torch.float32, device=DEV)
+    i = lambda *s: torch.full(s, 77, dtype=torch.int32, device=DEV)
+    out = dict(logprob=f(R), rank=i(R), entropy=f(R), lse=f(R))
+    if top_k:
+        out.update(top_ids=i(R, top_k), top_logprobs=f(R, top_k))
+    td = torch.tensor(tokens, dtype=torch.int32, device=DEV)
+    op = dg.logprobs(x, tokens=td, scale=scale, **out)
+    need = dg.logprobs_workspace_bytes(op)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV) if need else None
+    dg.token_logprobs(op, ws, stream=stream)
+    sync()
+    return {n: t.cpu().numpy() for n, t in out.items()}
+
+
+def check(x, tokens, top_k, scale=1.0, what="", got=None):
+    got = run(x, tokens, top_k, scale) if got is None else got
+    s = float(np.float32(scale))
+    lse, lp, H, rank, ids, tops, b_lse, b_lp, b_H = serve_ref.logprobs(ref.f64(x), tokens, top_k, s)
+    ref.check(got["lse"], lse, b_lse, what + " lse")
+    ref.check(got["logprob"], lp, b_lp, what + " logprob")
+    ref.check(got["entropy"], H, b_H, what + " entropy")
+    assert np.array_equal(got["rank"], rank), what + " rank"
+    if top_k:
+        assert np.array_equal(got["top_ids"], ids), what + " ids"
+        bound = np.maximum(b_lp, b_lse)[:, None] + 4 * ref.U32 * np.abs(np.where(np.isfinite(tops), tops, 0))
+        ref.check(got["top_logprobs"], tops, bound, what + " top")
+
+
+def logits(R, V, ftype, seed, std=2.5):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(R, V, generator=g) * std).to(DT[ftype])
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("V,top_k", [(1, 1), (2, 2), (3, 0), (7, 7), (8, 5), (9, 1), (33, 32), (255, 20), (1000, 5),
+                                     (4095, 20), (4096, 32), (4097, 5), (8191, 32), (8193, 20), (32769, 5)])
+def test_lengths(ftype, V, top_k):
+    """Rows of odd lengths side by side start at every alignment; few rows go in parts."""
+    need_gpu()
+    x = logits(9, V, ftype, V)
+    tokens = np.random.RandomState(V).randint(0, V, 9)
+    tokens[0], tokens[1] = 0, V - 1
+    check(x.to(DEV), tokens, top_k, what="V %d" % V)
+
+
+@pytest.mark.parametrize("ftype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,V,top_k,scale", [(1, 128256, 32, 1.0), (1, 248320, 5, 0.5), (700, 1537, 20, 1.25),
+                                             (3, 250001, 20, 2.0), (650, 9000, 1, 1.0)])
+def test_wide_and_many_rows(ftype, R, V, top_k, scale):
+    need_gpu()
+    x = logits(R, V, ftype, R)
+    tokens = np.random.RandomState(R).randint(0, V, R)
+    check(x.to(DEV), tokens, top_k, scale)
+
+
+@pytest.mark.parametrize("ftype", ["f16", "f32"])
+@pytest.mark.parametrize("R,V", [(2, 30000), (650, 30000)])
+@pytest.mark.parametrize("kind", ["equal", "few values", "ascending", "descending", "zeros of both signs", "blocks"])
+def test_ties_and_orders(ftype, kind, R, V):
+    """Equal logits go by index; every order of the row must find the same words."""
+    need_gpu()
+    g = torch.Generator().manual_seed(3)
+    x = {"equal": lambda: torch.full((V,), 1.5), "few values": lambda: torch.randint(0, 3, (V,), generator=g).float(),
+         "ascending": lambda: torch.linspace(-9, 9, V), "descending": lambda: torch.linspace(9, -9, V),
+         "zeros of both signs": lambda: torch.where(torch.rand(V, generator=g) < 0.5, 0.0, -0.0),
+         "blocks": lambda: torch.arange(V).div(97, rounding_mode="floor").remainder(11).float()}[kind]()
+    x = x.to(DT[ftype]).to(DEV).expand(R, V).contiguous()
+    tokens = np.random.RandomState(4).randint(0, V, R)
+    got = run(x, tokens, 32)
+    few = min(R, 4)
+    check(x[:few], tokens[:few], 32, what=kind, got={n: t[:few] for n, t in got.items()})
+    assert (got["top_ids"] == got["top_ids"][0]).all() and (got["lse"] == got["lse"][0]).all()
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("parts", [False, True])
+def test_masked_words_infinities_and_nan(ftype, parts):
+    need_gpu()
+    V = 20000
+    low = torch.finfo(DT[ftype]).min
+    x = logits(12, V, ftype, 5)
+    x[0] = -float("inf")                       # nothing left
+    x[1] = -float("inf")
+    x[1, [5, 19999, 700]] = torch.tensor([1.0, 2.0, 1.0], dtype=x.dtype)   # three words left, 20 asked for
+    x[2, ::2] = -float("inf")
+    x[3, 3::7] = low                           # masks of the type's lowest value
+    x[4] = low
+    x[5, 77] = float("nan")
+    x[6, 77] = float("inf")
+    x[7] = float("nan")
+    x[8, [0, V - 1]] = float("nan")
+    x[9, 11] = float("inf")
+    x[9, 12] = float("inf")
+    tokens = np.array([3, 19999, 2, 3, 9, 77, 77, 5, 100, 12, -1, V])
+    if not parts:                              # many rows: a row is one CTA's
+        x = x.repeat(60, 1)
+        tokens = np.tile(tokens, 60)
+    got = run(x.to(DEV), tokens, 20)
+    check(x[:12].to(DEV), tokens[:12], 20, got={n: t[:12] for n, t in got.items()})
+    if not parts:
+        for n, t in got.items():
+            for i in range(1, 60):
+                assert np.array_equal(t[:12], t[12 * i:12 * i + 12], equal_nan=True), n
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("scale,std", [(1e-20, 3.0), (20.0, 3.0), (1.0, 100.0), (1e30, 1.0), (1.0, 1e-3)])
+def test_scales(ftype, scale, std):
+    need_gpu()
+    x = logits(5, 5000, ftype, 6, std)
+    if scale == 1e30:                          # distances of whole logits: one word has all
+        x = x.float().round().to(x.dtype)
+        x[:, 17] = 50.0
+    check(x.to(DEV), [17, 17, 17, 17, 17] if scale == 1e30 else [0, 1, 2, 3, 4999], 3, scale)
+
+
+@pytest.mark.parametrize("ftype", ["f16", "f32"])
+def test_strided_rows_and_left_out_outputs(ftype):
+    need_gpu()
+    V = 3001
+    big = torch.full((6, 3500), float("nan"), dtype=DT[ftype])
+    big[:, 3:3 + V] = logits(6, V, ftype, 7)
+    d = big.to(DEV)
+    x = d[:, 3:3 + V]
+    tokens = np.arange(6) * 500
+    check(x, tokens, 4)
+    H = torch.empty(6, dtype=torch.float32, device=DEV)
+    op = dg.logprobs(x, entropy=H)
+    need = dg.logprobs_workspace_bytes(op)
+    dg.token_logprobs(op, torch.empty(need, dtype=torch.uint8, device=DEV) if need else None)
+    ids = torch.empty(6, 4, dtype=torch.int32, device=DEV)
+    op = dg.logprobs(x, top_ids=ids)
+    need = dg.logprobs_workspace_bytes(op)
+    dg.token_logprobs(op, torch.empty(need, dtype=torch.uint8, device=DEV) if need else None)
+    sync()
+    full = run(x, tokens, 4)
+    assert np.array_equal(H.cpu().numpy(), full["entropy"]) and np.array_equal(ids.cpu().numpy(), full["top_ids"])
+
+
+def test_far_rows_streams_graphs_and_repeats():
+    need_gpu()
+    V = 200000
+    far = torch.empty(2, 5 * 10 ** 9, dtype=torch.bfloat16, device=DEV)    # rows more than 2^32 logits apart
+    x = far[:, :V]
+    x.copy_(logits(2, V, "bf16", 8).to(DEV))
+    check(x, [5, 199999], 20)
+    td = torch.tensor([5, 199999], dtype=torch.int32, device=DEV)
+    lp, rank = torch.empty(2, dtype=torch.float32, device=DEV), torch.empty(2, dtype=torch.int32, device=DEV)
+    op = dg.logprobs(x, tokens=td, logprob=lp, rank=rank)
+    ws = torch.empty(dg.logprobs_workspace_bytes(op), dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dg.token_logprobs(op, ws)
+    side = torch.cuda.Stream()
+    for seed in (9, 10):
+        x.copy_(logits(2, V, "bf16", seed).to(DEV))
+        graph.replay()
+        sync()
+        got = run(x, [5, 199999], 0, stream=side)
+        assert np.array_equal(lp.cpu().numpy(), got["logprob"]) and np.array_equal(rank.cpu().numpy(), got["rank"])
+        check(x, [5, 199999], 0, got=got)
