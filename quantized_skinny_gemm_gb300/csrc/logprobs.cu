@@ -3,17 +3,25 @@
 //
 // A row (or a part of it, where the rows are few) is a CTA's, taken in tiles of 1024
 // 16-byte vectors, four a thread, the next tile loading while one is used.  Each thread
-// keeps a base m, l = sum 2^((x - m) c) and a = sum 2^((x - m) c) (x - m) of its own, c =
-// scale log2(e); the base follows the maximum only when that has grown by 2^8, so that a
-// logit costs a difference, a product and one exponential; the entropy is ln l - scale a / l,
-// whose terms have the size of the result.  Rows may start anywhere: the
-// vectors are aligned ones, those at the row's ends are read one logit at a time.
+// keeps a base m and, with c = scale log2(e) and B = m c rounded, the sums l of w = 2^(x c - B)
+// and a of w (x c - B): an exponent is one fused multiply-add, rounded once, B
+// being a number like any other (a softmax of scale c / log2(e), 2^-24 off).  The base
+// follows the maximum only when that has grown by 2^8.  lse = ln 2 (B + log2 l), the entropy is
+// ln 2 (log2 l - a / l), whose terms have the size of the result.  Past |m c| = 2^22, where
+// B's rounding nears a whole power of two (rows of nothing but masks, mostly), the sums are taken
+// again with exponents (x - m) c.
 //
-// The best top_k: a candidate list in shared memory and a threshold that every candidate
-// reaches.  Where more than 32 threads of a tile hold something above it, it is
-// raised first to the top_k-th largest of the threads' maxima, so that
-// hardly more than top_k logits of a tile are ever put in the list.  Keys are (logit,
-// lowest index) in one 64-bit number, no two alike: what is chosen depends on no order.
+// Rows may start anywhere: the vectors are aligned ones, and the logits before the first and behind
+// the last are a thread's each.
+//
+// The rank is counted where a thread's four vectors hold something that is not below the token's
+// logit, 16-bit logits two at a time.  The best top_k cost the stream next to nothing: a thread only keeps its
+// maximum, and that of each eighth of its tiles.  The top_k-th largest of 64 groups' maxima is
+// then a floor that about top_k logits of the row reach; the threads read the eighths that
+// reach it once more (from L2, mostly) and list what does.  Keys are (logit, lowest index)
+// in one 64-bit number, no two alike: what is chosen depends on no order.  (Lists that each warp kept while it
+// streamed, cut to top_k again and again: 173 us for one alternative and 376 for 20, 2048 x
+// 128256 bf16, where the sums alone take 94.)
 #include <cfloat>
 #include <climits>
 
@@ -22,11 +30,12 @@
 namespace dg {
 
 constexpr int kLpThreads = 256, kLpVecs = 4, kLpTile = kLpThreads * kLpVecs;   // vectors of a tile
-constexpr int kLpMaxParts = 64;
-constexpr int kLpRaise = 32;                  // threads above the threshold before it is raised
-constexpr int kLpKeep = 256;                  // candidates before the list is cut to top_k
-constexpr int kLpList = kLpKeep + kLpRaise * kLpVecs * 8;
-constexpr float kLpLog2e = 1.4426950408889634f;
+constexpr int kLpWarps = kLpThreads / 32, kLpMaxParts = 64;
+constexpr int kLpGroups = 64;                 // of four threads: more than top_k
+constexpr int kLpSlices = 8;                  // of a part's tiles, with a maximum of a thread each
+constexpr int kLpList = 1024;                 // candidates; where more reach the floor it is raised
+constexpr float kNan = __builtin_nanf("");
+constexpr float kLpLog2e = 1.4426950408889634f, kLpLn2 = 0.6931471805599453f;
 using Key = unsigned long long;
 
 struct LpPart {
@@ -37,6 +46,7 @@ struct LpParams {
     dg_logprobs op;
     int parts;
     float c, grow;      // scale * log2(e); how far the maximum may pass the base
+    float most;         // bases up to this size have |m c| <= 2^22
     LpPart* part;       // [rows][parts]
     Key* keys;          // [rows][parts][top_k]
     FastDiv by_parts;
@@ -45,6 +55,12 @@ struct LpParams {
 __device__ __forceinline__ float ex2(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float mul_rn(float a, float b) {   // (never part of a fused operation)
+    float r;
+    asm("mul.rn.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 
@@ -57,25 +73,43 @@ __device__ __forceinline__ Key key_of(float v, int i) {
 __device__ __forceinline__ int index_of(Key k) { return (int)(0xffffffffu - (uint32_t)k); }
 __device__ __forceinline__ float logit_of(Key k) {
     const uint32_t o = (uint32_t)(k >> 32);
-    if (o <= 1u) return __uint_as_float(0x7fffffffu);
+    if (o <= 1u) return kNan;
     return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
 }
 
-// (m, l, a) of two sets of logits.  An empty set's base is -infinity.
-__device__ __forceinline__ void join(float& m, float& l, float& a, float m2, float l2, float a2, float c) {
-    const float top = fmaxf(m, m2);
-    auto moved = [&](float& mm, float& ll, float& aa) {
-        if (mm == top) return;
-        const float d = mm - top, f = ex2(d * c);   // ll 0: nothing to move (d may be -infinity)
-        aa = ll == 0.f ? 0.f : f * (aa + d * ll);
-        ll = f * ll;
-    };
-    moved(m, l, a);
-    moved(m2, l2, a2);
-    m = top;
-    l += l2;
-    a += a2;
-}
+// The sums of a set of logits; an empty set's base is -infinity.
+struct Sums {
+    float m, l, a;
+    // other's base seen from this one's, in powers of two
+    __device__ __forceinline__ static float distance(float from, float to, const LpParams& p) {
+        if (fabsf(from) <= p.most && fabsf(to) <= p.most) return mul_rn(from, p.c) - mul_rn(to, p.c);
+        return (from - to) * p.c;
+    }
+    __device__ __forceinline__ void move(float to, const LpParams& p) {
+        if (m == to) return;
+        const float d = distance(m, to, p), f = ex2(d);
+        a = f == 0.f || l == 0.f ? 0.f : f * (a + d * l);   // (d may be -infinity)
+        l = f * l;
+        m = to;
+    }
+    __device__ __forceinline__ void join(Sums o, const LpParams& p) {
+        const float top = fmaxf(m, o.m);
+        move(top, p);
+        o.move(top, p);
+        l += o.l;
+        a += o.a;
+    }
+    __device__ __forceinline__ void join_warp(const LpParams& p) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            Sums x;
+            x.m = __shfl_xor_sync(0xffffffffu, m, o);
+            x.l = __shfl_xor_sync(0xffffffffu, l, o);
+            x.a = __shfl_xor_sync(0xffffffffu, a, o);
+            join(x, p);
+        }
+    }
+};
 
 template <int TYPE>   // 0 fp16, 1 bf16, 2 fp32
 __device__ __forceinline__ float logit_at(const void* p, long long i) {
@@ -85,33 +119,91 @@ __device__ __forceinline__ float logit_at(const void* p, long long i) {
 
 // A row's numbers from its sums; those of a row of only -infinity stand in the header.
 struct Row {
-    float m, l, log_l, scale;
-    __device__ __forceinline__ Row(float m_, float l_, float s) : m(m_), l(l_), log_l(logf(l_)), scale(s) {}
-    __device__ __forceinline__ float lse() const { return l == 0.f ? -INFINITY : fmaf(scale, m, log_l); }
-    __device__ __forceinline__ float logprob(float x) const { return l == 0.f ? -INFINITY : scale * (x - m) - log_l; }
-    __device__ __forceinline__ float entropy(float a) const { return l == 0.f ? 0.f : log_l - scale * (a / l); }
+    Sums s;
+    float log_l, base, scale, c, most;
+    bool near;
+    __device__ __forceinline__ Row(const Sums& sums, const LpParams& p)
+        : s(sums), log_l(log2f(sums.l)), base(mul_rn(sums.m, p.c)), scale(p.op.scale), c(p.c),
+          most(p.most), near(fabsf(sums.m) <= p.most) {}
+    __device__ __forceinline__ float lse() const {
+        if (s.l == 0.f) return -INFINITY;
+        return near ? (base + log_l) * kLpLn2 : fmaf(scale, s.m, log_l * kLpLn2);
+    }
+    __device__ __forceinline__ float logprob(float x) const {
+        if (s.l == 0.f) return -INFINITY;
+        return near && fabsf(x) <= most ? (fmaf(x, c, -base) - log_l) * kLpLn2 : scale * (x - s.m) - log_l * kLpLn2;
+    }
+    __device__ __forceinline__ float entropy() const { return s.l == 0.f ? 0.f : (log_l - s.a / s.l) * kLpLn2; }
 };
 
 template <int TYPE>
-__device__ __forceinline__ void write_row(const dg_logprobs& op, int row, float m, float l, float a, int before,
-                                          const void* x) {
-    const Row r(m == -INFINITY ? 0.f : m, l, op.scale);
+__device__ __forceinline__ void write_row(const LpParams& p, const Row& r, int row, int before, const void* x) {
+    const dg_logprobs& op = p.op;
     if (op.lse) op.lse[row] = r.lse();
-    if (op.entropy) op.entropy[row] = r.entropy(a);
+    if (op.entropy) op.entropy[row] = r.entropy();
     if (!op.tokens) return;
     const int tok = op.tokens[row];
     const bool there = tok >= 0 && tok < op.V;
     if (op.rank) op.rank[row] = there ? before : op.V;
     // of a row of NaN everything is NaN
-    if (op.logprob) op.logprob[row] = there ? r.logprob(logit_at<TYPE>(x, tok)) : l != l ? l : -INFINITY;
+    if (op.logprob)
+        op.logprob[row] = there ? r.logprob(logit_at<TYPE>(x, tok)) : r.s.l != r.s.l ? r.s.l : -INFINITY;
+}
+
+// The largest of a vector; NaN only where all are.
+template <int TYPE>
+__device__ __forceinline__ float vec_max(uint4 v) {
+    if (TYPE == 2)
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    uint32_t m, n;
+    if (TYPE == 1) {
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(v.x), "r"(v.y));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(v.z), "r"(v.w));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
+    } else {
+        asm("max.f16x2 %0, %1, %2;" : "=r"(m) : "r"(v.x), "r"(v.y));
+        asm("max.f16x2 %0, %1, %2;" : "=r"(n) : "r"(v.z), "r"(v.w));
+        asm("max.f16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
+    }
+    const float2 f = pair_f32<TYPE == 1>(m);
+    return fmaxf(f.x, f.y);
+}
+
+// How many of a vector's logits are above (or, or_equal) one of their kind: 16-bit ones are counted
+// as pairs of ones.
+template <int TYPE, bool OR_EQUAL>
+__device__ __forceinline__ void count_above(uint4 v, float than, uint32_t than2, uint32_t& pairs, int& n) {
+    if (TYPE == 2) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) n += OR_EQUAL ? __uint_as_float(w[e]) >= than : __uint_as_float(w[e]) > than;
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (TYPE == 1) {
+            __nv_bfloat162 a, b, c;
+            memcpy(&a, &w[e], 4);
+            memcpy(&b, &than2, 4);
+            memcpy(&c, &pairs, 4);
+            c = __hadd2(c, OR_EQUAL ? __hge2(a, b) : __hgt2(a, b));
+            memcpy(&pairs, &c, 4);
+        } else {
+            const __half2 a = u32_as_h2(w[e]), b = u32_as_h2(than2);
+            pairs = h2_as_u32(__hadd2(u32_as_h2(pairs), OR_EQUAL ? __hge2(a, b) : __hgt2(a, b)));
+        }
+    }
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kLpThreads) k_logprobs(const LpParams p) {
+__global__ void __launch_bounds__(kLpThreads, 3) k_logprobs(const LpParams p) {
     constexpr int kEl = TYPE == 2 ? 4 : 8, kSize = TYPE == 2 ? 4 : 2;   // of a vector; bytes of a logit
+    constexpr uint32_t kNone = TYPE == 2 ? 0xFF800000u : TYPE == 1 ? 0xFF80FF80u : 0xFC00FC00u;   // -infinity
     __shared__ Key list[kLpList];
-    __shared__ Key maxima[kLpThreads];
-    __shared__ float red[3][kLpThreads / 32];
+    __shared__ __align__(16) Key maxima[kLpGroups];
+    __shared__ float slice_max[kLpSlices][kLpThreads];
+    __shared__ Sums red[kLpWarps];
     __shared__ Key s_floor;
     __shared__ int s_n, s_before;
     const dg_logprobs& op = p.op;
@@ -121,200 +213,253 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs(const LpParams p) {
     griddep_launch_dependents();
     griddep_wait();
     const unsigned char* x = static_cast<const unsigned char*>(op.logits) + (long long)row * op.stride * kSize;
-    // vector v holds logits [v * kEl - skew, ..) of the row
+    // vectors [first, last) lie inside the row, vector v holding logits [v * kEl - skew, ..)
     const int skew = (int)(((uintptr_t)x & 15) / kSize);
     const uint4* vecs = reinterpret_cast<const uint4*>(x - skew * kSize);
-    const int nvec = (int)(((long long)V + skew + kEl - 1) / kEl);
-    const int tiles = (nvec + kLpTile - 1) / kLpTile;
+    const int first = skew ? 1 : 0, last = (int)(((long long)V + skew) / kEl);
+    const int tiles = (last - first + kLpTile - 1) / kLpTile;   // 0 where last < first
     const int tile0 = (int)((long long)part * tiles / p.parts), tile1 = (int)((long long)(part + 1) * tiles / p.parts);
+    uint4 next[kLpVecs];
+    auto fetch = [&](int tile) {
+#pragma unroll
+        for (int q = 0; q < kLpVecs; ++q) {
+            const int v = first + tile * kLpTile + q * kLpThreads + tid;
+            next[q] = make_uint4(kNone, kNone, kNone, kNone);
+            if (tile < tile1 && v < last) next[q] = __ldcs(vecs + v);
+        }
+    };
+    fetch(tile0);
     if (tid == 0) {
-        s_n = s_before = 0;
+        s_before = s_n = 0;
         s_floor = 0;
     }
     int tok = -1;
-    float mine = 0.f;   // the given token's logit
+    float mine = kNan;   // the given token's logit
     if (op.rank && op.tokens) {
         tok = op.tokens[row];
         if (tok < 0 || tok >= V) tok = -1;
         else mine = logit_at<TYPE>(x, tok);
     }
-    const bool count = tok >= 0;
+    const uint32_t mine2 = TYPE == 2 ? 0u : pair_16<TYPE == 1>(mine, mine);   // (it has 16 bits)
+    const bool nan_token = tok >= 0 && mine != mine;
     auto before = [&](float v, int i) {   // whether logit v of word i comes before the token
-        if (mine != mine) return v == v || i < tok;
+        if (nan_token) return v == v || i < tok;
         return v > mine || (v == mine && i < tok);
     };
-    auto whole = [&](int v) { return v * (long long)kEl >= skew && (v + 1) * (long long)kEl - skew <= V; };
-    uint4 next[kLpVecs];
-    auto fetch = [&](int tile) {
-#pragma unroll
-        for (int q = 0; q < kLpVecs; ++q) {
-            const int v = tile * kLpTile + q * kLpThreads + tid;
-            if (tile < tile1 && v < nvec && whole(v)) next[q] = __ldcs(vecs + v);
-        }
-    };
-    float m = -INFINITY, base = 0.f;
-    float2 l = make_float2(0.f, 0.f), a = l;
+    Sums s = {-INFINITY, 0.f, 0.f};
     int ahead = 0;
-    Key floor = 0;
-    float floor_logit = -INFINITY;
-    fetch(tile0);
-    __syncthreads();
+    // ---- the logits outside the vectors, by the first part ---------------------------------------
+    const int head = min(V, skew ? kEl - skew : 0), tail = max(head, last * kEl - skew);
+    const bool end = part == 0 && tid < head + (V - tail);
+    const int end_i = tid < head ? tid : tail + tid - head;
+    if (end) {
+        const float v = logit_at<TYPE>(x, end_i);
+        if (v > -INFINITY) s = {v, 1.f, 0.f};
+        if (v != v || v == INFINITY) s = {v == v ? v : -INFINITY, kNan, 0.f};
+        ahead = tok >= 0 && before(v, end_i);
+        list[tid] = key_of(v, end_i);   // always a candidate
+    }
+    const int ends = part == 0 ? head + (V - tail) : 0;
+    float2 l = make_float2(s.l, 0.f), a = make_float2(0.f, 0.f);
+    float m = s.m, base = fabsf(m) <= p.most ? mul_rn(m, p.c) : 0.f;
+    if (m > -INFINITY && fabsf(m) > p.most) {   // (the sums are taken again if this is the part's maximum)
+        base = m > 0.f ? p.most * p.c : -p.most * p.c;
+        l.x = m == INFINITY ? l.x : 0.f;
+    }
+    // logit e of a vector; the index of the first of this thread's vector q; where vectors end
+    auto logit = [&](const uint4& v, int e) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if (TYPE == 2) return __uint_as_float(w[e & 3]);
+        return elem_f32<TYPE == 1>((uint16_t)(w[e / 2 & 3] >> (e & 1) * 16));
+    };
+    auto index = [&](int tile, int q) { return (first + tile * kLpTile + q * kLpThreads + tid) * kEl - skew; };
+    const int inside = last * kEl - skew;
+    const float2 c2 = make_float2(p.c, p.c), one = make_float2(1.f, 1.f);
+    float greatest = -INFINITY, sliced = -INFINITY;   // of the thread's vectors, and of this slice of tiles
+    int greatest_at = tile0, slice = 0;
+    const int per_slice = max(1, (tile1 - tile0 + kLpSlices - 1) / kLpSlices);
+    int slice_end = tile0 + per_slice;
     for (int tile = tile0; tile < tile1; ++tile) {
         uint4 now[kLpVecs];
 #pragma unroll
         for (int q = 0; q < kLpVecs; ++q) now[q] = next[q];
         fetch(tile + 1);
-        float tile_max = -INFINITY;
-        bool any = false;
-        auto unpack = [&](int q, float (&f)[kEl]) {
-            if constexpr (TYPE == 2) {
-                f[0] = __uint_as_float(now[q].x), f[1] = __uint_as_float(now[q].y);
-                f[2] = __uint_as_float(now[q].z), f[3] = __uint_as_float(now[q].w);
-            } else {
-                unpack8<TYPE == 1>(now[q], f);
+        float top = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < kLpVecs; ++q) top = fmaxf(top, vec_max<TYPE>(now[q]));
+        if (K) {
+            if (top > greatest) {   // the first tile that holds it
+                greatest = top;
+                greatest_at = tile;
             }
-        };
+            sliced = fmaxf(sliced, top);
+            if (tile + 1 == slice_end || tile + 1 == tile1) {
+                slice_max[slice++][tid] = sliced;
+                sliced = -INFINITY;
+                slice_end += per_slice;
+            }
+        }
+        if (top > m + p.grow) {
+            // (bases past 2^22 stand there; the sums are taken again if that was the part's maximum)
+            const float to = mul_rn(fminf(fmaxf(top, -p.most), p.most), p.c);
+            const float d = base - to, k = ex2(d);
+            const bool none = m == -INFINITY;   // then l is 0, or NaN, and a is 0
+            a = none ? make_float2(0.f, 0.f) : make_float2(k * (a.x + d * l.x), k * (a.y + d * l.y));
+            l = none ? make_float2(l.x * 0.f, l.y * 0.f) : make_float2(l.x * k, l.y * k);
+            m = top;
+            base = to;
+        }
+        const float2 off = make_float2(-base, -base);
 #pragma unroll
         for (int q = 0; q < kLpVecs; ++q) {
-            const int v = tile * kLpTile + q * kLpThreads + tid;
-            if (v >= nvec) continue;
-            float f[kEl];
-            const int i0 = v * kEl - skew;
-            if (whole(v)) {
-                unpack(q, f);
-            } else {   // an end of the row: what is not there has no part in anything
+            const uint32_t w[4] = {now[q].x, now[q].y, now[q].z, now[q].w};
 #pragma unroll
-                for (int e = 0; e < kEl; ++e)
-                    f[e] = i0 + e >= 0 && i0 + e < V ? logit_at<TYPE>(x, i0 + e) : -INFINITY;
+            for (int e = 0; e < kEl / 2; ++e) {
+                const float2 f = TYPE == 2 ? make_float2(__uint_as_float(w[2 * e & 3]), __uint_as_float(w[(2 * e + 1) & 3]))
+                                           : pair_f32<TYPE == 1>(w[e]);
+                const float2 d = fma2(f, c2, off);
+                const float2 t = make_float2(ex2(d.x), ex2(d.y));
+                l = fma2(t, one, l);
+                a = fma2(t, make_float2(fmaxf(d.x, -FLT_MAX), fmaxf(d.y, -FLT_MAX)), a);   // -infinity has no part
             }
-            any = true;
-            float top = f[0];
+        }
+        if (tok >= 0 && (top >= mine || nan_token)) {
+            const int from = (first + tile * kLpTile) * kEl - skew;   // of the tile
+            if (nan_token || (from <= tok && tok < from + kLpTile * kEl)) {
+#pragma unroll 1
+                for (int q = 0; q < kLpVecs; ++q) {
+                    const uint4 v = q == 0 ? now[0] : q == 1 ? now[1] : q == 2 ? now[2] : now[3];
+                    const int i = index(tile, q);
+                    if (i >= inside) break;
 #pragma unroll
-            for (int e = 1; e < kEl; ++e) top = fmaxf(top, f[e]);
-            tile_max = fmaxf(tile_max, top);
-            if (top > m + p.grow) {
-                const float d = m - top, k = ex2(d * p.c);
-                const bool none = m == -INFINITY;   // then l is 0, or NaN, and a is 0
-                a = none ? make_float2(0.f, 0.f) : make_float2(k * (a.x + d * l.x), k * (a.y + d * l.y));
-                l.x *= k;
-                l.y *= k;
-                m = base = top;
-            }
+                    for (int e = 0; e < kEl; ++e) ahead += before(logit(v, e), i + e);
+                }
+            } else {
+                uint32_t pairs = 0;   // at most 16 each
 #pragma unroll
-            for (int e = 0; e < kEl; e += 2) {
-                const float2 one = make_float2(1.f, 1.f);
-                const float2 d = fma2(make_float2(f[e], f[e + 1]), one, make_float2(-base, -base));
-                const float2 w = make_float2(ex2(d.x * p.c), ex2(d.y * p.c));
-                l = fma2(w, one, l);
-                a = fma2(w, make_float2(fmaxf(d.x, -FLT_MAX), fmaxf(d.y, -FLT_MAX)), a);   // -infinity has no part
-            }
-            if (count) {
-                const bool edge = !whole(v) || mine != mine || (i0 <= tok && tok < i0 + kEl);
-                if (edge) {
-#pragma unroll
-                    for (int e = 0; e < kEl; ++e)
-                        ahead += i0 + e >= 0 && i0 + e < V && before(f[e], i0 + e);
-                } else if (i0 < tok) {
-#pragma unroll
-                    for (int e = 0; e < kEl; ++e) ahead += f[e] >= mine;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kEl; ++e) ahead += f[e] > mine;
+                for (int q = 0; q < kLpVecs; ++q) {
+                    if (from < tok) count_above<TYPE, true>(now[q], mine, mine2, pairs, ahead);
+                    else count_above<TYPE, false>(now[q], mine, mine2, pairs, ahead);
+                }
+                if (TYPE != 2) {
+                    const float2 f = pair_f32<TYPE == 1>(pairs);
+                    ahead += (int)(f.x + f.y);
                 }
             }
         }
-        if (K == 0) continue;
-        const int above = __syncthreads_count(any && (floor == 0 || tile_max >= floor_logit));
-        if (above == 0) continue;
-        // every logit of this thread's vectors, with its index
-        auto each = [&](auto&& use) {
-#pragma unroll
-            for (int q = 0; q < kLpVecs; ++q) {
-                const int v = tile * kLpTile + q * kLpThreads + tid;
-                if (v >= nvec) continue;
-                float f[kEl];
-                const int i0 = v * kEl - skew;
-                const bool in = whole(v);
-                if (in) unpack(q, f);
-#pragma unroll
-                for (int e = 0; e < kEl; ++e) {
-                    const int i = i0 + e;
-                    if (in) use(f[e], i);
-                    else if (i >= 0 && i < V) use(logit_at<TYPE>(x, i), i);
-                }
-            }
-        };
-        if (s_n > kLpKeep) {   // (the same for all threads: read between two barriers)
-            const int n = s_n;
-            Key kept[kLpList / kLpThreads + 1];
-            int rank[kLpList / kLpThreads + 1], have = 0;
-            for (int i = tid; i < n; i += kLpThreads, ++have) {
-                const Key k = list[i];
-                int r = 0;
-                for (int j = 0; j < n; ++j) r += list[j] > k;
-                kept[have] = k;
-                rank[have] = r;
-            }
-            __syncthreads();
-            have = 0;
-            for (int i = tid; i < n; i += kLpThreads, ++have)
-                if (rank[have] < K) {
-                    list[rank[have]] = kept[have];
-                    if (rank[have] == K - 1) s_floor = max(s_floor, kept[have]);
-                }
-            if (tid == 0) s_n = K;
-            __syncthreads();
-        }
-        if (above > kLpRaise) {
-            Key best = 0;
-            each([&](float v, int i) { best = max(best, key_of(v, i)); });
-            maxima[tid] = best;
-            __syncthreads();
-            int r = 0;
-#pragma unroll 8
-            for (int j = 0; j < kLpThreads; ++j) r += maxima[j] > best;
-            if (best && r == K - 1) s_floor = max(s_floor, best);
-        }
-        __syncthreads();
-        floor = s_floor;
-        floor_logit = floor ? logit_of(floor) : -INFINITY;
-        if (floor_logit != floor_logit) floor_logit = -INFINITY;   // a floor of NaN: all reach it
-        if (any && (floor == 0 || tile_max >= floor_logit))
-            each([&](float v, int i) {
-                const Key k = key_of(v, i);
-                if (k >= floor) list[atomicAdd(&s_n, 1)] = k;
-            });
-        __syncthreads();
     }
     // ---- the part's sums ------------------------------------------------------------------
-    float sl = l.x + l.y, sa = a.x + a.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, sl, o);
-        const float a2 = __shfl_xor_sync(0xffffffffu, sa, o);
-        join(m, sl, sa, m2, l2, a2, p.c);
-    }
-    if (count) {
+    auto whole = [&] {   // the CTA's, in every thread
+        s.join_warp(p);
+        if (lane == 0) red[warp] = s;
+        __syncthreads();
+        s = red[0];
+        for (int w = 1; w < kLpWarps; ++w) s.join(red[w], p);
+        __syncthreads();
+    };
+    s = {m, l.x + l.y, a.x + a.y};
+    if (m == INFINITY) s.l = kNan;
+    else if (m > -INFINITY) s.m = fminf(fmaxf(m, -p.most), p.most);   // as its base
+    __syncthreads();
+    if (tok >= 0) {
         ahead = warp_sum(ahead);
         if (lane == 0 && ahead) atomicAdd(&s_before, ahead);
     }
-    if (lane == 0) {
-        red[0][warp] = m;
-        red[1][warp] = sl;
-        red[2][warp] = sa;
+    whole();
+    // (the threads' bases may lie 2^8 below their maxima)
+    const bool far = __syncthreads_or(m < INFINITY && m > p.most) || (s.l == 0.f && __syncthreads_or(m > -INFINITY));
+    if (far) {   // logits past what a base reaches: exponents as differences
+        const long long i0 = (long long)(first + tile0 * kLpTile) * kEl - skew;
+        const long long i1 = (long long)min(last, first + tile1 * kLpTile) * kEl - skew;
+        auto all = [&](auto&& use) {
+            if (end) use(logit_at<TYPE>(x, end_i));
+            for (long long i = i0 + tid; i < i1; i += kLpThreads) use(logit_at<TYPE>(x, i));
+        };
+        s = {-INFINITY, 0.f, 0.f};
+        all([&](float v) { s.m = fmaxf(s.m, v); });
+        all([&](float v) {
+            const float d = (v - s.m) * p.c, t = ex2(d);
+            if (v == -INFINITY) return;
+            s.l += t;
+            s.a = fmaf(t, fmaxf(d, -FLT_MAX), s.a);
+        });
+        whole();
     }
-    __syncthreads();
-    m = red[0][0];
-    sl = red[1][0];
-    sa = red[2][0];
-    for (int w = 1; w < kLpThreads / 32; ++w) join(m, sl, sa, red[0][w], red[1][w], red[2][w], p.c);
+    const Row r(s, p);
     if (tid == 0) {
-        if (p.parts == 1) write_row<TYPE>(op, row, m, sl, sa, s_before, x);
-        else p.part[blockIdx.x] = {m, sl, sa, s_before};
+        if (p.parts == 1) write_row<TYPE>(p, r, row, s_before, x);
+        else p.part[blockIdx.x] = {s.m, s.l, s.a, s_before};
     }
     if (K == 0) return;
-    const int n = s_n;
-    const Row r(m == -INFINITY ? 0.f : m, sl, op.scale);
+    // ---- the best -------------------------------------------------------------------------------
+    // the threads' largest keys, by fours: K of them, of different groups, are not below the floor
+    Key largest = 0;
+    if (tile0 < tile1) {
+#pragma unroll
+        for (int q = 0; q < kLpVecs; ++q) {
+            const int i = index(greatest_at, q);
+            if (i >= inside) break;
+            const uint4 v = vecs[first + greatest_at * kLpTile + q * kLpThreads + tid];
+#pragma unroll
+            for (int e = 0; e < kEl; ++e) largest = max(largest, key_of(logit(v, e), i + e));
+        }
+    }
+    largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
+    largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
+    if ((tid & 3) == 0) maxima[tid >> 2] = largest;
+    __syncthreads();
+    if (tid < kLpGroups) {
+        const Key k = maxima[tid];
+        int above = 0;
+#pragma unroll 8
+        for (int j = 0; j < kLpGroups; j += 2) {
+            const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(maxima + j);
+            above += (o.x > k) + (o.y > k);
+        }
+        if (k && above == K - 1) s_floor = k;
+    }
+    int n;
+    while (true) {
+        if (tid == 0) s_n = ends;
+        __syncthreads();
+        const Key floor = s_floor;
+        float at_least = floor ? logit_of(floor) : -INFINITY;
+        if (at_least != at_least) at_least = -INFINITY;   // a floor of NaN: any logit may reach it
+        if (greatest >= at_least)
+            for (int h = 0; h < slice; ++h) {
+                if (!(slice_max[h][tid] >= at_least)) continue;
+                const int to = min(tile1, tile0 + (h + 1) * per_slice);
+                for (int tile = tile0 + h * per_slice; tile < to; ++tile) {
+                    uint4 v[kLpVecs];
+#pragma unroll
+                    for (int q = 0; q < kLpVecs; ++q)
+                        if (index(tile, q) < inside) v[q] = vecs[first + tile * kLpTile + q * kLpThreads + tid];
+#pragma unroll
+                    for (int q = 0; q < kLpVecs; ++q) {
+                        const int i = index(tile, q);
+                        if (i >= inside || vec_max<TYPE>(v[q]) < at_least) continue;   // (not where all are NaN)
+#pragma unroll
+                        for (int e = 0; e < kEl; ++e) {
+                            const Key k = key_of(logit(v[q], e), i + e);
+                            if (k < floor) continue;
+                            const int to_list = atomicAdd(&s_n, 1);
+                            if (to_list < kLpList) list[to_list] = k;
+                        }
+                    }
+                }
+            }
+        __syncthreads();
+        n = s_n;
+        if (n <= kLpList) break;
+        // too many: the top_k-th of those that found room is a higher floor
+        for (int i = tid; i < kLpList; i += kLpThreads) {
+            const Key k = list[i];
+            int above = 0;
+            for (int j = 0; j < kLpList; ++j) above += list[j] > k;
+            if (above == K - 1) s_floor = k;
+        }
+        __syncthreads();
+    }
     Key* keys = p.parts == 1 ? nullptr : p.keys + (size_t)blockIdx.x * K;
     for (int i = tid; i < n; i += kLpThreads) {
         const Key k = list[i];
@@ -342,23 +487,18 @@ __global__ void __launch_bounds__(32) k_logprobs_join(const LpParams p) {
     const dg_logprobs& op = p.op;
     const int row = blockIdx.x, lane = threadIdx.x, K = op.top_k, n = p.parts;
     const unsigned char* x = static_cast<const unsigned char*>(op.logits) + (long long)row * op.stride * (TYPE == 2 ? 4 : 2);
-    float m = -INFINITY, l = 0.f, a = 0.f;
+    Sums s = {-INFINITY, 0.f, 0.f};
     int before = 0;
     for (int i = lane; i < n; i += 32) {   // (two parts a lane at most)
         const LpPart q = p.part[(size_t)row * n + i];
-        join(m, l, a, q.m, q.l, q.a, p.c);
+        s.join({q.m, q.l, q.a}, p);
         before += q.before;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-        const float a2 = __shfl_xor_sync(0xffffffffu, a, o);
-        join(m, l, a, m2, l2, a2, p.c);
-    }
+    s.join_warp(p);
     before = warp_sum(before);
-    if (lane == 0) write_row<TYPE>(op, row, m, l, a, before, x);
+    const Row r(s, p);
+    if (lane == 0) write_row<TYPE>(p, r, row, before, x);
     if (K == 0) return;
-    const Row r(m == -INFINITY ? 0.f : m, l, op.scale);
     const Key* keys = p.keys + (size_t)row * n * K;
     int at[2] = {0, 0};
     Key head[2];
@@ -400,6 +540,7 @@ static cudaError_t launch_lp(const dg_logprobs& op, void* ws, cudaStream_t s) {
     p.parts = lp_parts(op);
     p.c = op.scale * kLpLog2e;
     p.grow = fminf(8.f / p.c, FLT_MAX);   // finite: the first maximum is always taken
+    p.most = fminf(4194304.f / p.c, FLT_MAX);
     p.part = static_cast<LpPart*>(ws);
     p.keys = reinterpret_cast<Key*>(static_cast<char*>(ws) + (size_t)op.rows * p.parts * sizeof(LpPart));
     p.by_parts = fast_div((uint32_t)p.parts);

@@ -34,6 +34,9 @@ def check(x, tokens, top_k, scale=1.0, what="", got=None):
     got = run(x, tokens, top_k, scale) if got is None else got
     s = float(np.float32(scale))
     lse, lp, H, rank, ids, tops, b_lse, b_lp, b_H = serve_ref.logprobs(ref.f64(x), tokens, top_k, s)
+    with np.errstate(over="ignore"):           # what lies past fp32 is infinite there
+        lse, lp, tops = (a.astype(np.float32).astype(np.float64) for a in (lse, lp, tops))
+    b_lse, b_lp = b_lse + ref.U32 * np.abs(np.nan_to_num(lse, posinf=0, neginf=0)), b_lp * 1.01
     ref.check(got["lse"], lse, b_lse, what + " lse")
     ref.check(got["logprob"], lp, b_lp, what + " logprob")
     ref.check(got["entropy"], H, b_H, what + " entropy")
@@ -130,6 +133,28 @@ def test_scales(ftype, scale, std):
         x = x.float().round().to(x.dtype)
         x[:, 17] = 50.0
     check(x.to(DEV), [17, 17, 17, 17, 17] if scale == 1e30 else [0, 1, 2, 3, 4999], 3, scale)
+
+
+@pytest.mark.parametrize("ftype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1.0, 3.0])
+@pytest.mark.parametrize("V", [5, 3001, 20001])
+def test_logits_at_the_ends_of_fp32(ftype, scale, V):
+    """Masks of the lowest value around a few words, in every part and at the row's ends; rows of nothing else;
+    logits near the largest number."""
+    need_gpu()
+    low, high = torch.finfo(DT[ftype]).min, torch.finfo(DT[ftype]).max
+    x = torch.full((8, V), low, dtype=DT[ftype])
+    x[0, V // 2] = 3.0
+    x[1, 0], x[1, 1] = 1.0, 0.5
+    x[2, V - 1], x[2, V - 2] = 1.0, 0.5
+    x[3] = logits(1, V, ftype, 9)[0]
+    x[3, :V // 2] = low
+    x[4, 1:3] = -float("inf")
+    x[5, 2] = high
+    x[6, 1], x[6, 3] = high, high
+    x[7] = torch.linspace(-3e38, 3e38, V)
+    tokens = [V // 2, 1, V - 1, V - 1, 0, 2, 1, V - 1]
+    check(x.to(DEV), tokens, min(V, 5), scale)
 
 
 @pytest.mark.parametrize("ftype", ["f16", "f32"])
