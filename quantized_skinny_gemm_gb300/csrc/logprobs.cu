@@ -197,13 +197,15 @@ __device__ __forceinline__ void count_above(uint4 v, float than, uint32_t than2,
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kLpThreads, 3) k_logprobs(const LpParams p) {
+__global__ void __launch_bounds__(kLpThreads, TYPE == 2 ? 3 : 4) k_logprobs(const LpParams p) {
     constexpr int kEl = TYPE == 2 ? 4 : 8, kSize = TYPE == 2 ? 4 : 2;   // of a vector; bytes of a logit
     constexpr uint32_t kNone = TYPE == 2 ? 0xFF800000u : TYPE == 1 ? 0xFF80FF80u : 0xFC00FC00u;   // -infinity
     __shared__ Key list[kLpList];
-    __shared__ __align__(16) Key maxima[kLpGroups];
+    __shared__ __align__(16) Key group_key[kLpGroups];
+    __shared__ __align__(16) float group_max[kLpGroups];
     __shared__ float slice_max[kLpSlices][kLpThreads];
     __shared__ Sums red[kLpWarps];
+    __shared__ unsigned odd[kLpWarps];
     __shared__ Key s_floor;
     __shared__ int s_n, s_before;
     const dg_logprobs& op = p.op;
@@ -225,12 +227,12 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_logprobs(const LpParams p) {
         for (int q = 0; q < kLpVecs; ++q) {
             const int v = first + tile * kLpTile + q * kLpThreads + tid;
             next[q] = make_uint4(kNone, kNone, kNone, kNone);
-            if (tile < tile1 && v < last) next[q] = __ldcs(vecs + v);
+            if (tile < tile1 && v < last) next[q] = TYPE == 2 ? vecs[v] : __ldcs(vecs + v);   // (measured: fp32 15 us against 16, 16 bits 125 against 130)
         }
     };
     fetch(tile0);
     if (tid == 0) {
-        s_before = s_n = 0;
+        s_before = 0;
         s_floor = 0;
     }
     int tok = -1;
@@ -353,21 +355,30 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_logprobs(const LpParams p) {
         s.join_warp(p);
         if (lane == 0) red[warp] = s;
         __syncthreads();
-        s = red[0];
-        for (int w = 1; w < kLpWarps; ++w) s.join(red[w], p);
-        __syncthreads();
+        s = lane < kLpWarps ? red[lane] : Sums{-INFINITY, 0.f, 0.f};
+        s.join_warp(p);
     };
     s = {m, l.x + l.y, a.x + a.y};
     if (m == INFINITY) s.l = kNan;
     else if (m > -INFINITY) s.m = fminf(fmaxf(m, -p.most), p.most);   // as its base
-    __syncthreads();
     if (tok >= 0) {
         ahead = warp_sum(ahead);
         if (lane == 0 && ahead) atomicAdd(&s_before, ahead);
     }
-    whole();
     // (the threads' bases may lie 2^8 below their maxima)
-    const bool far = __syncthreads_or(m < INFINITY && m > p.most) || (s.l == 0.f && __syncthreads_or(m > -INFINITY));
+    const unsigned past = __any_sync(0xffffffffu, m < INFINITY && m > p.most);
+    const unsigned some = __any_sync(0xffffffffu, m > -INFINITY);
+    if (lane == 0) odd[warp] = past | some << 1;
+    if (K) {
+        float four = fmaxf(greatest, __shfl_xor_sync(0xffffffffu, greatest, 1));
+        four = fmaxf(four, __shfl_xor_sync(0xffffffffu, four, 2));
+        if ((tid & 3) == 0) group_max[tid >> 2] = four;
+    }
+    whole();
+    unsigned any = 0;
+#pragma unroll
+    for (int w = 0; w < kLpWarps; ++w) any |= odd[w];
+    const bool far = (any & 1u) || (s.l == 0.f && (any & 2u));
     if (far) {   // logits past what a base reaches: exponents as differences
         const long long i0 = (long long)(first + tile0 * kLpTile) * kEl - skew;
         const long long i1 = (long long)min(last, first + tile1 * kLpTile) * kEl - skew;
@@ -375,6 +386,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_logprobs(const LpParams p) {
             if (end) use(logit_at<TYPE>(x, end_i));
             for (long long i = i0 + tid; i < i1; i += kLpThreads) use(logit_at<TYPE>(x, i));
         };
+        __syncthreads();   // red has been read
         s = {-INFINITY, 0.f, 0.f};
         all([&](float v) { s.m = fmaxf(s.m, v); });
         all([&](float v) {
@@ -392,34 +404,21 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_logprobs(const LpParams p) {
     }
     if (K == 0) return;
     // ---- the best -------------------------------------------------------------------------------
-    // the threads' largest keys, by fours: K of them, of different groups, are not below the floor
-    Key largest = 0;
-    if (tile0 < tile1) {
-#pragma unroll
-        for (int q = 0; q < kLpVecs; ++q) {
-            const int i = index(greatest_at, q);
-            if (i >= inside) break;
-            const uint4 v = vecs[first + greatest_at * kLpTile + q * kLpThreads + tid];
-#pragma unroll
-            for (int e = 0; e < kEl; ++e) largest = max(largest, key_of(logit(v, e), i + e));
-        }
-    }
-    largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
-    largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
-    if ((tid & 3) == 0) maxima[tid >> 2] = largest;
-    __syncthreads();
+    // K groups' maxima are not below the floor
     if (tid < kLpGroups) {
-        const Key k = maxima[tid];
-        int above = 0;
-#pragma unroll 8
-        for (int j = 0; j < kLpGroups; j += 2) {
-            const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(maxima + j);
-            above += (o.x > k) + (o.y > k);
+        const float v = group_max[tid];
+        int above = 0, same = 0;
+#pragma unroll 4
+        for (int j = 0; j < kLpGroups; j += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(group_max + j);
+            above += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
+            same += (o.x == v) + (o.y == v) + (o.z == v) + (o.w == v);
         }
-        if (k && above == K - 1) s_floor = k;
+        // (a maximum of -infinity may be of NaN only)
+        if (above < K && above + same >= K) s_floor = v > -INFINITY ? key_of(v, -1) : 0;
     }
     int n;
-    while (true) {
+    for (int turn = 0;; ++turn) {
         if (tid == 0) s_n = ends;
         __syncthreads();
         const Key floor = s_floor;
@@ -451,12 +450,37 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_logprobs(const LpParams p) {
         __syncthreads();
         n = s_n;
         if (n <= kLpList) break;
-        // too many: the top_k-th of those that found room is a higher floor
-        for (int i = tid; i < kLpList; i += kLpThreads) {
-            const Key k = list[i];
-            int above = 0;
-            for (int j = 0; j < kLpList; ++j) above += list[j] > k;
-            if (above == K - 1) s_floor = k;
+        // too many: next time from the groups' keys (equal logits differ there), and then from the
+        // top_k-th of those that found room
+        if (turn == 0) {
+            Key largest = 0;
+            if (tile0 < tile1) {
+#pragma unroll
+                for (int q = 0; q < kLpVecs; ++q) {
+                    const int i = index(greatest_at, q);
+                    if (i >= inside) break;
+                    const uint4 v = vecs[first + greatest_at * kLpTile + q * kLpThreads + tid];
+#pragma unroll
+                    for (int e = 0; e < kEl; ++e) largest = max(largest, key_of(logit(v, e), i + e));
+                }
+            }
+            largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
+            largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
+            if ((tid & 3) == 0) group_key[tid >> 2] = largest;
+            __syncthreads();
+            if (tid < kLpGroups) {
+                const Key k = group_key[tid];
+                int above = 0;
+                for (int j = 0; j < kLpGroups; ++j) above += group_key[j] > k;
+                if (k && above == K - 1) s_floor = max(s_floor, k);
+            }
+        } else {
+            for (int i = tid; i < kLpList; i += kLpThreads) {
+                const Key k = list[i];
+                int above = 0;
+                for (int j = 0; j < kLpList; ++j) above += list[j] > k;
+                if (above == K - 1) s_floor = k;
+            }
         }
         __syncthreads();
     }
@@ -479,14 +503,19 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_logprobs(const LpParams p) {
 }
 
 // The parts of a row: their sums in order, and top_k times the largest of the parts' next
-// keys.  A warp a row.
+// keys.  A CTA a row; its first warp does it, when all have brought the keys to shared memory.
+constexpr int kLpJoinThreads = 128;
 template <int TYPE>
-__global__ void __launch_bounds__(32) k_logprobs_join(const LpParams p) {
+__global__ void __launch_bounds__(kLpJoinThreads) k_logprobs_join(const LpParams p) {
+    __shared__ Key keys[kLpMaxParts * 32];
     griddep_launch_dependents();
     griddep_wait();
     const dg_logprobs& op = p.op;
     const int row = blockIdx.x, lane = threadIdx.x, K = op.top_k, n = p.parts;
     const unsigned char* x = static_cast<const unsigned char*>(op.logits) + (long long)row * op.stride * (TYPE == 2 ? 4 : 2);
+    for (int i = threadIdx.x; i < n * K; i += kLpJoinThreads) keys[i] = p.keys[(size_t)row * n * K + i];
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
     Sums s = {-INFINITY, 0.f, 0.f};
     int before = 0;
     for (int i = lane; i < n; i += 32) {   // (two parts a lane at most)
@@ -499,24 +528,28 @@ __global__ void __launch_bounds__(32) k_logprobs_join(const LpParams p) {
     const Row r(s, p);
     if (lane == 0) write_row<TYPE>(p, r, row, before, x);
     if (K == 0) return;
-    const Key* keys = p.keys + (size_t)row * n * K;
     int at[2] = {0, 0};
-    Key head[2];
+    Key head[2], mine = 0;   // the two lists' next keys; the key of this lane's place
 #pragma unroll
-    for (int h = 0; h < 2; ++h) head[h] = lane + 32 * h < n ? keys[(size_t)(lane + 32 * h) * K] : 0;
+    for (int h = 0; h < 2; ++h) head[h] = lane + 32 * h < n ? keys[(lane + 32 * h) * K] : 0;
     for (int i = 0; i < K; ++i) {
         const int h = head[1] > head[0];
-        Key best = h ? head[1] : head[0];
+        const Key best = h ? head[1] : head[0];
         const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
         const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
         const Key win = (Key)hi << 32 | lo;
+        if (lane == i) mine = win;
         if (win == best && win) {   // keys are unique: one lane
-            const long long to = (long long)row * K + i;
-            if (op.top_ids) op.top_ids[to] = index_of(win);
-            if (op.top_logprobs) op.top_logprobs[to] = r.logprob(logit_of(win));
-            ++at[h];
-            head[h] = at[h] < K ? keys[(size_t)(lane + 32 * h) * K + at[h]] : 0;
+            const int next = h ? ++at[1] : ++at[0];
+            const Key k = next < K ? keys[(lane + 32 * h) * K + next] : 0;
+            if (h) head[1] = k;
+            else head[0] = k;
         }
+    }
+    if (lane < K && mine) {
+        const long long to = (long long)row * K + lane;
+        if (op.top_ids) op.top_ids[to] = index_of(mine);
+        if (op.top_logprobs) op.top_logprobs[to] = r.logprob(logit_of(mine));
     }
 }
 
@@ -548,7 +581,7 @@ static cudaError_t launch_lp(const dg_logprobs& op, void* ws, cudaStream_t s) {
     const cudaError_t e = launch_pdl((const void*)k_logprobs<TYPE>, dim3((unsigned)op.rows * p.parts),
                                      dim3(kLpThreads), 0, s, args);
     if (e != cudaSuccess || p.parts == 1) return e;
-    return launch_pdl((const void*)k_logprobs_join<TYPE>, dim3(op.rows), dim3(32), 0, s, args);
+    return launch_pdl((const void*)k_logprobs_join<TYPE>, dim3(op.rows), dim3(kLpJoinThreads), 0, s, args);
 }
 
 cudaError_t launch_logprobs(const dg_logprobs& op, void* ws, cudaStream_t s) {
