@@ -522,7 +522,8 @@ size_t dg_moe_workspace_bytes(const dg_moe* op);
  * and its head_dim / 16 scales at k_scale with the scale_* strides; v and v_scale
  * likewise.  [page][head][slot][..] reads each head's rows in one piece and is the
  * faster order.  Codes of -8 are read as such (the append writes none).  k, v and
- * the strides of codes are multiples of 8 bytes; scales may lie anywhere. */
+ * the strides of codes are multiples of 8 bytes; scales may lie anywhere.  Strides of
+ * 2^32 bytes or more return DG_ERR_UNSUPPORTED. */
 typedef struct {
     int32_t type;      /* dg_ftype of q, k, v, out beside the cache */
     int32_t batch;

@@ -32,12 +32,12 @@ struct Attn4Shape {
     static constexpr int kPitch = DP == 192 ? 128 : DP / 2;          // bytes of a key's codes
     static constexpr int kScales = DP / 16;
     static constexpr int kCodes = kKeys * kPitch;
-    static constexpr int kStage = 2 * (kCodes + kKeys * kScales);    // K codes, V codes, K scales, V scales
+    static constexpr int kStage = 2 * (kCodes + kKeys * kScales) + kKeys * 4;   // codes (k, v), scales (k, v), positions
+    static constexpr int kPos = kStage - kKeys * 4;
     static constexpr int kRows = RT * 8;
     static constexpr int kOut = kRows * DP * 4;                      // a warp's output, in place of stages
     static constexpr int kNeed = (kOut + kStage - 1) / kStage + 1;
-    static constexpr int kLeast = DP <= 128 ? 3 : 2;
-    static constexpr int kStages = kNeed < kLeast ? kLeast : kNeed;
+    static constexpr int kStages = kNeed < 2 ? 2 : kNeed;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kKeyWords = 4 * kWide + 2 * kHalf;          // words (8 dims) of a lane, of a key
     static constexpr int kValWords = 2 * kWide + kHalf;              // of a value
@@ -47,7 +47,7 @@ struct Attn4Shape {
     static constexpr int kFit = 228 * 1024 / (kSmem + 2048), kWish = RT * DP <= 128 ? 4 : RT * DP <= 256 ? 3 : 2;
     static constexpr int kCtas = kFit < kWish ? kFit : kWish;
     static constexpr int kPart = part_floats(kRows, DP);
-    // Byte of 16-byte piece c of row r.  Pieces change places inside 128 bytes, so that what a
+    // Byte of 16-byte piece c of row r; eight rows on it is 8 kPitch more.  Pieces change places inside 128 bytes, so that what a
     // phase of the reads below takes lies in different banks: 8 lanes 16 bytes of two
     // neighbouring keys, 16 lanes 8 bytes (or 32 lanes 4 bytes) of every second value row.
     __device__ static constexpr int piece(int r, int c) {
@@ -62,11 +62,14 @@ struct Attn4Shape {
 
 struct Attn4Params {
     AttnParams a;                 // a.op: the same masks and outputs; its k and v are not read
-    const uint8_t *k, *v, *k_scale, *v_scale;
-    int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+    const uint8_t *k, *k_scale;
+    int64_t to_v, to_v_scale;     // bytes from a key's codes and scales to its value's
+    uint32_t page_stride, token_stride, head_stride;                     // of codes, in 8 bytes
+    uint32_t scale_page_stride, scale_token_stride, scale_head_stride;   // bytes
     float c2;                     // |scale| k_factor log2(e) 16; 0 for a scale of zero
     float out_factor;             // 16 v_factor
     int wide;                     // code rows in pieces of 16 bytes, not 8
+    int runs;                     // and sixteen keys of a stage lie in one page
     int scale_piece;              // bytes that scales are copied by: 16, 8, 4; 1: by ordinary loads
 };
 
@@ -84,15 +87,15 @@ struct Scales {
         hi_off = h2mul(s, 0xC480C480u);   // -4.5
     }
 };
-__device__ __forceinline__ uint32_t h2fma(uint32_t a, __half2 b, __half2 c) {
-    return h2_as_u32(__hfma2(u32_as_h2(a), b, c));
+__device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
+    return h2_as_u32(__hfma2(u32_as_h2(a), u32_as_h2(b), u32_as_h2(c)));
 }
 // The codes in bits 0-3 and 16-19 (lower), 4-7 and 20-23 (upper) of w, times their scales.
-__device__ __forceinline__ uint32_t lower(uint32_t w, __half2 s, __half2 off) {
-    return h2fma(and_xor(w, 0x000F000Fu, 0x64086408u), s, off);
+__device__ __forceinline__ uint32_t lower(uint32_t w, const Scales& s) {
+    return h2fma(and_xor(w, 0x000F000Fu, 0x64086408u), s.lo, s.lo_off);
 }
-__device__ __forceinline__ uint32_t upper(uint32_t w, __half2 s, __half2 off) {
-    return h2fma(and_xor(w, 0x00F000F0u, 0x64806480u), s, off);
+__device__ __forceinline__ uint32_t upper(uint32_t w, const Scales& s) {
+    return h2fma(and_xor(w, 0x00F000F0u, 0x64806480u), s.hi, s.hi_off);
 }
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
@@ -143,8 +146,18 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
         Span sp;
         int key0, lim, n;  // this warp's n stages: kKeys keys from key0 on, then every
                            // kStep further, up to lim
+        const uint8_t *k, *ks;   // codes and scales of the head's keys
+        const uint8_t* k_row;    // this lane's piece of its row of the first ones
     } sg;
+    auto times = [](int a, uint32_t b) { return (long long)((unsigned long long)(unsigned)a * b); };
     constexpr int kKeys = S::kKeys, kStep = kAttnWarps * kKeys, kStages = S::kStages;
+    const int row_bytes = D / 2, scale_bytes = D / 16;
+    constexpr int kChunks16 = DP / 32;                    // 16-byte pieces of a row
+    constexpr bool kEven = 32 % kChunks16 == 0;           // a warp's pieces are whole rows
+    constexpr int kAtOnce = kEven ? 32 / kChunks16 : 1;   // rows
+    const int my_row = lane / kChunks16, my_piece = lane % kChunks16;
+    const int my_byte = my_piece * 16 < row_bytes ? my_piece * 16 : 0;
+    const uint32_t my_place = S::piece(my_row, my_piece);
     auto enter = [&](long long blk, bool first) {
         sg.sp = span_of(op, b);
         sg.nb = blocks_of(sg.sp);
@@ -162,32 +175,96 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
         sg.key0 = sg.kb * kBlockKeys + warp * kKeys;
         sg.lim = sg.ke == sg.nb ? sg.sp.count() : sg.ke * kBlockKeys;   // nb * kBlockKeys may be 2^31
         sg.n = sg.key0 < sg.lim ? (int)((unsigned)(sg.lim - sg.key0 + kStep - 1) / kStep) : 0;
+        sg.k = p.k + 8 * times(sg.hk, p.head_stride);
+        sg.ks = p.k_scale + times(sg.hk, p.scale_head_stride);
+        sg.k_row = sg.k + times(my_row, 8 * p.token_stride) + my_byte;
         if (sg.kb == 0 && tid == 0 && p.a.info)
             p.a.info[(long long)b * heads + unit] = unit_parts(range, blk, sg.nb, sg.ke, first);
     };
-    // Position, code offset and scale offset (bytes; -1: nothing there) of key `lane` of stage i.
-    auto locate = [&](int i, int& pos, long long& off, long long& soff) {
-        const unsigned c = (unsigned)sg.key0 + (unsigned)i * kStep + lane;
+    // Position, code offset and scale offset (bytes from the head's base; -1: nothing there) of
+    // position c of the segment's walk.
+    auto find = [&](unsigned c, int& pos, long long& off, long long& soff) {
         pos = INT_MAX;
         off = -1;
         soff = 0;
-        if (i < sg.n && c < (unsigned)sg.lim) {
+        if (c < (unsigned)sg.lim) {
             const int j = sg.sp.position((int)c);
             int slot = 0;
-            const int page = sg.sp.seen(j) ? page_slot(op.kv, p.a.page_size, sg.b, j, slot) : -1;
+            const int page = page_slot(op.kv, p.a.page_size, sg.b, j, slot);
             if (page >= 0) {
                 pos = j;
-                off = page * op.kv.page_stride + slot * op.kv.token_stride + sg.hk * op.kv.head_stride;
-                soff = page * p.scale_page_stride + slot * p.scale_token_stride + sg.hk * p.scale_head_stride;
+                off = 8 * (times(page, p.page_stride) + times(slot, p.token_stride));
+                soff = times(page, p.scale_page_stride) + times(slot, p.scale_token_stride);
+            }
+        }
+    };
+    // Where sixteen positions in a row lie in one page (p.runs), the lanes find the next sixteen stages'
+    // halves at once, 32 places, and a stage takes its two from them; else each lane finds its
+    // key of the next stage.
+    int pos_at;
+    long long off_at, soff_at;
+    auto locate = [&](int i) {
+        if (p.runs) {
+            if (i % 16 == 0)
+                find((unsigned)sg.key0 + (unsigned)(i + (lane >> 1)) * kStep + (lane & 1) * 16, pos_at, off_at, soff_at);
+        } else {
+            find(i < sg.n ? (unsigned)sg.key0 + (unsigned)i * kStep + lane : UINT_MAX, pos_at, off_at, soff_at);
+            if (pos_at != INT_MAX && !sg.sp.seen(pos_at)) {
+                pos_at = INT_MAX;
+                off_at = -1;
             }
         }
     };
     auto place = [](int i) { return (i + kStages - 1) % kStages; };
-    const int row_bytes = D / 2, scale_bytes = D / 16;
-    auto issue = [&](int i, long long off, long long soff) {
+    // the byte of a row's piece, `rows` (a multiple of kAtOnce) further
+    auto piece_on = [](uint32_t at, int rows) {
+        return rows % 8 == 0 ? at + rows * S::kPitch : (at + rows * S::kPitch) ^ 64;   // kPitch 128, 4 rows
+    };
+    auto issue = [&](int i) {
         if (i < sg.n) {
             const uint32_t dst = ring_a + place(i) * S::kStage;
-            if (p.wide) {
+            int pos = pos_at;
+            long long off = off_at, soff = soff_at;
+            if (p.runs) {
+                const int from = (i % 16) * 2 + (lane >> 4);
+                pos = __shfl_sync(0xffffffffu, pos_at, from);
+                soff = __shfl_sync(0xffffffffu, soff_at, from) + times(lane & 15, p.scale_token_stride);
+                const unsigned c = (unsigned)sg.key0 + (unsigned)i * kStep + lane;
+                if (pos != INT_MAX) pos += lane & 15;
+                if (!(c < (unsigned)sg.lim && sg.sp.seen(pos))) pos = INT_MAX;
+            }
+            const bool there = pos != INT_MAX;
+            *reinterpret_cast<int*>(ring + place(i) * S::kStage + S::kPos + lane * 4) = pos;
+            if (kEven && p.runs) {
+                // addresses without an exchange for each row: a half's sixteen rows exist where its page
+                // does (else page 0's stand in for them), whether or not they are copied
+                const unsigned have = __ballot_sync(0xffffffffu, there);
+                const bool all = have == 0xffffffffu && D == DP;
+                const long long step = (long long)(8 * kAtOnce) * p.token_stride;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const long long o = max(__shfl_sync(0xffffffffu, off_at, (i % 16) * 2 + half), 0ll);
+                    const uint8_t *k = sg.k_row + o, *v = k + p.to_v;
+#pragma unroll
+                    for (int it = 0; it < 16 / kAtOnce; ++it) {
+                        const uint32_t d = dst + piece_on(my_place, half * 16 + it * kAtOnce);
+                        if (all) {
+                            cp_async16(d, k);
+                            cp_async16(d + S::kCodes, v);
+                        } else {
+                            const bool in = my_piece * 16 < row_bytes && (have >> (half * 16 + it * kAtOnce + my_row)) & 1u;
+                            cp_async16(d, k, in);
+                            cp_async16(d + S::kCodes, v, in);
+                        }
+                        k += step;
+                        v += step;
+                    }
+                }
+            } else if (p.wide) {
+                if (p.runs) {
+                    off = __shfl_sync(0xffffffffu, off_at, (i % 16) * 2 + (lane >> 4));
+                    off = there ? off + times(lane & 15, 8 * p.token_stride) : -1;
+                }
                 constexpr int kChunks = DP / 32;   // 16-byte pieces of a row
 #pragma unroll
                 for (int it = 0; it < kChunks; ++it) {
@@ -196,8 +273,8 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
                     const bool in = o >= 0 && ch * 16 < row_bytes;
                     const long long at = in ? o + ch * 16 : 0;
                     const uint32_t d = dst + S::piece(row, ch);
-                    cp_async16(d, p.k + at, in);
-                    cp_async16(d + S::kCodes, p.v + at, in);
+                    cp_async16(d, sg.k + at, in);
+                    cp_async16(d + S::kCodes, sg.k + p.to_v + at, in);
                 }
             } else {
                 constexpr int kChunks = DP / 16;   // 8-byte ones
@@ -208,35 +285,41 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
                     const bool in = o >= 0 && ch * 8 < row_bytes;
                     const long long at = in ? o + ch * 8 : 0;
                     const uint32_t d = dst + S::piece(row, ch >> 1) + (ch & 1) * 8;
-                    cp_async_n(d, p.k + at, 8, in);
-                    cp_async_n(d + S::kCodes, p.v + at, 8, in);
+                    cp_async_n(d, sg.k + at, 8, in);
+                    cp_async_n(d + S::kCodes, sg.k + p.to_v + at, 8, in);
                 }
             }
             // this lane's key: its scales
             const uint32_t d = dst + 2 * S::kCodes + lane * S::kScales;
-            const bool there = off >= 0;
-            if (p.scale_piece > 1) {
+            const uint8_t *ks = sg.ks + (there ? soff : 0), *vs = ks + p.to_v_scale;
+            constexpr bool kOnce = S::kScales == 4 || S::kScales == 8 || S::kScales == 16;
+            if (kOnce && p.scale_piece == S::kScales) {
+                cp_async_n(d, ks, S::kScales, there);
+                cp_async_n(d + kKeys * S::kScales, vs, S::kScales, there);
+            } else if (p.scale_piece > 1) {
                 const int step = p.scale_piece;
+#pragma unroll 1
                 for (int at = 0; at < S::kScales; at += step) {
                     const bool in = there && at < scale_bytes;
-                    const long long from = in ? soff + at : 0;
-                    cp_async_n(d + at, p.k_scale + from, step, in);
-                    cp_async_n(d + kKeys * S::kScales + at, p.v_scale + from, step, in);
+                    const int from = in ? at : 0;
+                    cp_async_n(d + at, ks + from, step, in);
+                    cp_async_n(d + kKeys * S::kScales + at, vs + from, step, in);
                 }
             } else {
                 unsigned char* to = ring + place(i) * S::kStage + 2 * S::kCodes + lane * S::kScales;
+#pragma unroll 1
                 for (int at = 0; at < S::kScales; ++at) {
                     const bool in = there && at < scale_bytes;
-                    to[at] = in ? __ldcg(p.k_scale + soff + at) : 0;
-                    to[kKeys * S::kScales + at] = in ? __ldcg(p.v_scale + soff + at) : 0;
+                    to[at] = in ? __ldcg(ks + at) : 0;
+                    to[kKeys * S::kScales + at] = in ? __ldcg(vs + at) : 0;
                 }
             }
         }
         cp_commit();
     };
-    // q as the matrix instruction's operand B: for tile r and word w of a lane, the pairs of dims
-    // (0, 4), (1, 5), (2, 6), (3, 7) of the eight that the lane unpacks there, in row
-    // r * 8 + g.  bf16 rows are scaled to 2^14..2^15.  A warp takes tiles warp, warp + 4, ..
+    // q as the matrix instruction's operand B: for tile r, the pairs of dims (a + e, b + e), e < 4, that
+    // the lane unpacks together (unit w), in row r * 8 + g.  bf16 rows are scaled to 2^14..2^15.
+    // A warp takes tiles warp, warp + 4, ..
     auto stage_q = [&] {
         const float sign = op.scale > 0.f ? 1.f : op.scale < 0.f ? -1.f : 0.f;
         for (int r = warp; r < RT; r += kAttnWarps) {
@@ -246,9 +329,13 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
                                 ((long long)sg.b * op.q_len + (have ? tok : 0)) * op.q_stride +
                                 (long long)(sg.hk * G + (have ? row - tok * G : 0)) * D;
             auto load = [&](int w) {
-                const int d = w < 4 * S::kWide ? (w >> 2) * 128 + t4 * 32 + (w & 3) * 8
-                                               : S::kWide * 128 + t4 * 16 + (w - 4 * S::kWide) * 8;
-                return have && d < D ? __ldcg(reinterpret_cast<const uint4*>(q + d)) : make_uint4(0, 0, 0, 0);
+                const bool wide = w < 4 * S::kWide;
+                const int a = wide ? (w >> 2) * 128 + t4 * 32 + (w & 3) * 4
+                                   : S::kWide * 128 + t4 * 16 + (w - 4 * S::kWide) * 4, b = a + (wide ? 16 : 8);
+                uint2 x = make_uint2(0, 0), y = x;
+                if (have && a < D) x = __ldcg(reinterpret_cast<const uint2*>(q + a));
+                if (have && b < D) y = __ldcg(reinterpret_cast<const uint2*>(q + b));
+                return make_uint4(x.x, x.y, y.x, y.y);
             };
             float up = 1.f, c2 = p.c2;
             if (BF16) {
@@ -284,23 +371,14 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
         }
     };
 
-    int pos[kStages];   // positions of the stages in flight, by stage mod kStages
-    int pos_next;
-    long long off_next, soff_next;
     long long blk = begin;
     enter(blk, true);
     auto start = [&](int from, int to) {   // the first stages, one after the other
 #pragma unroll
         for (int i = 0; i < kStages; ++i) {
             if (i < from || i >= to) continue;
-            long long off, soff;
-            locate(i, pos[i], off, soff);
-            if (i < kStages - 1) issue(i, off, soff);
-            else {
-                pos_next = pos[i];
-                off_next = off;
-                soff_next = soff;
-            }
+            locate(i);
+            if (i < kStages - 1) issue(i);
         }
     };
     start(0, 1);
@@ -312,7 +390,7 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
         const int row0 = sg.row0, n = sg.n, last = sp.first + op.q_len - 1;
 
         // output: word u of a lane, its dims 2 x and 2 x + 1, rows 2 t4 and 2 t4 + 1 of a tile
-        float o[RT][S::kValWords][4][4], m[RT][2], l[RT][2], c2[RT][2], grow[RT][2];
+        float o[RT][S::kValWords][4][4], m[RT][2], shift[RT][2], l[RT][2], c2[RT][2], grow[RT][2];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
 #pragma unroll
@@ -322,12 +400,17 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 m[r][h] = -INFINITY;
+                shift[r][h] = 0.f;   // -m, or 0 while m is -infinity
                 l[r][h] = 0.f;
                 c2[r][h] = sm_c[r * 8 + 2 * t4 + h];
                 grow[r][h] = fminf(8.f / c2[r][h], FLT_MAX);   // finite: the first maximum is always taken
             }
         }
 
+        // this lane's places in a stage: keys g, g + 8, ..; values 2 t4 and 2 t4 + 1, + 8, ..
+        const int key_at = S::piece(g, S::kWide ? t4 : t4 >> 1) + (S::kWide ? 0 : (t4 & 1) * 8);
+        const int val_at = S::piece(2 * t4, S::kWide ? g >> 1 : g >> 2) + (S::kWide ? (g & 1) * 8 : (g & 3) * 4);
+        const int val_at1 = S::piece(2 * t4 + 1, S::kWide ? g >> 1 : g >> 2) + (S::kWide ? (g & 1) * 8 : (g & 3) * 4);
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             cp_wait<kStages - 2>();
@@ -336,17 +419,11 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
             unsigned char* stage = ring + slot * S::kStage;
             unsigned char* ks = stage + 2 * S::kCodes;      // scales of the keys, then of the values
             unsigned char* vs = ks + kKeys * S::kScales;
-            int my_pos = pos[0];
-#pragma unroll
-            for (int q = 1; q < kStages; ++q)
-                if (i % kStages == q) my_pos = pos[q];
+            const int my_pos = *reinterpret_cast<const int*>(stage + S::kPos + lane * 4);
             // the place that the last stage left is free: refill it
             const int ni = i + kStages - 1;
-#pragma unroll
-            for (int q = 0; q < kStages; ++q)
-                if (ni % kStages == q) pos[q] = pos_next;
-            issue(ni, off_next, soff_next);
-            locate(ni + 1, pos_next, off_next, soff_next);
+            issue(ni);
+            locate(ni + 1);
 
             const bool all = my_pos <= sp.first &&
                              (!op.window || last - my_pos < op.window || my_pos < op.sinks);
@@ -355,54 +432,57 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
                 const int pr = sp.first + (row0 + r * 8 + 2 * t4 + h) / G;
                 return kp <= pr && (!op.window || pr - kp < op.window || kp < op.sinks);
             };
-#pragma unroll
+#pragma unroll 1
             for (int sub = 0; sub < 2; ++sub) {
                 // ---- scores of 16 keys: rows g and g + 8 of operand A ---------------------------
                 float s[RT][4];
 #pragma unroll
                 for (int r = 0; r < RT; ++r) s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.f;
+                float s_odd[4] = {0.f, 0.f, 0.f, 0.f};   // of one tile: two chains of products
                 const int k0 = sub * 16 + g, k1 = k0 + 8;
-                auto score_words = [&](const uint32_t* w0, const uint32_t* w1, int words, int first_word,
-                                       const Scales& s0, const Scales& s1, bool two) {
+                // words a and b of two keys: nibble e of both side by side
+                auto score_words = [&](uint32_t a0, uint32_t b0, uint32_t a1, uint32_t b1, const Scales& s0,
+                                       const Scales& s1, int unit) {
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        if (w >= words) break;
-                        const bool hi = two && w >= 2;   // the second scale of the pair
-                        auto of = [&](uint32_t v) { return hi ? __high2half2(u32_as_h2(v)) : __low2half2(u32_as_h2(v)); };
-                        uint32_t a0[4], a1[4];
-                        a0[0] = lower(w0[w], of(s0.lo), of(s0.lo_off));
-                        a0[1] = lower(w1[w], of(s1.lo), of(s1.lo_off));
-                        a0[2] = upper(w0[w], of(s0.hi), of(s0.hi_off));
-                        a0[3] = upper(w1[w], of(s1.hi), of(s1.hi_off));
-                        a1[0] = lower(w0[w] >> 8, of(s0.lo), of(s0.lo_off));
-                        a1[1] = lower(w1[w] >> 8, of(s1.lo), of(s1.lo_off));
-                        a1[2] = upper(w0[w] >> 8, of(s0.hi), of(s0.hi_off));
-                        a1[3] = upper(w1[w] >> 8, of(s1.hi), of(s1.hi_off));
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t pick = y ? 0x7632u : 0x5410u;
+                        const uint32_t x0 = __byte_perm(a0, b0, pick), x1 = __byte_perm(a1, b1, pick);
+                        const uint32_t f0[4] = {lower(x0, s0), lower(x1, s1), upper(x0, s0), upper(x1, s1)};
+                        const uint32_t f1[4] = {lower(x0 >> 8, s0), lower(x1 >> 8, s1), upper(x0 >> 8, s0),
+                                                upper(x1 >> 8, s1)};
 #pragma unroll
                         for (int r = 0; r < RT; ++r) {
                             const uint4 q = *reinterpret_cast<const uint4*>(
-                                qs + (r * S::kKeyWords + first_word + w) * 512 + lane * 16);
-                            mma16816<false>(s[r], a0, q.x, q.y);
-                            mma16816<false>(s[r], a1, q.z, q.w);
+                                qs + (r * S::kKeyWords + unit + y) * 512 + lane * 16);
+                            mma16816<false>(s[r], f0, q.x, q.y);
+                            if constexpr (RT == 1) mma16816<false>(s_odd, f1, q.z, q.w);
+                            else mma16816<false>(s[r], f1, q.z, q.w);
                         }
                     }
                 };
 #pragma unroll
                 for (int h = 0; h < S::kWide; ++h) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(stage + S::piece(k0, h * 4 + t4));
-                    const uint4 y = *reinterpret_cast<const uint4*>(stage + S::piece(k1, h * 4 + t4));
+                    // (64 bytes on, inside 128, is another piece's bit 2)
+                    const unsigned char* at = stage + (key_at ^ (h * 64)) + sub * 16 * S::kPitch;
+                    const uint4 x = *reinterpret_cast<const uint4*>(at);
+                    const uint4 y = *reinterpret_cast<const uint4*>(at + 8 * S::kPitch);
                     const Scales s0(*reinterpret_cast<const uint16_t*>(ks + k0 * S::kScales + h * 8 + t4 * 2));
                     const Scales s1(*reinterpret_cast<const uint16_t*>(ks + k1 * S::kScales + h * 8 + t4 * 2));
-                    const uint32_t w0[4] = {x.x, x.y, x.z, x.w}, w1[4] = {y.x, y.y, y.z, y.w};
-                    score_words(w0, w1, 4, h * 4, s0, s1, true);
+                    score_words(x.x, x.z, y.x, y.z, s0, s1, h * 4);
+                    score_words(x.y, x.w, y.y, y.w, s0, s1, h * 4 + 2);
                 }
                 if constexpr (S::kHalf) {
                     constexpr int base = S::kWide * 4;   // piece of the last 64 dims
-                    const uint2 x = *reinterpret_cast<const uint2*>(stage + S::piece(k0, base + (t4 >> 1)) + (t4 & 1) * 8);
-                    const uint2 y = *reinterpret_cast<const uint2*>(stage + S::piece(k1, base + (t4 >> 1)) + (t4 & 1) * 8);
-                    const Scales s0(ks[k0 * S::kScales + S::kWide * 8 + t4]), s1(ks[k1 * S::kScales + S::kWide * 8 + t4]);
-                    const uint32_t w0[2] = {x.x, x.y}, w1[2] = {y.x, y.y};
-                    score_words(w0, w1, 2, S::kWide * 4, s0, s1, false);
+                    const unsigned char* at =
+                        stage + (S::kWide ? S::piece(g, base + (t4 >> 1)) + (t4 & 1) * 8 : key_at) + sub * 16 * S::kPitch;
+                    const uint2 x = *reinterpret_cast<const uint2*>(at);
+                    const uint2 y = *reinterpret_cast<const uint2*>(at + 8 * S::kPitch);
+                    const uint32_t e0 = ks[k0 * S::kScales + S::kWide * 8 + t4], e1 = ks[k1 * S::kScales + S::kWide * 8 + t4];
+                    score_words(x.x, x.y, y.x, y.y, Scales(e0 | e0 << 8), Scales(e1 | e1 << 8), S::kWide * 4);
+                }
+                if constexpr (RT == 1) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s[0][x] += s_odd[x];
                 }
                 // ---- masks, where some row does not see some key of the stage -----------------
                 if (!whole_stage) {
@@ -465,6 +545,7 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
                             v = fmaxf(v, m[r][h]);
                             const float f = v == m[r][h] ? 1.f : exp2_fast((m[r][h] - v) * c2[r][h]);
                             m[r][h] = v;
+                            shift[r][h] = v == -INFINITY ? 0.f : -v;
                             l[r][h] *= f;
 #pragma unroll
                             for (int u = 0; u < S::kValWords; ++u)
@@ -475,17 +556,18 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
                                 }
                         }
                     }
-                    float w[4];
+                    const float2 one = make_float2(1.f, 1.f), lift = make_float2(kLift<false>, kLift<false>);
+                    const float2 cc = make_float2(c2[r][0], c2[r][1]), off = make_float2(shift[r][0], shift[r][1]);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float shift = m[r][h] == -INFINITY ? 0.f : m[r][h];
-                        w[h] = exp2_fast(fmaf(s[r][h] - shift, c2[r][h], kLift<false>));
-                        w[2 + h] = exp2_fast(fmaf(s[r][2 + h] - shift, c2[r][h], kLift<false>));
-                        l[r][h] += w[h] + w[2 + h];
+                    for (int x = 0; x < 2; ++x) {   // key g + 8 x, rows 2 t4 and 2 t4 + 1
+                        const float2 d = fma2(make_float2(s[r][2 * x], s[r][2 * x + 1]), one, off);
+                        const float2 z = fma2(d, cc, lift);
+                        const float2 w = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                        const float2 sum = fma2(w, one, make_float2(l[r][0], l[r][1]));
+                        l[r][0] = sum.x;
+                        l[r][1] = sum.y;
+                        split_pair<false>(w.x, w.y, hi[r][x], lo[r][x]);   // [key][row], operand B is [row][key]
                     }
-                    // [key][row] -> operand B, [row][key]
-                    split_pair<false>(w[0], w[1], hi[r][0], lo[r][0]);
-                    split_pair<false>(w[2], w[3], hi[r][1], lo[r][1]);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         hi[r][x] = movmatrix(hi[r][x]);
@@ -505,10 +587,7 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {   // dims 4 y + 2 z, + 1
                             const uint32_t e0 = z ? x0 >> 8 : x0, e1 = z ? x1 >> 8 : x1;
-                            const uint32_t a[4] = {lower(e0, u32_as_h2(s0.lo), u32_as_h2(s0.lo_off)),
-                                                   upper(e0, u32_as_h2(s0.hi), u32_as_h2(s0.hi_off)),
-                                                   lower(e1, u32_as_h2(s1.lo), u32_as_h2(s1.lo_off)),
-                                                   upper(e1, u32_as_h2(s1.hi), u32_as_h2(s1.hi_off))};
+                            const uint32_t a[4] = {lower(e0, s0), upper(e0, s0), lower(e1, s1), upper(e1, s1)};
 #pragma unroll
                             for (int r = 0; r < RT; ++r) {
                                 mma16816<false>(o[r][u][2 * y + z], a, hi[r][0], hi[r][1]);
@@ -525,7 +604,8 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const int key = v0 + (x & 1) + (x >> 1) * 8;
-                        w[x] = *reinterpret_cast<const uint2*>(vals + S::piece(key, h * 4 + (g >> 1)) + (g & 1) * 8);
+                        w[x] = *reinterpret_cast<const uint2*>(vals + ((x & 1 ? val_at1 : val_at) ^ (h * 64)) +
+                                                               (sub * 16 + (x >> 1) * 8) * S::kPitch);
                         e[x] = scale_of(key, h * 8 + g);
                     }
                     const Scales s0(e[0] | e[1] << 8), s1(e[2] | e[3] << 8);
@@ -537,8 +617,9 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const int key = v0 + (x & 1) + (x >> 1) * 8;
-                        w[x] = *reinterpret_cast<const uint32_t*>(vals + S::piece(key, S::kWide * 4 + (g >> 2)) +
-                                                                  (g & 3) * 4);
+                        const int at = S::kWide ? S::piece(2 * t4 + (x & 1), S::kWide * 4 + (g >> 2)) + (g & 3) * 4
+                                                : x & 1 ? val_at1 : val_at;
+                        w[x] = *reinterpret_cast<const uint32_t*>(vals + at + (sub * 16 + (x >> 1) * 8) * S::kPitch);
                         e[x] = scale_of(key, S::kWide * 8 + (g >> 1));
                     }
                     add(2 * S::kWide, w[0], w[1], w[2], w[3], Scales(e[0] | e[1] << 8), Scales(e[2] | e[3] << 8));
@@ -684,17 +765,21 @@ static cudaError_t launch_attn4_t(const dg_attn4& op, void* ws, cudaStream_t s) 
     p.a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + info_bytes(p.a.op, p.a.groups));
     p.a.page_size = fast_div((uint32_t)op.kv.page_size);
     p.k = op.kv.k;
-    p.v = op.kv.v;
     p.k_scale = op.kv.k_scale;
-    p.v_scale = op.kv.v_scale;
-    p.scale_page_stride = op.kv.scale_page_stride;
-    p.scale_token_stride = op.kv.scale_token_stride;
-    p.scale_head_stride = op.kv.scale_head_stride;
+    p.to_v = (int64_t)((intptr_t)op.kv.v - (intptr_t)op.kv.k);
+    p.to_v_scale = (int64_t)((intptr_t)op.kv.v_scale - (intptr_t)op.kv.k_scale);
+    p.page_stride = (uint32_t)(op.kv.page_stride / 8);
+    p.token_stride = (uint32_t)(op.kv.token_stride / 8);
+    p.head_stride = (uint32_t)(op.kv.head_stride / 8);
+    p.scale_page_stride = (uint32_t)op.kv.scale_page_stride;
+    p.scale_token_stride = (uint32_t)op.kv.scale_token_stride;
+    p.scale_head_stride = (uint32_t)op.kv.scale_head_stride;
     p.c2 = op.scale == 0.f ? 0.f : fmaxf(fabsf(op.scale) * kLog2e * 16.f * op.kv.k_factor, FLT_MIN);
     p.out_factor = 16.f * op.kv.v_factor;
     const uintptr_t rows = (uintptr_t)op.kv.k | (uintptr_t)op.kv.v | (uintptr_t)op.kv.page_stride |
                            (uintptr_t)op.kv.token_stride | (uintptr_t)op.kv.head_stride;
     p.wide = rows % 16 == 0 && op.kv.head_dim % 32 == 0;
+    p.runs = p.wide && op.kv.page_size % 16 == 0;
     const uintptr_t scales = (uintptr_t)op.kv.k_scale | (uintptr_t)op.kv.v_scale | (uintptr_t)op.kv.scale_page_stride |
                              (uintptr_t)op.kv.scale_token_stride | (uintptr_t)op.kv.scale_head_stride |
                              (uintptr_t)(op.kv.head_dim / 16) | (uintptr_t)S::kScales;

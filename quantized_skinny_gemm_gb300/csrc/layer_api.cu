@@ -161,6 +161,11 @@ static dg_status check_kv4(const dg_paged_kv4& kv, int heads) {
     if (kv.table_stride < (kv.batch > 1 ? kv.max_pages : 0)) return DG_ERR_INVALID_ARG;
     if (kv.batch > kMaxBatch || kv.kv_heads > kMaxHeads || heads > kMaxHeads) return DG_ERR_UNSUPPORTED;
     if (kv.head_dim % 16 || kv.head_dim > 256) return DG_ERR_UNSUPPORTED;
+    // (the kernels multiply by strides of 32 bits)
+    const int64_t strides[] = {kv.page_stride,       kv.token_stride,       kv.head_stride,
+                               kv.scale_page_stride, kv.scale_token_stride, kv.scale_head_stride};
+    for (const int64_t x : strides)
+        if (x > 0xffffffffll) return DG_ERR_UNSUPPORTED;
     if (!aligned(kv.block_table, 4) || !aligned(kv.seq_lens, 4) || !aligned(kv.k, 8) || !aligned(kv.v, 8) ||
         kv.page_stride % 8 || kv.token_stride % 8 || kv.head_stride % 8)
         return DG_ERR_MISALIGNED;

@@ -98,7 +98,9 @@ def test_cache_refusals(lib):
                 dict(k_factor=0.0), dict(v_factor=0.0), dict(k_factor=-1.0), dict(v_factor=NAN),
                 dict(k_factor=INF), dict(v_factor=INF), dict(k_factor=1e38), dict(v_factor=1e38)):
         assert every(_kv4(**bad)) == INVALID, bad
-    for bad in (dict(head_dim=24), dict(head_dim=8), dict(head_dim=272), dict(batch=(1 << 20) + 1), dict(kv_heads=2048)):
+    for bad in (dict(head_dim=24), dict(head_dim=8), dict(head_dim=272), dict(batch=(1 << 20) + 1), dict(kv_heads=2048),
+                dict(page_stride=1 << 32), dict(token_stride=1 << 32), dict(head_stride=1 << 40),
+                dict(scale_page_stride=1 << 32), dict(scale_token_stride=1 << 32), dict(scale_head_stride=1 << 32)):
         assert every(_kv4(**bad)) == UNSUPPORTED, bad
     for bad in (dict(block_table=E + 2), dict(seq_lens=F + 2), dict(k=A + 4), dict(v=B + 4), dict(page_stride=1028),
                 dict(token_stride=36), dict(head_stride=516)):
