@@ -306,12 +306,23 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
                     cp_async_n(d + kKeys * S::kScales + at, vs + from, step, in);
                 }
             } else {
-                unsigned char* to = ring + place(i) * S::kStage + 2 * S::kCodes + lane * S::kScales;
-#pragma unroll 1
-                for (int at = 0; at < S::kScales; ++at) {
-                    const bool in = there && at < scale_bytes;
-                    to[at] = in ? __ldcg(ks + at) : 0;
-                    to[kKeys * S::kScales + at] = in ? __ldcg(vs + at) : 0;
+                // all loads before the first store
+                uint32_t* to = reinterpret_cast<uint32_t*>(ring + place(i) * S::kStage + 2 * S::kCodes + lane * S::kScales);
+                uint32_t kw[S::kScales / 4], vw[S::kScales / 4];
+#pragma unroll
+                for (int w = 0; w < S::kScales / 4; ++w) {
+                    kw[w] = vw[w] = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (there && w * 4 + e < scale_bytes) {
+                            kw[w] |= (uint32_t)__ldcg(ks + w * 4 + e) << (8 * e);
+                            vw[w] |= (uint32_t)__ldcg(vs + w * 4 + e) << (8 * e);
+                        }
+                }
+#pragma unroll
+                for (int w = 0; w < S::kScales / 4; ++w) {
+                    to[w] = kw[w];
+                    to[kKeys * S::kScales / 4 + w] = vw[w];
                 }
             }
         }
@@ -350,10 +361,10 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // 2^(14 - exponent of top), in two factors inside fp32's range
-                const int e = top > 0.f ? 14 - ilogbf(top) : 0;
-                up = ldexpf(1.f, max(-126, min(126, e)));
-                c2 = ldexpf(c2, -max(-126, min(126, e)));
+                // 2^(14 - exponent of top), inside fp32's normal numbers
+                const int e = top > 0.f ? max(-126, min(126, 141 - (int)(__float_as_uint(top) >> 23))) : 0;
+                up = __uint_as_float((uint32_t)(127 + e) << 23);
+                c2 *= __uint_as_float((uint32_t)(127 - e) << 23);
             }
             c2 = p.c2 == 0.f ? 1.f : fminf(fmaxf(c2, FLT_MIN), FLT_MAX);
             if (t4 == 0) sm_c[r * 8 + g] = c2;
