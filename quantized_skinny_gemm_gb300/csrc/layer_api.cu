@@ -192,9 +192,9 @@ static dg_status check_head_append(const dg_head_append& op) {
     if (op.q_stride < 0 || op.k_stride < 0 || op.v_stride < 0) return DG_ERR_INVALID_ARG;
     if (op.heads && op.q_out_stride < (int64_t)op.heads * D) return DG_ERR_INVALID_ARG;
     if (op.heads && op.q_out == op.q && op.q_out_stride != op.q_stride) return DG_ERR_INVALID_ARG;
-    // a CTA takes four heads at least
+    // a warp takes a head at least
     const int64_t tokens = op.slots ? op.tokens : (int64_t)batch * op.q_len;
-    if (tokens * ((op.heads + 2 * kvh + 3) / 4) > 0x7fffffff) return DG_ERR_UNSUPPORTED;
+    if (tokens * (op.heads + 2 * kvh) > 0x7fffffff) return DG_ERR_UNSUPPORTED;
     const void* p2[] = {op.q, op.k, op.v, op.q_out, op.w_q, op.w_k, op.bits == 16 ? op.kv.k : nullptr,
                         op.bits == 16 ? op.kv.v : nullptr};
     for (const void* p : p2)
