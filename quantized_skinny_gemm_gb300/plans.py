@@ -16,9 +16,10 @@ from typing import Dict, List, Optional
 import torch
 
 from . import (EPI_RESIDUAL, EPI_SWIGLU, LINEAR_F16, LINEAR_W4A16, LINEAR_W4A8, LINEAR_W8A8,
-               StepPlan, append, attention, attn_decode, attn_workspace_bytes, decode_step_weights,
-               kv_append, linear, moe, moe_forward, moe_workspace_bytes, norm, norm_residual,
-               paged_kv, residual_add, swiglu)
+               StepPlan, append, assign_pages, attention, attention4, attn4_decode, attn4_workspace_bytes,
+               attn_decode, attn_workspace_bytes, decode_step_weights, head_append, kv_append, linear, moe,
+               moe_forward, moe_workspace_bytes, norm, norm_residual, page_plan, paged_kv, paged_kv4,
+               pages_workspace_bytes, qkv_append, residual_add, swiglu)
 
 
 class Arena:
@@ -320,7 +321,12 @@ class SparseStep:
     run() enqueues one step: h in, h_out and x_out (normed) out, and the new
     tokens' keys and values into the caches.  Before each run seq_lens must
     count the new tokens and block_table must name the pages they fall in; both
-    are read on the device, so a captured graph follows them."""
+    are read on the device, so a captured graph follows them.  With a pool,
+    run() does that itself: it takes pages from the pool and counts the tokens.
+    A sequence that the pool or its table has no room for stays as it is (its
+    positions are -1) and its rows of the outputs mean nothing; end(ended), int32
+    [batch], gives back the pages of the sequences where it holds -1 (0: the
+    sequence goes on)."""
     run: object
     h: torch.Tensor                            # fp32 [batch * q_len][hidden]
     h_out: torch.Tensor                        # fp32
@@ -328,19 +334,28 @@ class SparseStep:
     seq_lens: torch.Tensor                     # int32 [batch]
     block_table: torch.Tensor                  # int32 [batch][max_pages]
     caches: List[tuple]                        # per layer: k, v [pages][page_size][kv_heads][head_dim]
+    #                                            (4 bits: codes of k and v, [..][head_dim / 2], then their scales)
     layers: List[Dict[str, torch.Tensor]]      # per layer: q, k, v, q_rot, att, o, x, h_mid, x_mid, y, ids, weights
     keep: list = field(default_factory=list)
+    end: object = None                         # with a pool
+    pool: Optional[torch.Tensor] = None        # int32 [pages], and its queue's first place and length
+    pool_state: Optional[torch.Tensor] = None
+    slots: Optional[torch.Tensor] = None       # int64 and int32 [batch * q_len]: where the last step's tokens went
+    positions: Optional[torch.Tensor] = None
 
 
 def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None, batch=1, q_len=1,
                         page_size=64, max_pages=16, window=0, sinks=0, group=32, rope=None,
-                        share=None) -> SparseStep:
+                        share=None, cache_bits=16, k_factor=1.0, v_factor=1.0, pool_pages=None) -> SparseStep:
     """layers: synth.sparse_decoder_workload(...) output; batch * q_len from 1 to
     16; rope: (cos, sin) fp32 [max_pos][rot / 2] or None; share: another
-    SparseStep of the same layers and batch (with another q_len) whose weights,
-    tables, caches and lengths this one uses.  Per layer
+    SparseStep of the same layers, batch and cache (with another q_len) whose weights,
+    tables, caches, lengths and pool this one uses; cache_bits: 16, or 4 with
+    k_factor and v_factor (see paged_kv4); pool_pages: pages that the sequences share
+    as they grow (None: each sequence has the pages of its whole table).  Per layer
       h += y (of the layer before); x = norm_attn(h); q, k, v = W x;
-      rotate q and k, k and v into the cache; att = attention; o = W_o att;
+      norm the heads of q and k (layers with norm_q and norm_k), rotate them,
+      k and v into the cache; att = attention; o = W_o att;
       h += o; x = norm_mlp(h); y = experts(x)
     and last h += y; x_out = final_norm(h).  The residual stream stays fp32; the
     adds are part of the norms."""
@@ -349,6 +364,12 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
         raise ValueError("batch * q_len: the products and the experts take 1 to 16 rows")
     if share is not None and share.block_table.shape[0] != batch:
         raise ValueError("share: another batch")
+    if cache_bits not in (4, 16):
+        raise ValueError("cache_bits: 4 or 16")
+    if share is not None and len(share.caches[0]) != (4 if cache_bits == 4 else 2):
+        raise ValueError("share: another kind of cache")
+    if pool_pages is not None and (pool_pages < 1 or share is not None):
+        raise ValueError("pool_pages: a page at least; with share, the other step's pool is used")
     hidden = layers[0].q.shape[1]
     dim = layers[0].q.shape[0] // heads
     for L in layers:
@@ -358,21 +379,43 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
             raise ValueError("heads, kv_heads: the layers' q, k, v, o have other sizes")
     new = lambda *shape, dtype=f16: torch.zeros(shape, dtype=dtype, device=device)
     if share is None:
-        pages = batch * max_pages
+        pages = batch * max_pages if pool_pages is None else pool_pages
         lens = new(batch, dtype=i32)
-        table = torch.arange(pages, dtype=i32, device=device).view(batch, max_pages)
+        if pool_pages is None:
+            pool = state = None
+            table = torch.arange(pages, dtype=i32, device=device).view(batch, max_pages)
+        else:
+            pool = torch.arange(pages, dtype=i32, device=device)
+            state = torch.tensor([0, pages], dtype=i32, device=device)
+            table = torch.full((batch, max_pages), -1, dtype=i32, device=device)
         weights = [{k: v.to(device) for k, v in vars(L).items() if torch.is_tensor(v)} for L in layers]
         scales = [{k: v.to(device) for k, v in L.scales.items()} for L in layers]
-        caches = [(new(pages, page_size, kv_heads, dim), new(pages, page_size, kv_heads, dim)) for _ in layers]
+        if cache_bits == 16:
+            caches = [(new(pages, page_size, kv_heads, dim), new(pages, page_size, kv_heads, dim)) for _ in layers]
+        else:   # a head's rows in one piece
+            if dim % 16:
+                raise ValueError("cache_bits 4: heads of a multiple of 16")
+            part = lambda width: new(pages, kv_heads, page_size, width, dtype=torch.uint8).transpose(1, 2)
+            caches = [(part(dim // 2), part(dim // 2), part(dim // 16), part(dim // 16)) for _ in layers]
         final = (torch.ones(hidden, dtype=f16) if final_norm is None else final_norm).to(device)
         cos, sin = (None, None) if rope is None else (t.to(device) for t in rope)
     else:
         lens, table, caches = share.seq_lens, share.block_table, share.caches
+        pool, state = share.pool, share.pool_state
         weights, scales, final, cos, sin = share.keep[0]
+        page_size = caches[0][0].shape[1]
+    slots = positions = plan = plan_ws = None
+    if pool is not None:
+        slots, positions = new(M, dtype=torch.int64), new(M, dtype=i32)
+        plan = page_plan(lens, table, pool, state, page_size, new_len=q_len, slots=slots, positions=positions)
+        plan_ws = new(max(pages_workspace_bytes(plan), 16), dtype=torch.uint8)
     first = h = new(M, hidden, dtype=f32)
     y, ops, views, attn_ws, moe_ws, lin_ws = None, [], [], 0, 0, 0
-    for W, S, (kc, vc) in zip(weights, scales, caches):
-        kv = paged_kv(kc, vc, table, lens)
+    describe, attend, attn_bytes = ((attention, attn_decode, attn_workspace_bytes) if cache_bits == 16 else
+                                    (attention4, attn4_decode, attn4_workspace_bytes))
+    for W, S, cache in zip(weights, scales, caches):
+        kv = (paged_kv(*cache, table, lens) if cache_bits == 16 else
+              paged_kv4(*cache, table, lens, k_factor=k_factor, v_factor=v_factor))
         t = {"x": new(M, hidden), "q": new(M, heads * dim), "k": new(M, kv_heads * dim), "v": new(M, kv_heads * dim),
              "q_rot": new(M, heads * dim), "att": new(M, heads * dim), "o": new(M, hidden),
              "h": new(M, hidden, dtype=f32), "h_mid": new(M, hidden, dtype=f32), "x_mid": new(M, hidden),
@@ -380,19 +423,25 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
         lin = lambda w, a, b: linear(LINEAR_F16, W[w], M, b.shape[1], a.shape[1], x=a, y=b)
         qkv = StepPlan([lin(n, t["x"], t[n]) for n in ("q", "k", "v")])
         out = StepPlan([lin("o", t["att"], t["o"])])
-        att = attention(kv, t["q_rot"], t["att"], q_len=q_len, window=window, sinks=sinks)
+        att = describe(kv, t["q_rot"], t["att"], q_len=q_len, window=window, sinks=sinks)
+        where = {"q_len": q_len} if slots is None else {"slots": slots, "positions": positions}
+        if cache_bits == 16 and slots is None and "norm_q" not in W:
+            write = (kv_append, append(kv, t["q"], t["k"], t["v"], q_out=t["q_rot"], cos=cos, sin=sin, **where))
+        else:
+            write = (qkv_append, head_append(kv, t["q"], t["k"], t["v"], q_out=t["q_rot"], cos=cos, sin=sin,
+                                             w_q=W.get("norm_q"), w_k=W.get("norm_k"), **where))
         kind = LINEAR_W4A16 if S else LINEAR_F16
         experts = moe(kind, t["x_mid"], t["y"], W["router"], W["gate"], W["up"], W["down"], top_k,
                       gate_scale=S.get("gate"), up_scale=S.get("up"), down_scale=S.get("down"), ids=t["ids"],
                       weights=t["weights"], group_size=group, renormalize=True)
         ops.append((norm(h, t["h"], t["x"], W["norm_attn"], y=y), qkv,
-                    append(kv, t["q"], t["k"], t["v"], q_out=t["q_rot"], q_len=q_len, cos=cos, sin=sin), att, out,
+                    write, att, out,
                     norm(t["h"], t["h_mid"], t["x_mid"], W["norm_mlp"], y=t["o"]), experts))
-        if not attn_workspace_bytes(att):
+        if not attn_bytes(att):
             raise ValueError("the attention refuses these heads, window or strides")
         if not moe_workspace_bytes(experts):
             raise ValueError("the expert layer refuses these sizes")
-        attn_ws = max(attn_ws, attn_workspace_bytes(att))
+        attn_ws = max(attn_ws, attn_bytes(att))
         moe_ws = max(moe_ws, moe_workspace_bytes(experts))
         lin_ws = max(lin_ws, qkv.workspace_bytes(), out.workspace_bytes())
         h, y = t["h_mid"], t["y"]
@@ -402,14 +451,25 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
     ws_a, ws_m, ws_l = (new(max(n, 16), dtype=torch.uint8) for n in (attn_ws, moe_ws, lin_ws))
 
     def run(stream=None):
-        for pre, qkv, app, att, out, mid, experts in ops:
+        if plan is not None:
+            assign_pages(plan, plan_ws, stream=stream)
+        for pre, qkv, (put, app), att, out, mid, experts in ops:
             norm_residual(pre, stream=stream)
             decode_step_weights(qkv, ws_l, stream=stream)
-            kv_append(app, stream=stream)
-            attn_decode(att, ws_a, stream=stream)
+            put(app, stream=stream)
+            attend(att, ws_a, stream=stream)
             decode_step_weights(out, ws_l, stream=stream)
             norm_residual(mid, stream=stream)
             moe_forward(experts, ws_m, stream=stream)
         norm_residual(last, stream=stream)
+
+    def end(ended, stream=None):
+        op = page_plan(lens, table, pool, state, page_size, new_lens=ended)
+        assign_pages(op, end_ws, stream=stream)
+    end_ws = None
+    if pool is not None:   # (as large as a step's of this batch without a map)
+        some = page_plan(lens, table, pool, state, page_size, new_lens=torch.zeros_like(lens))
+        end_ws = new(max(pages_workspace_bytes(some), 16), dtype=torch.uint8)
     return SparseStep(run, first, h_out, x_out, lens, table, caches, views,
-                      [(weights, scales, final, cos, sin), ws_a, ws_m, ws_l, share])
+                      [(weights, scales, final, cos, sin), ws_a, ws_m, ws_l, share, plan_ws, end_ws],
+                      end if pool is not None else None, pool, state, slots, positions)

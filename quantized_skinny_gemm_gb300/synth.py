@@ -30,7 +30,7 @@ Workloads (the shapes of the decoders the pages run single-request decode on):
   [4096], x_down [14336] and the lm_head input [4096], fp16 ~N(0, 1).
 * ``sparse_decoder`` -- layers of a sparse decoder of any size: norms, q, k, v,
   o, router and experts (fp16 or int4), every matrix ~N(0, 1 / K) (the residual
-  stream keeps its scale through the layers).
+  stream keeps its scale through the layers), and norms of the q and k heads if asked.
 """
 from dataclasses import dataclass, field
 from typing import Dict, List, Optional
@@ -219,11 +219,15 @@ class SparseLayer:
     up: torch.Tensor
     down: torch.Tensor                      # [experts][hidden][inter]
     scales: Dict[str, torch.Tensor] = field(default_factory=dict)   # int4: gate, up, down
+    norm_q: Optional[torch.Tensor] = None   # [head_dim], or no norms of the heads
+    norm_k: Optional[torch.Tensor] = None
 
 
 def sparse_decoder_workload(seed=0, layers=2, hidden=1536, heads=12, kv_heads=2, head_dim=128, inter=512,
-                            experts=16, int4=False, group=32):
-    g = generator(seed)
+                            experts=16, int4=False, group=32, head_norms=False):
+    """head_norms: each layer norms its q and k heads (their weights have a generator of
+    their own, so the other draws stay the same)."""
+    g, g_norms = generator(seed), generator(seed + 15485863)
     fan = lambda *shape: normal(shape, shape[-1] ** -0.5, g)
     out = []
     for _ in range(layers):
@@ -238,6 +242,8 @@ def sparse_decoder_workload(seed=0, layers=2, hidden=1536, heads=12, kv_heads=2,
             else:
                 w = fan(experts, rows, cols)
             setattr(L, name, w)
+        if head_norms:
+            L.norm_q, L.norm_k = 1 + normal((head_dim,), 0.1, g_norms), 1 + normal((head_dim,), 0.1, g_norms)
         out.append(L)
     return out
 
