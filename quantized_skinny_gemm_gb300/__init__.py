@@ -697,9 +697,10 @@ def kv4_rows(kv, k=None, v=None, q_len=None, slots=None):
         q_len = 1 if q_len is None else q_len
     tokens = slots.numel() if slots is not None else kv.batch * q_len
     _fits(tokens > 0, where)
-    row = kv.kv_heads * kv.head_dim
-    rows = lambda t: 0 if t is None else max(row, _head_rows(t, tokens, kv.kv_heads, kv.head_dim, dt, where))
-    return KV4Rows(kv, 0 if slots is not None else q_len, tokens, _ptr(k), _ptr(v), rows(k), rows(v), _ptr(slots))
+    ks, vs = (0 if t is None else _head_rows(t, tokens, kv.kv_heads, kv.head_dim, dt, where) for t in (k, v))
+    for t, stride in ((k, ks), (v, vs)):
+        _fits(t is None or stride >= kv.kv_heads * kv.head_dim, where)   # rows that overlap
+    return KV4Rows(kv, 0 if slots is not None else q_len, tokens, _ptr(k), _ptr(v), ks, vs, _ptr(slots))
 
 
 def kv4_read(op, stream=None):

@@ -244,6 +244,8 @@ def test_builders_refuse_tensors_that_do_not_fit():
     refused(lambda: dg.head_append(kv, q, k, k, cos=t(9, 32)))
     refused(lambda: dg.kv4_rows(kv, None, None))
     refused(lambda: dg.kv4_rows(kv, five))
+    refused(lambda: dg.kv4_rows(kv, k[:1].expand(2, 2, 64)))          # rows over each other
+    assert dg.kv4_rows(kv, k).k_stride == 128
     refused(lambda: dg.attention4(kv, q, t(2, 4, 32, dtype=f16)))
     refused(lambda: dg.attention4(kv, q.bfloat16(), q.bfloat16()))
     pool, state = t(20, dtype=i32), t(2, dtype=i32)
