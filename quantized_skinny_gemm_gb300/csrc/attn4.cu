@@ -37,14 +37,17 @@ struct Attn4Shape {
     static constexpr int kRows = RT * 8;
     static constexpr int kOut = kRows * DP * 4;                      // a warp's output, in place of stages
     static constexpr int kNeed = (kOut + kStage - 1) / kStage + 1;
-    static constexpr int kStages = kNeed < 2 ? 2 : kNeed;
+    static constexpr int kLeast = DP <= 128 ? 3 : 2;
+    static constexpr int kStages = kNeed < kLeast ? kLeast : kNeed;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kKeyWords = 4 * kWide + 2 * kHalf;          // words (8 dims) of a lane, of a key
     static constexpr int kValWords = 2 * kWide + kHalf;              // of a value
     static constexpr int kQ = RT * kKeyWords * 512;
     static constexpr size_t kSmem = (size_t)kAttnWarps * kRing + kQ + (2 * kAttnWarps + 1) * kRows * 4;
-    // by the output's registers, and by the shared memory of an SM
-    static constexpr int kFit = 228 * 1024 / (kSmem + 2048), kWish = RT * DP <= 128 ? 4 : RT * DP <= 256 ? 3 : 2;
+    // Two CTAs an SM, whose 255 registers leave the compiler room to interleave the unpacking with
+    // the products.  (One row tile of 128 dims, bf16: three CTAs of 168 registers 66 us for 200001 positions
+    // and 32 for 50000, four of 128 registers 70 and 33, these 68 and 26.)
+    static constexpr int kFit = 228 * 1024 / (kSmem + 2048), kWish = 2;
     static constexpr int kCtas = kFit < kWish ? kFit : kWish;
     static constexpr int kPart = part_floats(kRows, DP);
     // Byte of 16-byte piece c of row r; eight rows on it is 8 kPitch more.  Pieces change places inside 128 bytes, so that what a
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
                 const int pr = sp.first + (row0 + r * 8 + 2 * t4 + h) / G;
                 return kp <= pr && (!op.window || pr - kp < op.window || kp < op.sinks);
             };
-#pragma unroll 1
+#pragma unroll(RT == 1 ? 2 : 1)
             for (int sub = 0; sub < 2; ++sub) {
                 // ---- scores of 16 keys: rows g and g + 8 of operand A ---------------------------
                 float s[RT][4];

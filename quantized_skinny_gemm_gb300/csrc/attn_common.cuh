@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
                 v[x].y = v[x].y * f + w[x].y * k;
             }
         };
-#pragma unroll 4
+#pragma unroll 8
         for (int i = few ? 0 : warp; i < n; i += few ? 1 : kJoinWarps) {
             const float* q = parts + (size_t)i * 2 * kPart + (i == 0 ? skip : 0);
             const float2* o = reinterpret_cast<const float2*>(q + 2 * ROWS + r * DP) + lane;
