@@ -1,8 +1,10 @@
 // Log probabilities of given tokens, entropy, rank and the best alternatives of rows of
 // logits, in one pass over them.
 //
-// A row (or a part of it, where the rows are few) is a CTA's, taken in tiles of 1024
-// 16-byte vectors, four a thread, the next tile loading while one is used.  Each thread
+// A row (or a part of it, where the rows are few) is a CTA's, taken in tiles of 512
+// 16-byte vectors, four a thread, the next tile loading while one is used.  Small CTAs, eight an SM
+// (fp32: five): while one looks for its row's best the others stream (2047 x 128255 bf16 with
+// everything and one alternative: 101 us, with four CTAs of 256 threads 110).  Each thread
 // keeps a base m and, with c = scale log2(e) and B = m c rounded, the sums l of w = 2^(x c - B)
 // and a of w (x c - B): an exponent is one fused multiply-add, rounded once, B
 // being a number like any other (a softmax of scale c / log2(e), 2^-24 off).  The base
@@ -15,28 +17,33 @@
 // the last are a thread's each.
 //
 // The rank is counted where a thread's four vectors hold something that is not below the token's
-// logit, 16-bit logits two at a time.  The best top_k cost the stream next to nothing: a thread only keeps its
-// maximum, and that of each eighth of its tiles.  The top_k-th largest of 64 groups' maxima is
-// then a floor that about top_k logits of the row reach; the threads read the eighths that
+// logit, 16-bit logits two at a time, by one comparison: what equals the token and comes before it
+// is what is above the next number below.  The best top_k cost the stream next to nothing: a thread only keeps its
+// maximum, and that of each sixteenth of its tiles.  The top_k-th largest of 64 groups' maxima is
+// then a floor that about top_k logits of the row reach; the threads read the sixteenths that
 // reach it once more (from L2, mostly) and list what does.  Keys are (logit, lowest index)
 // in one 64-bit number, no two alike: what is chosen depends on no order.  (Lists that each warp kept while it
 // streamed, cut to top_k again and again: 173 us for one alternative and 376 for 20, 2048 x
 // 128256 bf16, where the sums alone take 94.)
+#include <algorithm>
 #include <cfloat>
 #include <climits>
+#include <cmath>
 
 #include "elem.cuh"
 
 namespace dg {
 
-constexpr int kLpThreads = 256, kLpVecs = 4, kLpTile = kLpThreads * kLpVecs;   // vectors of a tile
+constexpr int kLpThreads = 128, kLpVecs = 4, kLpTile = kLpThreads * kLpVecs;   // vectors of a tile
 constexpr int kLpWarps = kLpThreads / 32, kLpMaxParts = 64;
-constexpr int kLpGroups = 64;                 // of four threads: more than top_k
-constexpr int kLpSlices = 8;                  // of a part's tiles, with a maximum of a thread each
+constexpr int kLpGroups = 64, kLpTeam = kLpThreads / kLpGroups;   // groups of threads: more than top_k
+constexpr int kLpSlices = 16;                 // of a part's tiles, with a maximum of a thread each
 constexpr int kLpList = 1024;                 // candidates; where more reach the floor it is raised
 constexpr float kNan = __builtin_nanf("");
 constexpr float kLpLog2e = 1.4426950408889634f, kLpLn2 = 0.6931471805599453f;
 using Key = unsigned long long;
+template <int TYPE>
+constexpr int kLpCtas = TYPE == 2 ? 5 : 8;   // of an SM
 
 struct LpPart {
     float m, l, a;
@@ -44,11 +51,13 @@ struct LpPart {
 };
 struct LpParams {
     dg_logprobs op;
-    int parts;
+    int whole, parts;   // rows that are a CTA's each; parts of the others
     float c, grow;      // scale * log2(e); how far the maximum may pass the base
     float most;         // bases up to this size have |m c| <= 2^22
-    LpPart* part;       // [rows][parts]
-    Key* keys;          // [rows][parts][top_k]
+    uint32_t low;       // bf16: a pair of -2^k, 2^24 <= 2^k c < 2^25: no weight beside any base, and finite
+    int always_far;     // there is no such k (a temperature of 2^102)
+    LpPart* part;       // [rows - whole][parts]
+    Key* keys;          // [rows - whole][parts][top_k]
     FastDiv by_parts;
 };
 
@@ -169,35 +178,44 @@ __device__ __forceinline__ float vec_max(uint4 v) {
     return fmaxf(f.x, f.y);
 }
 
-// How many of a vector's logits are above (or, or_equal) one of their kind: 16-bit ones are counted
-// as pairs of ones.
-template <int TYPE, bool OR_EQUAL>
-__device__ __forceinline__ void count_above(uint4 v, float than, uint32_t than2, uint32_t& pairs, int& n) {
+// How many of a vector's logits are above one of their kind (16-bit ones twice in a word), which
+// 16-bit ones count as pairs of ones.
+template <int TYPE>
+__device__ __forceinline__ void count_above(uint4 v, uint32_t than, uint32_t& pairs, int& n) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     if (TYPE == 2) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) n += OR_EQUAL ? __uint_as_float(w[e]) >= than : __uint_as_float(w[e]) > than;
+        for (int e = 0; e < 4; ++e) n += __uint_as_float(w[e]) > __uint_as_float(than);
         return;
     }
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (TYPE == 1) {
             __nv_bfloat162 a, b, c;
             memcpy(&a, &w[e], 4);
-            memcpy(&b, &than2, 4);
+            memcpy(&b, &than, 4);
             memcpy(&c, &pairs, 4);
-            c = __hadd2(c, OR_EQUAL ? __hge2(a, b) : __hgt2(a, b));
+            c = __hadd2(c, __hgt2(a, b));
             memcpy(&pairs, &c, 4);
         } else {
-            const __half2 a = u32_as_h2(w[e]), b = u32_as_h2(than2);
-            pairs = h2_as_u32(__hadd2(u32_as_h2(pairs), OR_EQUAL ? __hge2(a, b) : __hgt2(a, b)));
+            pairs = h2_as_u32(__hadd2(u32_as_h2(pairs), __hgt2(u32_as_h2(w[e]), u32_as_h2(than))));
         }
     }
 }
+// The next number below a finite one, as bits of its type.
+__device__ __forceinline__ uint32_t bits_below(uint32_t u, uint32_t sign) {
+    return u == 0 || u == sign ? sign + 1 : u & sign ? u + 1 : u - 1;
+}
+// 16-bit pairs, -infinity (and what has no weight in any sum) raised to `low`; NaN stays.
+__device__ __forceinline__ uint32_t raise_bf16x2(uint32_t v, uint32_t low) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(low));
+    return r;
+}
+
 
 template <int TYPE>
-__global__ void __launch_bounds__(kLpThreads, TYPE == 2 ? 3 : 4) k_logprobs(const LpParams p) {
+__global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const LpParams p) {
     constexpr int kEl = TYPE == 2 ? 4 : 8, kSize = TYPE == 2 ? 4 : 2;   // of a vector; bytes of a logit
     constexpr uint32_t kNone = TYPE == 2 ? 0xFF800000u : TYPE == 1 ? 0xFF80FF80u : 0xFC00FC00u;   // -infinity
     __shared__ Key list[kLpList];
@@ -210,7 +228,8 @@ __global__ void __launch_bounds__(kLpThreads, TYPE == 2 ? 3 : 4) k_logprobs(cons
     __shared__ int s_n, s_before;
     const dg_logprobs& op = p.op;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = (int)blockIdx.x / p.by_parts, part = blockIdx.x - row * p.parts;
+    const int cut = (int)blockIdx.x - p.whole, parts = cut < 0 ? 1 : p.parts;   // whole rows first, then the cut ones
+    const int row = cut < 0 ? blockIdx.x : p.whole + cut / p.by_parts, part = cut < 0 ? 0 : cut - (row - p.whole) * parts;
     const int V = op.V, K = op.top_k;
     griddep_launch_dependents();
     griddep_wait();
@@ -220,14 +239,21 @@ __global__ void __launch_bounds__(kLpThreads, TYPE == 2 ? 3 : 4) k_logprobs(cons
     const uint4* vecs = reinterpret_cast<const uint4*>(x - skew * kSize);
     const int first = skew ? 1 : 0, last = (int)(((long long)V + skew) / kEl);
     const int tiles = (last - first + kLpTile - 1) / kLpTile;   // 0 where last < first
-    const int tile0 = (int)((long long)part * tiles / p.parts), tile1 = (int)((long long)(part + 1) * tiles / p.parts);
+    const int tile0 = (int)((long long)part * tiles / parts), tile1 = (int)((long long)(part + 1) * tiles / parts);
+    const int full = min(tile1, (last - first) / kLpTile);   // tiles before this one need no bounds
     uint4 next[kLpVecs];
     auto fetch = [&](int tile) {
+        const uint4* from = vecs + (first + tile * kLpTile + tid);
+        auto load = [](const uint4* v) { return TYPE == 2 ? *v : __ldcs(v); };
+        if (tile < full) {
 #pragma unroll
-        for (int q = 0; q < kLpVecs; ++q) {
-            const int v = first + tile * kLpTile + q * kLpThreads + tid;
-            next[q] = make_uint4(kNone, kNone, kNone, kNone);
-            if (tile < tile1 && v < last) next[q] = TYPE == 2 ? vecs[v] : __ldcs(vecs + v);   // (measured: fp32 15 us against 16, 16 bits 125 against 130)
+            for (int q = 0; q < kLpVecs; ++q) next[q] = load(from + q * kLpThreads);
+        } else if (tile < tile1) {
+#pragma unroll
+            for (int q = 0; q < kLpVecs; ++q) {
+                next[q] = make_uint4(kNone, kNone, kNone, kNone);
+                if (first + tile * kLpTile + q * kLpThreads + tid < last) next[q] = load(from + q * kLpThreads);
+            }
         }
     };
     fetch(tile0);
@@ -242,12 +268,17 @@ __global__ void __launch_bounds__(kLpThreads, TYPE == 2 ? 3 : 4) k_logprobs(cons
         if (tok < 0 || tok >= V) tok = -1;
         else mine = logit_at<TYPE>(x, tok);
     }
-    const uint32_t mine2 = TYPE == 2 ? 0u : pair_16<TYPE == 1>(mine, mine);   // (it has 16 bits)
     const bool nan_token = tok >= 0 && mine != mine;
     auto before = [&](float v, int i) {   // whether logit v of word i comes before the token
         if (nan_token) return v == v || i < tok;
         return v > mine || (v == mine && i < tok);
     };
+    // Vectors before the token's own count what is above `under`, the next number below its logit,
+    // others what is above the logit itself.  Tokens of NaN or -infinity have their own pass.
+    const bool ranked = tok >= 0 && mine > -INFINITY, pass = tok >= 0 && !ranked;
+    const uint32_t bits = TYPE == 2 ? __float_as_uint(mine) : pair_16<TYPE == 1>(mine, mine);   // (it has 16 bits)
+    const uint32_t below = TYPE == 2 ? bits_below(bits, 0x80000000u) : bits_below(bits & 0xFFFFu, 0x8000u) * 0x10001u;
+    const int tok_vec = (tok + skew) / kEl;
     Sums s = {-INFINITY, 0.f, 0.f};
     int ahead = 0;
     // ---- the logits outside the vectors, by the first part ---------------------------------------
@@ -262,6 +293,10 @@ __global__ void __launch_bounds__(kLpThreads, TYPE == 2 ? 3 : 4) k_logprobs(cons
         list[tid] = key_of(v, end_i);   // always a candidate
     }
     const int ends = part == 0 ? head + (V - tail) : 0;
+    if (ranked && tid < kEl && tok_vec >= first + tile0 * kLpTile && tok_vec < min(last, first + tile1 * kLpTile)) {
+        const int i = tok_vec * kEl - skew + tid;   // in the token's own vector, before it
+        if (i < tok) ahead += logit_at<TYPE>(x, i) == mine;
+    }
     float2 l = make_float2(s.l, 0.f), a = make_float2(0.f, 0.f);
     float m = s.m, base = fabsf(m) <= p.most ? mul_rn(m, p.c) : 0.f;
     if (m > -INFINITY && fabsf(m) > p.most) {   // (the sums are taken again if this is the part's maximum)
@@ -318,38 +353,30 @@ __global__ void __launch_bounds__(kLpThreads, TYPE == 2 ? 3 : 4) k_logprobs(cons
 #pragma unroll
             for (int e = 0; e < kEl / 2; ++e) {
                 const float2 f = TYPE == 2 ? make_float2(__uint_as_float(w[2 * e & 3]), __uint_as_float(w[(2 * e + 1) & 3]))
-                                           : pair_f32<TYPE == 1>(w[e]);
+                                           : pair_f32<TYPE == 1>(TYPE == 1 ? raise_bf16x2(w[e], p.low) : w[e]);
                 const float2 d = fma2(f, c2, off);
                 const float2 t = make_float2(ex2(d.x), ex2(d.y));
                 l = fma2(t, one, l);
-                a = fma2(t, make_float2(fmaxf(d.x, -FLT_MAX), fmaxf(d.y, -FLT_MAX)), a);   // -infinity has no part
+                // -infinity has no part: 0 times a number
+                a = fma2(t, TYPE == 1 ? d : make_float2(fmaxf(d.x, -FLT_MAX), fmaxf(d.y, -FLT_MAX)), a);
             }
         }
-        if (tok >= 0 && (top >= mine || nan_token)) {
-            const int from = (first + tile * kLpTile) * kEl - skew;   // of the tile
-            if (nan_token || (from <= tok && tok < from + kLpTile * kEl)) {
-#pragma unroll 1
-                for (int q = 0; q < kLpVecs; ++q) {
-                    const uint4 v = q == 0 ? now[0] : q == 1 ? now[1] : q == 2 ? now[2] : now[3];
-                    const int i = index(tile, q);
-                    if (i >= inside) break;
+        if (ranked && top >= mine) {
+            uint32_t pairs = 0;   // at most 16 each
 #pragma unroll
-                    for (int e = 0; e < kEl; ++e) ahead += before(logit(v, e), i + e);
-                }
-            } else {
-                uint32_t pairs = 0;   // at most 16 each
-#pragma unroll
-                for (int q = 0; q < kLpVecs; ++q) {
-                    if (from < tok) count_above<TYPE, true>(now[q], mine, mine2, pairs, ahead);
-                    else count_above<TYPE, false>(now[q], mine, mine2, pairs, ahead);
-                }
-                if (TYPE != 2) {
-                    const float2 f = pair_f32<TYPE == 1>(pairs);
-                    ahead += (int)(f.x + f.y);
-                }
+            for (int q = 0; q < kLpVecs; ++q)
+                count_above<TYPE>(now[q], first + tile * kLpTile + q * kLpThreads + tid < tok_vec ? below : bits, pairs,
+                                  ahead);
+            if (TYPE != 2) {
+                const float2 f = pair_f32<TYPE == 1>(pairs);
+                ahead += (int)(f.x + f.y);
             }
         }
     }
+    const long long i0 = (long long)(first + tile0 * kLpTile) * kEl - skew;   // the part's vectors
+    const long long i1 = (long long)min(last, first + tile1 * kLpTile) * kEl - skew;
+    if (pass)
+        for (long long i = i0 + tid; i < i1; i += kLpThreads) ahead += before(logit_at<TYPE>(x, i), (int)i);
     // ---- the part's sums ------------------------------------------------------------------
     auto whole = [&] {   // the CTA's, in every thread
         s.join_warp(p);
@@ -370,18 +397,17 @@ __global__ void __launch_bounds__(kLpThreads, TYPE == 2 ? 3 : 4) k_logprobs(cons
     const unsigned some = __any_sync(0xffffffffu, m > -INFINITY);
     if (lane == 0) odd[warp] = past | some << 1;
     if (K) {
-        float four = fmaxf(greatest, __shfl_xor_sync(0xffffffffu, greatest, 1));
-        four = fmaxf(four, __shfl_xor_sync(0xffffffffu, four, 2));
-        if ((tid & 3) == 0) group_max[tid >> 2] = four;
+        float group = greatest;
+#pragma unroll
+        for (int o = 1; o < kLpTeam; o <<= 1) group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, o));
+        if (tid % kLpTeam == 0) group_max[tid / kLpTeam] = group;
     }
     whole();
     unsigned any = 0;
 #pragma unroll
     for (int w = 0; w < kLpWarps; ++w) any |= odd[w];
-    const bool far = (any & 1u) || (s.l == 0.f && (any & 2u));
+    const bool far = p.always_far || (any & 1u) || (s.l == 0.f && (any & 2u));
     if (far) {   // logits past what a base reaches: exponents as differences
-        const long long i0 = (long long)(first + tile0 * kLpTile) * kEl - skew;
-        const long long i1 = (long long)min(last, first + tile1 * kLpTile) * kEl - skew;
         auto all = [&](auto&& use) {
             if (end) use(logit_at<TYPE>(x, end_i));
             for (long long i = i0 + tid; i < i1; i += kLpThreads) use(logit_at<TYPE>(x, i));
@@ -399,8 +425,8 @@ __global__ void __launch_bounds__(kLpThreads, TYPE == 2 ? 3 : 4) k_logprobs(cons
     }
     const Row r(s, p);
     if (tid == 0) {
-        if (p.parts == 1) write_row<TYPE>(p, r, row, s_before, x);
-        else p.part[blockIdx.x] = {s.m, s.l, s.a, s_before};
+        if (cut < 0) write_row<TYPE>(p, r, row, s_before, x);
+        else p.part[cut] = {s.m, s.l, s.a, s_before};
     }
     if (K == 0) return;
     // ---- the best -------------------------------------------------------------------------------
@@ -464,9 +490,9 @@ __global__ void __launch_bounds__(kLpThreads, TYPE == 2 ? 3 : 4) k_logprobs(cons
                     for (int e = 0; e < kEl; ++e) largest = max(largest, key_of(logit(v, e), i + e));
                 }
             }
-            largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
-            largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
-            if ((tid & 3) == 0) group_key[tid >> 2] = largest;
+#pragma unroll
+            for (int o = 1; o < kLpTeam; o <<= 1) largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+            if (tid % kLpTeam == 0) group_key[tid / kLpTeam] = largest;
             __syncthreads();
             if (tid < kLpGroups) {
                 const Key k = group_key[tid];
@@ -484,7 +510,7 @@ __global__ void __launch_bounds__(kLpThreads, TYPE == 2 ? 3 : 4) k_logprobs(cons
         }
         __syncthreads();
     }
-    Key* keys = p.parts == 1 ? nullptr : p.keys + (size_t)blockIdx.x * K;
+    Key* keys = cut < 0 ? nullptr : p.keys + (size_t)cut * K;
     for (int i = tid; i < n; i += kLpThreads) {
         const Key k = list[i];
         int place = 0;
@@ -511,15 +537,15 @@ __global__ void __launch_bounds__(kLpJoinThreads) k_logprobs_join(const LpParams
     griddep_launch_dependents();
     griddep_wait();
     const dg_logprobs& op = p.op;
-    const int row = blockIdx.x, lane = threadIdx.x, K = op.top_k, n = p.parts;
+    const int cut = blockIdx.x, row = p.whole + cut, lane = threadIdx.x, K = op.top_k, n = p.parts;
     const unsigned char* x = static_cast<const unsigned char*>(op.logits) + (long long)row * op.stride * (TYPE == 2 ? 4 : 2);
-    for (int i = threadIdx.x; i < n * K; i += kLpJoinThreads) keys[i] = p.keys[(size_t)row * n * K + i];
+    for (int i = threadIdx.x; i < n * K; i += kLpJoinThreads) keys[i] = p.keys[(size_t)cut * n * K + i];
     __syncthreads();
     if (threadIdx.x >= 32) return;
     Sums s = {-INFINITY, 0.f, 0.f};
     int before = 0;
     for (int i = lane; i < n; i += 32) {   // (two parts a lane at most)
-        const LpPart q = p.part[(size_t)row * n + i];
+        const LpPart q = p.part[(size_t)cut * n + i];
         s.join({q.m, q.l, q.a}, p);
         before += q.before;
     }
@@ -553,35 +579,47 @@ __global__ void __launch_bounds__(kLpJoinThreads) k_logprobs_join(const LpParams
     }
 }
 
-static int lp_parts(const dg_logprobs& op) {
-    // as many CTAs as the SMs hold, where the rows alone are fewer
-    const int el = op.logits_f32 ? 4 : 8;
-    const long long tiles = ((long long)op.V + el - 1) / el / kLpTile + 1, want = (4ll * 152 + op.rows - 1) / op.rows;
-    long long n = want < tiles ? want : tiles;
-    return (int)(n > kLpMaxParts ? kLpMaxParts : n);
+// Rows come in rounds of as many CTAs as the SMs hold.  Those of a last round that would leave half of
+// the places empty, or of a call of so few, are cut into parts.
+struct LpSplit {
+    int whole, parts;
+};
+static LpSplit lp_split(const dg_logprobs& op) {
+    const int el = op.logits_f32 ? 4 : 8, places = 152 * (op.logits_f32 ? kLpCtas<2> : kLpCtas<0>);
+    const int rest = op.rows % places;
+    if (rest == 0 || rest * 2 > places) return {op.rows, 1};
+    const long long tiles = ((long long)op.V + el - 1) / el / kLpTile + 1, want = places / rest;
+    const int parts = (int)std::min({want, tiles, (long long)kLpMaxParts});
+    return parts == 1 ? LpSplit{op.rows, 1} : LpSplit{op.rows - rest, parts};
 }
 
 size_t lp_ws_bytes(const dg_logprobs& op) {
-    const int parts = lp_parts(op);
-    return parts == 1 ? 0 : (size_t)op.rows * parts * (sizeof(LpPart) + sizeof(Key) * op.top_k);
+    const LpSplit c = lp_split(op);
+    return (size_t)(op.rows - c.whole) * c.parts * (sizeof(LpPart) + sizeof(Key) * op.top_k);
 }
 
 template <int TYPE>
 static cudaError_t launch_lp(const dg_logprobs& op, void* ws, cudaStream_t s) {
     LpParams p;
     p.op = op;
-    p.parts = lp_parts(op);
+    const LpSplit split = lp_split(op);
+    p.whole = split.whole;
+    p.parts = split.parts;
+    const int cut = op.rows - p.whole;
     p.c = op.scale * kLpLog2e;
     p.grow = fminf(8.f / p.c, FLT_MAX);   // finite: the first maximum is always taken
     p.most = fminf(4194304.f / p.c, FLT_MAX);
+    const int k = 24 - std::ilogb(p.c);
+    p.always_far = TYPE == 1 && k > 126;
+    p.low = (0x8000u | (uint32_t)(127 + std::min(k, 126)) << 7) * 0x10001u;
     p.part = static_cast<LpPart*>(ws);
-    p.keys = reinterpret_cast<Key*>(static_cast<char*>(ws) + (size_t)op.rows * p.parts * sizeof(LpPart));
+    p.keys = reinterpret_cast<Key*>(static_cast<char*>(ws) + (size_t)cut * p.parts * sizeof(LpPart));
     p.by_parts = fast_div((uint32_t)p.parts);
     void* args[] = {&p};
-    const cudaError_t e = launch_pdl((const void*)k_logprobs<TYPE>, dim3((unsigned)op.rows * p.parts),
+    const cudaError_t e = launch_pdl((const void*)k_logprobs<TYPE>, dim3((unsigned)(p.whole + cut * p.parts)),
                                      dim3(kLpThreads), 0, s, args);
-    if (e != cudaSuccess || p.parts == 1) return e;
-    return launch_pdl((const void*)k_logprobs_join<TYPE>, dim3(op.rows), dim3(kLpJoinThreads), 0, s, args);
+    if (e != cudaSuccess || cut == 0) return e;
+    return launch_pdl((const void*)k_logprobs_join<TYPE>, dim3(cut), dim3(kLpJoinThreads), 0, s, args);
 }
 
 cudaError_t launch_logprobs(const dg_logprobs& op, void* ws, cudaStream_t s) {

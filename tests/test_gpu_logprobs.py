@@ -202,3 +202,46 @@ def test_far_rows_streams_graphs_and_repeats():
         got = run(x, [5, 199999], 0, stream=side)
         assert np.array_equal(lp.cpu().numpy(), got["logprob"]) and np.array_equal(rank.cpu().numpy(), got["rank"])
         check(x, [5, 199999], 0, got=got)
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("R,V", [(70, 20011), (640, 8300)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_ranks_between_neighbouring_numbers(ftype, R, V, wide):
+    """Zeros of both signs, the smallest and largest numbers and their neighbours, with tokens around the
+    ends of vectors and tiles: a rank counts equal ones before the token, and no other number."""
+    need_gpu()
+    it = {"f16": torch.int16, "bf16": torch.int16, "f32": torch.int32}[ftype]
+    one = int(torch.tensor(1.0, dtype=DT[ftype]).view(it))
+    few = [0, 1, 2, one - 1, one, one + 1]
+    if wide:
+        top = int(torch.tensor(torch.finfo(DT[ftype]).max, dtype=DT[ftype]).view(it))
+        few += [top - 1, top, top + 1]         # the last: infinity, below only with a sign
+    sign = 1 << (15 if it == torch.int16 else 31)
+    all_ = [v - 2 * sign for v in (sign + f for f in few)] + [f for f in few if not wide or f != top + 1]
+    g = torch.Generator().manual_seed(12)
+    bits = torch.tensor(all_, dtype=torch.int64)[torch.randint(0, len(all_), (4, V), generator=g)].to(it)
+    x = bits.view(DT[ftype]).repeat(R // 4, 1).contiguous()
+    R = x.shape[0]
+    tokens = np.concatenate([np.arange(24), 4090 + np.arange(12), 8184 + np.arange(16), V - 1 - np.arange(8)])
+    tokens = np.resize(np.repeat(tokens, 4), R)
+    got = run(x.to(DEV), tokens, 0)
+    for r in range(R):
+        row = ref.f64(x[r])
+        t = tokens[r]
+        assert got["rank"][r] == (row > row[t]).sum() + (row[:t] == row[t]).sum(), (r, t, row[t])
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("scale", [1e-38, 1e-31, 2.5e-31, 1e-20])
+@pytest.mark.parametrize("V", [7, 30001])
+def test_high_temperatures(ftype, scale, V):
+    """Every finite logit weighs the same; masked ones nothing."""
+    need_gpu()
+    x = logits(5, V, ftype, 9)
+    x[1, ::3] = -float("inf")
+    x[2] = -float("inf")
+    x[3, ::2] = torch.finfo(DT[ftype]).min
+    x[4] = -float("inf")
+    x[4, 5] = 2.0
+    check(x.to(DEV), [0, 1, 2, 3, 5], 3, scale)
