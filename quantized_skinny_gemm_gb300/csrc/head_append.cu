@@ -7,7 +7,11 @@
 // token, all of q, of k or of v: their position and place, the norm's weights, the cosines and sines
 // and the addresses are worked out once for all of them, and all heads are loaded before the
 // first is used.  (A head a team and a launch-wide list of heads: 450 instructions a warp,
-// bound by issue, 80 us for 6700 tokens of 32 + 2 x 8 heads of 128.)  A 4-bit value
+// bound by issue, 80 us for 6700 tokens of 32 + 2 x 8 heads of 128.)  Where pairs are half a
+// rotation apart a lane has four dims of either half, so that it turns them by itself, and lanes
+// change to neighbouring dims just before a key becomes codes.  (Eight neighbouring dims, and
+// the other of each pair by an exchange: 57 us for 6825 tokens of 32 + 2 x 8 into 4 bits and 47 into 16;
+// these 46 and 35, with 72 and 64 registers instead of 80.)  A 4-bit value
 // is divided by its scale with one rounding, not just multiplied by a reciprocal: 16-bit inputs meet halves of
 // a scale often enough for ties to show (they go to the even code).
 #include "elem.cuh"
@@ -20,7 +24,6 @@ struct HeadParams {
     dg_head_append op;
     int batch, kvh, D, page_size, num_pages;   // of the cache meant
     int q_warps, k_warps, units;               // warps of a token for q, and for k (and v); of all tokens
-    float k_div, v_div;                        // 7 x factor
     FastDiv by_warps, by_q_len, by_page;
 };
 
@@ -67,9 +70,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 // VEC: 16-byte rows and a rotation of whole vectors; else values one by one and pairs
-// through shared memory.
-template <bool BF16, bool Q4, int TEAM, bool VEC, int kRounds>
-__global__ void __launch_bounds__(kHeadThreads, kRounds == 1 ? 8 : 6) k_head_append(const HeadParams p) {
+// through shared memory.  SPLIT (VEC, not interleaved): a lane's dims below rot_dim are four of
+// either half.
+template <bool BF16, bool Q4, int TEAM, bool VEC, int kRounds, bool SPLIT>
+__global__ void __launch_bounds__(kHeadThreads, kRounds == 1 || !Q4 ? 8 : 7) k_head_append(const HeadParams p) {
     constexpr int kTeams = 32 / TEAM;   // of a warp
     __shared__ float shared[VEC ? 1 : kHeadThreads / TEAM][VEC ? 1 : TEAM * 8];
     griddep_launch_dependents();
@@ -82,14 +86,22 @@ __global__ void __launch_bounds__(kHeadThreads, kRounds == 1 ? 8 : 6) k_head_app
     const int heads = kind == 0 ? op.heads : p.kvh;
     const int chunk = kind == 0 ? part : kind == 1 ? part - p.q_warps : part - p.q_warps - p.k_warps;
     const int team = lane / TEAM, i = lane % TEAM, h0 = chunk * kTeams * kRounds + team;
-    const int D = p.D, d0 = i * 8;
-    const bool mine = d0 < D;   // (head sizes are multiples of 8)
+    const int D = p.D, half = op.rot_dim / 2;
+    // dims d0 .. d0 + 3 and d1 .. d1 + 3
+    const bool pair = SPLIT && kind != 2 && i * 8 < op.rot_dim;
+    const int d0 = pair ? i * 4 : i * 8, d1 = pair ? half + i * 4 : d0 + 4;
+    const bool mine = i * 8 < D;   // (head sizes are multiples of 8)
     const uint16_t* src = kind == 0   ? static_cast<const uint16_t*>(op.q) + t * op.q_stride
                           : kind == 1 ? static_cast<const uint16_t*>(op.k) + t * op.k_stride
                                       : static_cast<const uint16_t*>(op.v) + t * op.v_stride;
-    src += (long long)h0 * D + d0;
+    src += (long long)h0 * D;
     const uint16_t* w = static_cast<const uint16_t*>(kind == 0 ? op.w_q : kind == 1 ? op.w_k : nullptr);
-    auto load8 = [&](const uint16_t* at) {
+    auto load8 = [&](const uint16_t* at) {   // of a head that starts at `at`
+        if (SPLIT) {
+            const uint2 a = *reinterpret_cast<const uint2*>(at + d0), b = *reinterpret_cast<const uint2*>(at + d1);
+            return make_uint4(a.x, a.y, b.x, b.y);
+        }
+        at += d0;
         if (VEC) return *reinterpret_cast<const uint4*>(at);
         uint32_t r[4];
 #pragma unroll
@@ -98,6 +110,12 @@ __global__ void __launch_bounds__(kHeadThreads, kRounds == 1 ? 8 : 6) k_head_app
     };
     auto store8 = [&](uint16_t* to, const float (&x)[8]) {
         const uint4 v = pack8<BF16>(x);
+        if (SPLIT) {
+            *reinterpret_cast<uint2*>(to + d0) = make_uint2(v.x, v.y);
+            *reinterpret_cast<uint2*>(to + d1) = make_uint2(v.z, v.w);
+            return;
+        }
+        to += d0;
         if (VEC) {
             *reinterpret_cast<uint4*>(to) = v;
         } else {
@@ -118,7 +136,7 @@ __global__ void __launch_bounds__(kHeadThreads, kRounds == 1 ? 8 : 6) k_head_app
     float g[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = 0.f;
-    if (w && mine) unpack8<BF16>(load8(w + d0), g);
+    if (w && mine) unpack8<BF16>(load8(w), g);
     // ---- the token's position and place ---------------------------------------------------
     int pos, b = 0;
     if (op.slots) {
@@ -140,13 +158,11 @@ __global__ void __launch_bounds__(kHeadThreads, kRounds == 1 ? 8 : 6) k_head_app
 #pragma unroll
         for (int u = 0; u < kRounds; ++u)
             if (mine && h0 + u * kTeams < heads)
-                store8(static_cast<uint16_t*>(op.q_out) + t * op.q_out_stride + (long long)(h0 + u * kTeams) * D + d0,
-                       zero);
+                store8(static_cast<uint16_t*>(op.q_out) + t * op.q_out_stride + (long long)(h0 + u * kTeams) * D, zero);
         return;
     }
     // ---- cosines and sines of this lane's dims: x c + (the other of the pair) s --------------------
-    const int half = op.rot_dim / 2;
-    const bool turn = kind != 2 && mine && d0 < op.rot_dim;
+    const bool turn = kind != 2 && mine && i * 8 < op.rot_dim;
     const int lanes = half / 8, other = op.interleaved ? i : i < lanes ? i + lanes : i - lanes;   // VEC
     float c[8], s[8];
 #pragma unroll
@@ -154,7 +170,10 @@ __global__ void __launch_bounds__(kHeadThreads, kRounds == 1 ? 8 : 6) k_head_app
     if (turn) {
         const float* cos = op.cos + (long long)pos * half;
         const float* sin = op.sin + (long long)pos * half;
-        if (VEC && !op.interleaved) {
+        if (SPLIT) {   // pairs (e, e + 4)
+            *reinterpret_cast<float4*>(c) = __ldg(reinterpret_cast<const float4*>(cos + d0));
+            *reinterpret_cast<float4*>(s) = __ldg(reinterpret_cast<const float4*>(sin + d0));
+        } else if (VEC && !op.interleaved) {
             const bool low = d0 < half;
             const int j = low ? d0 : d0 - half;
 #pragma unroll
@@ -186,7 +205,16 @@ __global__ void __launch_bounds__(kHeadThreads, kRounds == 1 ? 8 : 6) k_head_app
     // pair: k (u (g c) + u' (g' s)), the products in brackets once for all heads
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = w ? g[e] + op.w_offset : 1.f;
-    if (VEC) {
+    if (SPLIT) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float z = s[e], y = turn ? c[e] : 1.f;
+            s[e] = -z * g[e + 4];
+            s[e + 4] = z * g[e];
+            g[e] *= y;
+            g[e + 4] *= y;
+        }
+    } else if (VEC) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float z = op.interleaved ? g[e ^ 1] : __shfl_sync(0xffffffffu, g[e], other & (TEAM - 1), TEAM);
@@ -202,25 +230,26 @@ __global__ void __launch_bounds__(kHeadThreads, kRounds == 1 ? 8 : 6) k_head_app
     };
     const float inv_d = 1.f / (float)D;
     // where the first head goes, and the next one
-    uint16_t* out = nullptr;
-    uint8_t *codes = nullptr, *scales = nullptr;
-    long long next = 0, next_scale = 0;
+    const int d8 = !pair ? i * 8 : i & 1 ? half + (i - 1) * 4 : i * 4;   // the eight dims that this lane makes codes of
+    unsigned char* to;   // (of codes: this lane's)
+    uint8_t* scales = nullptr;
+    long long next, next_scale = 0;   // bytes
     if (kind == 0) {
-        out = static_cast<uint16_t*>(op.q_out) + t * op.q_out_stride + (long long)h0 * D + d0;
-        next = (long long)kTeams * D;
+        to = static_cast<unsigned char*>(op.q_out) + 2 * (t * op.q_out_stride + (long long)h0 * D);
+        next = 2ll * kTeams * D;
     } else if (!Q4) {
-        out = static_cast<uint16_t*>(kind == 1 ? op.kv.k : op.kv.v) + at.page * op.kv.page_stride +
-              at.at * op.kv.token_stride + h0 * op.kv.head_stride + d0;
-        next = kTeams * op.kv.head_stride;
+        to = static_cast<unsigned char*>(kind == 1 ? op.kv.k : op.kv.v) +
+             2 * (at.page * op.kv.page_stride + at.at * op.kv.token_stride + h0 * op.kv.head_stride);
+        next = 2 * kTeams * op.kv.head_stride;
     } else {
-        codes = (kind == 1 ? op.kv4.k : op.kv4.v) + at.page * op.kv4.page_stride + at.at * op.kv4.token_stride +
-                h0 * op.kv4.head_stride + d0 / 2;
+        to = (kind == 1 ? op.kv4.k : op.kv4.v) + at.page * op.kv4.page_stride + at.at * op.kv4.token_stride +
+             h0 * op.kv4.head_stride + d8 / 2;
         scales = (kind == 1 ? op.kv4.k_scale : op.kv4.v_scale) + at.page * op.kv4.scale_page_stride +
-                 at.at * op.kv4.scale_token_stride + h0 * op.kv4.scale_head_stride + i / 2;
+                 at.at * op.kv4.scale_token_stride + h0 * op.kv4.scale_head_stride + d8 / 16;
         next = kTeams * op.kv4.head_stride;
         next_scale = kTeams * op.kv4.scale_head_stride;
     }
-    const float factor = kind == 1 ? op.kv4.k_factor : op.kv4.v_factor, divisor = kind == 1 ? p.k_div : p.v_div;
+    const float factor = kind == 1 ? op.kv4.k_factor : op.kv4.v_factor;
 
 #pragma unroll
     for (int u = 0; u < kRounds; ++u) {
@@ -248,7 +277,19 @@ __global__ void __launch_bounds__(kHeadThreads, kRounds == 1 ? 8 : 6) k_head_app
             k = rsqrtf(team_sum(sq.x + sq.y) * inv_d + op.eps);
         }
         if (VEC) {
-            if (kind != 2) {
+            if (SPLIT && kind != 2) {
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 a = two(e), b = two(e + 4), kk = make_float2(k, k);
+                    float2 v = fma2(a, make_float2(g[e], g[e + 1]), zero), z = fma2(b, make_float2(g[e + 4], g[e + 5]), zero);
+                    if (turn) {
+                        v = fma2(b, make_float2(s[e], s[e + 1]), v);
+                        z = fma2(a, make_float2(s[e + 4], s[e + 5]), z);
+                    }
+                    put(e, fma2(v, kk, zero));
+                    put(e + 4, fma2(z, kk, zero));
+                }
+            } else if (kind != 2) {
                 float y[8];
                 if (half) {
 #pragma unroll
@@ -279,17 +320,25 @@ __global__ void __launch_bounds__(kHeadThreads, kRounds == 1 ? 8 : 6) k_head_app
             }
         }
         if (!Q4 || kind == 0) {
-            if (have) store8(out, x);
-            out += next;
+            if (have) store8(reinterpret_cast<uint16_t*>(to), x);
+            to += next;
             continue;
         }
         // ---- sixteen values and their scale, by two lanes ------------------------------------------
+        if (SPLIT && kind == 1) {   // a lane takes the low halves of two, its neighbour the high ones
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float z = __shfl_xor_sync(0xffffffffu, i & 1 ? x[e] : x[e + 4], 1);
+                if (pair && (i & 1)) x[e] = z;
+                if (pair && !(i & 1)) x[e + 4] = z;
+            }
+        }
         float top = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
-        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max_nan(top, SPLIT ? __shfl_sync(0xffffffffu, top, lane ^ (pair ? 2 : 1)) : __shfl_xor_sync(0xffffffffu, top, 1));
         const bool odd = !(top <= 3.402823466e38f);
-        const uint32_t byte = odd ? 0x7Fu : e4m3_of(__fdiv_rn(top, divisor));
+        const uint32_t byte = odd ? 0x7Fu : e4m3_of(__fdiv_rn(top, __fmul_rn(7.f, factor)));
         const float step = odd ? 0.f : e4m3_f32(byte) * factor;
         uint32_t word = 0;
         if (step > 1e-30f && step < 1e30f && top < 7.49f * step) {
@@ -318,25 +367,26 @@ __global__ void __launch_bounds__(kHeadThreads, kRounds == 1 ? 8 : 6) k_head_app
             }
         }
         if (have) {
-            *reinterpret_cast<uint32_t*>(codes) = word;
-            if ((i & 1) == 0) *scales = (uint8_t)byte;
+            *reinterpret_cast<uint32_t*>(to) = word;
+            if ((d8 & 8) == 0) *scales = (uint8_t)byte;
         }
-        codes += next;
+        to += next;
         scales += next_scale;
     }
 }
 
 template <bool BF16, bool Q4, int TEAM>
-static const void* head_kernel(bool vec, int rounds) {
-    if (!vec) return (const void*)k_head_append<BF16, Q4, TEAM, false, 1>;
-    return rounds == 1 ? (const void*)k_head_append<BF16, Q4, TEAM, true, 1>
-                       : (const void*)k_head_append<BF16, Q4, TEAM, true, 4>;
+static const void* head_kernel(bool vec, int rounds, bool split) {
+    if (!vec) return (const void*)k_head_append<BF16, Q4, TEAM, false, 1, false>;
+    return rounds == 1 ? (const void*)k_head_append<BF16, Q4, TEAM, true, 1, false>
+           : split     ? (const void*)k_head_append<BF16, Q4, TEAM, true, 4, true>
+                       : (const void*)k_head_append<BF16, Q4, TEAM, true, 4, false>;
 }
 template <bool BF16, bool Q4>
-static const void* head_kernel(int team, bool vec, int rounds) {
-    return team == 8    ? head_kernel<BF16, Q4, 8>(vec, rounds)
-           : team == 16 ? head_kernel<BF16, Q4, 16>(vec, rounds)
-                        : head_kernel<BF16, Q4, 32>(vec, rounds);
+static const void* head_kernel(int team, bool vec, int rounds, bool split) {
+    return team == 8    ? head_kernel<BF16, Q4, 8>(vec, rounds, split)
+           : team == 16 ? head_kernel<BF16, Q4, 16>(vec, rounds, split)
+                        : head_kernel<BF16, Q4, 32>(vec, rounds, split);
 }
 
 static bool vec_row(const void* p, int64_t stride) { return ((uintptr_t)p & 15u) == 0 && stride % 8 == 0; }
@@ -350,8 +400,6 @@ cudaError_t launch_head_append(const dg_head_append& op, cudaStream_t s) {
     p.D = q4 ? op.kv4.head_dim : op.kv.head_dim;
     p.page_size = q4 ? op.kv4.page_size : op.kv.page_size;
     p.num_pages = q4 ? op.kv4.num_pages : op.kv.num_pages;
-    p.k_div = (float)(7.0 * op.kv4.k_factor);
-    p.v_div = (float)(7.0 * op.kv4.v_factor);
     const bool bf = (q4 ? op.kv4.type : op.kv.type) == DG_BF16;
     const bool vec = op.rot_dim % (op.interleaved ? 8 : 16) == 0 && p.D % 8 == 0 && vec_row(op.k, op.k_stride) &&
                      vec_row(op.v, op.v_stride) && vec_row(op.w_q, 0) && vec_row(op.w_k, 0) &&
@@ -372,8 +420,11 @@ cudaError_t launch_head_append(const dg_head_append& op, cudaStream_t s) {
     p.by_warps = fast_div((uint32_t)warps);
     p.by_q_len = fast_div((uint32_t)(op.slots ? 1 : op.q_len));
     p.by_page = fast_div((uint32_t)p.page_size);
-    const void* fn = bf ? (q4 ? head_kernel<true, true>(team, vec, rounds) : head_kernel<true, false>(team, vec, rounds))
-                        : (q4 ? head_kernel<false, true>(team, vec, rounds) : head_kernel<false, false>(team, vec, rounds));
+    // (a half of whole scale groups: four lanes have two groups between them)
+    const bool split = !op.interleaved && op.rot_dim && op.rot_dim % (q4 ? 32 : 16) == 0;
+    const auto kernel = bf ? (q4 ? head_kernel<true, true> : head_kernel<true, false>)
+                           : (q4 ? head_kernel<false, true> : head_kernel<false, false>);
+    const void* fn = kernel(team, vec, rounds, split);
     void* args[] = {&p};
     return launch_pdl(fn, dim3((unsigned)((p.units + kHeadWarps - 1) / kHeadWarps)), dim3(kHeadThreads), 0, s, args);
 }
@@ -386,6 +437,8 @@ struct ReadParams {
     FastDiv by_q_len, by_page, by_token, by_head;
 };
 
+// Bound by the chain slot -> codes -> store (6825 tokens of 2 x 8 heads of 128: 11 us, of which the bytes are
+// 5): as many threads as pieces.
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_kv4_read(const ReadParams p) {
     griddep_launch_dependents();
@@ -408,18 +461,22 @@ __global__ void __launch_bounds__(256) k_kv4_read(const ReadParams p) {
         const long long code = at.page * kv.page_stride + at.at * kv.token_stride + h * kv.head_stride + c * 4;
         const long long scale =
             at.page * kv.scale_page_stride + at.at * kv.scale_token_stride + h * kv.scale_head_stride + c / 2;
+        uint32_t word[2] = {0, 0}, byte[2] = {0, 0};
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            if (at.page < 0 || !(which ? op.v : op.k)) continue;
+            word[which] = *reinterpret_cast<const uint32_t*>((which ? kv.v : kv.k) + code);
+            byte[which] = (which ? kv.v_scale : kv.k_scale)[scale];
+        }
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             uint16_t* to = static_cast<uint16_t*>(which ? op.v : op.k);
             if (!to) continue;
             to += t * (which ? op.v_stride : op.k_stride) + (long long)h * kv.head_dim + c * 8;
-            float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (at.page >= 0) {
-                const uint32_t w = *reinterpret_cast<const uint32_t*>((which ? kv.v : kv.k) + code);
-                const float s = e4m3_f32((which ? kv.v_scale : kv.k_scale)[scale]) * (which ? kv.v_factor : kv.k_factor);
+            const float s = e4m3_f32(byte[which]) * (which ? kv.v_factor : kv.k_factor);
+            float f[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = (float)((int)(w << (28 - 4 * e)) >> 28) * s;
-            }
+            for (int e = 0; e < 8; ++e) f[e] = (float)((int)(word[which] << (28 - 4 * e)) >> 28) * s;
             if (((uintptr_t)to & 15) == 0) {
                 *reinterpret_cast<uint4*>(to) = pack8<BF16>(f);
             } else {
@@ -439,7 +496,7 @@ cudaError_t launch_kv4_read(const dg_kv4_rows& op, cudaStream_t s) {
     p.by_head = fast_div((uint32_t)p.pieces);
     p.by_q_len = fast_div((uint32_t)(op.slots ? 1 : op.q_len));
     p.by_page = fast_div((uint32_t)op.kv.page_size);
-    const long long want = (p.units + 255) / 256, most = sm_count() * 16ll;
+    const long long want = (p.units + 255) / 256, most = 1 << 30;
     void* args[] = {&p};
     return launch_pdl(op.kv.type == DG_BF16 ? (const void*)k_kv4_read<true> : (const void*)k_kv4_read<false>,
                       dim3((unsigned)(want < most ? want : most)), dim3(256), 0, s, args);

@@ -313,3 +313,27 @@ def test_read_of_whole_sequences_and_one_side():
             if page >= 0:
                 want[b, L - n + p] = values[page, p % 16]
     ref.check(ref.f64(k).reshape(want.shape), want, ref.U16["f16"] * np.abs(want) * 1.001 + ref.TINY["f16"], "read")
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("ftype,heads,kvh,dim,rot,inter,layer,tokens", [
+    ("f16", 12, 3, 128, None, False, True, 700),
+    ("bf16", 9, 1, 256, 64, False, False, 560),        # lanes with and without a pair in a team
+    ("f16", 20, 5, 64, 32, False, False, 800),
+    ("bf16", 20, 5, 64, 16, False, True, 800),         # half of a scale group
+    ("f16", 17, 2, 96, 96, False, False, 560),
+    ("bf16", 13, 4, 80, 48, False, True, 560),
+    ("f16", 10, 5, 192, None, True, False, 300),
+    ("bf16", 12, 4, 128, 0, False, True, 560),
+    ("f16", 0, 18, 112, 96, False, False, 300),
+    ("bf16", 3, 1, 16, 16, False, False, 4200),
+    ("f16", 3, 1, 32, 32, False, True, 4200),
+])
+def test_many_tokens(bits, ftype, heads, kvh, dim, rot, inter, layer, tokens):
+    """More heads than the GPU has warps for at a time, in prompts that end inside pages."""
+    need_gpu()
+    c = Case(ftype, bits, heads, kvh, dim, 16, [1, tokens // 2, 3, tokens - tokens // 2 - 4], seed=11, rot=rot, inter=inter,
+             layer=layer, by_map=True, kf=0.5, vf=2.0)
+    got = c.check()
+    if heads:
+        assert torch.equal(c.run(in_place=True)["q"], got["q"])
