@@ -8,8 +8,9 @@
 // sequence by a search over the records and is written by a thread of its own.
 //
 // Bound by latency: small calls are one CTA that keeps the records in shared memory and
-// writes everything itself; others two launches, the sums by one CTA and the rest by
-// many.
+// writes everything itself (64 sequences, a token each: 3.6 us); others two launches, the sums by
+// one CTA and the rest by many (3000 sequences, 2.1 million places: 24 us, 4 of them the bytes, about 8 the
+// sums, the rest search -> table -> store).
 #include <climits>
 
 #include "elem.cuh"
@@ -171,6 +172,7 @@ __device__ __forceinline__ int find(const int4* rec, int B, int v, int lo = 0) {
 // Tokens, pages taken and pages given back, by all threads of the launch.  A warp takes runs of
 // up to 256 tokens, so that a lane searches for its first token's sequence and mostly stays there
 // (2.1 million places of 3000 sequences: 18 us cold, 21 with a search for each).
+template <bool ALONE>   // the launch is one CTA
 __device__ __forceinline__ void plan_fill(const PlanParams& p, const int4* rec, const PlanTotals& t, unsigned id,
                                           unsigned threads) {
     const dg_page_plan& op = p.op;
@@ -215,10 +217,38 @@ __device__ __forceinline__ void plan_fill(const PlanParams& p, const int4* rec, 
         op.block_table[(long long)b * op.table_stride + pages_of(r.w, op.page_size) + ((int)i - r.y)] =
             op.pool[queue((int)i)];
     }
-    for (long long i = id; i < t.given; i += threads) {
-        const int b = find<2>(rec, op.batch, (int)i);
-        op.pool[(int)((t.first + (t.count + i)) % N)] =
-            op.block_table[(long long)b * op.table_stride + ((int)i - rec[b].z)];
+    if constexpr (!ALONE) {
+        for (long long i = id; i < t.given; i += threads) {
+            const int b = find<2>(rec, op.batch, (int)i);
+            op.pool[queue(t.count + (int)i)] =
+                op.block_table[(long long)b * op.table_stride + ((int)i - rec[b].z)];
+        }
+        return;
+    }
+    // One CTA: runs of a warp here too, four entries of a lane at once (64 sequences of 4096 tokens that end, pages
+    // of 16: 25 us, with a search for each entry 58).
+    const int run = (int)min(256ll, max(32ll, ((long long)t.given + threads - 1) / threads * 32));
+    for (long long i0 = (long long)(id >> 5) * run; i0 < t.given; i0 += (long long)(threads >> 5) * run) {
+        int b = -1, first = 0, last = -1;
+        for (int k = id & 31; k < run; k += 32 * 4) {
+            int page[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const long long i = i0 + k + 32 * j;
+                if (k + 32 * j >= run || i >= t.given) continue;
+                if (i >= last) {
+                    b = find<2>(rec, op.batch, (int)i, max(b, 0));
+                    first = rec[b].z;
+                    last = rec[b + 1].z;
+                }
+                page[j] = op.block_table[(long long)b * op.table_stride + ((int)i - first)];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const long long i = i0 + k + 32 * j;
+                if (k + 32 * j < run && i < t.given) op.pool[queue(t.count + (int)i)] = page[j];
+            }
+        }
     }
 }
 
@@ -229,7 +259,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_small(const PlanParams p)
     PlanTotals t;
     plan_sums<1>(p, rec, t);
     __syncthreads();
-    plan_fill(p, rec, t, threadIdx.x, blockDim.x);
+    plan_fill<true>(p, rec, t, threadIdx.x, blockDim.x);
 }
 
 __global__ void __launch_bounds__(kPlanThreads) k_plan_sums(const PlanParams p) {
@@ -244,7 +274,7 @@ __global__ void __launch_bounds__(256) k_plan_fill(const PlanParams p) {
     griddep_launch_dependents();
     griddep_wait();
     const PlanTotals t = *p.totals;
-    plan_fill(p, p.rec, t, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+    plan_fill<false>(p, p.rec, t, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
 }
 
 static bool plan_small(const dg_page_plan& op) {

@@ -163,3 +163,16 @@ def test_another_stream():
     side = torch.cuda.Stream()
     check(run(lens, new, table, pool, state, 16, 4000, stream=side),
           serve_ref.pages(lens, new, table, pool, state, 16, 4000))
+
+
+@pytest.mark.parametrize("B,len_max", [(1, 40000), (5, 9001), (90, 1500), (1024, 200), (1500, 60)])
+@pytest.mark.parametrize("page", [1, 16])
+def test_long_sequences_that_end_together(B, len_max, page):
+    """More pages come back than the launch has threads, in runs that start and end inside a row."""
+    need_gpu()
+    r = np.random.RandomState(6)
+    new = np.where(r.rand(B) < 0.8, -1, r.randint(0, 4, B))
+    new[0] = -1
+    lens, table, pool, state = setup(B, page, len_max, new, 7)
+    tokens = int(np.maximum(new, 0).sum()) + 3
+    check(run(lens, new, table, pool, state, page, tokens), serve_ref.pages(lens, new, table, pool, state, page, tokens))
