@@ -21,6 +21,12 @@
 //  - Weights meet the values as two fp16 numbers, as in the 16-bit kernel.
 //  - A score is checked against the running maximum by each lane for its own keys; lanes
 //    exchange only when that has grown by 2^8.
+//
+// Measured: 200001 positions of 8 x 128, 32 heads, bf16: 68 us with the join, 3.4 TB/s; 50000: 26;
+// 16 sequences of 1..8191, 2 x 128: 12; 100 positions: 5.3.  Long calls are bound by unpacking: 370
+// instructions for 16 keys of 128 dims, of which 64 LOP3, 64 HFMA2, 64 PRMT and shifts and 24
+// matrix instructions; half of the issue slots are taken (ALU 40 %, tensor pipe 26 %), and 8, 12 or 16 warps an
+// SM take the same time.  Short ones are bound by the chain length -> page -> key -> sum, and by the join.
 #include "attn_common.cuh"
 
 namespace dg {

@@ -4,7 +4,9 @@
 // A row (or a part of it, where the rows are few) is a CTA's, taken in tiles of 512
 // 16-byte vectors, four a thread, the next tile loading while one is used.  Small CTAs, eight an SM
 // (fp32: five): while one looks for its row's best the others stream (2047 x 128255 bf16 with
-// everything and one alternative: 101 us, with four CTAs of 256 threads 110).  Each thread
+// everything and one alternative: 101 us, with four CTAs of 256 threads 110; 97, 5.4 TB/s, since lanes
+// take one base before their sums are added).  Bound by issue; one row of 128256 fp32 with five alternatives
+// by two launches, 7.4 us.  Each thread
 // keeps a base m and, with c = scale log2(e) and B = m c rounded, the sums l of w = 2^(x c - B)
 // and a of w (x c - B): an exponent is one fused multiply-add, rounded once, B
 // being a number like any other (a softmax of scale c / log2(e), 2^-24 off).  The base
@@ -108,14 +110,17 @@ struct Sums {
         l += o.l;
         a += o.a;
     }
+    // Those of LANES neighbouring lanes: one base for all first, so that each moves once.
+    template <int LANES = 32>
     __device__ __forceinline__ void join_warp(const LpParams& p) {
+        float top = m;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            Sums x;
-            x.m = __shfl_xor_sync(0xffffffffu, m, o);
-            x.l = __shfl_xor_sync(0xffffffffu, l, o);
-            x.a = __shfl_xor_sync(0xffffffffu, a, o);
-            join(x, p);
+        for (int o = LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        move(top, p);
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) {
+            l += __shfl_xor_sync(0xffffffffu, l, o);
+            a += __shfl_xor_sync(0xffffffffu, a, o);
         }
     }
 };
@@ -145,18 +150,26 @@ struct Row {
     __device__ __forceinline__ float entropy() const { return s.l == 0.f ? 0.f : (log_l - s.a / s.l) * kLpLn2; }
 };
 
+// The given token, -1 where there is none inside the row, and its logit.
+struct Given {
+    int tok;
+    float logit;
+};
 template <int TYPE>
-__device__ __forceinline__ void write_row(const LpParams& p, const Row& r, int row, int before, const void* x) {
+__device__ __forceinline__ Given given(const dg_logprobs& op, int row, const void* x) {
+    Given g = {-1, kNan};
+    if (!op.tokens) return g;
+    const int tok = op.tokens[row];
+    if (tok >= 0 && tok < op.V) g = {tok, logit_at<TYPE>(x, tok)};
+    return g;
+}
+__device__ __forceinline__ void write_row(const LpParams& p, const Row& r, int row, int before, Given g) {
     const dg_logprobs& op = p.op;
     if (op.lse) op.lse[row] = r.lse();
     if (op.entropy) op.entropy[row] = r.entropy();
-    if (!op.tokens) return;
-    const int tok = op.tokens[row];
-    const bool there = tok >= 0 && tok < op.V;
-    if (op.rank) op.rank[row] = there ? before : op.V;
+    if (op.rank) op.rank[row] = g.tok >= 0 ? before : op.V;
     // of a row of NaN everything is NaN
-    if (op.logprob)
-        op.logprob[row] = there ? r.logprob(logit_at<TYPE>(x, tok)) : r.s.l != r.s.l ? r.s.l : -INFINITY;
+    if (op.logprob) op.logprob[row] = g.tok >= 0 ? r.logprob(g.logit) : r.s.l != r.s.l ? r.s.l : -INFINITY;
 }
 
 // The largest of a vector; NaN only where all are.
@@ -261,13 +274,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
         s_before = 0;
         s_floor = 0;
     }
-    int tok = -1;
-    float mine = kNan;   // the given token's logit
-    if (op.rank && op.tokens) {
-        tok = op.tokens[row];
-        if (tok < 0 || tok >= V) tok = -1;
-        else mine = logit_at<TYPE>(x, tok);
-    }
+    const Given token = given<TYPE>(op, row, x);   // (now: at the row's end all of the CTA would wait for it)
+    const int tok = op.rank ? token.tok : -1;
+    const float mine = token.logit;
     const bool nan_token = tok >= 0 && mine != mine;
     auto before = [&](float v, int i) {   // whether logit v of word i comes before the token
         if (nan_token) return v == v || i < tok;
@@ -382,8 +391,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
         s.join_warp(p);
         if (lane == 0) red[warp] = s;
         __syncthreads();
-        s = lane < kLpWarps ? red[lane] : Sums{-INFINITY, 0.f, 0.f};
-        s.join_warp(p);
+        s = red[lane % kLpWarps];
+        s.join_warp<kLpWarps>(p);
     };
     s = {m, l.x + l.y, a.x + a.y};
     if (m == INFINITY) s.l = kNan;
@@ -425,7 +434,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
     }
     const Row r(s, p);
     if (tid == 0) {
-        if (cut < 0) write_row<TYPE>(p, r, row, s_before, x);
+        if (cut < 0) write_row(p, r, row, s_before, token);
         else p.part[cut] = {s.m, s.l, s.a, s_before};
     }
     if (K == 0) return;
@@ -528,51 +537,61 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
         for (int i = n + tid; i < K; i += kLpThreads) keys[i] = 0;
 }
 
-// The parts of a row: their sums in order, and top_k times the largest of the parts' next
-// keys.  A CTA a row; its first warp does it, when all have brought the keys to shared memory.
+// The parts of a row, a CTA a row: its first warp joins their sums, while the second takes top_k times the
+// largest of the parts' next keys, when all have brought those to shared memory.
 constexpr int kLpJoinThreads = 128;
 template <int TYPE>
 __global__ void __launch_bounds__(kLpJoinThreads) k_logprobs_join(const LpParams p) {
     __shared__ Key keys[kLpMaxParts * 32];
+    __shared__ Sums total;
     griddep_launch_dependents();
     griddep_wait();
     const dg_logprobs& op = p.op;
-    const int cut = blockIdx.x, row = p.whole + cut, lane = threadIdx.x, K = op.top_k, n = p.parts;
+    const int cut = blockIdx.x, row = p.whole + cut, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = op.top_k,
+              n = p.parts;
     const unsigned char* x = static_cast<const unsigned char*>(op.logits) + (long long)row * op.stride * (TYPE == 2 ? 4 : 2);
     for (int i = threadIdx.x; i < n * K; i += kLpJoinThreads) keys[i] = p.keys[(size_t)cut * n * K + i];
+    const Given token = warp == 0 ? given<TYPE>(op, row, x) : Given{-1, kNan};
     __syncthreads();
-    if (threadIdx.x >= 32) return;
-    Sums s = {-INFINITY, 0.f, 0.f};
-    int before = 0;
-    for (int i = lane; i < n; i += 32) {   // (two parts a lane at most)
-        const LpPart q = p.part[(size_t)cut * n + i];
-        s.join({q.m, q.l, q.a}, p);
-        before += q.before;
-    }
-    s.join_warp(p);
-    before = warp_sum(before);
-    const Row r(s, p);
-    if (lane == 0) write_row<TYPE>(p, r, row, before, x);
-    if (K == 0) return;
-    int at[2] = {0, 0};
-    Key head[2], mine = 0;   // the two lists' next keys; the key of this lane's place
+    Key mine = 0;   // of this lane's place
+    if (warp == 0) {
+        Sums s = {-INFINITY, 0.f, 0.f};
+        int before = 0;
+        for (int i = lane; i < n; i += 32) {   // (two parts a lane at most)
+            const LpPart q = p.part[(size_t)cut * n + i];
+            s.join({q.m, q.l, q.a}, p);
+            before += q.before;
+        }
+        s.join_warp(p);
+        before = warp_sum(before);
+        if (lane == 0) {
+            total = s;
+            write_row(p, Row(s, p), row, before, token);
+        }
+    } else if (warp == 1 && K) {
+        int at[2] = {0, 0};
+        Key head[2];   // the two lists' next keys
 #pragma unroll
-    for (int h = 0; h < 2; ++h) head[h] = lane + 32 * h < n ? keys[(lane + 32 * h) * K] : 0;
-    for (int i = 0; i < K; ++i) {
-        const int h = head[1] > head[0];
-        const Key best = h ? head[1] : head[0];
-        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
-        const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-        const Key win = (Key)hi << 32 | lo;
-        if (lane == i) mine = win;
-        if (win == best && win) {   // keys are unique: one lane
-            const int next = h ? ++at[1] : ++at[0];
-            const Key k = next < K ? keys[(lane + 32 * h) * K + next] : 0;
-            if (h) head[1] = k;
-            else head[0] = k;
+        for (int h = 0; h < 2; ++h) head[h] = lane + 32 * h < n ? keys[(lane + 32 * h) * K] : 0;
+        for (int i = 0; i < K; ++i) {
+            const int h = head[1] > head[0];
+            const Key best = h ? head[1] : head[0];
+            const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
+            const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+            const Key win = (Key)hi << 32 | lo;
+            if (lane == i) mine = win;
+            if (win == best && win) {   // keys are unique: one lane
+                const int next = h ? ++at[1] : ++at[0];
+                const Key k = next < K ? keys[(lane + 32 * h) * K + next] : 0;
+                if (h) head[1] = k;
+                else head[0] = k;
+            }
         }
     }
-    if (lane < K && mine) {
+    if (K == 0) return;
+    __syncthreads();
+    if (warp == 1 && lane < K && mine) {
+        const Row r(total, p);
         const long long to = (long long)row * K + lane;
         if (op.top_ids) op.top_ids[to] = index_of(mine);
         if (op.top_logprobs) op.top_logprobs[to] = r.logprob(logit_of(mine));
