@@ -245,3 +245,25 @@ def test_high_temperatures(ftype, scale, V):
     x[4] = -float("inf")
     x[4, 5] = 2.0
     check(x.to(DEV), [0, 1, 2, 3, 5], 3, scale)
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("R,V,top_k", [(1217, 20000, 5), (1260, 9001, 32), (763, 9001, 0), (800, 30000, 20), (2500, 5000, 1)])
+def test_whole_rows_and_rows_in_parts_in_one_call(ftype, R, V, top_k):
+    """Rows behind the last full round go in parts: the same rows there and before have the same words and ranks."""
+    need_gpu()
+    x = logits(17, V, ftype, R)
+    x[3, ::2] = -float("inf")
+    x[5] = x[5].clamp(-1, 1)                   # ties
+    x[7, V // 2] = float("nan")
+    tokens = np.random.RandomState(R).randint(-1, V + 1, 17)
+    tokens[3] = 1
+    n = -(-R // 17)
+    got = run(x.repeat(n, 1)[:R].to(DEV), np.tile(tokens, n)[:R], top_k, 0.75)
+    check(x.to(DEV), tokens, top_k, 0.75, "first", {k: t[:17] for k, t in got.items()})
+    at = (R - 17) // 17 * 17
+    check(x.to(DEV), tokens, top_k, 0.75, "last whole", {k: t[at:at + 17] for k, t in got.items()})
+    last = np.arange(R - 17, R) % 17
+    check(x[last].to(DEV), tokens[last], top_k, 0.75, "last", {k: t[R - 17:] for k, t in got.items()})
+    for k in ("rank", "top_ids")[:2 if top_k else 1]:
+        assert np.array_equal(got[k], np.concatenate([got[k][:17]] * n)[:R]), k
