@@ -9,7 +9,7 @@
 //
 // Bound by latency: small calls are one CTA that keeps the records in shared memory and
 // writes everything itself (64 sequences, a token each: 3.6 us); others two launches, the sums by
-// one CTA and the rest by many (3000 sequences, 2.1 million places: 21 us, 4 of them the bytes, about 6 the
+// one CTA and the rest by many (3000 sequences, 2.1 million places: 18 us, 4 of them the bytes, about 6 the
 // sums, the rest search -> table -> store).
 #include <climits>
 
@@ -19,6 +19,7 @@ namespace dg {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanItems = 4;            // sequences of a thread in a round of the large form
+constexpr int kAtOnce = 4;              // entries of a thread under way
 constexpr int kPlanSmallBatch = 1024, kPlanSmallTokens = 16384;
 
 struct PlanTotals {
@@ -73,7 +74,7 @@ __device__ __forceinline__ Pair block_scan(Pair v, Pair* warps, Pair& total) {
 }
 
 // Pages of 0 <= tokens < 2^31, without a division and its many instructions (of 64 bits, 12 a thread in the sums:
-// 3000 sequences and 2.1 million places 24 us, this way 21).
+// 3000 sequences and 2.1 million places 24 us, this way 21.5).
 __device__ __forceinline__ int pages_of(int tokens, FastDiv page) { return tokens > 0 ? (tokens - 1) / page + 1 : 0; }
 
 // All running sums, by one CTA.  rec may be shared memory.
@@ -173,8 +174,10 @@ __device__ __forceinline__ int find(const int4* rec, int B, int v, int lo = 0) {
 }
 
 // Tokens, pages taken and pages given back, by all threads of the launch.  A warp takes runs of
-// up to 256 tokens, so that a lane searches for its first token's sequence and mostly stays there
-// (2.1 million places of 3000 sequences: 18 us cold, 21 with a search for each).
+// up to 256 tokens and looks for the sequences of the run's first and last one, 32 records a step;
+// a lane then searches between these for its first token's sequence and mostly stays there.  Four
+// tokens of a lane are under way at once.  (2.1 million places of 3000 sequences, the whole call: 18 us; 21.5
+// with a lane's own search over all records and one token after the other, 22 and 20 with one of the two.)
 template <bool ALONE>   // the launch is one CTA
 __device__ __forceinline__ void plan_fill(const PlanParams& p, const int4* rec, const PlanTotals& t, unsigned id,
                                           unsigned threads) {
@@ -190,27 +193,49 @@ __device__ __forceinline__ void plan_fill(const PlanParams& p, const int4* rec, 
         for (long long i0 = (long long)(id >> 5) * run; i0 < op.max_tokens; i0 += (long long)(threads >> 5) * run) {
             int b = -1, last = -1;   // the sequence of the last token, and the first token behind it
             int4 r = make_int4(0, 0, 0, 0);
-            for (int k = id & 31; k < run; k += 32) {
-                const long long i = i0 + k;
-                if (i >= op.max_tokens) break;
-                long long slot = -1;
-                int pos = -1;
-                if (i < tokens) {
+            // the sequences of the run's first and last token, by the warp: 32 places a step
+            int b0 = 0, b1 = op.batch;   // rec[b0].x <= first, rec[b1].x > last
+            if (!ALONE && i0 < tokens) {
+                const int v = (int)i0, w = (int)min(i0 + run, (long long)tokens) - 1;
+                int hi = op.batch, lo = 0;
+                while (hi - b0 > 1 || b1 - lo > 1) {
+                    const int s0 = (hi - b0 + 31) >> 5, s1 = (b1 - lo + 31) >> 5;
+                    const int a0 = b0 + (int)(id & 31) * s0, a1 = lo + (int)(id & 31) * s1;
+                    const unsigned m0 = __ballot_sync(0xffffffffu, a0 < hi && rec[min(a0, hi)].x <= v);
+                    const unsigned m1 = __ballot_sync(0xffffffffu, a1 < b1 && rec[min(a1, b1)].x <= w);
+                    b0 += (31 - __clz(m0)) * s0;
+                    hi = min(hi, b0 + s0);
+                    lo += (31 - __clz(m1)) * s1;
+                    b1 = min(b1, lo + s1);
+                }
+            }
+            for (int k = id & 31; k < run; k += 32 * kAtOnce) {
+                int page[kAtOnce], pos[kAtOnce], in[kAtOnce];
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const long long i = i0 + k + 32 * j;
+                    page[j] = pos[j] = -1;
+                    in[j] = 0;
+                    if (k + 32 * j >= run || i >= tokens) continue;
                     if (i >= last) {
-                        b = find<0>(rec, op.batch, (int)i, max(b, 0));
+                        b = find<0>(rec, ALONE ? op.batch : b1, (int)i, max(b, b0));
                         r = rec[b];
                         last = rec[b + 1].x;
                     }
-                    if (r.w >= 0) {
-                        pos = r.w + ((int)i - r.x);
-                        const int at = pos / p.page, held = pages_of(r.w, p.page);
-                        const int page = at < held ? op.block_table[(long long)b * op.table_stride + at]
-                                                   : op.pool[queue(r.y + at - held)];
-                        if (page >= 0) slot = (long long)page * op.page_size + (pos - at * op.page_size);
-                    }
+                    if (r.w < 0) continue;
+                    pos[j] = r.w + ((int)i - r.x);
+                    const int at = pos[j] / p.page, held = pages_of(r.w, p.page);
+                    in[j] = pos[j] - at * op.page_size;
+                    page[j] = at < held ? op.block_table[(long long)b * op.table_stride + at]
+                                        : op.pool[queue(r.y + at - held)];
                 }
-                op.slots[i] = slot;
-                if (op.positions) op.positions[i] = pos;
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const long long i = i0 + k + 32 * j;
+                    if (k + 32 * j >= run || i >= op.max_tokens) continue;
+                    op.slots[i] = page[j] >= 0 ? (long long)page[j] * op.page_size + in[j] : -1;
+                    if (op.positions) op.positions[i] = pos[j];
+                }
             }
         }
     }
@@ -233,10 +258,10 @@ __device__ __forceinline__ void plan_fill(const PlanParams& p, const int4* rec, 
     const int run = (int)min(256ll, max(32ll, ((long long)t.given + threads - 1) / threads * 32));
     for (long long i0 = (long long)(id >> 5) * run; i0 < t.given; i0 += (long long)(threads >> 5) * run) {
         int b = -1, first = 0, last = -1;
-        for (int k = id & 31; k < run; k += 32 * 4) {
-            int page[4];
+        for (int k = id & 31; k < run; k += 32 * kAtOnce) {
+            int page[kAtOnce];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kAtOnce; ++j) {
                 const long long i = i0 + k + 32 * j;
                 if (k + 32 * j >= run || i >= t.given) continue;
                 if (i >= last) {
@@ -247,7 +272,7 @@ __device__ __forceinline__ void plan_fill(const PlanParams& p, const int4* rec, 
                 page[j] = op.block_table[(long long)b * op.table_stride + ((int)i - first)];
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kAtOnce; ++j) {
                 const long long i = i0 + k + 32 * j;
                 if (k + 32 * j < run && i < t.given) op.pool[queue(t.count + (int)i)] = page[j];
             }

@@ -176,3 +176,19 @@ def test_long_sequences_that_end_together(B, len_max, page):
     lens, table, pool, state = setup(B, page, len_max, new, 7)
     tokens = int(np.maximum(new, 0).sum()) + 3
     check(run(lens, new, table, pool, state, page, tokens), serve_ref.pages(lens, new, table, pool, state, page, tokens))
+
+
+@pytest.mark.parametrize("kind", ["mixed", "one", "tiny", "few"])
+def test_maps_of_many_tokens(kind):
+    """Runs of several tokens a lane: sequences of none, of one and of thousands side by side, some not served."""
+    need_gpu()
+    r = np.random.RandomState(8)
+    new = {"mixed": lambda: np.where(r.rand(3000) < 0.4, 0, np.where(r.rand(3000) < 0.6, r.randint(1, 4, 3000),
+                                                                     r.randint(500, 2500, 3000))),
+           "one": lambda: np.array([0, 0, 650000, 0]), "tiny": lambda: r.randint(0, 2, 900000 // 4) * 3,
+           "few": lambda: np.array([1, 300001, 0, 255, 257, 256, 1, 1, 200000, 0])}[kind]()
+    lens, table, pool, state = setup(len(new), 16, 60, new, 9)
+    total = int(new.sum())
+    assert total > 330000
+    for tokens in (total, total - 1000, total + 70):
+        check(run(lens, new, table, pool, state, 16, tokens), serve_ref.pages(lens, new, table, pool, state, 16, tokens))
