@@ -6,7 +6,7 @@
 // (fp32: five): while one looks for its row's best the others stream (2047 x 128255 bf16 with
 // everything and one alternative: 101 us, with four CTAs of 256 threads 110; 97, 5.4 TB/s, since lanes
 // take one base before their sums are added).  Bound by issue; one row of 128256 fp32 with five alternatives
-// by two launches, 7.4 us.  Each thread
+// by two launches, 7.9 us.  Each thread
 // keeps a base m and, with c = scale log2(e) and B = m c rounded, the sums l of w = 2^(x c - B)
 // and a of w (x c - B): an exponent is one fused multiply-add, rounded once, B
 // being a number like any other (a softmax of scale c / log2(e), 2^-24 off).  The base
