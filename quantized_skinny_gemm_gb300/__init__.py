@@ -651,7 +651,7 @@ def head_append(kv, q, k, v, q_out=None, q_len=None, cos=None, sin=None, interle
         _contiguous(where, torch.int64, slots)
         _contiguous(where, torch.int32, positions)
         tokens, q_len = slots.numel(), 0
-        _fits(tokens > 0 and positions.numel() == tokens, where)
+        _fits(0 < tokens < 2 ** 31 and positions.numel() == tokens, where)
     else:
         q_len = 1 if q_len is None else q_len
         _fits(q_len > 0, where)
@@ -696,7 +696,7 @@ def kv4_rows(kv, k=None, v=None, q_len=None, slots=None):
     if slots is None:
         q_len = 1 if q_len is None else q_len
     tokens = slots.numel() if slots is not None else kv.batch * q_len
-    _fits(tokens > 0, where)
+    _fits(0 < tokens < 2 ** 31, where)
     ks, vs = (0 if t is None else _head_rows(t, tokens, kv.kv_heads, kv.head_dim, dt, where) for t in (k, v))
     for t, stride in ((k, ks), (v, vs)):
         _fits(t is None or stride >= kv.kv_heads * kv.head_dim, where)   # rows that overlap
@@ -748,6 +748,7 @@ def page_plan(lens, block_table, pool, pool_state, page_size, new_lens=None, new
     for t, n in ((new_lens, batch), (lens_out, batch), (pool_state, 2), (pool_state_out, 2), (starts, batch + 1)):
         _fits(t is None or t.numel() == n, where)
     tokens = 0 if slots is None else slots.numel()
+    _fits(max(tokens, pool.numel(), max_pages) < 2 ** 31, where)
     _fits(positions is None or positions.numel() == tokens, where)
     return PagePlan(batch, page_size, max_pages, pool.numel(), new_len, tokens, stride, _ptr(lens), _ptr(new_lens),
                     _ptr(lens_out), _ptr(block_table), _ptr(pool), _ptr(pool_state), _ptr(pool_state_out),
@@ -774,6 +775,7 @@ def logprobs(logits, tokens=None, logprob=None, rank=None, entropy=None, lse=Non
     kind = F16 if f32 else _ftype(logits, where)
     _fits(logits.dim() in (1, 2) and logits.numel() > 0 and (logits.shape[-1] == 1 or logits.stride(-1) == 1), where)
     rows, V = (1, logits.shape[0]) if logits.dim() == 1 else logits.shape
+    _fits(max(rows, V) < 2 ** 31, where)
     stride = logits.stride(0) if rows > 1 else V
     _contiguous(where, torch.int32, tokens, rank, top_ids)
     _contiguous(where, torch.float32, logprob, entropy, lse, top_logprobs)

@@ -261,3 +261,26 @@ def test_builders_refuse_tensors_that_do_not_fit():
     refused(lambda: dg.logprobs(x.t(), entropy=t(100)))
     refused(lambda: dg.logprobs(x, tokens=t(3, dtype=torch.int64), logprob=one))
     refused(lambda: dg.logprobs(x, top_ids=t(3, 4, dtype=i32), top_logprobs=t(3, 5)))
+
+
+def test_builders_refuse_sizes_past_32_bits():
+    """A count of 2^32 + 5 is not one of 5."""
+    big = 2 ** 32 + 5
+    meta = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device="meta")
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32)
+    with pytest.raises(dg.DGError):
+        dg.page_plan(i32(2), i32(2, 4), i32(8), i32(2), 16, slots=meta(big, dtype=torch.int64))
+    with pytest.raises(dg.DGError):
+        dg.page_plan(i32(2), i32(2, 4), meta(big), i32(2), 16)
+    with pytest.raises(dg.DGError):
+        dg.logprobs(meta(big, 4, dtype=torch.float16), lse=meta(big, dtype=torch.float32))
+    with pytest.raises(dg.DGError):
+        dg.logprobs(meta(1, big, dtype=torch.float16), lse=meta(1, dtype=torch.float32))
+    codes = lambda w: torch.zeros(4, 16, 1, w, dtype=torch.uint8)
+    kv = dg.paged_kv4(codes(8), codes(8), codes(1), codes(1), i32(2, 4), i32(2))
+    half = lambda: meta(big, 1, 16, dtype=torch.float16)
+    slots = meta(big, dtype=torch.int64)
+    with pytest.raises(dg.DGError):
+        dg.kv4_rows(kv, half(), slots=slots)
+    with pytest.raises(dg.DGError):
+        dg.head_append(kv, None, half(), half(), slots=slots, positions=meta(big))
