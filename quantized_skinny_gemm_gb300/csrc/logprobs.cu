@@ -238,8 +238,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
     __shared__ float slice_max[kLpSlices][kLpThreads];
     __shared__ Sums red[kLpWarps];
     __shared__ unsigned odd[kLpWarps];
+    __shared__ int ranked_ahead[kLpWarps];   // what a warp saw before the token
     __shared__ Key s_floor;
-    __shared__ int s_n, s_before, s_hot;
+    __shared__ int s_n, s_hot;
     __shared__ uint16_t hot[kLpSlices * kLpThreads];
     const dg_logprobs& op = p.op;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -272,10 +273,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
         }
     };
     fetch(tile0);
-    if (tid == 0) {
-        s_before = 0;
-        s_floor = 0;
-    }
+    if (tid == 0) s_floor = 0;   // (the sums' barriers lie before its next use)
     const Given token = given<TYPE>(op, row, x);   // (now: at the row's end all of the CTA would wait for it)
     const int tok = op.rank ? token.tok : -1;
     const float mine = token.logit;
@@ -399,10 +397,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
     s = {m, l.x + l.y, a.x + a.y};
     if (m == INFINITY) s.l = kNan;
     else if (m > -INFINITY) s.m = fminf(fmaxf(m, -p.most), p.most);   // as its base
-    if (tok >= 0) {
-        ahead = warp_sum(ahead);
-        if (lane == 0 && ahead) atomicAdd(&s_before, ahead);
-    }
+    // a place for each warp, read behind the sums' barrier: nobody has to clear a common one first
+    ahead = warp_sum(ahead);
+    if (lane == 0) ranked_ahead[warp] = ahead;
     // (the threads' bases may lie 2^8 below their maxima)
     const unsigned past = __any_sync(0xffffffffu, m < INFINITY && m > p.most);
     const unsigned some = __any_sync(0xffffffffu, m > -INFINITY);
@@ -436,8 +433,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
     }
     const Row r(s, p);
     if (tid == 0) {
-        if (cut < 0) write_row(p, r, row, s_before, token);
-        else p.part[cut] = {s.m, s.l, s.a, s_before};
+        int all_ahead = 0;
+#pragma unroll
+        for (int w = 0; w < kLpWarps; ++w) all_ahead += ranked_ahead[w];
+        if (cut < 0) write_row(p, r, row, all_ahead, token);
+        else p.part[cut] = {s.m, s.l, s.a, all_ahead};
     }
     if (K == 0) return;
     // ---- the best -------------------------------------------------------------------------------

@@ -267,3 +267,18 @@ def test_whole_rows_and_rows_in_parts_in_one_call(ftype, R, V, top_k):
     check(x[last].to(DEV), tokens[last], top_k, 0.75, "last", {k: t[R - 17:] for k, t in got.items()})
     for k in ("rank", "top_ids")[:2 if top_k else 1]:
         assert np.array_equal(got[k], np.concatenate([got[k][:17]] * n)[:R]), k
+
+
+@pytest.mark.parametrize("ftype", ["f16", "f32"])
+@pytest.mark.parametrize("V", [129, 260, 517, 1030, 2053])
+def test_ranks_of_many_short_rows(ftype, V):
+    """Rows of about as many vectors as a CTA has threads, a token that all others come before: the warps reach the
+    row's end at different times, some with nothing of it, and none of their counts may be lost."""
+    need_gpu()
+    R = 6000
+    x = logits(1, V, ftype, V).repeat(R, 1)
+    tokens = np.random.RandomState(V).randint(0, V, R)
+    x[torch.arange(R), torch.from_numpy(tokens)] = -60.0
+    for _ in range(3):
+        got = run(x.to(DEV), tokens, 0)
+        assert (got["rank"] == V - 1).all()
