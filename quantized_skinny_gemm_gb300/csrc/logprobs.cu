@@ -12,8 +12,9 @@
 // being a number like any other (a softmax of scale c / log2(e), 2^-24 off).  The base
 // follows the maximum only when that has grown by 2^8.  lse = ln 2 (B + log2 l), the entropy is
 // ln 2 (log2 l - a / l), whose terms have the size of the result.  Past |m c| = 2^22, where
-// B's rounding nears a whole power of two (rows of nothing but masks, mostly), the sums are taken
-// again with exponents (x - m) c.
+// B's rounding nears a whole power of two (rows of nothing but masks, mostly), bases stand and the sums are taken
+// again with exponents (x - m) c.  Sums of either kind join by what their weights were counted from, B or m c itself:
+// parts of a row may lie on both sides.
 //
 // Rows may start anywhere: the vectors are aligned ones, and the logits before the first and behind
 // the last are a thread's each.
@@ -89,13 +90,18 @@ __device__ __forceinline__ float logit_of(Key k) {
     return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
 }
 
-// The sums of a set of logits; an empty set's base is -infinity.
+// The sums of a set of logits; an empty set's base is -infinity.  Their weights are counted from m c rounded where
+// |m| <= most, else from m c.
 struct Sums {
     float m, l, a;
+    // what rounding left of m c
+    __device__ __forceinline__ static float rest(float m, const LpParams& p) {
+        return fabsf(m) <= p.most ? fmaf(m, p.c, -mul_rn(m, p.c)) : 0.f;
+    }
     // other's base seen from this one's, in powers of two
     __device__ __forceinline__ static float distance(float from, float to, const LpParams& p) {
         if (fabsf(from) <= p.most && fabsf(to) <= p.most) return mul_rn(from, p.c) - mul_rn(to, p.c);
-        return (from - to) * p.c;
+        return (from - to) * p.c - rest(from, p) + rest(to, p);
     }
     __device__ __forceinline__ void move(float to, const LpParams& p) {
         if (m == to) return;
@@ -135,18 +141,19 @@ __device__ __forceinline__ float logit_at(const void* p, long long i) {
 // A row's numbers from its sums; those of a row of only -infinity stand in the header.
 struct Row {
     Sums s;
-    float log_l, base, scale, c, most;
+    float log_l, base, scale, c;
     bool near;
     __device__ __forceinline__ Row(const Sums& sums, const LpParams& p)
         : s(sums), log_l(log2f(sums.l)), base(mul_rn(sums.m, p.c)), scale(p.op.scale), c(p.c),
-          most(p.most), near(fabsf(sums.m) <= p.most) {}
+          near(fabsf(sums.m) <= p.most) {}
     __device__ __forceinline__ float lse() const {
         if (s.l == 0.f) return -INFINITY;
         return near ? (base + log_l) * kLpLn2 : fmaf(scale, s.m, log_l * kLpLn2);
     }
     __device__ __forceinline__ float logprob(float x) const {
         if (s.l == 0.f) return -INFINITY;
-        return near && fabsf(x) <= most ? (fmaf(x, c, -base) - log_l) * kLpLn2 : scale * (x - s.m) - log_l * kLpLn2;
+        const float d = fmaf(x, c, -base);   // (may pass fp32 where the result does not)
+        return near && fabsf(d) <= FLT_MAX ? (d - log_l) * kLpLn2 : scale * (x - s.m) - log_l * kLpLn2;
     }
     __device__ __forceinline__ float entropy() const { return s.l == 0.f ? 0.f : (log_l - s.a / s.l) * kLpLn2; }
 };
@@ -288,7 +295,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
     const uint32_t bits = TYPE == 2 ? __float_as_uint(mine) : pair_16<TYPE == 1>(mine, mine);   // (it has 16 bits)
     const uint32_t below = TYPE == 2 ? bits_below(bits, 0x80000000u) : bits_below(bits & 0xFFFFu, 0x8000u) * 0x10001u;
     const int tok_vec = (tok + skew) / kEl;
-    Sums s = {-INFINITY, 0.f, 0.f};
+    // the thread's sums: weights of 2^(x c - base), base m c rounded, or most c with m's sign past it
+    float m = -INFINITY, base = 0.f;
+    float2 l = make_float2(0.f, 0.f), a = l;
+    auto base_of = [&](float v) { return mul_rn(fminf(fmaxf(v, -p.most), p.most), p.c); };
     int ahead = 0;
     // ---- the logits outside the vectors, by the first part ---------------------------------------
     const int head = min(V, skew ? kEl - skew : 0), tail = max(head, last * kEl - skew);
@@ -296,8 +306,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
     const int end_i = tid < head ? tid : tail + tid - head;
     if (end) {
         const float v = logit_at<TYPE>(x, end_i);
-        if (v > -INFINITY) s = {v, 1.f, 0.f};
-        if (v != v || v == INFINITY) s = {v == v ? v : -INFINITY, kNan, 0.f};
+        if (v > -INFINITY) {
+            m = v;
+            base = base_of(v);
+            const float d = fmaf(v, p.c, -base);
+            l.x = ex2(d);
+            a.x = l.x * fmaxf(d, -FLT_MAX);
+        }
+        if (v != v || v == INFINITY) l.x = kNan;
         ahead = tok >= 0 && before(v, end_i);
         list[tid] = key_of(v, end_i);   // always a candidate
     }
@@ -305,12 +321,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
     if (ranked && tid < kEl && tok_vec >= first + tile0 * kLpTile && tok_vec < min(last, first + tile1 * kLpTile)) {
         const int i = tok_vec * kEl - skew + tid;   // in the token's own vector, before it
         if (i < tok) ahead += logit_at<TYPE>(x, i) == mine;
-    }
-    float2 l = make_float2(s.l, 0.f), a = make_float2(0.f, 0.f);
-    float m = s.m, base = fabsf(m) <= p.most ? mul_rn(m, p.c) : 0.f;
-    if (m > -INFINITY && fabsf(m) > p.most) {   // (the sums are taken again if this is the part's maximum)
-        base = m > 0.f ? p.most * p.c : -p.most * p.c;
-        l.x = m == INFINITY ? l.x : 0.f;
     }
     // logit e of a vector; the index of the first of this thread's vector q; where vectors end
     auto logit = [&](const uint4& v, int e) {
@@ -347,7 +357,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
         }
         if (top > m + p.grow) {
             // (bases past 2^22 stand there; the sums are taken again if that was the part's maximum)
-            const float to = mul_rn(fminf(fmaxf(top, -p.most), p.most), p.c);
+            const float to = base_of(top);
             const float d = base - to, k = ex2(d);
             const bool none = m == -INFINITY;   // then l is 0, or NaN, and a is 0
             a = none ? make_float2(0.f, 0.f) : make_float2(k * (a.x + d * l.x), k * (a.y + d * l.y));
@@ -387,6 +397,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
     if (pass)
         for (long long i = i0 + tid; i < i1; i += kLpThreads) ahead += before(logit_at<TYPE>(x, i), (int)i);
     // ---- the part's sums ------------------------------------------------------------------
+    Sums s = {m, l.x + l.y, a.x + a.y};
+    if (m == INFINITY) s.l = kNan;
+    else if (m > -INFINITY) s.m = fminf(fmaxf(m, -p.most), p.most);   // as its base
     auto whole = [&] {   // the CTA's, in every thread
         s.join_warp(p);
         if (lane == 0) red[warp] = s;
@@ -394,16 +407,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
         s = red[lane % kLpWarps];
         s.join_warp<kLpWarps>(p);
     };
-    s = {m, l.x + l.y, a.x + a.y};
-    if (m == INFINITY) s.l = kNan;
-    else if (m > -INFINITY) s.m = fminf(fmaxf(m, -p.most), p.most);   // as its base
     // a place for each warp, read behind the sums' barrier: nobody has to clear a common one first
     ahead = warp_sum(ahead);
     if (lane == 0) ranked_ahead[warp] = ahead;
-    // (the threads' bases may lie 2^8 below their maxima)
+    // where the threads' maxima lie (those that their bases follow, up to 2^8 below the true ones)
     const unsigned past = __any_sync(0xffffffffu, m < INFINITY && m > p.most);
     const unsigned some = __any_sync(0xffffffffu, m > -INFINITY);
-    if (lane == 0) odd[warp] = past | some << 1;
+    const unsigned inside_most = __any_sync(0xffffffffu, m >= -p.most);
+    if (lane == 0) odd[warp] = past | some << 1 | inside_most << 2;
     if (K) {
         float group = greatest;
 #pragma unroll
@@ -414,8 +425,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
     unsigned any = 0;
 #pragma unroll
     for (int w = 0; w < kLpWarps; ++w) any |= odd[w];
-    const bool far = p.always_far || (any & 1u) || (s.l == 0.f && (any & 2u));
-    if (far) {   // logits past what a base reaches: exponents as differences
+    // A maximum past most has weights that pass fp32 beside its base; with all of them below -most the best one's may be so
+    // small that weaker ones vanish.
+    const bool far = p.always_far || (any & 1u) || (any & 6u) == 2u;
+    if (far) {   // exponents as differences, or from the true maximum's base
         auto all = [&](auto&& use) {
             if (end) use(logit_at<TYPE>(x, end_i));
             for (long long i = i0 + tid; i < i1; i += kLpThreads) use(logit_at<TYPE>(x, i));
@@ -423,8 +436,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
         __syncthreads();   // red has been read
         s = {-INFINITY, 0.f, 0.f};
         all([&](float v) { s.m = fmaxf(s.m, v); });
+        const bool near = fabsf(s.m) <= p.most;
+        const float from = mul_rn(s.m, p.c);
         all([&](float v) {
-            const float d = (v - s.m) * p.c, t = ex2(d);
+            const float d = near ? fmaf(v, p.c, -from) : (v - s.m) * p.c, t = ex2(d);
             if (v == -INFINITY) return;
             s.l += t;
             s.a = fmaf(t, fmaxf(d, -FLT_MAX), s.a);

@@ -282,3 +282,54 @@ def test_ranks_of_many_short_rows(ftype, V):
     for _ in range(3):
         got = run(x.to(DEV), tokens, 0)
         assert (got["rank"] == V - 1).all()
+
+
+BORDER = 2 ** 22 * float(np.log(2))            # of z, where its size in powers of two passes 2^22
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("side", [-1, 1])
+@pytest.mark.parametrize("V,lower", [(5, 1.0), (5, 40.0), (129, 1.0), (130, 6.0), (3001, 3.0), (20001, 1.0), (20001, 9.0)])
+def test_best_logits_around_a_border_of_the_arithmetic(ftype, side, V, lower):
+    """The best z on both sides of +-2^22 powers of two, the others a little lower: no weight is lost, and sums and
+    log probabilities count from the same number, in rows at every alignment, whole and in parts."""
+    need_gpu()
+    past = [-300.0, -90.0, -7.0, -1.0, 0.0, 0.25, 1.0, 5.0, 30.0, 60.0, 80.0, 86.0, 87.0, 88.0, 89.0, 95.0, 128.0, 400.0]
+    if ftype == "f32":                         # steps of 0.25 around 2907270
+        best, scale, step = [side * BORDER - p for p in past], 1.0, lower
+    else:                                      # 33 is the border; steps of 1 / 32 (f16) and 1 / 4 (bf16) there
+        best, scale, step = [side * 33.0 - p / 1024 for p in past], BORDER / 33.0, lower * 2 ** -7
+        if ftype == "bf16":
+            step = 0.25
+    R = len(best)
+    x = torch.empty(R, V)
+    g = torch.Generator().manual_seed(V)
+    for r, b in enumerate(best):
+        x[r] = round(b * 64) / 64 - step * torch.randint(1, 3, (V,), generator=g)
+        x[r, (r * 37) % V] = round(b * 64) / 64
+    x = x.to(DT[ftype])
+    x[3, V // 2] = 1.0 if side < 0 else -1.0   # one word far above the rest, or below
+    x[7, 0] = torch.finfo(DT[ftype]).min       # and a masked one
+    tokens = np.arange(R) * 37 % V
+    tokens[::2] = (tokens[::2] + 1) % V
+    check(x.to(DEV), tokens, min(V, 4), scale)
+    if V == 5:                                 # every row a CTA's
+        many = x.repeat(45, 1)
+        got = run(many.to(DEV), np.tile(tokens, 45), 4, scale)
+        check(x.to(DEV), tokens, 4, scale, "whole", {n: t[:R] for n, t in got.items()})
+
+
+@pytest.mark.parametrize("where", ["first", "last", "spread"])
+@pytest.mark.parametrize("scale", [1.0, 1000.0, 1e5])
+@pytest.mark.parametrize("V", [20003, 60001])
+def test_parts_on_both_sides_of_the_border(where, scale, V):
+    """The parts of one row lie on different sides of the border, with weights of about the same size."""
+    need_gpu()
+    for side in (-1, 1):
+        x = torch.full((3, V), (side * BORDER - 60.0) / scale)
+        near = {"first": np.arange(0, V // 3), "last": np.arange(V - V // 3, V), "spread": np.arange(0, V, 5000)}[where]
+        for r, over in enumerate((0.5, 3.0, 20.0)):
+            x[r] = x[r] + 60.0 / scale - 2.0 / scale
+            x[r, near] += over / scale
+        tokens = [0, V - 1, V // 2]
+        check(x.to(DEV), tokens, 5, scale)
