@@ -153,7 +153,9 @@ struct Row {
     __device__ __forceinline__ float logprob(float x) const {
         if (s.l == 0.f) return -INFINITY;
         const float d = fmaf(x, c, -base);   // (may pass fp32 where the result does not)
-        return near && fabsf(d) <= FLT_MAX ? (d - log_l) * kLpLn2 : scale * (x - s.m) - log_l * kLpLn2;
+        if (near && fabsf(d) <= FLT_MAX) return (d - log_l) * kLpLn2;
+        const float z = x - s.m;   // (passes fp32 for two finite numbers of different signs only: nothing cancels)
+        return (z < -FLT_MAX && x >= -FLT_MAX ? scale * x - scale * s.m : scale * z) - log_l * kLpLn2;
     }
     __device__ __forceinline__ float entropy() const { return s.l == 0.f ? 0.f : (log_l - s.a / s.l) * kLpLn2; }
 };

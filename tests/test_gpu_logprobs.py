@@ -333,3 +333,17 @@ def test_parts_on_both_sides_of_the_border(where, scale, V):
             x[r, near] += over / scale
         tokens = [0, V - 1, V // 2]
         check(x.to(DEV), tokens, 5, scale)
+
+
+@pytest.mark.parametrize("ftype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1e-30, 3e-25, 0.5])
+@pytest.mark.parametrize("V", [6, 20001])
+def test_differences_past_fp32_of_logits_inside_it(ftype, scale, V):
+    """Two logits 6e38 apart: their difference is no number of fp32, a small multiple of it is."""
+    need_gpu()
+    x = torch.full((3, V), 2.5e38, dtype=DT[ftype])
+    x[0, 1], x[0, V - 1] = 3e38, -3e38
+    x[1] = -3e38
+    x[1, V // 2] = 3e38
+    x[2, 0], x[2, 3] = -2e38, 1.5e38
+    check(x.to(DEV), [V - 1, 0, 0], 6, scale)
