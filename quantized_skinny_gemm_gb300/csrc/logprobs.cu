@@ -100,7 +100,8 @@ struct Sums {
     }
     // other's base seen from this one's, in powers of two
     __device__ __forceinline__ static float distance(float from, float to, const LpParams& p) {
-        if (fabsf(from) <= p.most && fabsf(to) <= p.most) return mul_rn(from, p.c) - mul_rn(to, p.c);
+        const float near = mul_rn(from, p.c) - mul_rn(to, p.c);
+        if (__builtin_expect(fabsf(from) <= p.most && fabsf(to) <= p.most, 1)) return near;
         return (from - to) * p.c - rest(from, p) + rest(to, p);
     }
     __device__ __forceinline__ void move(float to, const LpParams& p) {
