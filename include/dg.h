@@ -555,8 +555,8 @@ typedef struct {
  * there), all in fp32.  q goes to q_out (which may be q), k and v to the cache:
  *   bits 16 (kv):  rounded once
  *   bits 4 (kv4):  per 16 dims s = e4m3(max |x| / (7 factor)), to nearest even and at
- *       most 448, c = min(max(rne(x / (s factor)), -7), 7), 0 where s is 0; a group
- *       that holds an infinity or a NaN gets s = NaN and c = 0.
+ *       most 448, c = min(max(rne(x / (s factor)), -7), 7), 0 where s is 0 (products and
+ *       quotients each rounded to fp32); a group that holds an infinity or a NaN gets s = NaN and c = 0.
  * Without slots: token t = b * q_len + i of batch * q_len, 1 <= q_len <= 16, has
  * position p = seq_lens[b] - q_len + i and its place by the block table.  With slots
  * (int64 [tokens]; positions int32 [tokens], both needed): token t has position
