@@ -346,12 +346,12 @@ class SparseStep:
 
 def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None, batch=1, q_len=1,
                         page_size=64, max_pages=16, window=0, sinks=0, group=32, rope=None,
-                        share=None, cache_bits=16, k_factor=1.0, v_factor=1.0, pool_pages=None) -> SparseStep:
+                        share=None, cache_bits=16, k_factor=None, v_factor=None, pool_pages=None) -> SparseStep:
     """layers: synth.sparse_decoder_workload(...) output; batch * q_len from 1 to
     16; rope: (cos, sin) fp32 [max_pos][rot / 2] or None; share: another
     SparseStep of the same layers, batch and cache (with another q_len) whose weights,
-    tables, caches, lengths and pool this one uses; cache_bits: 16, or 4 with
-    k_factor and v_factor (see paged_kv4); pool_pages: pages that the sequences share
+    tables, caches with their factors, lengths and pool this one uses; cache_bits: 16, or 4 with
+    k_factor and v_factor (see paged_kv4; 1 by default); pool_pages: pages that the sequences share
     as they grow (None: each sequence has the pages of its whole table).  Per layer
       h += y (of the layer before); x = norm_attn(h); q, k, v = W x;
       norm the heads of q and k (layers with norm_q and norm_k), rotate them,
@@ -397,12 +397,15 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
                 raise ValueError("cache_bits 4: heads of a multiple of 16")
             part = lambda width: new(pages, kv_heads, page_size, width, dtype=torch.uint8).transpose(1, 2)
             caches = [(part(dim // 2), part(dim // 2), part(dim // 16), part(dim // 16)) for _ in layers]
+        factors = tuple(1.0 if f is None else f for f in (k_factor, v_factor))
         final = (torch.ones(hidden, dtype=f16) if final_norm is None else final_norm).to(device)
         cos, sin = (None, None) if rope is None else (t.to(device) for t in rope)
     else:
         lens, table, caches = share.seq_lens, share.block_table, share.caches
         pool, state = share.pool, share.pool_state
-        weights, scales, final, cos, sin = share.keep[0]
+        weights, scales, final, cos, sin, factors = share.keep[0]
+        if any(f is not None and f != g for f, g in zip((k_factor, v_factor), factors)):
+            raise ValueError("share: a cache with other factors")
         page_size = caches[0][0].shape[1]
     slots = positions = plan = plan_ws = None
     if pool is not None:
@@ -415,7 +418,7 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
                                     (attention4, attn4_decode, attn4_workspace_bytes))
     for W, S, cache in zip(weights, scales, caches):
         kv = (paged_kv(*cache, table, lens) if cache_bits == 16 else
-              paged_kv4(*cache, table, lens, k_factor=k_factor, v_factor=v_factor))
+              paged_kv4(*cache, table, lens, k_factor=factors[0], v_factor=factors[1]))
         t = {"x": new(M, hidden), "q": new(M, heads * dim), "k": new(M, kv_heads * dim), "v": new(M, kv_heads * dim),
              "q_rot": new(M, heads * dim), "att": new(M, heads * dim), "o": new(M, hidden),
              "h": new(M, hidden, dtype=f32), "h_mid": new(M, hidden, dtype=f32), "x_mid": new(M, hidden),
@@ -471,5 +474,5 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
         some = page_plan(lens, table, pool, state, page_size, new_lens=torch.zeros_like(lens))
         end_ws = new(max(pages_workspace_bytes(some), 16), dtype=torch.uint8)
     return SparseStep(run, first, h_out, x_out, lens, table, caches, views,
-                      [(weights, scales, final, cos, sin), ws_a, ws_m, ws_l, share, plan_ws, end_ws],
+                      [(weights, scales, final, cos, sin, factors), ws_a, ws_m, ws_l, share, plan_ws, end_ws],
                       end if pool is not None else None, pool, state, slots, positions)

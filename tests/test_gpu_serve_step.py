@@ -205,3 +205,23 @@ def test_the_example_decodes_the_same_in_a_graph(prompt, bits, pool, head_norms,
         assert (a["rank"] == 0).all() and torch.equal(a["top_ids"][:, 0], runs[0][0])
         assert torch.equal(a["top_logprobs"][:, 0], a["logprob"].view(-1))
         assert (a["top_logprobs"][:, 1:] <= a["top_logprobs"][:, :-1]).all() and (a["entropy"] > 0).all()
+
+
+def test_a_step_that_shares_a_cache_takes_its_factors():
+    need_gpu()
+    layers, rope = _layers(), synth.rotary_tables(64, DIM)
+    one = _step(4, 1, 1, 4, rope, layers)
+    build = lambda **kw: plans.sparse_decoder_step(layers, DEV, HEADS, KV_HEADS, TOP_K, q_len=11, rope=rope, share=one,
+                                                   max_pages=4, cache_bits=4, **kw)
+    many = build()
+    g = torch.Generator().manual_seed(12)
+    for step, n in ((many, 11), (one, 1)):
+        step.h.copy_(torch.randn(n, HIDDEN, generator=g))
+        before, caches = _state(one), [_held(c) for c in one.caches]
+        step.run()
+        sync()
+        _check_step(step, before, caches, 4, n, rope, layers)
+    build(k_factor=KF, v_factor=VF)
+    for kw in (dict(k_factor=1.0), dict(v_factor=VF * 2)):
+        with pytest.raises(ValueError):
+            build(**kw)
