@@ -354,7 +354,7 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
     k_factor and v_factor (see paged_kv4; 1 by default); pool_pages: pages that the sequences share
     as they grow (None: each sequence has the pages of its whole table).  Per layer
       h += y (of the layer before); x = norm_attn(h); q, k, v = W x;
-      norm the heads of q and k (layers with norm_q and norm_k), rotate them,
+      norm the heads of q and of k (where a layer has norm_q, norm_k), rotate them,
       k and v into the cache; att = attention; o = W_o att;
       h += o; x = norm_mlp(h); y = experts(x)
     and last h += y; x_out = final_norm(h).  The residual stream stays fp32; the
@@ -428,7 +428,7 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
         out = StepPlan([lin("o", t["att"], t["o"])])
         att = describe(kv, t["q_rot"], t["att"], q_len=q_len, window=window, sinks=sinks)
         where = {"q_len": q_len} if slots is None else {"slots": slots, "positions": positions}
-        if cache_bits == 16 and slots is None and "norm_q" not in W:
+        if cache_bits == 16 and slots is None and not ("norm_q" in W or "norm_k" in W):
             write = (kv_append, append(kv, t["q"], t["k"], t["v"], q_out=t["q_rot"], cos=cos, sin=sin, **where))
         else:
             write = (qkv_append, head_append(kv, t["q"], t["k"], t["v"], q_out=t["q_rot"], cos=cos, sin=sin,

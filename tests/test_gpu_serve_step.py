@@ -225,3 +225,30 @@ def test_a_step_that_shares_a_cache_takes_its_factors():
     for kw in (dict(k_factor=1.0), dict(v_factor=VF * 2)):
         with pytest.raises(ValueError):
             build(**kw)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_layers_that_norm_only_q_or_only_k(bits, which):
+    need_gpu()
+    layers, rope = _layers(), synth.rotary_tables(64, DIM)
+    for L in layers:
+        setattr(L, "norm_" + ("k" if which == "q" else "q"), None)
+    step = _step(bits, 2, 3, None, rope, layers)
+    step.h.copy_(torch.randn(6, HIDDEN, generator=torch.Generator().manual_seed(13)))
+    step.seq_lens += 3
+    step.run()
+    sync()
+    pos, cos, sin = np.tile(np.arange(3), 2), ref.f64(rope[0]), ref.f64(rope[1])
+    for L, t, cache in zip(layers, step.layers, step.caches):
+        rows = lambda n, heads: ref.f64(t[n]).reshape(6, heads, DIM)
+        w_q, w_k = (None if w is None else ref.f64(w) for w in (L.norm_q, L.norm_k))
+        q, eq, k, ek, _ = serve_ref.head_append(rows("q", HEADS), rows("k", KV_HEADS), w_q, w_k, EPS, 0.0, False, pos,
+                                                cos, sin, False)
+        ref.check(rows("q_rot", HEADS), q, eq + ref.U16["f16"] * (np.abs(q) + eq) + ref.TINY["f16"], "q")
+        held = _held(cache)[0].reshape(2, 4 * PAGE, KV_HEADS, DIM)[:, :3].reshape(6, KV_HEADS, DIM)
+        if bits == 4:
+            w = [serve_ref.coded(a, e, KF) for a, e in zip(k, ek)]
+            ref.check(held, np.stack([a for a, _ in w]), np.stack([b for _, b in w]), "k")
+        else:
+            ref.check(held, k, ek + ref.U16["f16"] * (np.abs(k) + ek) + ref.TINY["f16"], "k")
