@@ -260,7 +260,8 @@ static dg_status check_plan(const dg_page_plan& op) {
     const Area in[] = {{op.lens, B}, {op.pool_state, 8}, {op.new_lens, B}};
     for (const Area& o : out) {
         for (const Area& i : in)
-            if (overlap(o.p, o.bytes, i.p, i.bytes) && !(o.p == i.p && &o - out == &i - in)) return DG_ERR_INVALID_ARG;
+            if (overlap(o.p, o.bytes, i.p, i.bytes) && !(o.p == i.p && &o - out == &i - in && &i - in < 2))
+                return DG_ERR_INVALID_ARG;
         for (const Area& x : out)
             if (&x != &o && overlap(o.p, o.bytes, x.p, x.bytes)) return DG_ERR_INVALID_ARG;
     }

@@ -284,3 +284,10 @@ def test_builders_refuse_sizes_past_32_bits():
         dg.kv4_rows(kv, half(), slots=slots)
     with pytest.raises(dg.DGError):
         dg.head_append(kv, None, half(), half(), slots=slots, positions=meta(big))
+
+
+def test_only_lengths_and_state_may_be_their_own_outputs(lib):
+    f = lambda **kw: lib.dg_assign_pages(ctypes.byref(_plan(**kw)), A + 0x900000, 1 << 30, None)
+    for at in (D, C, E, G, H, H + 4096, H + 8192):      # what is written
+        assert f(new_lens=at) == INVALID
+    assert f(lens=G, lens_out=C, pool_state_out=G) == INVALID and f(pool_state=C, lens_out=C) == INVALID
