@@ -600,6 +600,11 @@ def moe_forward(op, ws, stream=None):
 
 # ---- a serving step -----------------------------------------------------------------
 
+def _i32(where, *numbers):
+    """Whole numbers that a 32-bit field would cut off without a word."""
+    _fits(all(-2 ** 31 <= n < 2 ** 31 for n in numbers), where)
+
+
 def _paging(block_table, seq_lens, where):
     """batch, max_pages and table stride of a block table int32 [batch][max_pages]."""
     import torch
@@ -712,6 +717,7 @@ def attention4(kv, q, out, lse=None, q_len=1, scale=None, window=0, sinks=0):
     """Describes attn4_decode over a paged_kv4; the rest as for attention."""
     import torch
     where, dt = "attention4", _kv_dtype(kv)
+    _i32(where, window, sinks)
     _fits(q_len > 0, where)
     tokens, dim = kv.batch * q_len, kv.head_dim
     heads = q.numel() // (tokens * dim)
@@ -740,6 +746,7 @@ def page_plan(lens, block_table, pool, pool_state, page_size, new_lens=None, new
     output; starts int32 [batch + 1], slots int64 and positions int32 [tokens] or None."""
     import torch
     where = "page_plan"
+    _i32(where, page_size, new_len)
     batch, max_pages, stride = _paging(block_table, lens, where)
     lens_out = lens if lens_out is None else lens_out
     pool_state_out = pool_state if pool_state_out is None else pool_state_out

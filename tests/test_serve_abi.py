@@ -291,3 +291,20 @@ def test_only_lengths_and_state_may_be_their_own_outputs(lib):
     for at in (D, C, E, G, H, H + 4096, H + 8192):      # what is written
         assert f(new_lens=at) == INVALID
     assert f(lens=G, lens_out=C, pool_state_out=G) == INVALID and f(pool_state=C, lens_out=C) == INVALID
+
+
+def test_builders_refuse_whole_numbers_past_32_bits():
+    """A page of 2^32 + 16 positions is not one of 16, a window of 2^32 not none."""
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32)
+    f16 = lambda *shape: torch.zeros(shape, dtype=torch.float16)
+    codes = lambda w: torch.zeros(4, 16, 1, w, dtype=torch.uint8)
+    kv = dg.paged_kv4(codes(8), codes(8), codes(1), codes(1), i32(2, 4), i32(2))
+    plan = lambda page=16, **kw: dg.page_plan(i32(2), i32(2, 4), i32(8), i32(2), page, **kw)
+    attn = lambda **kw: dg.attention4(kv, f16(2, 1, 16), f16(2, 1, 16), **kw)
+    assert plan(new_len=-2 ** 31).new_len == -2 ** 31 and plan(2 ** 31 - 1).page_size == 2 ** 31 - 1
+    assert attn(window=2 ** 31 - 1, sinks=2 ** 31 - 1).window == 2 ** 31 - 1
+    for build in (lambda: plan(2 ** 32 + 16), lambda: plan(2 ** 31), lambda: plan(new_len=2 ** 32 + 1),
+                  lambda: plan(new_len=-2 ** 32), lambda: attn(window=2 ** 32), lambda: attn(window=2 ** 32 + 100),
+                  lambda: attn(sinks=2 ** 32 + 4), lambda: attn(sinks=-2 ** 32)):
+        with pytest.raises(dg.DGError):
+            build()
