@@ -473,10 +473,11 @@ __global__ void __launch_bounds__(256) k_kv4_read(const ReadParams p) {
             uint16_t* to = static_cast<uint16_t*>(which ? op.v : op.k);
             if (!to) continue;
             to += t * (which ? op.v_stride : op.k_stride) + (long long)h * kv.head_dim + c * 8;
-            const float s = e4m3_f32(byte[which]) * (which ? kv.v_factor : kv.k_factor);
+            // code times scale is exact; scale times factor might pass fp32 beside a code of zero
+            const float s = e4m3_f32(byte[which]), factor = which ? kv.v_factor : kv.k_factor;
             float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = (float)((int)(word[which] << (28 - 4 * e)) >> 28) * s;
+            for (int e = 0; e < 8; ++e) f[e] = (float)((int)(word[which] << (28 - 4 * e)) >> 28) * s * factor;
             if (((uintptr_t)to & 15) == 0) {
                 *reinterpret_cast<uint4*>(to) = pack8<BF16>(f);
             } else {

@@ -337,3 +337,26 @@ def test_many_tokens(bits, ftype, heads, kvh, dim, rot, inter, layer, tokens):
     got = c.check()
     if heads:
         assert torch.equal(c.run(in_place=True)["q"], got["q"])
+
+
+@pytest.mark.parametrize("ftype", ["f16", "bf16"])
+@pytest.mark.parametrize("factor", [1e37, 4e36, 1e33, 1.0, 1e-30, 1e-37])
+def test_read_with_factors_at_the_ends(ftype, factor):
+    """Codes of zero are zeros under every scale that is a number, also where scale and factor pass fp32."""
+    need_gpu()
+    r = np.random.RandomState(13)
+    codes = torch.from_numpy(r.choice([0, 0x10, 0x0F, 0x80, 0x71, 0x90], (5, 16, 2, 32)).astype(np.uint8))
+    scales = torch.from_numpy(r.choice([0, 1, 0x38, 0x7D, 0x7E, 0xFE, 0x7F], (5, 16, 2, 4)).astype(np.uint8))
+    table, lens = torch.arange(5, dtype=torch.int32, device=DEV).view(1, 5), torch.tensor([80], dtype=torch.int32, device=DEV)
+    c, s = codes.to(DEV), scales.to(DEV)
+    kv = dg.paged_kv4(c, c, s, s, table, lens, dtype=DT[ftype], k_factor=factor, v_factor=factor)
+    out = [torch.full((80, 2, 64), 3.0, dtype=DT[ftype], device=DEV) for _ in "kv"]
+    dg.kv4_read(dg.kv4_rows(kv, *out, q_len=80))
+    sync()
+    want = serve_ref.decode4(codes.numpy(), scales.numpy(), float(np.float32(factor))).reshape(80, 2, 64)
+    most = torch.finfo(DT[ftype]).max * (1 + ref.U16[ftype])       # rounds to infinity from here on
+    with np.errstate(invalid="ignore"):
+        want = np.where(np.abs(want) >= most, np.copysign(np.inf, want), want)
+    bound = ref.U16[ftype] * np.abs(np.where(np.isfinite(want), want, 0)) * 1.001 + ref.TINY[ftype]
+    for t in out:
+        ref.check(ref.f64(t), want, bound, "read")
