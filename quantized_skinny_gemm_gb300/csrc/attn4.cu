@@ -76,7 +76,6 @@ struct Attn4Params {
     uint32_t page_stride, token_stride, head_stride;                     // of codes, in 8 bytes
     uint32_t scale_page_stride, scale_token_stride, scale_head_stride;   // bytes
     float c2;                     // |scale| k_factor log2(e) 16; 0 for a scale of zero
-    float out_factor;             // 16 v_factor
     int wide;                     // code rows in pieces of 16 bytes, not 8
     int runs;                     // and sixteen keys of a stage lie in one page
     int scale_piece;              // bytes that scales are copied by: 16, 8, 4; 1: by ordinary loads
@@ -703,9 +702,10 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
                 v[6] = fmaf(f, y.z, v[6]), v[7] = fmaf(f, y.w, v[7]);
             }
             if (whole) {
+                // (the factor last: its product with the sum or with the sum's reciprocal might leave fp32's range)
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-                for (int x = 0; x < 8; ++x) v[x] *= inv * p.out_factor;
+                for (int x = 0; x < 8; ++x) v[x] = v[x] * inv * p.a.out_factor;
                 const int tok = row / G, h = hk * G + row - tok * G;
                 const long long t = (long long)cur_b * op.q_len + tok;
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(op.out) + t * op.out_stride +
@@ -717,10 +717,9 @@ __global__ void __launch_bounds__(kAttnThreads, Attn4Shape<DP, RT>::kCtas) k_att
                     part[r] = top;
                     part[S::kRows + r] = sum;
                 }
-                const float f = p.out_factor;
                 float4* dst = reinterpret_cast<float4*>(part + 2 * S::kRows + r * DP + d);
-                dst[0] = make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
-                dst[1] = make_float4(v[4] * f, v[5] * f, v[6] * f, v[7] * f);
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
             }
         }
         if (!more) return;
@@ -795,7 +794,7 @@ static cudaError_t launch_attn4_t(const dg_attn4& op, void* ws, cudaStream_t s) 
     p.scale_token_stride = (uint32_t)op.kv.scale_token_stride;
     p.scale_head_stride = (uint32_t)op.kv.scale_head_stride;
     p.c2 = op.scale == 0.f ? 0.f : fmaxf(fabsf(op.scale) * kLog2e * 16.f * op.kv.k_factor, FLT_MIN);
-    p.out_factor = 16.f * op.kv.v_factor;
+    p.a.out_factor = 16.f * op.kv.v_factor;
     const uintptr_t rows = (uintptr_t)op.kv.k | (uintptr_t)op.kv.v | (uintptr_t)op.kv.page_stride |
                            (uintptr_t)op.kv.token_stride | (uintptr_t)op.kv.head_stride;
     p.wide = rows % 16 == 0 && op.kv.head_dim % 32 == 0;

@@ -25,6 +25,7 @@ struct AttnParams {
     int2* info;          // [units] a unit's first part and the number of its parts
     float* part;         // [grid][2] parts of a row group
     FastDiv page_size;
+    float out_factor;    // of the sums over the weights' sum: 1, or what a 4-bit cache's values are counted in
 };
 // Floats of a part: a maximum and a sum for each row, then the rows.
 constexpr int part_floats(int rows, int dp) { return rows * (dp + 2); }
@@ -270,7 +271,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
                                                         (long long)h * D);
 #pragma unroll
             for (int x = 0; x < kPairs; ++x)
-                if (x * 64 + lane * 2 < D) out[x * 32 + lane] = pair_16<BF16>(v[x].x * inv, v[x].y * inv);
+                if (x * 64 + lane * 2 < D)
+                    out[x * 32 + lane] = pair_16<BF16>(v[x].x * inv * p.out_factor, v[x].y * inv * p.out_factor);
             if (lane == 0 && op.lse)
                 op.lse[t * op.heads + h] = lse_of<W16>(top, sum);
         }

@@ -548,6 +548,7 @@ static cudaError_t launch_attn_t(const dg_attn& op, void* ws, cudaStream_t s) {
     p.info = never_split(op) ? nullptr : static_cast<int2*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + info_bytes(op, p.groups));
     p.page_size = fast_div((uint32_t)op.kv.page_size);
+    p.out_factor = 1.f;
     const void* fn = (const void*)k_attn<BF16, DP, RT>;
     cudaError_t e = tc::smem_attr_once(fn, S::kSmem);
     if (e != cudaSuccess) return e;

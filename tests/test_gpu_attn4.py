@@ -316,3 +316,16 @@ def test_scales_anywhere_and_codes_at_eight_bytes(dim, off):
     sync()
     ro, _, bo, _ = want(cache, table, lens, q)
     ref.check(ref.f64(out), ro, bo, "odd places")
+
+
+@pytest.mark.parametrize("vf,lo,hi", [(1e36, 0x01, 0x18), (1e37, 0x01, 0x08), (3e-37, 0x60, 0x7F), (1e-36, 0x38, 0x40),
+                                      (1e30, 0x20, 0x38)])
+@pytest.mark.parametrize("lens", [[20000], [100, 5000, 3], [40]])
+def test_value_factors_at_the_ends(vf, lo, hi, lens):
+    """Values that bf16 holds: neither the weights' sum in front of the factor nor the factor over that sum may leave
+    fp32's range, in sequences of one part and of many."""
+    need_gpu()
+    cache, table = pool(lens, 16, 1, 128, 21, lo=lo, hi=hi)
+    cache["ks"] = torch.full_like(cache["ks"], 0x28)
+    q = query(len(lens), 4, 128, torch.bfloat16, 22)
+    check(cache, table, lens, q, vf=vf)
