@@ -10,6 +10,7 @@ once; every activation a step reads lives in one input arena and every result
 it writes in one output arena (256-byte aligned views), so moving a step's
 inputs in and its results out is one copy each way.
 """
+import contextlib
 from dataclasses import dataclass, field
 from typing import Dict, List, Optional
 
@@ -326,7 +327,10 @@ class SparseStep:
     A sequence that the pool or its table has no room for stays as it is (its
     positions are -1) and its rows of the outputs mean nothing; end(ended), int32
     [batch], gives back the pages of the sequences where it holds -1 (0: the
-    sequence goes on)."""
+    sequence goes on).  Every run takes pages for q_len tokens of every sequence, also
+    of one that ended, which so begins anew; with new_lens, int32 [batch], for those
+    where it holds q_len: 0 leaves a sequence as it is (its positions are -1, its rows of
+    the outputs mean nothing), -1 ends it."""
     run: object
     h: torch.Tensor                            # fp32 [batch * q_len][hidden]
     h_out: torch.Tensor                        # fp32
@@ -342,17 +346,28 @@ class SparseStep:
     pool_state: Optional[torch.Tensor] = None
     slots: Optional[torch.Tensor] = None       # int64 and int32 [batch * q_len]: where the last step's tokens went
     positions: Optional[torch.Tensor] = None
+    new_lens: Optional[torch.Tensor] = None
+
+
+def _on(stream, device):
+    """torch's own launches on the stream that run() was given."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
 
 
 def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None, batch=1, q_len=1,
                         page_size=64, max_pages=16, window=0, sinks=0, group=32, rope=None,
-                        share=None, cache_bits=16, k_factor=None, v_factor=None, pool_pages=None) -> SparseStep:
+                        share=None, cache_bits=16, k_factor=None, v_factor=None, pool_pages=None,
+                        new_lens=None) -> SparseStep:
     """layers: synth.sparse_decoder_workload(...) output; batch * q_len from 1 to
     16; rope: (cos, sin) fp32 [max_pos][rot / 2] or None; share: another
     SparseStep of the same layers, batch and cache (with another q_len) whose weights,
     tables, caches with their factors, lengths and pool this one uses; cache_bits: 16, or 4 with
     k_factor and v_factor (see paged_kv4; 1 by default); pool_pages: pages that the sequences share
-    as they grow (None: each sequence has the pages of its whole table).  Per layer
+    as they grow (None: each sequence has the pages of its whole table); new_lens: with a pool,
+    int32 [batch] on the device, read by each run: q_len for a sequence that takes its tokens, 0 for an idle one, -1
+    for one that ends (None: q_len for all; a sharing step has its own).  Per layer
       h += y (of the layer before); x = norm_attn(h); q, k, v = W x;
       norm the heads of q and of k (where a layer has norm_q, norm_k), rotate them,
       k and v into the cache; att = attention; o = W_o att;
@@ -370,6 +385,9 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
         raise ValueError("share: another kind of cache")
     if pool_pages is not None and (pool_pages < 1 or share is not None):
         raise ValueError("pool_pages: a page at least; with share, the other step's pool is used")
+    if new_lens is not None and ((pool_pages is None and (share is None or share.pool is None)) or
+                                 new_lens.dtype != i32 or new_lens.numel() != batch or not new_lens.is_contiguous()):
+        raise ValueError("new_lens: int32 [batch], with a pool")
     hidden = layers[0].q.shape[1]
     dim = layers[0].q.shape[0] // heads
     for L in layers:
@@ -407,10 +425,24 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
         if any(f is not None and f != g for f, g in zip((k_factor, v_factor), factors)):
             raise ValueError("share: a cache with other factors")
         page_size = caches[0][0].shape[1]
-    slots = positions = plan = plan_ws = None
+    slots = positions = plan = plan_ws = lay_out = None
     if pool is not None:
         slots, positions = new(M, dtype=torch.int64), new(M, dtype=i32)
-        plan = page_plan(lens, table, pool, state, page_size, new_len=q_len, slots=slots, positions=positions)
+        if new_lens is None:
+            plan = page_plan(lens, table, pool, state, page_size, new_len=q_len, slots=slots, positions=positions)
+        else:
+            # The map counts on from one sequence that takes tokens to the next; a step's rows are q_len a sequence.  The
+            # map's last place is behind all tokens and holds -1.
+            starts, of_map = new(batch + 1, dtype=i32), (new(M + 1, dtype=torch.int64), new(M + 1, dtype=i32))
+            plan = page_plan(lens, table, pool, state, page_size, new_lens=new_lens, starts=starts, slots=of_map[0],
+                             positions=of_map[1])
+            token, at = torch.arange(q_len, dtype=i32, device=device), new(batch, q_len, dtype=i32)
+
+            def lay_out():
+                torch.add(starts[:batch, None], token, out=at)
+                at.masked_fill_(token >= new_lens.view(batch, 1), M).clamp_(max=M)
+                for a, b in zip(of_map, (slots, positions)):
+                    torch.index_select(a, 0, at.view(M), out=b)
         plan_ws = new(max(pages_workspace_bytes(plan), 16), dtype=torch.uint8)
     first = h = new(M, hidden, dtype=f32)
     y, ops, views, attn_ws, moe_ws, lin_ws = None, [], [], 0, 0, 0
@@ -456,6 +488,9 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
     def run(stream=None):
         if plan is not None:
             assign_pages(plan, plan_ws, stream=stream)
+            if lay_out is not None:
+                with _on(stream, device):
+                    lay_out()
         for pre, qkv, (put, app), att, out, mid, experts in ops:
             norm_residual(pre, stream=stream)
             decode_step_weights(qkv, ws_l, stream=stream)
@@ -475,4 +510,4 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
         end_ws = new(max(pages_workspace_bytes(some), 16), dtype=torch.uint8)
     return SparseStep(run, first, h_out, x_out, lens, table, caches, views,
                       [(weights, scales, final, cos, sin, factors), ws_a, ws_m, ws_l, share, plan_ws, end_ws],
-                      end if pool is not None else None, pool, state, slots, positions)
+                      end if pool is not None else None, pool, state, slots, positions, new_lens)

@@ -252,3 +252,87 @@ def test_layers_that_norm_only_q_or_only_k(bits, which):
             ref.check(held, np.stack([a for a, _ in w]), np.stack([b for _, b in w]), "k")
         else:
             ref.check(held, k, ek + ref.U16["f16"] * (np.abs(k) + ek) + ref.TINY["f16"], "k")
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("batch,q_len,pool_pages", [(1, 1, 3), (4, 1, 7), (3, 4, 6), (2, 8, 8)])
+def test_idle_sequences(bits, batch, q_len, pool_pages):
+    """Sequences that take tokens, rest, end or are refused, in any order, eagerly and by a graph: an idle one keeps its
+    pages, its length and its cache, and takes nothing."""
+    need_gpu()
+    layers, rope = _layers(1), synth.rotary_tables(64, DIM)
+    T, M = batch * q_len, batch * q_len
+    runs = []
+    for graph in (False, True):
+        new = torch.full((batch,), q_len, dtype=torch.int32, device=DEV)
+        step = _step(bits, batch, q_len, pool_pages, rope, layers, new_lens=new)
+        assert step.new_lens is new
+        call = step.run
+        if graph:
+            captured = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(captured):
+                step.run()
+            call = captured.replay
+        elif batch == 4:                       # another stream, by its handle
+            side = torch.cuda.Stream()
+            call = lambda: (torch.cuda.synchronize(), step.run(stream=side.cuda_stream))
+        r, g, seen = np.random.RandomState(14), torch.Generator().manual_seed(15), []
+        for turn in range(30):
+            asked = r.choice([q_len, 0, -1], batch, p=[0.6, 0.3, 0.1])
+            if turn < 2:
+                asked[:] = [0, q_len][turn]
+            new.copy_(torch.from_numpy(asked).int())
+            step.h.copy_(torch.randn(M, HIDDEN, generator=g))
+            before, caches = _state(step), [_held(c) for c in step.caches]
+            call()
+            sync()
+            want = serve_ref.pages(before[0], asked, before[1], before[2], before[3], PAGE, T + 1)
+            for got, w in zip(_state(step), want):
+                assert np.array_equal(got, w)
+            lens, table, starts = want[0], want[1], want[4]
+            slots, pos = np.full(T, -1, np.int64), np.full(T, -1, np.int64)
+            for b in np.flatnonzero(asked > 0):
+                slots[b * q_len:(b + 1) * q_len] = want[5][starts[b]:starts[b] + q_len]
+                pos[b * q_len:(b + 1) * q_len] = want[6][starts[b]:starts[b] + q_len]
+            assert np.array_equal(step.slots.cpu().numpy(), slots) and np.array_equal(step.positions.cpu().numpy(), pos)
+            grown = lens > np.maximum(before[0], 0)
+            assert (grown == ((asked > 0) & (lens != before[0]))).all()
+            t, written = step.layers[0], slots >= 0
+            rows = lambda n, heads: ref.f64(t[n]).reshape(T, heads, DIM)
+            now = _held(step.caches[0])
+            for name, held, old, f in (("k", now[0], caches[0][0], KF), ("v", now[1], caches[0][1], VF)):
+                flat, was = (c.reshape(-1, KV_HEADS, DIM) for c in (held, old))
+                rest = np.setdiff1d(np.arange(len(flat)), slots[written])
+                assert np.array_equal(flat[rest], was[rest]), name + ": a place that no token owns"
+                if name == "v" and written.any():
+                    x = rows("v", KV_HEADS)[written]
+                    w = [serve_ref.coded(a, 0 * a, f) for a in x] if bits == 4 else [(a, 0 * a) for a in x]
+                    ref.check(flat[slots[written]], np.stack([a for a, _ in w]), np.stack([b for _, b in w]), name)
+            args = (rows("q_rot", HEADS), now[0], now[1], table, lens, q_len, DIM ** -0.5)
+            ro, _, bo, _ = serve_ref.attention4(*args) if bits == 4 else ref.attention(*args)
+            served = np.repeat(grown, q_len)
+            ref.check(rows("att", HEADS)[served], ro[served], bo[served], "attention")
+            seen.append([step.slots.clone(), step.seq_lens.clone()])
+        assert len({tuple(s[1].tolist()) for s in seen}) > 5
+        runs.append(seen)
+    for a, b in zip(*runs):   # (products of eight rows and more round differently while a graph is captured)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_what_new_lens_may_be():
+    need_gpu()
+    layers, rope = _layers(1), synth.rotary_tables(64, DIM)
+    t = lambda *a, dtype=torch.int32: torch.zeros(a, dtype=dtype, device=DEV)
+    for pool, new in ((None, t(2)), (4, t(3)), (4, t(2, dtype=torch.int64)), (4, t(4)[::2])):
+        with pytest.raises(ValueError):
+            _step(4, 2, 1, pool, rope, layers, new_lens=new)
+    one = _step(4, 2, 1, 4, rope, layers)
+    many = _step(4, 2, 5, None, rope, layers, share=one, new_lens=t(2))
+    many.run()
+    sync()
+    assert one.seq_lens.tolist() == [0, 0] and one.pool_state.tolist() == [0, 4]
+    assert (many.positions == -1).all() and (many.slots == -1).all()
+    many.new_lens[1] = 1000                    # more than a step's rows: nothing is read past them
+    many.run()
+    sync()
+    assert one.seq_lens.tolist() == [0, 0]
