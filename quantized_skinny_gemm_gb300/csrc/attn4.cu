@@ -23,10 +23,12 @@
 //    exchange only when that has grown by 2^8.
 //
 // Measured: 200001 positions of 8 x 128, 32 heads, bf16: 68 us with the join, 3.4 TB/s; 50000: 26;
-// 16 sequences of 1..8191, 2 x 128: 12; 100 positions: 5.3.  Long calls are bound by unpacking: 370
+// 16 sequences of 1..8191, 2 x 128: 12; 100 positions: 5.3.  Long calls fill no unit: 370
 // instructions for 16 keys of 128 dims, of which 64 LOP3, 64 HFMA2, 64 PRMT and shifts and 24
-// matrix instructions; half of the issue slots are taken (ALU 40 %, tensor pipe 26 %), and 8, 12 or 16 warps an
-// SM take the same time.  Short ones are bound by the chain length -> page -> key -> sum, and by the join.
+// matrix instructions, in chains that leave two warps a scheduler half of the issue slots (ALU 40 %, tensor pipe 26 %, DRAM
+// 44 %); 8, 12 or 16 warps an SM take the same time.  Short ones are bound by the chain length -> page -> key -> sum, and by
+// the join.  Several tokens (four row tiles: 251 registers at 64 dims; 255 and 60 bytes of spills at 128): 8 tokens of 8
+// sequences on windows of 4096, 32 heads on 8 of 64: 27.5 us, 31 % of the issue slots, four or five stages a warp.
 #include "attn_common.cuh"
 
 namespace dg {

@@ -11,7 +11,9 @@
 // rotation apart a lane has four dims of either half, so that it turns them by itself, and lanes
 // change to neighbouring dims just before a key becomes codes.  (Eight neighbouring dims, and
 // the other of each pair by an exchange: 57 us for 6825 tokens of 32 + 2 x 8 into 4 bits and 47 into 16;
-// these 46 and 35, with 72 and 64 registers instead of 80.)  A 4-bit value
+// these 47 and 36.  The 72 and 64 registers are what seven and eight CTAs an SM leave: into 4 bits the kernels of four
+// rounds spill 12 to 68 bytes a thread, into 16 bits none, or 36 to 64 where pairs are neighbours or absent; 4 % of the
+// instructions at 8 tokens of 256 sequences of 32 + 2 x 8 heads, interleaved, 16 us.)  A 4-bit value
 // is divided by its scale with one rounding, not just multiplied by a reciprocal: 16-bit inputs meet halves of
 // a scale often enough for ties to show (they go to the even code).
 #include "elem.cuh"
@@ -342,7 +344,9 @@ __global__ void __launch_bounds__(kHeadThreads, kRounds == 1 || !Q4 ? 8 : 7) k_h
         const float step = odd ? 0.f : e4m3_f32(byte) * factor;
         uint32_t word = 0;
         if (step > 1e-30f && step < 1e30f && top < 7.49f * step) {
-            // x / step rounded once: a quotient by the reciprocal and its remainder.  Added to 1.5 2^23 it
+            // x / step rounded once: a quotient by the correctly rounded reciprocal, corrected by its remainder, which
+            // one fused operation gives exactly (P. Markstein, Computation of elementary functions on the IBM RISC
+            // System/6000 processor, IBM J. Res. Dev. 34, 1990).  Added to 1.5 2^23 it
             // leaves the nearest whole number, ties to even, in the last bits; the sum of these times
             // 16^e with 8 added to each, and the eights taken off again, is the codes.
             const float inv = __frcp_rn(step);
@@ -437,8 +441,8 @@ struct ReadParams {
     FastDiv by_q_len, by_page, by_token, by_head;
 };
 
-// Bound by the chain slot -> codes -> store (6825 tokens of 2 x 8 heads of 128: 11 us, of which the bytes are
-// 5): as many threads as pieces.
+// Bound by issue (79 % of the slots in the middle of 6825 tokens of 2 x 8 heads of 128: 11 us, of which the bytes are 5; a
+// piece of eight values finds its token, head and page by itself): as many threads as pieces.
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_kv4_read(const ReadParams p) {
     griddep_launch_dependents();

@@ -4,14 +4,15 @@
 // A row (or a part of it, where the rows are few) is a CTA's, taken in tiles of 512
 // 16-byte vectors, four a thread, the next tile loading while one is used.  Small CTAs, eight an SM
 // (fp32: five): while one looks for its row's best the others stream (2047 x 128255 bf16 with
-// everything and one alternative: 101 us, with four CTAs of 256 threads 110; 97, 5.4 TB/s, since lanes
+// everything and one alternative: 101 us, with four CTAs of 256 threads 110; 95, 5.5 TB/s, since lanes
 // take one base before their sums are added).  Bound by issue; one row of 128256 fp32 with five alternatives
 // by two launches, 7.9 us.  Each thread
 // keeps a base m and, with c = scale log2(e) and B = m c rounded, the sums l of w = 2^(x c - B)
 // and a of w (x c - B): an exponent is one fused multiply-add, rounded once, B
 // being a number like any other (a softmax of scale c / log2(e), 2^-24 off).  The base
 // follows the maximum only when that has grown by 2^8.  lse = ln 2 (B + log2 l), the entropy is
-// ln 2 (log2 l - a / l), whose terms have the size of the result.  Past |m c| = 2^22, where
+// ln 2 (log2 l - a / l); the base may lie up to 8 below the row's maximum, and then both terms are 8 larger than the
+// result: an entropy near 0 is up to 1e-6 off, not a part of itself.  Past |m c| = 2^22, where
 // B's rounding nears a whole power of two (rows of nothing but masks, mostly), bases stand and the sums are taken
 // again with exponents (x - m) c.  Sums of either kind join by what their weights were counted from, B or m c itself:
 // parts of a row may lie on both sides.
@@ -25,7 +26,7 @@
 // maximum, and that of each sixteenth of its tiles.  The top_k-th largest of 64 groups' maxima is
 // then a floor that about top_k logits of the row reach; the sixteenths that
 // reach it are read once more (from L2, mostly), by all threads at once, and what does is listed.
-// (Each thread its own: 116 us with 20 alternatives instead of 94, and 95 with one.)  Keys are (logit, lowest index)
+// (Sums and 20 alternatives: 94 us, each thread its own sixteenths 116; with one alternative 95 both ways.)  Keys are (logit, lowest index)
 // in one 64-bit number, no two alike: what is chosen depends on no order.  (Lists that each warp kept while it
 // streamed, cut to top_k again and again: 173 us for one alternative and 376 for 20, 2048 x
 // 128256 bf16, where the sums alone take 94.)
@@ -631,7 +632,8 @@ __global__ void __launch_bounds__(kLpJoinThreads) k_logprobs_join(const LpParams
     }
 }
 
-// Rows come in rounds of as many CTAs as the SMs hold.  Those of a last round that would leave half of
+// Rows come in rounds of as many CTAs as the 152 SMs hold (a workspace's size must not depend on the device that asks for
+// it, so this is no question to one; with other numbers of SMs only the time changes).  Those of a last round that would leave half of
 // the places empty, or of a call of so few, are cut into parts.
 struct LpSplit {
     int whole, parts;

@@ -8,9 +8,9 @@
 // sequence by a search over the records and is written by a thread of its own.
 //
 // Bound by latency: small calls are one CTA that keeps the records in shared memory and
-// writes everything itself (64 sequences, a token each: 3.6 us); others two launches, the sums by
-// one CTA and the rest by many (3000 sequences, 2.1 million places: 18 us, 4 of them the bytes, about 6 the
-// sums, the rest search -> table -> store).
+// writes everything itself (64 sequences, a token each: 3.7 us); others two launches, the sums by
+// one CTA and the rest by many (3000 sequences, 2.1 million places: 18.5 us, 4 of them the bytes, about 6 the
+// sums, the rest search -> table -> store, at 56 % of the issue slots).
 #include <climits>
 
 #include "elem.cuh"
@@ -305,6 +305,10 @@ __global__ void __launch_bounds__(256) k_plan_fill(const PlanParams p) {
     plan_fill<false>(p, p.rec, t, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
 }
 
+// One CTA against two launches, us: 64 sequences with a map of 64 places 3.4 and 7.5, of 4096 7.2 and 8.0, of 16384 12.6
+// and 8.0, of 65536 36 and 7.8; 1024 sequences with 1024 places 5.9 and 8.5, with 16384 21 and 9.8.  So the forms cross
+// between 4096 and 8192 places.  Pages that move have no part in the rule, nor in the second launch's size: 64
+// sequences of 131072 tokens that end without a map take 704 and 979, of 4096 25 and 41.
 static bool plan_small(const dg_page_plan& op) {
     return op.batch <= kPlanSmallBatch && op.max_tokens <= kPlanSmallTokens;
 }
