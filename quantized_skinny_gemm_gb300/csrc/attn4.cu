@@ -22,7 +22,7 @@
 //  - A score is checked against the running maximum by each lane for its own keys; lanes
 //    exchange only when that has grown by 2^8.
 //
-// Measured: 200001 positions of 8 x 128, 32 heads, bf16: 68 us with the join, 3.4 TB/s; 50000: 26;
+// Measured: 200001 positions of 8 x 128, 32 heads, bf16: 69 us with the join, 3.3 TB/s; 50000: 26;
 // 16 sequences of 1..8191, 2 x 128: 12; 100 positions: 5.3.  Long calls fill no unit: 370
 // instructions for 16 keys of 128 dims, of which 64 LOP3, 64 HFMA2, 64 PRMT and shifts and 24
 // matrix instructions, in chains that leave two warps a scheduler half of the issue slots (ALU 40 %, tensor pipe 26 %, DRAM

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<TYPE>) k_logprobs(const Lp
         if (nan_token) return v == v || i < tok;
         return v > mine || (v == mine && i < tok);
     };
-    // Vectors before the token's own count what is above `under`, the next number below its logit,
+    // Vectors before the token's own count what is above `below`, the next number below its logit,
     // others what is above the logit itself.  Tokens of NaN or -infinity have their own pass.
     const bool ranked = tok >= 0 && mine > -INFINITY, pass = tok >= 0 && !ranked;
     const uint32_t bits = TYPE == 2 ? __float_as_uint(mine) : pair_16<TYPE == 1>(mine, mine);   // (it has 16 bits)
