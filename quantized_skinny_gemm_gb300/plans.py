@@ -386,8 +386,9 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
     if pool_pages is not None and (pool_pages < 1 or share is not None):
         raise ValueError("pool_pages: a page at least; with share, the other step's pool is used")
     if new_lens is not None and ((pool_pages is None and (share is None or share.pool is None)) or
-                                 new_lens.dtype != i32 or new_lens.numel() != batch or not new_lens.is_contiguous()):
-        raise ValueError("new_lens: int32 [batch], with a pool")
+                                 new_lens.dtype != i32 or new_lens.numel() != batch or not new_lens.is_contiguous() or
+                                 new_lens.device.type != torch.device(device).type):
+        raise ValueError("new_lens: int32 [batch] on the device, with a pool")
     hidden = layers[0].q.shape[1]
     dim = layers[0].q.shape[0] // heads
     for L in layers:
@@ -502,6 +503,8 @@ def sparse_decoder_step(layers, device, heads, kv_heads, top_k, final_norm=None,
         norm_residual(last, stream=stream)
 
     def end(ended, stream=None):
+        if ended.device != lens.device:
+            raise ValueError("end: int32 [batch] on the device")
         op = page_plan(lens, table, pool, state, page_size, new_lens=ended)
         assign_pages(op, end_ws, stream=stream)
     end_ws = None

@@ -336,3 +336,23 @@ def test_what_new_lens_may_be():
     many.run()
     sync()
     assert one.seq_lens.tolist() == [0, 0]
+
+
+def test_lengths_on_the_host_are_refused():
+    """Their address means nothing on the device."""
+    need_gpu()
+    layers, rope = _layers(1), synth.rotary_tables(64, DIM)
+    with pytest.raises(ValueError):
+        _step(4, 2, 1, 4, rope, layers, new_lens=torch.zeros(2, dtype=torch.int32))
+    step = _step(4, 2, 1, 4, rope, layers)
+    with pytest.raises(ValueError):
+        step.end(torch.full((2,), -1, dtype=torch.int32))
+
+
+def test_a_step_on_the_default_stream_by_its_handle():
+    need_gpu()
+    new = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    step = _step(4, 2, 1, 4, synth.rotary_tables(64, DIM), _layers(1), new_lens=new)
+    step.run(stream=torch.cuda.default_stream().cuda_stream)
+    sync()
+    assert step.seq_lens.tolist() == [0, 1] and step.slots.tolist() == [-1, 0] and step.positions.tolist() == [-1, 0]
